@@ -339,6 +339,159 @@ const char* dec_status_string(dec_status s);
 /* Release every device buffer of the engine (synchronises first). NULL is a no-op. */
 void dec_destroy(dec_engine* eng);
 
+/* ------------------------------------------------------------------------------------------
+   Operators beside the engine: a paged KV cache held in 4 bits, attention over it, and
+   log-probabilities. They keep no state of their own: the caller owns every buffer. Unlike the
+   engine's entry points they take no engine, so:
+    - stream == NULL is the legacy default stream; work is queued on `stream`, nothing is
+      synchronised, no call allocates device memory, and every call may be captured into a graph;
+    - the buffers must live on the current CUDA device (DEC_ERR_ARG when the cache's or the
+      logits' buffer does not);
+    - the reason of a failing call is dec_op_error(), one per host thread;
+    - calls that share no buffer they write may run at the same time on several streams. Calls
+      sharing a workspace, a status word's meaning or pages they write must be ordered by the
+      caller. */
+
+/* Reason for the last failing operator call of this host thread ("" if none). */
+const char* dec_op_error(void);
+
+/* A paged KV cache of one layer. pages is n_pages consecutive pages of dec_kvq_page_bytes()
+   bytes, 16-byte aligned; their content is the library's, and no page has to be initialised
+   before it is appended to. A page holds page_tokens positions of every KV head. Each run of 16
+   consecutive values x of a (position, KV head) row is kept as one scale s and 16 codes c:
+   s = max|x| / 7 rounded to nearest even among the values with 3 mantissa and 5 exponent bits
+   (steps of 2^-14 below 2^-11, at most 480), c = x / s rounded to nearest even and clamped to
+   -8 .. 7 (0 where s = 0), the value held is c * s, which bf16 represents exactly. A run with an
+   infinity or NaN is held as NaNs.
+   status (device int32, may be NULL; zero it once) receives DEC_ERR_ARG when a kernel meets a
+   page id outside 0 .. n_pages - 1 or a negative position, and DEC_ERR_CAPACITY when a position
+   lies beyond the page table or the rotation table (the first one met stays). The kernel skips
+   such a row or such positions and touches nothing out of range. */
+typedef struct {
+  void* pages;
+  int32_t n_pages;
+  int32_t page_tokens; /* 16, 32, 64, 128 or 256 */
+  int32_t n_kv_heads;  /* 1 .. 1024 */
+  int32_t head_dim;    /* 64 or 128 */
+  int32_t* status;
+} dec_kvq_cache;
+
+/* The sequences of a call. Token rows are numbered 0 .. n_tokens - 1; sequence b's are
+   cu_tokens[b] .. cu_tokens[b + 1] - 1 (device int32 [batch + 1]; NULL: one row per sequence and
+   n_tokens == batch). Its row j stands at position lengths[b] + j (device int32 [batch]), and
+   position p is in page table[b * table_stride + p / page_tokens] (device int32; max_pages
+   entries of each row are valid). cu_tokens must ascend. Rows before cu_tokens[0] or from cu_tokens[batch] on belong to
+   no sequence: outputs leave them as they were. */
+typedef struct {
+  int32_t batch;
+  int32_t n_tokens;
+  const int32_t* cu_tokens;
+  const int32_t* lengths;
+  const int32_t* table;
+  int32_t max_pages;
+  int64_t table_stride;
+} dec_kvq_seqs;
+
+typedef enum { DEC_BF16 = 0, DEC_F32 = 1 } dec_dtype;
+
+/* Rows of heads: element (row, head, d) at p[row * token_stride + head * head_stride + d]; p
+   16-byte aligned, strides multiples of 16 bytes. */
+typedef struct {
+  void* p;
+  int64_t token_stride;
+  int64_t head_stride;
+} dec_rows;
+
+/* Bytes of one page (0 for a shape the cache does not have). */
+int64_t dec_kvq_page_bytes(int32_t page_tokens, int32_t n_kv_heads, int32_t head_dim);
+
+/* Append the call's keys and values to the cache, in one pass with the per-head RMSNorm and the
+   rotation of queries and keys:
+     q, k, v    rows of n_heads, n_kv_heads, n_kv_heads heads of `dtype` (q.p NULL: none)
+     q_norm, k_norm  device bf16 [head_dim], NULL: no norm. x -> x / sqrt(mean(x^2) + eps) * w
+     rope       device fp32 [rope_len][rotary_dim / 2][2]: cos, sin of position p's angles; NULL
+                (rotary_dim 0): no rotation. The first rotary_dim (a multiple of 16) values of a
+                head are rotated: pair i is (i, i + rotary_dim / 2), or with interleaved != 0
+                (2i, 2i + 1): (a, b) -> (a cos - b sin, a sin + b cos)
+     q_out      bf16 rows (may be q.p itself when that is bf16 with the same strides)
+   Everything is computed in fp32 and rounded once, to bf16 or to the cache's codes. The same
+   position must not be appended twice in one call. */
+typedef struct {
+  dec_dtype dtype;
+  int32_t n_heads;
+  dec_rows q, k, v, q_out;
+  const void* q_norm;
+  const void* k_norm;
+  float eps;
+  const float* rope;
+  int32_t rope_len;
+  int32_t rotary_dim;
+  int32_t interleaved;
+} dec_kvq_append_args;
+dec_status dec_kvq_append(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, const dec_kvq_append_args* args,
+                          void* stream);
+
+/* Read positions back: row j of sequence b receives position lengths[b] + j as bf16 (exact). */
+dec_status dec_kvq_gather(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, const dec_rows* k_out,
+                          const dec_rows* v_out, void* stream);
+
+/* Attention over the cache. Row j of sequence b attends to positions 0 .. lengths[b] + j (causal:
+   its own included, as dec_kvq_append of the same sequences has written it) or 0 ..
+   lengths[b] - 1 (causal == 0: a stored prefix; lse lets the caller join it with attention over
+   other keys). Query head h reads KV head h / (n_heads / n_kv_heads).
+     q, out     bf16 rows of n_heads heads (out may be q)
+     lse        device fp32 [n_tokens][n_heads], may be NULL: natural log of the sum of
+                exp(scale q.k) over the row's positions
+     scale      0: 1 / sqrt(head_dim)
+     max_tokens an upper bound of the rows of one sequence (host); rows beyond it are not computed
+     workspace  16-byte aligned device memory of dec_kvq_attention_workspace() bytes; its content
+                is of no interest before or after the call
+   A row with no position gives out = 0 and lse = -infinity. Scores, softmax statistics and the
+   output sum are fp32; queries enter the products exactly (bf16), probabilities with 11 bits. */
+typedef struct {
+  int32_t n_heads;
+  dec_rows q, out;
+  float* lse;
+  float scale;
+  int32_t causal;
+  int32_t max_tokens;
+  void* workspace;
+  int64_t workspace_bytes;
+} dec_kvq_attention_args;
+dec_status dec_kvq_attention(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, const dec_kvq_attention_args* args,
+                             void* stream);
+/* Workspace bytes for calls with these sizes on the current device (-1 for a refused shape). */
+int64_t dec_kvq_attention_workspace(const dec_kvq_cache* cache, int32_t n_heads, int32_t batch, int32_t max_tokens);
+
+/* Log-probabilities of rows of logits (fp32 or bf16; row r at logits + r * row_stride elements):
+     targets      device int32 [rows], may be NULL; a target outside 0 .. vocab - 1 gives
+                  logprob NaN and rank -1
+     logprob      fp32 [rows]: x[target] - lse, lse = log(sum(exp(x)))
+     rank         int32 [rows]: how many ids come before the target in the order by logit, larger
+                  first, equal logits by lower id
+     entropy      fp32 [rows], nats
+     top_ids, top_logprobs  int32, fp32 [rows][top_n]: the first top_n ids of that order (0 <=
+                  top_n <= DEC_MAX_TOP, <= vocab) and their log-probabilities
+   Each output may be NULL (logprob and rank need targets). Logits of -infinity have probability
+   0; a row with nothing else gives log-probabilities of -infinity and entropy 0. A row with a
+   NaN or +infinity gives NaN log-probabilities and entropy; a NaN orders as -infinity. */
+#define DEC_MAX_TOP 32
+typedef struct {
+  const void* logits;
+  dec_dtype dtype;
+  int32_t rows;
+  int32_t vocab;
+  int64_t row_stride;
+  const int32_t* targets;
+  float* logprob;
+  int32_t* rank;
+  float* entropy;
+  int32_t top_n;
+  int32_t* top_ids;
+  float* top_logprobs;
+} dec_logprobs_args;
+dec_status dec_logprobs(const dec_logprobs_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,8 +7,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdec.so")
-SOURCES = ["dec_engine.cu", "dec_wide.cu"]
-HEADERS = ["dec_common.h", "dec_prims.cuh", "dec_kernel.cuh", "dec_wide.cuh", "dec_wide_host.h"]
+SOURCES = ["dec_engine.cu", "dec_wide.cu", "dec_kvq.cu", "dec_logprobs.cu"]
+HEADERS = ["dec_common.h", "dec_prims.cuh", "dec_kernel.cuh", "dec_wide.cuh", "dec_wide_host.h", "dec_kvq.cuh",
+           "dec_ops.h"]
 
 
 def nvcc() -> str:

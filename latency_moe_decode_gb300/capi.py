@@ -59,6 +59,41 @@ class DecInfo(C.Structure):
                 ("workspace_bytes", C.c_int64), ("launches", C.c_int64), ("wide_min_batch", C.c_int32)]
 
 
+class DecKvqCache(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("n_pages", C.c_int32), ("page_tokens", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("status", C.c_void_p)]
+
+
+class DecKvqSeqs(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("n_tokens", C.c_int32), ("cu_tokens", C.c_void_p), ("lengths", C.c_void_p),
+                ("table", C.c_void_p), ("max_pages", C.c_int32), ("table_stride", C.c_int64)]
+
+
+class DecRows(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class DecKvqAppendArgs(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("n_heads", C.c_int32), ("q", DecRows), ("k", DecRows), ("v", DecRows),
+                ("q_out", DecRows), ("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("eps", C.c_float),
+                ("rope", C.c_void_p), ("rope_len", C.c_int32), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32)]
+
+
+class DecKvqAttentionArgs(C.Structure):
+    _fields_ = [("n_heads", C.c_int32), ("q", DecRows), ("out", DecRows), ("lse", C.c_void_p), ("scale", C.c_float),
+                ("causal", C.c_int32), ("max_tokens", C.c_int32), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_int64)]
+
+
+class DecLogprobsArgs(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("dtype", C.c_int), ("rows", C.c_int32), ("vocab", C.c_int32),
+                ("row_stride", C.c_int64), ("targets", C.c_void_p), ("logprob", C.c_void_p), ("rank", C.c_void_p),
+                ("entropy", C.c_void_p), ("top_n", C.c_int32), ("top_ids", C.c_void_p), ("top_logprobs", C.c_void_p)]
+
+
+DEC_BF16, DEC_F32 = 0, 1
+DEC_MAX_TOP = 32  # include/dec.h
+
 # name -> (restype, argtypes); the exported surface of dec.h
 PROTOTYPES = {
     "dec_validate_cfg": (C.c_int, [C.POINTER(DecModelCfg)]),
@@ -85,6 +120,16 @@ PROTOTYPES = {
     "dec_last_error": (C.c_char_p, [C.c_void_p]),
     "dec_status_string": (C.c_char_p, [C.c_int]),
     "dec_destroy": (None, [C.c_void_p]),
+    "dec_op_error": (C.c_char_p, []),
+    "dec_kvq_page_bytes": (C.c_int64, [C.c_int32, C.c_int32, C.c_int32]),
+    "dec_kvq_append": (C.c_int, [C.POINTER(DecKvqCache), C.POINTER(DecKvqSeqs), C.POINTER(DecKvqAppendArgs),
+                                 C.c_void_p]),
+    "dec_kvq_gather": (C.c_int, [C.POINTER(DecKvqCache), C.POINTER(DecKvqSeqs), C.POINTER(DecRows), C.POINTER(DecRows),
+                                 C.c_void_p]),
+    "dec_kvq_attention_workspace": (C.c_int64, [C.POINTER(DecKvqCache), C.c_int32, C.c_int32, C.c_int32]),
+    "dec_kvq_attention": (C.c_int, [C.POINTER(DecKvqCache), C.POINTER(DecKvqSeqs), C.POINTER(DecKvqAttentionArgs),
+                                    C.c_void_p]),
+    "dec_logprobs": (C.c_int, [C.POINTER(DecLogprobsArgs), C.c_void_p]),
 }
 
 _lib = None

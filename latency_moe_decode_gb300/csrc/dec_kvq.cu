@@ -1,0 +1,258 @@
+// Entry points of the paged 4-bit KV cache (dec_kvq_* of dec.h).
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdio>
+#include <mutex>
+
+#include "dec_kvq.cuh"
+#include "dec_ops.h"
+
+namespace dec {
+
+namespace {
+thread_local char g_op_error[256] = "";
+}
+
+dec_status op_fail(dec_status s, const char* msg) {
+  size_t i = 0;
+  for (; msg[i] && i + 1 < sizeof g_op_error; ++i) g_op_error[i] = msg[i];
+  g_op_error[i] = 0;
+  return s;
+}
+
+dec_status op_cuda(cudaError_t c, const char* what) {
+  char buf[256];
+  snprintf(buf, sizeof buf, "%s: %s", what, cudaGetErrorString(c));
+  return op_fail(c == cudaErrorMemoryAllocation ? DEC_ERR_OOM : DEC_ERR_CUDA, buf);
+}
+
+void op_clear() { g_op_error[0] = 0; }
+
+int op_sms() {
+  static std::mutex mu;
+  static int sms[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms[dev] = 0;
+  return sms[dev];
+}
+
+dec_status op_on_device(const void* p, const char* what) {
+  cudaPointerAttributes a;
+  int dev = -1;
+  cudaError_t ce = cudaGetDevice(&dev);
+  if (ce == cudaSuccess) ce = cudaPointerGetAttributes(&a, p);
+  if (ce != cudaSuccess) {
+    cudaGetLastError();  // (a pointer CUDA does not know, or no device: not a sticky error)
+    return op_cuda(ce, what);
+  }
+  if ((a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) || a.device != dev) {
+    char buf[200];
+    snprintf(buf, sizeof buf, "%s is not memory of the current CUDA device", what);
+    return op_fail(DEC_ERR_ARG, buf);
+  }
+  return DEC_OK;
+}
+
+namespace kvq {
+namespace {
+
+dec_status check_cache(const dec_kvq_cache* c) {
+  if (!c || !c->pages) return op_fail(DEC_ERR_ARG, "cache: NULL");
+  if (c->head_dim < 1 || c->n_kv_heads < 1 || c->page_tokens < 1 || c->n_pages < 1)
+    return op_fail(DEC_ERR_ARG, "cache: sizes must be positive");
+  if (c->head_dim != 64 && c->head_dim != 128) return op_fail(DEC_ERR_UNSUPPORTED, "cache: head_dim must be 64 or 128");
+  if (c->n_kv_heads > 1024) return op_fail(DEC_ERR_UNSUPPORTED, "cache: more than 1024 KV heads");
+  if (dec_kvq_page_bytes(c->page_tokens, c->n_kv_heads, c->head_dim) == 0)
+    return op_fail(DEC_ERR_UNSUPPORTED, "cache: page_tokens must be 16, 32, 64, 128 or 256");
+  if (!op_aligned(c->pages)) return op_fail(DEC_ERR_ARG, "cache: pages must be 16-byte aligned");
+  return DEC_OK;
+}
+
+dec_status check_seqs(const dec_kvq_seqs* s, const dec_kvq_cache* c) {
+  if (!s) return op_fail(DEC_ERR_ARG, "sequences: NULL");
+  if (s->batch < 0 || s->n_tokens < 0 || s->max_pages < 0) return op_fail(DEC_ERR_ARG, "sequences: negative size");
+  if (!s->cu_tokens && s->n_tokens != s->batch)
+    return op_fail(DEC_ERR_ARG, "sequences: without cu_tokens every sequence has one row (n_tokens == batch)");
+  if (s->batch == 0 || s->n_tokens == 0) return DEC_OK;
+  if (!s->lengths || !s->table || s->max_pages == 0) return op_fail(DEC_ERR_ARG, "sequences: lengths and table are needed");
+  if (s->table_stride < 0) return op_fail(DEC_ERR_ARG, "sequences: negative table_stride");
+  if ((long long)s->max_pages * c->page_tokens > INT_MAX - 65536)
+    return op_fail(DEC_ERR_UNSUPPORTED, "sequences: a page table of 2^31 positions or more");
+  return DEC_OK;
+}
+
+dec_status check_rows(const dec_rows* r, dec_dtype t, const char* name) {
+  char buf[120];
+  const int per = t == DEC_F32 ? 4 : 8;
+  if (!r || !r->p) {
+    snprintf(buf, sizeof buf, "%s: NULL", name);
+    return op_fail(DEC_ERR_ARG, buf);
+  }
+  if (!op_aligned(r->p) || r->token_stride % per || r->head_stride % per) {
+    snprintf(buf, sizeof buf, "%s: rows and strides must be multiples of 16 bytes", name);
+    return op_fail(DEC_ERR_ARG, buf);
+  }
+  return DEC_OK;
+}
+
+Cache cache_of(const dec_kvq_cache* c) {
+  Cache k;
+  k.pages = static_cast<uint8_t*>(c->pages);
+  k.n_pages = c->n_pages;
+  k.page_shift = 0;
+  while ((1 << k.page_shift) < c->page_tokens) ++k.page_shift;
+  k.hkv = c->n_kv_heads;
+  k.status = c->status;
+  return k;
+}
+Seqs seqs_of(const dec_kvq_seqs* s) {
+  Seqs k;
+  k.batch = s->batch;
+  k.n_tokens = s->n_tokens;
+  k.max_pages = s->max_pages;
+  k.cu = s->cu_tokens;
+  k.lengths = s->lengths;
+  k.table = s->table;
+  k.table_stride = s->table_stride;
+  return k;
+}
+Rows rows_of(const dec_rows& r) { return Rows{r.p, r.token_stride, r.head_stride}; }
+
+dec_status launched(const char* what) {
+  const cudaError_t ce = cudaGetLastError();
+  return ce == cudaSuccess ? DEC_OK : op_cuda(ce, what);
+}
+
+}  // namespace
+}  // namespace kvq
+}  // namespace dec
+
+using namespace dec;
+using namespace dec::kvq;
+
+extern "C" {
+
+const char* dec_op_error(void) { return g_op_error; }
+
+int64_t dec_kvq_page_bytes(int32_t page_tokens, int32_t n_kv_heads, int32_t head_dim) {
+  if (head_dim != 64 && head_dim != 128) return 0;
+  if (n_kv_heads < 1 || n_kv_heads > 1024) return 0;
+  if (page_tokens < 16 || page_tokens > 256 || (page_tokens & (page_tokens - 1))) return 0;
+  return (int64_t)n_kv_heads * (page_tokens / kGroup) * group_bytes(head_dim);
+}
+
+dec_status dec_kvq_append(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec_kvq_append_args* a, void* stream) {
+  op_clear();
+  if (dec_status st = check_cache(c)) return st;
+  if (dec_status st = check_seqs(s, c)) return st;
+  if (!a) return op_fail(DEC_ERR_ARG, "append: NULL arguments");
+  if (a->dtype != DEC_BF16 && a->dtype != DEC_F32) return op_fail(DEC_ERR_ARG, "append: unknown dtype");
+  const bool has_q = a->q.p != nullptr;
+  if (a->n_heads < 0 || a->n_heads > 16384 || has_q != (a->n_heads > 0))
+    return op_fail(DEC_ERR_ARG, "append: n_heads goes with q");
+  if (a->rotary_dim < 0 || a->rotary_dim > c->head_dim || a->rotary_dim % 16)
+    return op_fail(DEC_ERR_ARG, "append: rotary_dim must be a multiple of 16 within head_dim");
+  if ((a->rotary_dim > 0) != (a->rope != nullptr) || a->rope_len < 0)
+    return op_fail(DEC_ERR_ARG, "append: rope and rotary_dim go together");
+  if (a->rope && !op_aligned(a->rope)) return op_fail(DEC_ERR_ARG, "append: rope must be 16-byte aligned");
+  if ((a->q_norm && !op_aligned(a->q_norm)) || (a->k_norm && !op_aligned(a->k_norm)))
+    return op_fail(DEC_ERR_ARG, "append: norm weights must be 16-byte aligned");
+  if (!(a->eps >= 0.f)) return op_fail(DEC_ERR_ARG, "append: eps must not be negative");
+  if (s->batch == 0 || s->n_tokens == 0) return DEC_OK;
+  if (dec_status st = check_rows(&a->k, a->dtype, "append: k")) return st;
+  if (dec_status st = check_rows(&a->v, a->dtype, "append: v")) return st;
+  if (has_q) {
+    if (dec_status st = check_rows(&a->q, a->dtype, "append: q")) return st;
+    if (dec_status st = check_rows(&a->q_out, DEC_BF16, "append: q_out")) return st;
+  }
+  if (dec_status st = op_on_device(c->pages, "cache: pages")) return st;
+  AppendParams p;
+  p.c = cache_of(c);
+  p.s = seqs_of(s);
+  p.q = rows_of(a->q);
+  p.k = rows_of(a->k);
+  p.v = rows_of(a->v);
+  p.qo = rows_of(a->q_out);
+  p.qn = static_cast<const uint16_t*>(a->q_norm);
+  p.kn = static_cast<const uint16_t*>(a->k_norm);
+  p.rope = a->rope;
+  p.hq = a->n_heads;
+  p.rope_len = a->rope_len;
+  p.rot = a->rotary_dim;
+  p.inter = a->interleaved != 0;
+  p.eps = a->eps;
+  const long long rows = (long long)s->n_tokens * (a->n_heads + 2 * c->n_kv_heads);
+  const long long grid = (rows * (c->head_dim / 8) + 255) / 256;
+  if (grid > INT_MAX) return op_fail(DEC_ERR_UNSUPPORTED, "append: too many rows");
+  const bool f32 = a->dtype == DEC_F32;
+  auto* k = c->head_dim == 128 ? (f32 ? append_kernel<128, true> : append_kernel<128, false>)
+                               : (f32 ? append_kernel<64, true> : append_kernel<64, false>);
+  k<<<(unsigned)grid, 256, 0, op_stream(stream)>>>(p);
+  return launched("append");
+}
+
+dec_status dec_kvq_gather(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec_rows* k_out, const dec_rows* v_out,
+                          void* stream) {
+  op_clear();
+  if (dec_status st = check_cache(c)) return st;
+  if (dec_status st = check_seqs(s, c)) return st;
+  if (s->batch == 0 || s->n_tokens == 0) return DEC_OK;
+  if (dec_status st = check_rows(k_out, DEC_BF16, "gather: k_out")) return st;
+  if (dec_status st = check_rows(v_out, DEC_BF16, "gather: v_out")) return st;
+  if (dec_status st = op_on_device(c->pages, "cache: pages")) return st;
+  GatherParams p;
+  p.c = cache_of(c);
+  p.s = seqs_of(s);
+  p.k = rows_of(*k_out);
+  p.v = rows_of(*v_out);
+  const long long grid = ((long long)s->n_tokens * 2 * c->n_kv_heads * (c->head_dim / 8) + 255) / 256;
+  if (grid > INT_MAX) return op_fail(DEC_ERR_UNSUPPORTED, "gather: too many rows");
+  auto* k = c->head_dim == 128 ? gather_kernel<128> : gather_kernel<64>;
+  k<<<(unsigned)grid, 256, 0, op_stream(stream)>>>(p);
+  return launched("gather");
+}
+
+int64_t dec_kvq_attention_workspace(const dec_kvq_cache* c, int32_t n_heads, int32_t batch, int32_t max_tokens) {
+  if (!c || n_heads < 1 || c->n_kv_heads < 1 || n_heads % c->n_kv_heads || batch < 0 || max_tokens < 0) return -1;
+  if (dec_kvq_page_bytes(c->page_tokens, c->n_kv_heads, c->head_dim) == 0) return -1;
+  return 0;
+}
+
+dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec_kvq_attention_args* a,
+                             void* stream) {
+  op_clear();
+  if (dec_status st = check_cache(c)) return st;
+  if (dec_status st = check_seqs(s, c)) return st;
+  if (!a) return op_fail(DEC_ERR_ARG, "attention: NULL arguments");
+  if (a->n_heads < 1 || a->n_heads > 16384 || a->n_heads % c->n_kv_heads)
+    return op_fail(DEC_ERR_ARG, "attention: n_heads must be a multiple of the cache's KV heads");
+  if (a->max_tokens < 0 || !(a->scale >= 0.f) || std::isinf(a->scale))
+    return op_fail(DEC_ERR_ARG, "attention: max_tokens and scale must not be negative, scale finite");
+  if (s->batch == 0 || s->n_tokens == 0 || a->max_tokens == 0) return DEC_OK;
+  if (dec_status st = check_rows(&a->q, DEC_BF16, "attention: q")) return st;
+  if (dec_status st = check_rows(&a->out, DEC_BF16, "attention: out")) return st;
+  const int64_t need = dec_kvq_attention_workspace(c, a->n_heads, s->batch, a->max_tokens);
+  if (need > 0 && (!a->workspace || !op_aligned(a->workspace) || a->workspace_bytes < need))
+    return op_fail(DEC_ERR_ARG, "attention: workspace missing, misaligned or too small");
+  if (dec_status st = op_on_device(c->pages, "cache: pages")) return st;
+  AttnParams p;
+  p.c = cache_of(c);
+  p.s = seqs_of(s);
+  p.q = rows_of(a->q);
+  p.o = rows_of(a->out);
+  p.lse = a->lse;
+  p.scale = a->scale == 0.f ? 1.0f / std::sqrt((float)c->head_dim) : a->scale;
+  p.hq = a->n_heads;
+  p.group = a->n_heads / c->n_kv_heads;
+  p.causal = a->causal != 0;
+  p.max_tokens = a->max_tokens;
+  auto* k = c->head_dim == 128 ? attention_kernel<128> : attention_kernel<64>;
+  k<<<dim3(s->n_tokens, a->n_heads), 128, 0, op_stream(stream)>>>(p);
+  return launched("attention");
+}
+
+}  // extern "C"
