@@ -1,12 +1,15 @@
 // Entry points of the paged 4-bit KV cache (dec_kvq_* of dec.h).
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdio>
 #include <mutex>
 
 #include "dec_kvq.cuh"
+#include "dec_kvq_attn.cuh"
 #include "dec_ops.h"
 
 namespace dec {
@@ -127,6 +130,65 @@ dec_status launched(const char* what) {
   return ce == cudaSuccess ? DEC_OK : op_cuda(ce, what);
 }
 
+// A kernel's dynamic shared memory limit, raised once per device.
+template <class F>
+dec_status raise_smem(F* k, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t ce = cudaGetDevice(&dev);
+  if (ce != cudaSuccess) return op_cuda(ce, "cudaGetDevice");
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return DEC_OK;
+  ce = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (ce != cudaSuccess) return op_cuda(ce, "cudaFuncSetAttribute");
+  if (dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return DEC_OK;
+}
+
+// Query rows per unit: 8 as long as they hold the longest sequence's rows, else 16.
+int blocks_of(int n_heads, int hkv, int max_tokens) { return (long long)max_tokens * (n_heads / hkv) <= 8 ? 1 : 2; }
+
+template <int HD, int NB>
+int64_t workspace_of(int sms) {
+  using K = AttnCfg<HD, NB>;
+  return (int64_t)sms * ((2 + K::WARPS) * K::PART * 4 + 16);
+}
+
+template <int HD, int NB>
+dec_status launch_attention(AttnParams p, int batch, uint8_t* ws, cudaStream_t stream) {
+  using K = AttnCfg<HD, NB>;
+  static std::atomic<unsigned long long> done{0};
+  if (dec_status st = raise_smem(attention_kernel<HD, NB>, K::smem(), done)) return st;
+  const int sms = op_sms();
+  if (sms < 1) return op_fail(DEC_ERR_CUDA, "attention: no device");
+  p.meta = reinterpret_cast<int4*>(ws);
+  p.parts = reinterpret_cast<float*>(ws + (size_t)sms * 16);
+  p.wparts = p.parts + (size_t)sms * 2 * K::PART;
+  p.min_groups = kMinGroups;
+  const Seqs all = p.s;
+  for (int b = 0; b < batch; b += kMaxSeqs) {
+    p.s.batch = std::min(kMaxSeqs, batch - b);
+    p.s.lengths = all.lengths + b;
+    p.s.table = all.table + b * all.table_stride;
+    if (all.cu) p.s.cu = all.cu + b;
+    p.b0 = b;
+    attention_kernel<HD, NB><<<sms, K::THREADS, K::smem(), stream>>>(p);
+    cudaError_t ce = cudaGetLastError();
+    if (ce != cudaSuccess) return op_cuda(ce, "attention");
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sms, K::ROWS / 2);
+    cfg.blockDim = dim3(HD / 2);
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    ce = cudaLaunchKernelEx(&cfg, join_kernel<HD, NB>, p);
+    if (ce != cudaSuccess) return op_cuda(ce, "attention (join)");
+  }
+  return DEC_OK;
+}
+
 }  // namespace
 }  // namespace kvq
 }  // namespace dec
@@ -217,9 +279,14 @@ dec_status dec_kvq_gather(const dec_kvq_cache* c, const dec_kvq_seqs* s, const d
 }
 
 int64_t dec_kvq_attention_workspace(const dec_kvq_cache* c, int32_t n_heads, int32_t batch, int32_t max_tokens) {
-  if (!c || n_heads < 1 || c->n_kv_heads < 1 || n_heads % c->n_kv_heads || batch < 0 || max_tokens < 0) return -1;
+  if (!c || n_heads < 1 || n_heads > 16384 || c->n_kv_heads < 1 || n_heads % c->n_kv_heads || batch < 0 || max_tokens < 0)
+    return -1;
   if (dec_kvq_page_bytes(c->page_tokens, c->n_kv_heads, c->head_dim) == 0) return -1;
-  return 0;
+  const int sms = op_sms();
+  if (sms < 1) return -1;
+  const bool wide = blocks_of(n_heads, c->n_kv_heads, max_tokens) == 2;
+  if (c->head_dim == 128) return wide ? workspace_of<128, 2>(sms) : workspace_of<128, 1>(sms);
+  return wide ? workspace_of<64, 2>(sms) : workspace_of<64, 1>(sms);
 }
 
 dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec_kvq_attention_args* a,
@@ -235,9 +302,11 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
   if (s->batch == 0 || s->n_tokens == 0 || a->max_tokens == 0) return DEC_OK;
   if (dec_status st = check_rows(&a->q, DEC_BF16, "attention: q")) return st;
   if (dec_status st = check_rows(&a->out, DEC_BF16, "attention: out")) return st;
-  const int64_t need = dec_kvq_attention_workspace(c, a->n_heads, s->batch, a->max_tokens);
-  if (need > 0 && (!a->workspace || !op_aligned(a->workspace) || a->workspace_bytes < need))
-    return op_fail(DEC_ERR_ARG, "attention: workspace missing, misaligned or too small");
+  if ((long long)s->n_tokens * a->n_heads >= INT_MAX ||
+      (long long)s->max_pages * c->page_tokens + s->n_tokens >= INT_MAX - 65536 ||
+      (long long)c->n_pages * c->n_kv_heads * (c->page_tokens / kGroup) >= INT_MAX)
+    return op_fail(DEC_ERR_UNSUPPORTED, "attention: 2^31 query rows, positions or cache groups");
+  if (!a->workspace || !op_aligned(a->workspace)) return op_fail(DEC_ERR_ARG, "attention: workspace missing or misaligned");
   if (dec_status st = op_on_device(c->pages, "cache: pages")) return st;
   AttnParams p;
   p.c = cache_of(c);
@@ -245,14 +314,25 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
   p.q = rows_of(a->q);
   p.o = rows_of(a->out);
   p.lse = a->lse;
-  p.scale = a->scale == 0.f ? 1.0f / std::sqrt((float)c->head_dim) : a->scale;
+  // (scores in units of log2; the factor 8 of the scale bytes)
+  p.scale = (a->scale == 0.f ? 1.0f / std::sqrt((float)c->head_dim) : a->scale) * 1.4426950408889634f * 8.0f;
   p.hq = a->n_heads;
   p.group = a->n_heads / c->n_kv_heads;
   p.causal = a->causal != 0;
   p.max_tokens = a->max_tokens;
-  auto* k = c->head_dim == 128 ? attention_kernel<128> : attention_kernel<64>;
-  k<<<dim3(s->n_tokens, a->n_heads), 128, 0, op_stream(stream)>>>(p);
-  return launched("attention");
+  const int max_tokens = std::min(a->max_tokens, s->n_tokens);
+  const bool wide = blocks_of(a->n_heads, c->n_kv_heads, max_tokens) == 2;
+  if (a->workspace_bytes < dec_kvq_attention_workspace(c, a->n_heads, s->batch, max_tokens))
+    return op_fail(DEC_ERR_ARG, "attention: workspace too small");
+  // entries of the kernel's list of groups, at most: 32-bit
+  const long long units = (long long)c->n_kv_heads * ((long long)s->n_tokens * p.group / (wide ? 16 : 8) + s->batch);
+  if (units * (((long long)s->max_pages * c->page_tokens + kGroup - 1) / kGroup) >= (1LL << 32))
+    return op_fail(DEC_ERR_UNSUPPORTED, "attention: too much work for one call");
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  cudaStream_t st = op_stream(stream);
+  if (c->head_dim == 128)
+    return wide ? launch_attention<128, 2>(p, s->batch, ws, st) : launch_attention<128, 1>(p, s->batch, ws, st);
+  return wide ? launch_attention<64, 2>(p, s->batch, ws, st) : launch_attention<64, 1>(p, s->batch, ws, st);
 }
 
 }  // extern "C"

@@ -304,82 +304,5 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherParams p) {
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.p) + tok * o.ts + h * o.hs + l * 8) = pack8_bf16(x);
 }
 
-struct AttnParams {
-  Cache c;
-  Seqs s;
-  Rows q, o;
-  float* lse;
-  float scale;
-  int hq, group, causal, max_tokens;
-};
-
-// Attention of one (token row, query head) per CTA: HD / 8 lanes a position, an online softmax per
-// such lane group, the groups' states joined in a fixed order at the end.
-template <int HD>
-__global__ void __launch_bounds__(128) attention_kernel(const AttnParams p) {
-  constexpr int LPR = HD / 8, NG = 128 / LPR;
-  __shared__ float sm[NG], sl[NG], so[NG][HD];
-  const int tok = blockIdx.x, head = blockIdx.y, h = head / p.group;
-  const int l = threadIdx.x % LPR, gi = threadIdx.x / LPR;
-  int j = 0;
-  const int b = seq_of(p.s, tok, j);
-  if (b < 0 || j >= p.max_tokens) return;
-  const int len = __ldg(p.s.lengths + b);
-  const long long most = (long long)p.s.max_pages << p.c.page_shift;
-  long long want = p.causal ? (long long)len + j + 1 : len;
-  if (len < 0) {
-    raise(p.c.status, DEC_ERR_ARG);
-    want = 0;
-  } else if (want > most) {
-    raise(p.c.status, DEC_ERR_CAPACITY);
-    want = most;
-  }
-  const int n = (int)want;
-  float q[8], o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  load8<false>(p.q.p, tok * p.q.ts + head * p.q.hs + l * 8, q);
-  float m = -INFINITY, sum = 0.f;
-  for (int p0 = 0; p0 < n; p0 += NG) {
-    const int pos = p0 + gi;
-    const uint8_t* grp = pos < n ? group_at<HD>(p.c, p.s, b, pos, h) : nullptr;
-    const int pp = pos & 15;
-    float k[8], d = 0.f;
-    if (grp) {
-      decode8(*reinterpret_cast<const uint32_t*>(grp + k_word<HD>(pp, l)), scale_of(grp[k_scale<HD>(pp, l >> 1)]), k);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d = fmaf(q[i], k[i], d);
-    }
-#pragma unroll
-    for (int w = LPR / 2; w > 0; w >>= 1) d += __shfl_xor_sync(0xffffffffu, d, w);
-    if (!grp) continue;
-    d *= p.scale;
-    const float mn = fmaxf(m, d);
-    const float f = m == -INFINITY ? 0.f : expf(m - mn), e = d == -INFINITY ? 0.f : expf(d - mn);
-    float v[8];
-    decode8(*reinterpret_cast<const uint32_t*>(grp + v_word<HD>(pp, l)), scale_of(grp[v_scale<HD>(pp, l >> 1)]), v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * f + e * v[i];
-    sum = sum * f + e;
-    m = mn;
-  }
-  if (l == 0) {
-    sm[gi] = m;
-    sl[gi] = sum;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) so[gi][l * 8 + i] = o[i];
-  __syncthreads();
-  float mx = -INFINITY, tot = 0.f, acc = 0.f;
-  for (int i = 0; i < NG; ++i) mx = fmaxf(mx, sm[i]);
-  const int d = threadIdx.x;
-  for (int i = 0; i < NG; ++i) {
-    const float f = sm[i] == -INFINITY ? 0.f : expf(sm[i] - mx);
-    tot += f * sl[i];
-    if (d < HD) acc += f * so[i][d];
-  }
-  if (d < HD)
-    static_cast<__nv_bfloat16*>(p.o.p)[tok * p.o.ts + head * p.o.hs + d] = __float2bfloat16(tot == 0.f ? 0.f : acc / tot);
-  if (d == 0 && p.lse) p.lse[(long long)tok * p.hq + head] = mx + logf(tot);
-}
-
 }  // namespace kvq
 }  // namespace dec

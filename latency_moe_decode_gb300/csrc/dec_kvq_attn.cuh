@@ -1,0 +1,691 @@
+// Attention over the paged 4-bit cache for few query rows (decode and verify steps).
+//
+// The work is reading the cache once: 2 (hd / 2 + hd / 16) bytes per position and KV head against
+// 4 hd flops per query head, so the kernel is built around the stream of groups (16 positions of
+// one KV head) through each SM:
+//  - a unit is (sequence, KV head, block of 8 NB query rows), a query row being (token, head of
+//    the group); the groups of all units form one list, cut evenly over the CTAs and their warps
+//    (lengths are read on the device: the cut needs no host knowledge and adapts to ragged batches);
+//  - a warp streams its groups through its own ring with cp.async, two chunks ahead, without ever
+//    waiting for another warp;
+//  - S^T = K q^T and O^T = V^T P^T are 16 x 8 x 16 f16 products whose A operand, the codes, comes
+//    out of the ring in the lanes' own order: (code + 8) enters the low mantissa bits of the f16
+//    1024, and one fma turns it into code * scale exactly (4 x 4 significant bits). Tensor memory
+//    has nothing to offer here: 8 columns of queries leave the tensor cores mostly idle, and the
+//    codes would have to be written to shared memory again for tcgen05 to read them;
+//  - probabilities go from the first product's result layout to the second's operand layout by
+//    movmatrix; the running maximum and sum stay in fp32 registers;
+//  - what a warp leaves unfinished of a unit is joined per CTA in shared memory, and what a CTA
+//    leaves unfinished by a second small kernel, both in a fixed order.
+#pragma once
+#include "dec_kvq.cuh"
+
+namespace dec {
+namespace kvq {
+
+constexpr int kStages = 3;        // chunks of a warp's ring
+constexpr int kMaxSeqs = 2048;    // sequences of one launch (their prefix sums lie in shared memory)
+constexpr int kMinGroups = 16;    // groups a CTA takes at least
+constexpr float kPShift = 15.0f;  // probabilities are kept times 2^15: f16 then reaches 2^-39 of the largest
+
+template <int HD, int NB>
+struct AttnCfg {
+  static constexpr int KS = HD / 16;              // 16-value steps of a head
+  static constexpr int WARPS = NB == 1 ? 16 : 8;  // registers: 128 or 255 a thread
+  static constexpr int CH = NB == 1 ? 2 : 4;      // groups per softmax update
+  static constexpr int ROWS = 8 * NB;
+  static constexpr int GB = group_bytes(HD);
+  static constexpr int RING = kStages * CH * GB;  // bytes per warp
+  static constexpr int PART = ROWS * HD + 2 * ROWS;  // floats of a partial: outputs, maxima, sums
+  static constexpr int THREADS = WARPS * 32;
+  static_assert(RING >= PART * 4 && RING % 16 == 0 && GB % 16 == 0, "a partial has to fit into a warp's ring");
+  static constexpr int smem() { return WARPS * RING + (kMaxSeqs + 1) * 4; }
+};
+
+struct AttnParams {
+  Cache c;
+  Seqs s;
+  Rows q, o;
+  float* lse;
+  float scale;  // times log2(e) and the scale bytes' factor 8
+  int hq, group, causal, max_tokens;
+  int b0;         // (without cu: token row of sequence 0)
+  int min_groups; // groups a CTA takes at least
+  float* parts;   // [CTA][2] partials
+  float* wparts;  // [CTA][warp] partials
+  int4* meta;     // [CTA]: continued (1) and finished here (2) | opens a unit, its sequence and index
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+// Two scales (f16 pairs) and what turns (1024 + u) and (1024 + 16 u), u = code + 8, into code * s:
+// (1024 + u) s - 1032 s and (1024 + 16 u) (s / 16) - 72 s. All products are exact: s has 4
+// significant bits, 1032 = 129 * 8 and 72 = 9 * 8, and 1032 * 60 is still an f16.
+struct Scale2 {
+  __half2 s, s16, c, c16;
+  __device__ __forceinline__ void set(uint32_t two) {  // scale bytes in the low bytes of the halves
+    s = u2h(two << 7);
+    s16 = __hmul2(s, __float2half2_rn(0.0625f));
+    c = __hmul2(s, __float2half2_rn(-1032.0f));
+    c16 = __hmul2(s, __float2half2_rn(-72.0f));
+  }
+  // nibbles 0 and 1 of both halves of x
+  __device__ __forceinline__ void decode(uint32_t x, uint32_t& n0, uint32_t& n1) const {
+    n0 = h2u(__hfma2(u2h((x & 0x000F000Fu) | 0x64006400u), s, c));
+    n1 = h2u(__hfma2(u2h((x & 0x00F000F0u) | 0x64006400u), s16, c16));
+  }
+};
+
+// The list of groups: per sequence hkv * (row blocks) units of `ng` groups each.
+template <int NB>
+struct SeqWork {
+  int tok0, n, len, ng, nrb;
+  __device__ __forceinline__ void load(const AttnParams& p, int b) {
+    tok0 = p.s.cu ? __ldg(p.s.cu + b) : p.b0 + b;
+    n = p.s.cu ? __ldg(p.s.cu + b + 1) - tok0 : 1;
+    tok0 = max(tok0, 0);
+    n = max(0, min(min(n, p.max_tokens), p.s.n_tokens - tok0));
+    len = __ldg(p.s.lengths + b);
+    const long long most = (long long)p.s.max_pages << p.c.page_shift;
+    if (len < 0 && n > 0) raise(p.c.status, DEC_ERR_ARG);
+    long long want = len < 0 ? 0 : p.causal ? (long long)len + n : len;
+    if (want > most && n > 0) raise(p.c.status, DEC_ERR_CAPACITY);
+    want = min(want, most);
+    len = len < 0 ? -n : (int)min((long long)len, most);
+    ng = max(1, (int)((want + kGroup - 1) / kGroup));  // (a unit without positions still writes its rows)
+    nrb = (n * p.group + 8 * NB - 1) / (8 * NB);
+  }
+};
+
+template <int HD, int NB>
+__global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(const AttnParams p) {
+  using K = AttnCfg<HD, NB>;
+  constexpr int KS = K::KS, CH = K::CH;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t sh_scan[K::WARPS];
+  __shared__ uint32_t ent_uid[2 * K::WARPS];
+  __shared__ int ent_b[2 * K::WARPS], ent_u[2 * K::WARPS];
+  uint32_t* const pre = reinterpret_cast<uint32_t*>(smem + K::WARPS * K::RING);  // [batch + 1]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join kernel waits for this one's end)
+
+  // ---- the list's prefix sums over the sequences
+  if (tid < 2 * K::WARPS) ent_uid[tid] = 0xFFFFFFFFu;
+  uint32_t base = 0;
+  for (int b0 = 0; b0 < p.s.batch; b0 += K::THREADS) {
+    const int b = b0 + tid;
+    uint32_t w = 0;
+    if (b < p.s.batch) {
+      SeqWork<NB> sw;
+      sw.load(p, b);
+      w = (uint32_t)p.c.hkv * sw.nrb * sw.ng;
+    }
+    uint32_t x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh_scan[warp] = x;
+    __syncthreads();
+    uint32_t before = base, all = base;
+#pragma unroll
+    for (int i = 0; i < K::WARPS; ++i) {
+      const uint32_t y = sh_scan[i];
+      before += i < warp ? y : 0u;
+      all += y;
+    }
+    if (b < p.s.batch) pre[b] = before + x - w;
+    base = all;
+  }
+  if (tid == 0) pre[p.s.batch] = base;
+  __syncthreads();
+  const uint32_t W = base;
+  const int ctas = (int)min((uint32_t)gridDim.x, (W + p.min_groups - 1) / p.min_groups);
+  const int cta = blockIdx.x;
+  uint32_t clo = 0, chi = 0;
+  if (cta < ctas) {
+    clo = (uint32_t)((unsigned long long)W * cta / ctas);
+    chi = (uint32_t)((unsigned long long)W * (cta + 1) / ctas);
+  }
+  const uint32_t lo = clo + (uint32_t)((unsigned long long)(chi - clo) * warp / K::WARPS);
+  const uint32_t hi = clo + (uint32_t)((unsigned long long)(chi - clo) * (warp + 1) / K::WARPS);
+
+  // the sequence that entry f of the list belongs to
+  auto seq_at = [&](uint32_t f) {
+    int a = 0, z = p.s.batch;
+    while (z - a > 1) {
+      const int m = (a + z) >> 1;
+      if (pre[m] <= f) a = m;
+      else z = m;
+    }
+    return a;
+  };
+
+  uint8_t* const ring = smem + warp * K::RING;
+
+  // ---- the copies: 32 entries' group indices at a time, one per lane
+  uint32_t vb = lo, pf = lo;  // first entry of the lanes' window; next entry to copy
+  int vg = -1, vrem = 0;      // its group in the cache (-1: nothing to copy), entries left of its unit
+  auto window = [&](uint32_t f0) {
+    vb = f0;
+    const uint32_t f = f0 + lane;
+    vg = -1;
+    vrem = 0;
+    if (f < hi) {
+      const int b = seq_at(f);
+      SeqWork<NB> sw;
+      sw.load(p, b);
+      const uint32_t r = f - pre[b];
+      const int u = (int)(r / (uint32_t)sw.ng), gr = (int)(r - (uint32_t)u * sw.ng);
+      vrem = sw.ng - gr;
+      const int pos = gr * kGroup;
+      if (pos < (p.causal ? sw.len + sw.n : sw.len)) {
+        const int e = pos >> p.c.page_shift;
+        const int page = __ldg(p.s.table + b * p.s.table_stride + e);
+        const int gpp = 1 << (p.c.page_shift - 4);
+        if ((unsigned)page < (unsigned)p.c.n_pages) vg = (page * p.c.hkv + u / sw.nrb) * gpp + (gr & (gpp - 1));
+        else raise(p.c.status, DEC_ERR_ARG);
+      }
+    }
+  };
+  int pstage = 0;
+  auto prefetch = [&]() {  // the next chunk, if there is one
+    if (pf < hi) {
+      if (pf + CH > vb + 32) window(pf);
+      const int at = (int)(pf - vb);
+      const int n = min(min(CH, __shfl_sync(0xffffffffu, vrem, at)), (int)(hi - pf));
+      const uint32_t dst = smem_addr(ring + pstage * CH * K::GB) + lane * 16;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int gi = __shfl_sync(0xffffffffu, vg, (at + i) & 31);
+        if (i < n && gi >= 0) {
+          const uint8_t* src = p.c.pages + (size_t)gi * K::GB + lane * 16;
+#pragma unroll
+          for (int o = 0; o < K::GB; o += 512)
+            if (o + 512 <= K::GB || lane * 16 + o < K::GB) cp16(dst + i * K::GB + o, src + o);
+        }
+      }
+      pf += n;
+    }
+    cp_commit();
+    pstage = pstage == kStages - 1 ? 0 : pstage + 1;
+  };
+
+  float acc[NB][KS][4];
+  float m[NB][2], l[NB][2], sc[NB][2];
+  int seen[NB][2];
+  uint32_t qf[NB][KS][2];
+
+  if (lo < hi) {
+    window(lo);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) prefetch();
+  }
+  int cstage = 0;
+  for (uint32_t f = lo; f < hi;) {
+    // ---- a unit: its rows' queries as the second operand of S^T, halved down to magnitude 1 .. 2
+    const int b = seq_at(f);
+    SeqWork<NB> sw;
+    sw.load(p, b);
+    const uint32_t r = f - pre[b];
+    const int u = (int)(r / (uint32_t)sw.ng);
+    const uint32_t uid = pre[b] + (uint32_t)u * sw.ng;  // where the unit starts: its name
+    const int h = u / sw.nrb, row0 = (u % sw.nrb) * K::ROWS, rows = sw.n * p.group;
+    int smin = 0x7FFFFFFF, smax = 0;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = row0 + nb * 8 + g;
+      uint32_t w[KS * 2];  // HD / 4 values from t HD / 4 on, two a word
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) w[i] = 0;
+      if (row < rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q.p) + (sw.tok0 + row / p.group) * p.q.ts +
+            (h * p.group + row % p.group) * p.q.hs + t * (HD / 4));
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) {
+          const uint4 x = __ldg(src + i);
+          w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+        }
+      }
+      uint32_t mag = 0;
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) mag = max(mag, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+      mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+      mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+      // a power of two that leaves the row's largest value in 1 .. 2: bf16 values down to 2^-17 of it
+      // are exact in f16, smaller ones lose at most 2^-25 of it
+      const int e = mag == 0 || mag >= 0x7F800000u ? 0 : min(126, max(-126, (int)(mag >> 23) - 127));
+      const float down = __int_as_float((127 - e) << 23);
+      auto val = [&](int i) {  // value i of the lane's HD / 4
+        return down * __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+      };
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int i = 8 * (s >> 1) + 2 * (s & 1);
+        qf[nb][s][0] = h2u(__floats2half2_rn(val(i), val(i + 4)));
+        qf[nb][s][1] = h2u(__floats2half2_rn(val(i + 1), val(i + 5)));
+      }
+      const float up = p.scale * __int_as_float((127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sc[nb][i] = __shfl_sync(0xffffffffu, up, (2 * t + i) * 4);
+        const int rr = row0 + nb * 8 + 2 * t + i;
+        seen[nb][i] = rr < rows ? (p.causal ? max(0, sw.len + rr / p.group + 1) : max(0, sw.len)) : 0;
+        if (rr < rows) {
+          smin = min(smin, seen[nb][i]);
+          smax = max(smax, seen[nb][i]);
+        }
+        m[nb][i] = -INFINITY;
+        l[nb][i] = 0.f;
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nb][s][i] = 0.f;
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      smin = min(smin, __shfl_xor_sync(0xffffffffu, smin, o));
+      smax = max(smax, __shfl_xor_sync(0xffffffffu, smax, o));
+    }
+    const uint32_t fend = min(hi, uid + (uint32_t)sw.ng);
+
+    // ---- its groups, a chunk at a time
+    for (uint32_t f0 = f; f0 < fend; f0 += CH) {
+      const int n = min(CH, (int)(fend - f0));
+      const int pos0 = (int)(f0 - uid) * kGroup;
+      prefetch();
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const uint8_t* const buf = ring + cstage * CH * K::GB;
+      cstage = cstage == kStages - 1 ? 0 : cstage + 1;
+      float s[NB][CH][4];
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[nb][i][j] = 0.f;
+        if (i < n) {
+          const uint8_t* gp = buf + i * K::GB;
+          uint32_t k0[HD / 32], k1[HD / 32];  // words of positions g and g + 8
+          uint32_t sb;
+          if (HD == 128) {
+            const uint4 a = *reinterpret_cast<const uint4*>(gp + lane * 16);
+            const uint4 c = *reinterpret_cast<const uint4*>(gp + 512 + lane * 16);
+            k0[0] = a.x; k0[1] = a.y; k0[HD / 32 - 2] = a.z; k0[HD / 32 - 1] = a.w;
+            k1[0] = c.x; k1[1] = c.y; k1[HD / 32 - 2] = c.z; k1[HD / 32 - 1] = c.w;
+            sb = *reinterpret_cast<const uint32_t*>(gp + 2 * code_bytes(HD) + lane * 4);
+          } else {
+            const uint4 a = *reinterpret_cast<const uint4*>(gp + lane * 16);
+            k0[0] = a.x; k0[1] = a.y;
+            k1[0] = a.z; k1[1] = a.w;
+            sb = *reinterpret_cast<const uint16_t*>(gp + 2 * code_bytes(HD) + lane * 2);
+          }
+#pragma unroll
+          for (int w2 = 0; w2 < HD / 64; ++w2) {  // two words: one scale's run
+            Scale2 s0, s1;
+            if (HD == 128) {
+              s0.set(__byte_perm(sb, 0, w2 == 0 ? 0x4040 : 0x4141));
+              s1.set(__byte_perm(sb, 0, w2 == 0 ? 0x4242 : 0x4343));
+            } else {
+              s0.set(__byte_perm(sb, 0, 0x4040));
+              s1.set(__byte_perm(sb, 0, 0x4141));
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const int wi = 2 * w2 + v;
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                uint32_t a0, a1, a2, a3;
+                s0.decode(y ? k0[wi] >> 8 : k0[wi], a0, a2);
+                s1.decode(y ? k1[wi] >> 8 : k1[wi], a1, a3);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                  mma16816(s[nb][i], a0, a1, a2, a3, qf[nb][2 * wi + y][0], qf[nb][2 * wi + y][1]);
+              }
+            }
+          }
+        }
+      }
+      // scores in units of log2; what a row does not see is -infinity, whatever it held
+      const bool edge = n < CH || pos0 + CH * kGroup > smin;
+      uint32_t pb[NB][CH][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float mx0 = m[nb][0], mx1 = m[nb][1];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x = s[nb][i][j] * sc[nb][j & 1];
+            if (edge && (i >= n || pos0 + i * kGroup + g + (j >> 1) * 8 >= seen[nb][j & 1])) x = -INFINITY;
+            s[nb][i][j] = x;
+          }
+          mx0 = fmaxf(mx0, fmaxf(s[nb][i][0], s[nb][i][2]));
+          mx1 = fmaxf(mx1, fmaxf(s[nb][i][1], s[nb][i][3]));
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        }
+        if (__any_sync(0xffffffffu, mx0 > m[nb][0] || mx1 > m[nb][1])) {
+          const float f0_ = m[nb][0] == -INFINITY ? 0.f : ex2(m[nb][0] - mx0);
+          const float f1_ = m[nb][1] == -INFINITY ? 0.f : ex2(m[nb][1] - mx1);
+          l[nb][0] *= f0_;
+          l[nb][1] *= f1_;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            acc[nb][k][0] *= f0_;
+            acc[nb][k][1] *= f1_;
+            acc[nb][k][2] *= f0_;
+            acc[nb][k][3] *= f1_;
+          }
+          m[nb][0] = mx0;
+          m[nb][1] = mx1;
+        }
+        const float z0 = (mx0 == -INFINITY ? 0.f : mx0) - kPShift, z1 = (mx1 == -INFINITY ? 0.f : mx1) - kPShift;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const float e0 = ex2(s[nb][i][0] - z0), e1 = ex2(s[nb][i][1] - z1);
+          const float e2 = ex2(s[nb][i][2] - z0), e3 = ex2(s[nb][i][3] - z1);
+          l[nb][0] += e0 + e2;
+          l[nb][1] += e1 + e3;
+          pb[nb][i][0] = transpose8x8(h2u(__floats2half2_rn(e0, e1)));
+          pb[nb][i][1] = transpose8x8(h2u(__floats2half2_rn(e2, e3)));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        if (i >= n) continue;
+        const uint8_t* gp = buf + i * K::GB + code_bytes(HD);
+        uint32_t vw[4][HD / 64];  // words of positions 2t, 2t + 1, 2t + 8, 2t + 9
+        uint32_t sb;
+        if (HD == 128) {
+          const uint4 a = *reinterpret_cast<const uint4*>(gp + lane * 16);
+          const uint4 c = *reinterpret_cast<const uint4*>(gp + 512 + lane * 16);
+          vw[0][0] = a.x; vw[0][HD / 64 - 1] = a.y; vw[1][0] = a.z; vw[1][HD / 64 - 1] = a.w;
+          vw[2][0] = c.x; vw[2][HD / 64 - 1] = c.y; vw[3][0] = c.z; vw[3][HD / 64 - 1] = c.w;
+          sb = *reinterpret_cast<const uint32_t*>(gp + code_bytes(HD) + scale_bytes(HD) + lane * 4);
+        } else {
+          const uint4 a = *reinterpret_cast<const uint4*>(gp + lane * 16);
+          vw[0][0] = a.x; vw[1][0] = a.y; vw[2][0] = a.z; vw[3][0] = a.w;
+          sb = *reinterpret_cast<const uint32_t*>(gp + code_bytes(HD) + scale_bytes(HD) + ((g >> 1) * 4 + t) * 4);
+        }
+        // what no row sees counts nothing, whatever is there: scale 0
+        const int left = smax - (pos0 + i * kGroup);
+        if (left < kGroup) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (2 * t + (k & 1) + (k >> 1) * 8 >= left) sb &= ~(0xFFu << (8 * k));
+        }
+        auto product = [&](uint32_t bytes, auto&& put) {
+          Scale2 s0, s1;
+          s0.set(__byte_perm(bytes, 0, 0x4140));
+          s1.set(__byte_perm(bytes, 0, 0x4342));
+#pragma unroll
+          for (int w = 0; w < HD / 64; ++w)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {  // values 4 x .. 4 x + 3 of the word, positions paired
+              const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], x ? 0x7632 : 0x5410);
+              const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], x ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                uint32_t a0, a1, a2, a3;
+                s0.decode(y ? x0 >> 8 : x0, a0, a1);
+                s1.decode(y ? x1 >> 8 : x1, a2, a3);
+                put(4 * w + 2 * x + y, a0, a1, a2, a3);
+              }
+            }
+        };
+        // A run of NaNs at a position that some of the rows do not see (0 x NaN is NaN): each row by
+        // itself, with the positions it does not see left out. Rows of one decode token all see
+        // the same, and finite caches never come here.
+        bool odd = false;
+        if (edge && smin < smax) {
+          const uint32_t x = ~sb;  // a byte of 255
+          odd = __any_sync(0xffffffffu, ((x - 0x01010101u) & ~x & 0x80808080u) != 0);
+        }
+        if (!odd) {
+          product(sb, [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(acc[nb][k], a0, a1, a2, a3, pb[nb][i][0], pb[nb][i][1]);
+          });
+        } else {
+          for (int c = 0; c < K::ROWS; ++c) {
+            int mine = 0;  // what row c sees
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              const int s0 = __shfl_sync(0xffffffffu, seen[nb][0], (c & 7) >> 1);
+              const int s1 = __shfl_sync(0xffffffffu, seen[nb][1], (c & 7) >> 1);
+              if (c >> 3 == nb) mine = (c & 1) ? s1 : s0;
+            }
+            uint32_t mb = sb;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (pos0 + i * kGroup + 2 * t + (k & 1) + (k >> 1) * 8 >= mine) mb &= ~(0xFFu << (8 * k));
+            product(mb, [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                float d[4] = {acc[nb][k][0], acc[nb][k][1], acc[nb][k][2], acc[nb][k][3]};
+                mma16816(d, a0, a1, a2, a3, pb[nb][i][0], pb[nb][i][1]);
+                if (c == nb * 8 + 2 * t) {
+                  acc[nb][k][0] = d[0];
+                  acc[nb][k][2] = d[2];
+                }
+                if (c == nb * 8 + 2 * t + 1) {
+                  acc[nb][k][1] = d[1];
+                  acc[nb][k][3] = d[3];
+                }
+              }
+            });
+          }
+        }
+      }
+      __syncwarp();  // (the next copy goes where this chunk lay)
+    }
+
+    // ---- the unit, or this warp's part of it
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], o);
+    const bool whole = f == uid && fend == uid + (uint32_t)sw.ng;
+    const bool last = fend == hi;
+    float* part = nullptr;
+    if (!whole) {
+      const int e = 2 * warp + (last ? 1 : 0);
+      if (last) {
+        cp_wait<0>();
+        __syncwarp();
+        part = reinterpret_cast<float*>(ring);
+      } else {
+        part = p.wparts + ((size_t)cta * K::WARPS + warp) * K::PART;
+      }
+      if (lane == 0) {
+        ent_uid[e] = uid;
+        ent_b[e] = b;
+        ent_u[e] = u;
+      }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int rr = nb * 8 + 2 * t + i;
+        if (whole) {
+          if (row0 + rr < rows) {
+            const float inv = l[nb][i] == 0.f ? 0.f : 8.0f / l[nb][i];
+            const long long tok = sw.tok0 + (row0 + rr) / p.group;
+            const int head = h * p.group + (row0 + rr) % p.group;
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + g * (HD / 8));
+#pragma unroll
+            for (int k = 0; k < KS; k += 4) {
+              float x[8];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                x[2 * j] = acc[nb][k + j][i] * inv;
+                x[2 * j + 1] = acc[nb][k + j][2 + i] * inv;
+              }
+              dst[k / 4] = pack8_bf16(x);
+            }
+            if (p.lse && g == 0) p.lse[tok * p.hq + head] = (m[nb][i] - kPShift + log2f(l[nb][i])) * 0.6931471805599453f;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS; k += 2)
+            *reinterpret_cast<float4*>(part + rr * HD + g * (HD / 8) + 2 * k) =
+                make_float4(acc[nb][k][i], acc[nb][k][2 + i], acc[nb][k + 1][i], acc[nb][k + 1][2 + i]);
+          if (g == 0) {
+            part[K::ROWS * HD + rr] = m[nb][i];
+            part[K::ROWS * HD + K::ROWS + rr] = l[nb][i];
+          }
+        }
+      }
+    f = fend;
+  }
+  cp_wait<0>();
+
+  // ---- the CTA's unfinished units, in order; a thread keeps EPT values of one row
+  __syncthreads();
+  constexpr int EPT = K::ROWS * HD / K::THREADS;
+  const int row = tid / (HD / EPT), d0 = (tid % (HD / EPT)) * EPT;
+  uint32_t cur = 0xFFFFFFFFu;
+  int cb = 0, cu_ = 0;
+  float M = -INFINITY, L = 0.f, a[EPT];
+  int4 meta = make_int4(0, 0, 0, 0);
+  auto flush = [&]() {
+    if (cur == 0xFFFFFFFFu) return;
+    SeqWork<NB> sw;
+    sw.load(p, cb);
+    if (cur >= clo && cur + (uint32_t)sw.ng <= chi) {
+      const int rr = (cu_ % sw.nrb) * K::ROWS + row;
+      if (rr < sw.n * p.group) {
+        const long long tok = sw.tok0 + rr / p.group;
+        const int head = (cu_ / sw.nrb) * p.group + rr % p.group;
+        const float inv = L == 0.f ? 0.f : 8.0f / L;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o.p) + tok * p.o.ts + head * p.o.hs + d0;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) dst[i] = __float2bfloat16(a[i] * inv);
+        if (p.lse && d0 == 0) p.lse[tok * p.hq + head] = (M - kPShift + log2f(L)) * 0.6931471805599453f;
+      }
+      return;
+    }
+    const bool cont = cur < clo;
+    if (cont) meta.x = cur + (uint32_t)sw.ng <= chi ? 3 : 1;
+    else meta.y = 1, meta.z = cb, meta.w = cu_;
+    float* dst = p.parts + ((size_t)cta * 2 + (cont ? 0 : 1)) * K::PART;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) dst[row * HD + d0 + i] = a[i];
+    if (d0 == 0) {
+      dst[K::ROWS * HD + row] = M;
+      dst[K::ROWS * HD + K::ROWS + row] = L;
+    }
+  };
+#pragma unroll 1
+  for (int e = 0; e < 2 * K::WARPS; ++e) {
+    const uint32_t id = ent_uid[e];
+    if (id == 0xFFFFFFFFu) continue;
+    if (id != cur) {
+      flush();
+      cur = id;
+      cb = ent_b[e];
+      cu_ = ent_u[e];
+      M = -INFINITY;
+      L = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) a[i] = 0.f;
+    }
+    const float* part = (e & 1) ? reinterpret_cast<const float*>(smem + (e >> 1) * K::RING)
+                                : p.wparts + ((size_t)cta * K::WARPS + (e >> 1)) * K::PART;
+    const float me = part[K::ROWS * HD + row], le = part[K::ROWS * HD + K::ROWS + row];
+    const float mn = fmaxf(M, me);
+    const float fa = M == -INFINITY ? 0.f : ex2(M - mn), fe = me == -INFINITY ? (le == 0.f ? 0.f : 1.f) : ex2(me - mn);
+    L = L * fa + le * fe;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) a[i] = a[i] * fa + part[row * HD + d0 + i] * fe;
+    M = mn;
+  }
+  flush();
+  if (tid == 0) p.meta[cta] = meta;
+}
+
+// Units that more than one CTA worked on: block (c, y) joins rows 2y and 2y + 1 of the unit that CTA
+// c opened with the parts that the following CTAs continued.
+template <int HD, int NB>
+__global__ void __launch_bounds__(HD / 2) join_kernel(const AttnParams p) {
+  using K = AttnCfg<HD, NB>;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched before the attention kernel has ended)
+  const int c = blockIdx.x;
+  const int4 meta = p.meta[c];
+  if (!meta.y) return;
+  SeqWork<NB> sw;
+  sw.load(p, meta.z);
+  const int row = blockIdx.y * 2 + threadIdx.x / (HD / 4), d0 = (threadIdx.x % (HD / 4)) * 4;
+  const int rr = (meta.w % sw.nrb) * K::ROWS + row;
+  if (rr >= sw.n * p.group) return;
+  float M = -INFINITY, L = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float* part) {
+    const float me = part[K::ROWS * HD + row], le = part[K::ROWS * HD + K::ROWS + row];
+    const float4 x = *reinterpret_cast<const float4*>(part + row * HD + d0);
+    const float mn = fmaxf(M, me);
+    const float fa = M == -INFINITY ? 0.f : ex2(M - mn), fe = me == -INFINITY ? (le == 0.f ? 0.f : 1.f) : ex2(me - mn);
+    L = L * fa + le * fe;
+    a.x = a.x * fa + x.x * fe;
+    a.y = a.y * fa + x.y * fe;
+    a.z = a.z * fa + x.z * fe;
+    a.w = a.w * fa + x.w * fe;
+    M = mn;
+  };
+  add(p.parts + ((size_t)c * 2 + 1) * K::PART);
+  for (int i = c + 1; i < (int)gridDim.x; ++i) {
+    const int flags = p.meta[i].x;
+    if (!(flags & 1)) break;
+    add(p.parts + (size_t)i * 2 * K::PART);
+    if (flags & 2) break;
+  }
+  const long long tok = sw.tok0 + rr / p.group;
+  const int head = (meta.w / sw.nrb) * p.group + rr % p.group;
+  const float inv = L == 0.f ? 0.f : 8.0f / L;
+  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + d0);
+  dst[0] = __floats2bfloat162_rn(a.x * inv, a.y * inv);
+  dst[1] = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+  if (p.lse && d0 == 0) p.lse[tok * p.hq + head] = (M - kPShift + log2f(L)) * 0.6931471805599453f;
+}
+
+}  // namespace kvq
+}  // namespace dec

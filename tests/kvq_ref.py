@@ -44,7 +44,8 @@ def norm_rotate(x, w, eps, table, pos, interleaved):
 
 def attend(q, k, v, scale, seen):
     """q [hq, hd], k, v [positions, hkv, hd]: out, lse, and per (head, d) what sizes the error bounds:
-    sum_p p |v| and max over the seen positions of scale * sum_d |q k|."""
+    sum_p p |v| + 2^-29 sum_p |v| / sum_p e^(s - max) (out_bounds takes 2^-11 of it) and max over the
+    seen positions of scale * sum_d |q k|."""
     hq, hd = q.shape
     out, lse = np.zeros((hq, hd)), np.full(hq, -np.inf)
     mass, big = np.zeros((hq, hd)), np.zeros(hq)
@@ -58,7 +59,8 @@ def attend(q, k, v, scale, seen):
         e = np.exp(s - m)
         p = e / e.sum()
         out[h], lse[h] = p @ vv, m + np.log(e.sum())
-        mass[h], big[h] = p @ np.abs(vv), (np.abs(kk) @ np.abs(q[h])).max() * scale
+        mass[h] = p @ np.abs(vv) + 2.0 ** -29 * np.abs(vv).sum(0) / e.sum()
+        big[h] = (np.abs(kk) @ np.abs(q[h])).max() * scale
     return out, lse, mass, big
 
 
@@ -66,8 +68,11 @@ def out_bounds(out, lse, mass, big, hd, seen):
     """Bounds of the kernel's error. A score is a sum of hd exact products in fp32: off by at most
     d = hd 2^-23 big (an fp32 accumulator may truncate: a whole step, 2^-23, per addition) plus the
     queries' 2^-25 of the row's largest |q| (below big 2^-14 / hd), plus the exponent's own rounding,
-    2^-22 big. Every probability is then off by a factor e^(2 d'), rounds to 11 bits (2^-11, or
-    2^-24 of the largest term's 2^10) and sums in fp32 over `seen` terms; the output rounds to bf16."""
+    2^-22 big. Every probability is then off by a factor e^(2 d'), rounds to 11 bits and sums in fp32
+    over `seen` terms; the output rounds to bf16. Rounding to 11 bits is 2^-11 of a term as long as f16
+    has them: terms e^(s - max) are kept times 2^15, and f16's subnormal step is 2^-24, so a term is off
+    by half a step, 2^-25 / 2^15 = 2^-40 (of the largest term, 1, before the division by the sum), at
+    least; times |v| and summed that is 2^-11 of `mass`'s second part, 2^-29 sum |v| / sum e^(s - max)."""
     d = hd * 2.0 ** -23 * big + 2.0 ** -14 / hd * big * 2.0 ** -9 + 2.0 ** -21 * (big + 1)
     n = 2.0 ** -23 * (np.sqrt(seen) * 8 + 32)
     ob = 2.0 ** -8 * np.abs(out) + mass * (2.0 ** -11 + 2 * d[:, None] + n) + 1e-30

@@ -267,6 +267,43 @@ def test_a_nan_reaches_only_its_own_heads():
     assert torch.isnan(out[0, :4]).any(-1).all() and torch.equal(torch.isnan(out[0, 4:]).any(), torch.tensor(False, device="cuda"))
 
 
+@pytest.mark.parametrize("hd,hq,m", [(128, 8, 4), (64, 4, 8), (128, 4, 20)])
+def test_a_nan_value_reaches_only_rows_that_see_it(hd, hq, m):
+    """Token 2's key and value hold a NaN: the rows of tokens 0 and 1 are as if it were not there, and
+    later rows get it where their own formula puts it."""
+    cache, table, k, v, g = _filled([21 + m], 1, hd, 16, 13)
+    q = _rnd(g, m, hq, hd).cuda()
+    ln, cu = _ints([20]), _cu([m])
+    good = cache.attention(q, ln, table, cu_tokens=cu, max_tokens=m)
+    gk, gv = cache.gather(_ints([22]), table, 1)
+    bad = gv.clone()
+    bad[0, 0, 17] = float("nan")
+    cache.append(gk, bad, _ints([22]), table)
+    out = cache.attention(q, ln, table, cu_tokens=cu, max_tokens=m)
+    assert torch.equal(out[:2], good[:2])
+    nan = torch.isnan(out[2:])
+    assert nan[..., 16:32].all() and not nan[..., :16].any() and not nan[..., 32:].any()  # the value's run
+    bad = gk.clone()
+    bad[0, 0, 0] = float("nan")
+    cache.append(bad, gv, _ints([22]), table)
+    out = cache.attention(q, ln, table, cu_tokens=cu, max_tokens=m)
+    assert torch.equal(out[:2], good[:2]) and torch.isnan(out[2:]).all()
+
+
+def test_attention_over_many_sequences():
+    """More sequences than one launch lists, most of them empty or short."""
+    b = 4500
+    lens = [(i * 7) % 5 for i in range(b)]
+    lens[2047], lens[2048], lens[4499] = 70, 130, 33
+    cache, table, k, v, g = _filled([l + 1 for l in lens], 1, 64, 16, 14)
+    q = _rnd(g, b, 2, 64)
+    out, lse = cache.attention(q.cuda(), _ints(lens), table, return_lse=True)
+    two = cache.attention(q.cuda(), _ints(lens), table, cu_tokens=_cu([1] * b), max_tokens=1)
+    cache.check()
+    assert torch.equal(out, two)
+    _check(_np(out), _np(lse), _np(q), k, v, [1] * b, lens, True, 0.125, 64)
+
+
 def test_append_then_attend_as_a_model_does():
     """Prompt, then single tokens, then a verify step of three, each appended with norm and rotation
     and attended to; the reference keeps the rows in 64 bits and stores them the same way."""
