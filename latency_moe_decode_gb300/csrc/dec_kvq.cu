@@ -150,7 +150,7 @@ int blocks_of(int n_heads, int hkv, int max_tokens) { return (long long)max_toke
 template <int HD, int NB>
 int64_t workspace_of(int sms) {
   using K = AttnCfg<HD, NB>;
-  return (int64_t)sms * ((2 + K::WARPS) * K::PART * 4 + 16);
+  return (int64_t)sms * ((2 + K::WARPS) * K::PART * 4 + 32);
 }
 
 template <int HD, int NB>
@@ -161,9 +161,10 @@ dec_status launch_attention(AttnParams p, int batch, uint8_t* ws, cudaStream_t s
   const int sms = op_sms();
   if (sms < 1) return op_fail(DEC_ERR_CUDA, "attention: no device");
   p.meta = reinterpret_cast<int4*>(ws);
-  p.parts = reinterpret_cast<float*>(ws + (size_t)sms * 16);
+  p.parts = reinterpret_cast<float*>(ws + (size_t)sms * 32);
   p.wparts = p.parts + (size_t)sms * 2 * K::PART;
   p.min_groups = kMinGroups;
+  p.magic = Magic{0x64006400u, 0x54005400u};
   const Seqs all = p.s;
   for (int b = 0; b < batch; b += kMaxSeqs) {
     p.s.batch = std::min(kMaxSeqs, batch - b);
@@ -175,8 +176,8 @@ dec_status launch_attention(AttnParams p, int batch, uint8_t* ws, cudaStream_t s
     cudaError_t ce = cudaGetLastError();
     if (ce != cudaSuccess) return op_cuda(ce, "attention");
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sms, K::ROWS / 2);
-    cfg.blockDim = dim3(HD / 2);
+    cfg.gridDim = dim3(sms);
+    cfg.blockDim = dim3(K::ROWS * 32);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -6,8 +6,8 @@
 //  - a unit is (sequence, KV head, block of 8 NB query rows), a query row being (token, head of
 //    the group); the groups of all units form one list, cut evenly over the CTAs and their warps
 //    (lengths are read on the device: the cut needs no host knowledge and adapts to ragged batches);
-//  - a warp streams its groups through its own ring with cp.async, two chunks ahead, without ever
-//    waiting for another warp;
+//  - a warp streams its groups through its own ring with bulk copies, one a group, some chunks ahead,
+//    without ever waiting for another warp;
 //  - S^T = K q^T and O^T = V^T P^T are 16 x 8 x 16 f16 products whose A operand, the codes, comes
 //    out of the ring in the lanes' own order: (code + 8) enters the low mantissa bits of the f16
 //    1024, and one fma turns it into code * scale exactly (4 x 4 significant bits). Tensor memory
@@ -18,14 +18,16 @@
 //  - what a warp leaves unfinished of a unit is joined per CTA in shared memory, and what a CTA
 //    leaves unfinished by a second small kernel, both in a fixed order.
 #pragma once
+#include <type_traits>
+
 #include "dec_kvq.cuh"
 
 namespace dec {
 namespace kvq {
 
-constexpr int kStages = 3;        // chunks of a warp's ring
-constexpr int kMaxSeqs = 2048;    // sequences of one launch (their prefix sums lie in shared memory)
-constexpr int kMinGroups = 16;    // groups a CTA takes at least
+constexpr int kStages = 3;       // chunks of a warp's ring
+constexpr int kMaxSeqs = 512;    // sequences of one launch (their table lies in shared memory)
+constexpr int kMinGroups = 8;    // groups a CTA takes at least
 constexpr float kPShift = 15.0f;  // probabilities are kept times 2^15: f16 then reaches 2^-39 of the largest
 
 template <int HD, int NB>
@@ -39,9 +41,15 @@ struct AttnCfg {
   static constexpr int PART = ROWS * HD + 2 * ROWS;  // floats of a partial: outputs, maxima, sums
   static constexpr int THREADS = WARPS * 32;
   static_assert(RING >= PART * 4 && RING % 16 == 0 && GB % 16 == 0, "a partial has to fit into a warp's ring");
-  static constexpr int smem() { return WARPS * RING + (kMaxSeqs + 1) * 4; }
+  static constexpr int smem() { return WARPS * RING + (kMaxSeqs + 1) * 16; }
 };
 
+// The f16 pairs 1024, 1024 and 64, 64 that codes are put into (Scale2), from the kernel's arguments:
+// with constants the compiler makes an and and an or of each lop3, 64 more a group on the pipe that
+// bounds the kernel.
+struct Magic {
+  uint32_t lo, hi;
+};
 struct AttnParams {
   Cache c;
   Seqs s;
@@ -51,19 +59,37 @@ struct AttnParams {
   int hq, group, causal, max_tokens;
   int b0;         // (without cu: token row of sequence 0)
   int min_groups; // groups a CTA takes at least
+  Magic magic;
   float* parts;   // [CTA][2] partials
   float* wparts;  // [CTA][warp] partials
-  int4* meta;     // [CTA]: continued (1) and finished here (2) | opens a unit, its sequence and index
+  int4* meta;     // [CTA][2]: unit continued (1) and finished here (2), unit left open | the open unit's place
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void bar_init(uint64_t* b) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(b)) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* b) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
+               "l"(src), "r"(bytes), "r"(smem_addr(b))
+               : "memory");
+}
+// Wait for the barrier's phase; false after about a second (a copy always ends: this only keeps a
+// mistake from holding the GPU).
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
+  for (int i = 0; i < (1 << 23); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(b)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -84,42 +110,187 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
-// Two scales (f16 pairs) and what turns (1024 + u) and (1024 + 16 u), u = code + 8, into code * s:
-// (1024 + u) s - 1032 s and (1024 + 16 u) (s / 16) - 72 s. All products are exact: s has 4
-// significant bits, 1032 = 129 * 8 and 72 = 9 * 8, and 1032 * 60 is still an f16.
+// Two scales (an f16 pair) and what turns codes into code * s. A code + 8 = u in the low 4 bits of
+// the f16 1024 is 1024 + u, in the next 4 bits of the f16 64 it is 64 + u; (1024 + u) s - 1032 s and
+// (64 + u) s - 72 s are exact, being u - 8 and s of 4 significant bits each, and so are the addends:
+// 1032 = 129 * 8, 72 = 9 * 8, and 1032 * 60 is still an f16.
 struct Scale2 {
-  __half2 s, s16, c, c16;
+  __half2 s, c, c16;
   __device__ __forceinline__ void set(uint32_t two) {  // scale bytes in the low bytes of the halves
     s = u2h(two << 7);
-    s16 = __hmul2(s, __float2half2_rn(0.0625f));
     c = __hmul2(s, __float2half2_rn(-1032.0f));
     c16 = __hmul2(s, __float2half2_rn(-72.0f));
   }
   // nibbles 0 and 1 of both halves of x
-  __device__ __forceinline__ void decode(uint32_t x, uint32_t& n0, uint32_t& n1) const {
-    n0 = h2u(__hfma2(u2h((x & 0x000F000Fu) | 0x64006400u), s, c));
-    n1 = h2u(__hfma2(u2h((x & 0x00F000F0u) | 0x64006400u), s16, c16));
+  __device__ __forceinline__ void decode(uint32_t x, const Magic& m, uint32_t& n0, uint32_t& n1) const {
+    uint32_t y, z;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(y) : "r"(x), "r"(m.lo));
+    asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(z) : "r"(x), "r"(m.hi));
+    n0 = h2u(__hfma2(u2h(y), s, c));
+    n1 = h2u(__hfma2(u2h(z), s, c16));
   }
 };
 
-// The list of groups: per sequence hkv * (row blocks) units of `ng` groups each.
+// The list of groups: per sequence hkv * (row blocks) units of `ng` groups each. Its table, in shared
+// memory: {first list entry, first token row, rows, length}.
 template <int NB>
 struct SeqWork {
   int tok0, n, len, ng, nrb;
-  __device__ __forceinline__ void load(const AttnParams& p, int b) {
+  uint32_t pre;
+  __device__ __forceinline__ void shape(const AttnParams& p) {
+    // (a unit without positions still writes its rows)
+    const int held = p.causal ? len + n : len;
+    const int most = p.s.max_pages << (p.c.page_shift - 4);
+    ng = max(1, min(most, (held + kGroup - 1) / kGroup));
+    nrb = (n * p.group + 8 * NB - 1) / (8 * NB);
+  }
+  __device__ __forceinline__ void load(const AttnParams& p, int b) {  // from the caller's arrays
     tok0 = p.s.cu ? __ldg(p.s.cu + b) : p.b0 + b;
     n = p.s.cu ? __ldg(p.s.cu + b + 1) - tok0 : 1;
     tok0 = max(tok0, 0);
     n = max(0, min(min(n, p.max_tokens), p.s.n_tokens - tok0));
     len = __ldg(p.s.lengths + b);
     const long long most = (long long)p.s.max_pages << p.c.page_shift;
-    if (len < 0 && n > 0) raise(p.c.status, DEC_ERR_ARG);
-    long long want = len < 0 ? 0 : p.causal ? (long long)len + n : len;
-    if (want > most && n > 0) raise(p.c.status, DEC_ERR_CAPACITY);
-    want = min(want, most);
+    if (n > 0 && len < 0) raise(p.c.status, DEC_ERR_ARG);
+    if (n > 0 && (p.causal ? (long long)len + n : len) > most) raise(p.c.status, DEC_ERR_CAPACITY);
     len = len < 0 ? -n : (int)min((long long)len, most);
-    ng = max(1, (int)((want + kGroup - 1) / kGroup));  // (a unit without positions still writes its rows)
-    nrb = (n * p.group + 8 * NB - 1) / (8 * NB);
+    shape(p);
+  }
+  __device__ __forceinline__ void get(const AttnParams& p, const int4& e) {
+    pre = (uint32_t)e.x;
+    tok0 = e.y;
+    n = e.z;
+    len = e.w;
+    shape(p);
+  }
+};
+
+// (one division for the common single row block)
+__device__ __forceinline__ int over(int a, int d) { return d == 1 ? a : a / d; }
+
+// The operands of O^T's products with a group's values (vw: the lane's words of positions 2t, 2t + 1,
+// 2t + 8, 2t + 9; bytes: their scales): put(k, a0..a3) for 16 values of the head at a time, of which
+// the lane's are 2k and 2k + 1 of its run.
+template <int HD, class F>
+__device__ __forceinline__ void v_product(const uint32_t (&vw)[4][HD / 64], uint32_t bytes, const Magic& magic, F&& put) {
+  Scale2 s0, s1;
+  s0.set(__byte_perm(bytes, 0, 0x4140));
+  s1.set(__byte_perm(bytes, 0, 0x4342));
+#pragma unroll
+  for (int w = 0; w < HD / 64; ++w)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {  // values 4 x .. 4 x + 3 of the word, positions paired
+      const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], x ? 0x7632 : 0x5410);
+      const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], x ? 0x7632 : 0x5410);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t a0, a1, a2, a3;
+        s0.decode(y ? x0 >> 8 : x0, magic, a0, a1);
+        s1.decode(y ? x1 >> 8 : x1, magic, a2, a3);
+        put(4 * w + 2 * x + y, a0, a1, a2, a3);
+      }
+    }
+}
+
+// The same with each query row by itself, the positions it does not see left out.
+template <int HD, int NB>
+struct RowsApart {
+  float acc[NB][HD / 16][4];
+  uint32_t pb[NB][2];
+  int seen[NB][2];
+  __device__ __noinline__ void add(const uint32_t (&vw)[4][HD / 64], uint32_t sb, const Magic& magic, int pos0) {
+    const int t = threadIdx.x & 3;
+    for (int c = 0; c < 8 * NB; ++c) {
+      int mine = 0;  // what row c sees
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int s0 = __shfl_sync(0xffffffffu, seen[nb][0], (c & 7) >> 1);
+        const int s1 = __shfl_sync(0xffffffffu, seen[nb][1], (c & 7) >> 1);
+        if (c >> 3 == nb) mine = (c & 1) ? s1 : s0;
+      }
+      uint32_t mb = sb;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (pos0 + 2 * t + (k & 1) + (k >> 1) * 8 >= mine) mb &= ~(0xFFu << (8 * k));
+      v_product<HD>(vw, mb, magic, [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float d[4] = {acc[nb][k][0], acc[nb][k][1], acc[nb][k][2], acc[nb][k][3]};
+          mma16816(d, a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+          if (c == nb * 8 + 2 * t) {
+            acc[nb][k][0] = d[0];
+            acc[nb][k][2] = d[2];
+          }
+          if (c == nb * 8 + 2 * t + 1) {
+            acc[nb][k][1] = d[1];
+            acc[nb][k][3] = d[3];
+          }
+        }
+      });
+    }
+  }
+};
+
+// A unit's place: {first token row of its sequence, first query head, first query row, rows of the
+// sequence}. A row of it being joined from parts, HD / 32 values a lane.
+template <int HD>
+struct Joined {
+  static constexpr int V = HD / 32;
+  float M, L, w, a[V];  // the joined maximum and sum; the lane's part's weight; outputs
+  // parts' maxima and sums, one per lane (none: -infinity, 0). A part of NaNs (its maximum is
+  // -infinity, its sum NaN) makes the sum NaN.
+  __device__ __forceinline__ void weigh(float m, float l) {
+    M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    w = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);
+    L = l * w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = 0.f;
+  }
+  __device__ __forceinline__ void load(const float* part, int lane, float (&x)[V]) const {
+    if (V == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(part + lane * 4);
+      x[0] = f.x; x[1] = f.y; x[V - 2] = f.z; x[V - 1] = f.w;
+    } else {
+      const float2 f = *reinterpret_cast<const float2*>(part + lane * 2);
+      x[0] = f.x; x[1] = f.y;
+    }
+  }
+  __device__ __forceinline__ void mul(const float (&x)[V], float wt) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = fmaf(x[i], wt, a[i]);
+  }
+  __device__ __forceinline__ void add(const float* part, float wt, int lane) {
+    float x[V];
+    load(part, lane, x);
+    mul(x, wt);
+  }
+  __device__ __forceinline__ void join(const Joined& o) {
+    const float mn = fmaxf(M, o.M);
+    const float fa = M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : ex2(M - mn);
+    const float fo = o.M == -INFINITY ? (o.L == 0.f ? 0.f : 1.f) : ex2(o.M - mn);
+    M = mn;
+    L = L * fa + o.L * fo;
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = a[i] * fa + o.a[i] * fo;
+  }
+  __device__ __forceinline__ void keep(float* part, int lane) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) part[lane * V + i] = a[i];
+  }
+  __device__ __forceinline__ void store(const AttnParams& p, const int4& place, int row, int lane) const {
+    const int rr = place.z + row;
+    const long long tok = place.x + rr / p.group;
+    const int head = place.y + rr % p.group;
+    const float inv = L == 0.f ? 0.f : 8.0f / L;  // (8: the scale bytes' factor)
+    __nv_bfloat162* dst =
+        reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + lane * V);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) dst[i] = __floats2bfloat162_rn(a[2 * i] * inv, a[2 * i + 1] * inv);
+    if (p.lse && lane == 0) p.lse[tok * p.hq + head] = (M - kPShift + log2f(L)) * 0.6931471805599453f;
   }
 };
 
@@ -129,21 +300,29 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
   constexpr int KS = K::KS, CH = K::CH;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t sh_scan[K::WARPS];
-  __shared__ uint32_t ent_uid[2 * K::WARPS];
-  __shared__ int ent_b[2 * K::WARPS], ent_u[2 * K::WARPS];
-  uint32_t* const pre = reinterpret_cast<uint32_t*>(smem + K::WARPS * K::RING);  // [batch + 1]
+  // what the warps leave unfinished, in the list's order: two entries a warp (a unit it found begun, a
+  // unit it left open). First and last + 1 list entry of the unit; its place (see Place)
+  __shared__ uint2 ent_unit[32];
+  __shared__ int4 ent_place[32];
+  __shared__ uint64_t bars[K::WARPS][kStages];  // chunk landed
+  int4* const seqs = reinterpret_cast<int4*>(smem + K::WARPS * K::RING);  // [batch + 1]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join kernel waits for this one's end)
 
   // ---- the list's prefix sums over the sequences
-  if (tid < 2 * K::WARPS) ent_uid[tid] = 0xFFFFFFFFu;
+  static_assert(2 * K::WARPS <= 32, "one entry per lane in the join");
+  if (tid < 32) ent_unit[tid] = make_uint2(0u, 0u);
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) bar_init(bars[warp] + i);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   uint32_t base = 0;
   for (int b0 = 0; b0 < p.s.batch; b0 += K::THREADS) {
     const int b = b0 + tid;
     uint32_t w = 0;
+    SeqWork<NB> sw;
     if (b < p.s.batch) {
-      SeqWork<NB> sw;
       sw.load(p, b);
       w = (uint32_t)p.c.hkv * sw.nrb * sw.ng;
     }
@@ -163,14 +342,14 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
       before += i < warp ? y : 0u;
       all += y;
     }
-    if (b < p.s.batch) pre[b] = before + x - w;
+    if (b < p.s.batch) seqs[b] = make_int4((int)(before + x - w), sw.tok0, sw.n, sw.len);
     base = all;
   }
-  if (tid == 0) pre[p.s.batch] = base;
   __syncthreads();
   const uint32_t W = base;
   const int ctas = (int)min((uint32_t)gridDim.x, (W + p.min_groups - 1) / p.min_groups);
   const int cta = blockIdx.x;
+  if (tid == 0) p.meta[2 * cta] = make_int4(0, 0, 0, 0);  // (before the barrier that the join's marks come after)
   uint32_t clo = 0, chi = 0;
   if (cta < ctas) {
     clo = (uint32_t)((unsigned long long)W * cta / ctas);
@@ -184,7 +363,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
     int a = 0, z = p.s.batch;
     while (z - a > 1) {
       const int m = (a + z) >> 1;
-      if (pre[m] <= f) a = m;
+      if ((uint32_t)seqs[m].x <= f) a = m;
       else z = m;
     }
     return a;
@@ -192,7 +371,8 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
 
   uint8_t* const ring = smem + warp * K::RING;
 
-  // ---- the copies: 32 entries' group indices at a time, one per lane
+  // ---- the copies: 32 entries' group indices at a time, one per lane, and each lane copies its own
+  // (one bulk copy a group: a group is contiguous)
   uint32_t vb = lo, pf = lo;  // first entry of the lanes' window; next entry to copy
   int vg = -1, vrem = 0;      // its group in the cache (-1: nothing to copy), entries left of its unit
   auto window = [&](uint32_t f0) {
@@ -203,8 +383,8 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
     if (f < hi) {
       const int b = seq_at(f);
       SeqWork<NB> sw;
-      sw.load(p, b);
-      const uint32_t r = f - pre[b];
+      sw.get(p, seqs[b]);
+      const uint32_t r = f - sw.pre;
       const int u = (int)(r / (uint32_t)sw.ng), gr = (int)(r - (uint32_t)u * sw.ng);
       vrem = sw.ng - gr;
       const int pos = gr * kGroup;
@@ -212,31 +392,25 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
         const int e = pos >> p.c.page_shift;
         const int page = __ldg(p.s.table + b * p.s.table_stride + e);
         const int gpp = 1 << (p.c.page_shift - 4);
-        if ((unsigned)page < (unsigned)p.c.n_pages) vg = (page * p.c.hkv + u / sw.nrb) * gpp + (gr & (gpp - 1));
+        if ((unsigned)page < (unsigned)p.c.n_pages) vg = (page * p.c.hkv + over(u, sw.nrb)) * gpp + (gr & (gpp - 1));
         else raise(p.c.status, DEC_ERR_ARG);
       }
     }
   };
   int pstage = 0;
   auto prefetch = [&]() {  // the next chunk, if there is one
-    if (pf < hi) {
-      if (pf + CH > vb + 32) window(pf);
-      const int at = (int)(pf - vb);
-      const int n = min(min(CH, __shfl_sync(0xffffffffu, vrem, at)), (int)(hi - pf));
-      const uint32_t dst = smem_addr(ring + pstage * CH * K::GB) + lane * 16;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int gi = __shfl_sync(0xffffffffu, vg, (at + i) & 31);
-        if (i < n && gi >= 0) {
-          const uint8_t* src = p.c.pages + (size_t)gi * K::GB + lane * 16;
-#pragma unroll
-          for (int o = 0; o < K::GB; o += 512)
-            if (o + 512 <= K::GB || lane * 16 + o < K::GB) cp16(dst + i * K::GB + o, src + o);
-        }
-      }
-      pf += n;
-    }
-    cp_commit();
+    if (pf >= hi) return;
+    if (pf + CH > vb + 32) window(pf);
+    const int at = (int)(pf - vb);
+    const int n = min(min(CH, __shfl_sync(0xffffffffu, vrem, at)), (int)(hi - pf));
+    const bool copies = lane >= at && lane < at + n && vg >= 0;
+    const uint32_t who = __ballot_sync(0xffffffffu, copies);
+    uint64_t* const bar = bars[warp] + pstage;
+    if (lane == 0) bar_expect(bar, __popc(who) * K::GB);
+    __syncwarp();
+    if (copies)
+      bulk_copy(ring + (pstage * CH + lane - at) * K::GB, p.c.pages + (size_t)vg * K::GB, K::GB, bar);
+    pf += n;
     pstage = pstage == kStages - 1 ? 0 : pstage + 1;
   };
 
@@ -251,15 +425,17 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
     for (int i = 0; i < kStages - 1; ++i) prefetch();
   }
   int cstage = 0;
-  for (uint32_t f = lo; f < hi;) {
+  uint32_t cphase = 0;
+  bool dead = false;
+  const Magic magic = p.magic;
+  for (uint32_t f = lo; f < hi && !dead;) {
     // ---- a unit: its rows' queries as the second operand of S^T, halved down to magnitude 1 .. 2
     const int b = seq_at(f);
     SeqWork<NB> sw;
-    sw.load(p, b);
-    const uint32_t r = f - pre[b];
-    const int u = (int)(r / (uint32_t)sw.ng);
-    const uint32_t uid = pre[b] + (uint32_t)u * sw.ng;  // where the unit starts: its name
-    const int h = u / sw.nrb, row0 = (u % sw.nrb) * K::ROWS, rows = sw.n * p.group;
+    sw.get(p, seqs[b]);
+    const int u = (int)((f - sw.pre) / (uint32_t)sw.ng);
+    const uint32_t uid = sw.pre + (uint32_t)u * sw.ng;  // where the unit starts: its name
+    const int h = over(u, sw.nrb), row0 = (u - h * sw.nrb) * K::ROWS, rows = sw.n * p.group;
     int smin = 0x7FFFFFFF, smax = 0;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -295,7 +471,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
         qf[nb][s][0] = h2u(__floats2half2_rn(val(i), val(i + 4)));
         qf[nb][s][1] = h2u(__floats2half2_rn(val(i + 1), val(i + 5)));
       }
-      const float up = p.scale * __int_as_float((127 + e) << 23);
+      const float up = fmaxf(p.scale * __int_as_float((127 + e) << 23), 1e-37f);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         sc[nb][i] = __shfl_sync(0xffffffffu, up, (2 * t + i) * 4);
@@ -320,15 +496,9 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
     }
     const uint32_t fend = min(hi, uid + (uint32_t)sw.ng);
 
-    // ---- its groups, a chunk at a time
-    for (uint32_t f0 = f; f0 < fend; f0 += CH) {
-      const int n = min(CH, (int)(fend - f0));
-      const int pos0 = (int)(f0 - uid) * kGroup;
-      prefetch();
-      cp_wait<kStages - 1>();
-      __syncwarp();
-      const uint8_t* const buf = ring + cstage * CH * K::GB;
-      cstage = cstage == kStages - 1 ? 0 : cstage + 1;
+    // ---- its groups, a chunk at a time: with every group there and seen by every row, or not
+    auto chunk = [&](auto edge, const uint8_t* buf, int pos0, int n) {
+      constexpr bool EDGE = decltype(edge)::value;
       float s[NB][CH][4];
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
@@ -336,7 +506,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[nb][i][j] = 0.f;
-        if (i < n) {
+        if (!EDGE || i < n) {
           const uint8_t* gp = buf + i * K::GB;
           uint32_t k0[HD / 32], k1[HD / 32];  // words of positions g and g + 8
           uint32_t sb;
@@ -368,8 +538,8 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 uint32_t a0, a1, a2, a3;
-                s0.decode(y ? k0[wi] >> 8 : k0[wi], a0, a2);
-                s1.decode(y ? k1[wi] >> 8 : k1[wi], a1, a3);
+                s0.decode(y ? k0[wi] >> 8 : k0[wi], magic, a0, a2);
+                s1.decode(y ? k1[wi] >> 8 : k1[wi], magic, a1, a3);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
                   mma16816(s[nb][i], a0, a1, a2, a3, qf[nb][2 * wi + y][0], qf[nb][2 * wi + y][1]);
@@ -378,19 +548,17 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
           }
         }
       }
-      // scores in units of log2; what a row does not see is -infinity, whatever it held
-      const bool edge = n < CH || pos0 + CH * kGroup > smin;
+      // what a row does not see is -infinity, whatever it held; maxima in units of log2
       uint32_t pb[NB][CH][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float mx0 = m[nb][0], mx1 = m[nb][1];
+        float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
+          if (EDGE) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x = s[nb][i][j] * sc[nb][j & 1];
-            if (edge && (i >= n || pos0 + i * kGroup + g + (j >> 1) * 8 >= seen[nb][j & 1])) x = -INFINITY;
-            s[nb][i][j] = x;
+            for (int j = 0; j < 4; ++j)
+              if (i >= n || pos0 + i * kGroup + g + (j >> 1) * 8 >= seen[nb][j & 1]) s[nb][i][j] = -INFINITY;
           }
           mx0 = fmaxf(mx0, fmaxf(s[nb][i][0], s[nb][i][2]));
           mx1 = fmaxf(mx1, fmaxf(s[nb][i][1], s[nb][i][3]));
@@ -400,6 +568,8 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
           mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
         }
+        mx0 = fmaxf(m[nb][0], mx0 * sc[nb][0]);
+        mx1 = fmaxf(m[nb][1], mx1 * sc[nb][1]);
         if (__any_sync(0xffffffffu, mx0 > m[nb][0] || mx1 > m[nb][1])) {
           const float f0_ = m[nb][0] == -INFINITY ? 0.f : ex2(m[nb][0] - mx0);
           const float f1_ = m[nb][1] == -INFINITY ? 0.f : ex2(m[nb][1] - mx1);
@@ -418,8 +588,8 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
         const float z0 = (mx0 == -INFINITY ? 0.f : mx0) - kPShift, z1 = (mx1 == -INFINITY ? 0.f : mx1) - kPShift;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-          const float e0 = ex2(s[nb][i][0] - z0), e1 = ex2(s[nb][i][1] - z1);
-          const float e2 = ex2(s[nb][i][2] - z0), e3 = ex2(s[nb][i][3] - z1);
+          const float e0 = ex2(fmaf(s[nb][i][0], sc[nb][0], -z0)), e1 = ex2(fmaf(s[nb][i][1], sc[nb][1], -z1));
+          const float e2 = ex2(fmaf(s[nb][i][2], sc[nb][0], -z0)), e3 = ex2(fmaf(s[nb][i][3], sc[nb][1], -z1));
           l[nb][0] += e0 + e2;
           l[nb][1] += e1 + e3;
           pb[nb][i][0] = transpose8x8(h2u(__floats2half2_rn(e0, e1)));
@@ -428,7 +598,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
       }
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        if (i >= n) continue;
+        if (EDGE && i >= n) continue;
         const uint8_t* gp = buf + i * K::GB + code_bytes(HD);
         uint32_t vw[4][HD / 64];  // words of positions 2t, 2t + 1, 2t + 8, 2t + 9
         uint32_t sb;
@@ -445,74 +615,65 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
         }
         // what no row sees counts nothing, whatever is there: scale 0
         const int left = smax - (pos0 + i * kGroup);
-        if (left < kGroup) {
+        if (EDGE && left < kGroup) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (2 * t + (k & 1) + (k >> 1) * 8 >= left) sb &= ~(0xFFu << (8 * k));
         }
-        auto product = [&](uint32_t bytes, auto&& put) {
-          Scale2 s0, s1;
-          s0.set(__byte_perm(bytes, 0, 0x4140));
-          s1.set(__byte_perm(bytes, 0, 0x4342));
-#pragma unroll
-          for (int w = 0; w < HD / 64; ++w)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {  // values 4 x .. 4 x + 3 of the word, positions paired
-              const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], x ? 0x7632 : 0x5410);
-              const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], x ? 0x7632 : 0x5410);
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                uint32_t a0, a1, a2, a3;
-                s0.decode(y ? x0 >> 8 : x0, a0, a1);
-                s1.decode(y ? x1 >> 8 : x1, a2, a3);
-                put(4 * w + 2 * x + y, a0, a1, a2, a3);
-              }
-            }
-        };
         // A run of NaNs at a position that some of the rows do not see (0 x NaN is NaN): each row by
         // itself, with the positions it does not see left out. Rows of one decode token all see
         // the same, and finite caches never come here.
         bool odd = false;
-        if (edge && smin < smax) {
+        if (EDGE && smin < smax) {
           const uint32_t x = ~sb;  // a byte of 255
           odd = __any_sync(0xffffffffu, ((x - 0x01010101u) & ~x & 0x80808080u) != 0);
         }
         if (!odd) {
-          product(sb, [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          v_product<HD>(vw, sb, magic, [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) mma16816(acc[nb][k], a0, a1, a2, a3, pb[nb][i][0], pb[nb][i][1]);
           });
-        } else {
-          for (int c = 0; c < K::ROWS; ++c) {
-            int mine = 0;  // what row c sees
+        } else if constexpr (EDGE) {
+          RowsApart<HD, NB> r;  // (a copy: the accumulators themselves stay in registers)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              const int s0 = __shfl_sync(0xffffffffu, seen[nb][0], (c & 7) >> 1);
-              const int s1 = __shfl_sync(0xffffffffu, seen[nb][1], (c & 7) >> 1);
-              if (c >> 3 == nb) mine = (c & 1) ? s1 : s0;
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) r.acc[nb][k][j] = acc[nb][k][j];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              r.pb[nb][j] = pb[nb][i][j];
+              r.seen[nb][j] = seen[nb][j];
             }
-            uint32_t mb = sb;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (pos0 + i * kGroup + 2 * t + (k & 1) + (k >> 1) * 8 >= mine) mb &= ~(0xFFu << (8 * k));
-            product(mb, [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                float d[4] = {acc[nb][k][0], acc[nb][k][1], acc[nb][k][2], acc[nb][k][3]};
-                mma16816(d, a0, a1, a2, a3, pb[nb][i][0], pb[nb][i][1]);
-                if (c == nb * 8 + 2 * t) {
-                  acc[nb][k][0] = d[0];
-                  acc[nb][k][2] = d[2];
-                }
-                if (c == nb * 8 + 2 * t + 1) {
-                  acc[nb][k][1] = d[1];
-                  acc[nb][k][3] = d[3];
-                }
-              }
-            });
           }
+          r.add(vw, sb, magic, pos0 + i * kGroup);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[nb][k][j] = r.acc[nb][k][j];
         }
       }
+    };
+    for (uint32_t f0 = f; f0 < fend; f0 += CH) {
+      const int n = min(CH, (int)(fend - f0));
+      const int pos0 = (int)(f0 - uid) * kGroup;
+      prefetch();
+      if (!bar_wait(bars[warp] + cstage, cphase)) {
+        raise(p.c.status, DEC_ERR_TIMEOUT);
+        for (int i = 1; i < kStages; ++i) bar_wait(bars[warp] + (cstage + i) % kStages, i + cstage < kStages ? cphase : cphase ^ 1);
+        dead = true;
+        break;
+      }
+      const uint8_t* const buf = ring + cstage * CH * K::GB;
+      if (++cstage == kStages) {
+        cstage = 0;
+        cphase ^= 1;
+      }
+      if (n < CH || pos0 + CH * kGroup > smin) chunk(std::true_type(), buf, pos0, n);
+      else chunk(std::false_type(), buf, pos0, n);
       __syncwarp();  // (the next copy goes where this chunk lay)
     }
 
@@ -529,16 +690,13 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
     if (!whole) {
       const int e = 2 * warp + (last ? 1 : 0);
       if (last) {
-        cp_wait<0>();
-        __syncwarp();
         part = reinterpret_cast<float*>(ring);
       } else {
         part = p.wparts + ((size_t)cta * K::WARPS + warp) * K::PART;
       }
       if (lane == 0) {
-        ent_uid[e] = uid;
-        ent_b[e] = b;
-        ent_u[e] = u;
+        ent_unit[e] = make_uint2(uid, uid + (uint32_t)sw.ng);
+        ent_place[e] = make_int4(sw.tok0, h * p.group, row0, rows);
       }
     }
 #pragma unroll
@@ -577,114 +735,120 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
       }
     f = fend;
   }
-  cp_wait<0>();
 
-  // ---- the CTA's unfinished units, in order; a thread keeps EPT values of one row
+  // ---- the CTA's unfinished units: one warp per (unit, row), the parts in the list's order
   __syncthreads();
-  constexpr int EPT = K::ROWS * HD / K::THREADS;
-  const int row = tid / (HD / EPT), d0 = (tid % (HD / EPT)) * EPT;
-  uint32_t cur = 0xFFFFFFFFu;
-  int cb = 0, cu_ = 0;
-  float M = -INFINITY, L = 0.f, a[EPT];
-  int4 meta = make_int4(0, 0, 0, 0);
-  auto flush = [&]() {
-    if (cur == 0xFFFFFFFFu) return;
-    SeqWork<NB> sw;
-    sw.load(p, cb);
-    if (cur >= clo && cur + (uint32_t)sw.ng <= chi) {
-      const int rr = (cu_ % sw.nrb) * K::ROWS + row;
-      if (rr < sw.n * p.group) {
-        const long long tok = sw.tok0 + rr / p.group;
-        const int head = (cu_ / sw.nrb) * p.group + rr % p.group;
-        const float inv = L == 0.f ? 0.f : 8.0f / L;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o.p) + tok * p.o.ts + head * p.o.hs + d0;
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) dst[i] = __float2bfloat16(a[i] * inv);
-        if (p.lse && d0 == 0) p.lse[tok * p.hq + head] = (M - kPShift + log2f(L)) * 0.6931471805599453f;
+  const uint2 mine = lane < 2 * K::WARPS ? ent_unit[lane] : make_uint2(0u, 0u);
+  const bool there = mine.y != 0;
+  const uint32_t valid = __ballot_sync(0xffffffffu, there);
+  const uint32_t below = valid & ((1u << lane) - 1u);
+  const uint32_t prev = __shfl_sync(0xffffffffu, mine.x, below ? 31 - __clz(below) : 0);
+  const uint32_t leads = __ballot_sync(0xffffffffu, there && (!below || prev != mine.x));
+  for (int k = warp; k < __popc(leads); k += K::WARPS) {
+    uint32_t at = leads;
+    for (int i = k; i > 0; --i) at &= at - 1;
+    const int e0 = __ffs(at) - 1;
+    const uint32_t after = e0 == 31 ? 0u : leads >> (e0 + 1);
+    const uint32_t span = (after ? (1u << (e0 + __ffs(after))) - 1u : 0xFFFFFFFFu) & ~((1u << e0) - 1u) & valid;
+    const uint2 unit = ent_unit[e0];
+    const int4 place = ent_place[e0];
+    const bool cont = unit.x < clo, open = unit.y > chi;
+    if (lane == 0) {  // (at most one unit is continued and one left open)
+      if (cont) p.meta[2 * cta].x = open ? 1 : 3;
+      else if (open) {
+        p.meta[2 * cta].y = 1;
+        p.meta[2 * cta + 1] = place;
       }
-      return;
     }
-    const bool cont = cur < clo;
-    if (cont) meta.x = cur + (uint32_t)sw.ng <= chi ? 3 : 1;
-    else meta.y = 1, meta.z = cb, meta.w = cu_;
-    float* dst = p.parts + ((size_t)cta * 2 + (cont ? 0 : 1)) * K::PART;
+    auto part_of = [&](int e) {
+      return (e & 1) ? reinterpret_cast<const float*>(smem + (e >> 1) * K::RING)
+                     : p.wparts + ((size_t)cta * K::WARPS + (e >> 1)) * K::PART;
+    };
+    const bool has = span >> lane & 1u;
+    const float* const mp = part_of(has ? lane : e0) + K::ROWS * HD;
+    for (int r0 = 0; r0 < K::ROWS && place.z + r0 < place.w; r0 += 4) {  // four rows' loads at a time
+      Joined<HD> j[4];
+      float me[4], le[4];
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) dst[row * HD + d0 + i] = a[i];
-    if (d0 == 0) {
-      dst[K::ROWS * HD + row] = M;
-      dst[K::ROWS * HD + K::ROWS + row] = L;
+      for (int r = 0; r < 4; ++r) {
+        me[r] = mp[r0 + r];
+        le[r] = mp[K::ROWS + r0 + r];
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) j[r].weigh(has ? me[r] : -INFINITY, has ? le[r] : 0.f);
+      for (uint32_t x = span; x; x &= x - 1) {
+        const int e = __ffs(x) - 1;
+        const float* part = part_of(e) + r0 * HD;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) j[r].add(part + r * HD, __shfl_sync(0xffffffffu, j[r].w, e), lane);
+      }
+      if (!cont && !open) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (place.z + r0 + r < place.w) j[r].store(p, place, r0 + r, lane);
+      } else {
+        float* dst = p.parts + ((size_t)cta * 2 + (cont ? 0 : 1)) * K::PART;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          j[r].keep(dst + (r0 + r) * HD, lane);
+          if (lane == 0) {
+            dst[K::ROWS * HD + r0 + r] = j[r].M;
+            dst[K::ROWS * HD + K::ROWS + r0 + r] = j[r].L;
+          }
+        }
+      }
     }
-  };
-#pragma unroll 1
-  for (int e = 0; e < 2 * K::WARPS; ++e) {
-    const uint32_t id = ent_uid[e];
-    if (id == 0xFFFFFFFFu) continue;
-    if (id != cur) {
-      flush();
-      cur = id;
-      cb = ent_b[e];
-      cu_ = ent_u[e];
-      M = -INFINITY;
-      L = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) a[i] = 0.f;
-    }
-    const float* part = (e & 1) ? reinterpret_cast<const float*>(smem + (e >> 1) * K::RING)
-                                : p.wparts + ((size_t)cta * K::WARPS + (e >> 1)) * K::PART;
-    const float me = part[K::ROWS * HD + row], le = part[K::ROWS * HD + K::ROWS + row];
-    const float mn = fmaxf(M, me);
-    const float fa = M == -INFINITY ? 0.f : ex2(M - mn), fe = me == -INFINITY ? (le == 0.f ? 0.f : 1.f) : ex2(me - mn);
-    L = L * fa + le * fe;
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) a[i] = a[i] * fa + part[row * HD + d0 + i] * fe;
-    M = mn;
   }
-  flush();
-  if (tid == 0) p.meta[cta] = meta;
 }
 
-// Units that more than one CTA worked on: block (c, y) joins rows 2y and 2y + 1 of the unit that CTA
-// c opened with the parts that the following CTAs continued.
+// Units that more than one CTA worked on: warp r of block c joins row r of the unit that CTA c left
+// open with the parts of the CTAs that continued it.
 template <int HD, int NB>
-__global__ void __launch_bounds__(HD / 2) join_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(AttnCfg<HD, NB>::ROWS * 32) join_kernel(const AttnParams p) {
   using K = AttnCfg<HD, NB>;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched before the attention kernel has ended)
-  const int c = blockIdx.x;
-  const int4 meta = p.meta[c];
-  if (!meta.y) return;
-  SeqWork<NB> sw;
-  sw.load(p, meta.z);
-  const int row = blockIdx.y * 2 + threadIdx.x / (HD / 4), d0 = (threadIdx.x % (HD / 4)) * 4;
-  const int rr = (meta.w % sw.nrb) * K::ROWS + row;
-  if (rr >= sw.n * p.group) return;
-  float M = -INFINITY, L = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float* part) {
-    const float me = part[K::ROWS * HD + row], le = part[K::ROWS * HD + K::ROWS + row];
-    const float4 x = *reinterpret_cast<const float4*>(part + row * HD + d0);
-    const float mn = fmaxf(M, me);
-    const float fa = M == -INFINITY ? 0.f : ex2(M - mn), fe = me == -INFINITY ? (le == 0.f ? 0.f : 1.f) : ex2(me - mn);
-    L = L * fa + le * fe;
-    a.x = a.x * fa + x.x * fe;
-    a.y = a.y * fa + x.y * fe;
-    a.z = a.z * fa + x.z * fe;
-    a.w = a.w * fa + x.w * fe;
-    M = mn;
-  };
-  add(p.parts + ((size_t)c * 2 + 1) * K::PART);
-  for (int i = c + 1; i < (int)gridDim.x; ++i) {
-    const int flags = p.meta[i].x;
-    if (!(flags & 1)) break;
-    add(p.parts + (size_t)i * 2 * K::PART);
-    if (flags & 2) break;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, row = threadIdx.x >> 5, ctas = gridDim.x;
+  if (!p.meta[2 * c].y) return;
+  const int4 place = p.meta[2 * c + 1];
+  if (place.z + row >= place.w) return;
+  // the parts: CTA c's open one, then the following CTAs' up to the one that finished the unit
+  int n = 1;
+  for (;;) {
+    const int i = c + n + lane;
+    const int f = i < ctas ? p.meta[2 * i].x : 0;
+    const uint32_t stop = __ballot_sync(0xffffffffu, !(f & 1) || (f & 2));
+    if (!stop) {
+      n += 32;
+      continue;
+    }
+    const int z = __ffs(stop) - 1;
+    n += z + (__shfl_sync(0xffffffffu, f, z) & 1);
+    break;
   }
-  const long long tok = sw.tok0 + rr / p.group;
-  const int head = (meta.w / sw.nrb) * p.group + rr % p.group;
-  const float inv = L == 0.f ? 0.f : 8.0f / L;
-  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + d0);
-  dst[0] = __floats2bfloat162_rn(a.x * inv, a.y * inv);
-  dst[1] = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-  if (p.lse && d0 == 0) p.lse[tok * p.hq + head] = (M - kPShift + log2f(L)) * 0.6931471805599453f;
+  auto part_of = [&](int i) { return p.parts + ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * K::PART; };
+  Joined<HD> all;
+  all.weigh(-INFINITY, 0.f);
+  for (int b = 0; b < n; b += 32) {
+    float me = -INFINITY, le = 0.f;
+    if (b + lane < n) {
+      me = part_of(b + lane)[K::ROWS * HD + row];
+      le = part_of(b + lane)[K::ROWS * HD + K::ROWS + row];
+    }
+    Joined<HD> j;
+    j.weigh(me, le);
+    const int m = min(32, n - b);
+    int i = 0;
+    for (; i + 4 <= m; i += 4) {
+      float x[4][HD / 32];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) j.load(part_of(b + i + y) + row * HD, lane, x[y]);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) j.mul(x[y], __shfl_sync(0xffffffffu, j.w, i + y));
+    }
+    for (; i < m; ++i) j.add(part_of(b + i) + row * HD, __shfl_sync(0xffffffffu, j.w, i), lane);
+    all.join(j);
+  }
+  all.store(p, place, row, lane);
 }
 
 }  // namespace kvq
