@@ -130,15 +130,18 @@ dec_status launched(const char* what) {
   return ce == cudaSuccess ? DEC_OK : op_cuda(ce, what);
 }
 
-// A kernel's dynamic shared memory limit, raised once per device.
+// The attention kernel's dynamic shared memory limit, raised once per device. The join kernel asks for
+// the same division of the SM's memory, so that none is redivided between the two.
 template <class F>
-dec_status raise_smem(F* k, int bytes, std::atomic<unsigned long long>& done) {
+dec_status raise_smem(F* k, F* join, int bytes, std::atomic<unsigned long long>& done) {
   int dev = 0;
   cudaError_t ce = cudaGetDevice(&dev);
   if (ce != cudaSuccess) return op_cuda(ce, "cudaGetDevice");
   const unsigned long long bit = 1ull << (dev & 63);
   if (done.load(std::memory_order_acquire) & bit) return DEC_OK;
   ce = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (ce == cudaSuccess)
+    ce = cudaFuncSetAttribute((const void*)join, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (ce != cudaSuccess) return op_cuda(ce, "cudaFuncSetAttribute");
   if (dev < 64) done.fetch_or(bit, std::memory_order_release);
   return DEC_OK;
@@ -157,7 +160,7 @@ template <int HD, int NB>
 dec_status launch_attention(AttnParams p, int batch, uint8_t* ws, cudaStream_t stream) {
   using K = AttnCfg<HD, NB>;
   static std::atomic<unsigned long long> done{0};
-  if (dec_status st = raise_smem(attention_kernel<HD, NB>, K::smem(), done)) return st;
+  if (dec_status st = raise_smem(attention_kernel<HD, NB>, join_kernel<HD, NB>, K::smem(), done)) return st;
   const int sms = op_sms();
   if (sms < 1) return op_fail(DEC_ERR_CUDA, "attention: no device");
   p.meta = reinterpret_cast<int4*>(ws);
@@ -319,6 +322,7 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
   p.scale = (a->scale == 0.f ? 1.0f / std::sqrt((float)c->head_dim) : a->scale) * 1.4426950408889634f * 8.0f;
   p.hq = a->n_heads;
   p.group = a->n_heads / c->n_kv_heads;
+  p.ginv = reciprocal(p.group);
   p.causal = a->causal != 0;
   p.max_tokens = a->max_tokens;
   const int max_tokens = std::min(a->max_tokens, s->n_tokens);
@@ -327,7 +331,7 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
     return op_fail(DEC_ERR_ARG, "attention: workspace too small");
   // entries of the kernel's list of groups, at most: 32-bit
   const long long units = (long long)c->n_kv_heads * ((long long)s->n_tokens * p.group / (wide ? 16 : 8) + s->batch);
-  if (units * (((long long)s->max_pages * c->page_tokens + kGroup - 1) / kGroup) >= (1LL << 32))
+  if (units * ((long long)s->max_pages * c->page_tokens / kGroup + 1 + kUnitCost) >= (1LL << 32) - 64)
     return op_fail(DEC_ERR_UNSUPPORTED, "attention: too much work for one call");
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   cudaStream_t st = op_stream(stream);

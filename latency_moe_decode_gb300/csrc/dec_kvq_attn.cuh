@@ -26,10 +26,26 @@ namespace dec {
 namespace kvq {
 
 constexpr int kStages = 3;       // chunks of a warp's ring
-constexpr int kMaxSeqs = 512;    // sequences of one launch (their table lies in shared memory)
+constexpr int kMaxSeqs = 256;    // sequences of one launch (their table lies in shared memory)
+constexpr int kUnitCost = 2;     // what beginning and ending a unit costs, in groups' time
 constexpr int kMinGroups = 8;    // groups a CTA takes at least
 constexpr float kPShift = 15.0f;  // probabilities are kept times 2^15: f16 then reaches 2^-39 of the largest
 
+
+// The f16 pairs 1024, 1024 and 64, 64 that codes are put into (Scale2), from the kernel's arguments:
+// with constants the compiler makes an and and an or of each lop3, 64 more a group on the pipe that
+// bounds the kernel.
+struct Magic {
+  uint32_t lo, hi;
+};
+// A sequence's share of the list: hkv * (row blocks) units of ng groups and kUnitCost entries more
+// that stand for a unit's fixed cost (skipped: they only even out the cut where contexts are short).
+struct SeqWork {
+  uint32_t pre;  // first list entry
+  int tok0, n, len, ng;
+  uint32_t inv;  // reciprocal of ng + kUnitCost
+  int nrb, pad;
+};
 template <int HD, int NB>
 struct AttnCfg {
   static constexpr int KS = HD / 16;              // 16-value steps of a head
@@ -41,15 +57,9 @@ struct AttnCfg {
   static constexpr int PART = ROWS * HD + 2 * ROWS;  // floats of a partial: outputs, maxima, sums
   static constexpr int THREADS = WARPS * 32;
   static_assert(RING >= PART * 4 && RING % 16 == 0 && GB % 16 == 0, "a partial has to fit into a warp's ring");
-  static constexpr int smem() { return WARPS * RING + (kMaxSeqs + 1) * 16; }
+  static constexpr int smem() { return WARPS * RING + kMaxSeqs * (int)sizeof(SeqWork); }
 };
 
-// The f16 pairs 1024, 1024 and 64, 64 that codes are put into (Scale2), from the kernel's arguments:
-// with constants the compiler makes an and and an or of each lop3, 64 more a group on the pipe that
-// bounds the kernel.
-struct Magic {
-  uint32_t lo, hi;
-};
 struct AttnParams {
   Cache c;
   Seqs s;
@@ -57,6 +67,7 @@ struct AttnParams {
   float* lse;
   float scale;  // times log2(e) and the scale bytes' factor 8
   int hq, group, causal, max_tokens;
+  uint32_t ginv;  // reciprocal of group
   int b0;         // (without cu: token row of sequence 0)
   int min_groups; // groups a CTA takes at least
   Magic magic;
@@ -131,42 +142,15 @@ struct Scale2 {
   }
 };
 
-// The list of groups: per sequence hkv * (row blocks) units of `ng` groups each. Its table, in shared
-// memory: {first list entry, first token row, rows, length}.
-template <int NB>
-struct SeqWork {
-  int tok0, n, len, ng, nrb;
-  uint32_t pre;
-  __device__ __forceinline__ void shape(const AttnParams& p) {
-    // (a unit without positions still writes its rows)
-    const int held = p.causal ? len + n : len;
-    const int most = p.s.max_pages << (p.c.page_shift - 4);
-    ng = max(1, min(most, (held + kGroup - 1) / kGroup));
-    nrb = (n * p.group + 8 * NB - 1) / (8 * NB);
-  }
-  __device__ __forceinline__ void load(const AttnParams& p, int b) {  // from the caller's arrays
-    tok0 = p.s.cu ? __ldg(p.s.cu + b) : p.b0 + b;
-    n = p.s.cu ? __ldg(p.s.cu + b + 1) - tok0 : 1;
-    tok0 = max(tok0, 0);
-    n = max(0, min(min(n, p.max_tokens), p.s.n_tokens - tok0));
-    len = __ldg(p.s.lengths + b);
-    const long long most = (long long)p.s.max_pages << p.c.page_shift;
-    if (n > 0 && len < 0) raise(p.c.status, DEC_ERR_ARG);
-    if (n > 0 && (p.causal ? (long long)len + n : len) > most) raise(p.c.status, DEC_ERR_CAPACITY);
-    len = len < 0 ? -n : (int)min((long long)len, most);
-    shape(p);
-  }
-  __device__ __forceinline__ void get(const AttnParams& p, const int4& e) {
-    pre = (uint32_t)e.x;
-    tok0 = e.y;
-    n = e.z;
-    len = e.w;
-    shape(p);
-  }
-};
-
-// (one division for the common single row block)
+// x / d by the reciprocal inv = floor((2^32 - 1) / d): x inv / 2^32 is less than 1 below x / d, so the
+// quotient is at most one too small before the correction.
+__device__ __forceinline__ uint32_t fast_div(uint32_t x, uint32_t d, uint32_t inv) {
+  const uint32_t q = __umulhi(x, inv);
+  return q + (x - q * d >= d ? 1u : 0u);
+}
+// (no division for the common single row block)
 __device__ __forceinline__ int over(int a, int d) { return d == 1 ? a : a / d; }
+__host__ __device__ inline uint32_t reciprocal(uint32_t d) { return 0xFFFFFFFFu / d; }
 
 // The operands of O^T's products with a group's values (vw: the lane's words of positions 2t, 2t + 1,
 // 2t + 8, 2t + 9; bytes: their scales): put(k, a0..a3) for 16 values of the head at a time, of which
@@ -282,9 +266,9 @@ struct Joined {
     for (int i = 0; i < V; ++i) part[lane * V + i] = a[i];
   }
   __device__ __forceinline__ void store(const AttnParams& p, const int4& place, int row, int lane) const {
-    const int rr = place.z + row;
-    const long long tok = place.x + rr / p.group;
-    const int head = place.y + rr % p.group;
+    const int rr = place.z + row, tj = (int)fast_div(rr, p.group, p.ginv);
+    const long long tok = place.x + tj;
+    const int head = place.y + rr - tj * p.group;
     const float inv = L == 0.f ? 0.f : 8.0f / L;  // (8: the scale bytes' factor)
     __nv_bfloat162* dst =
         reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + lane * V);
@@ -305,7 +289,11 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
   __shared__ uint2 ent_unit[32];
   __shared__ int4 ent_place[32];
   __shared__ uint64_t bars[K::WARPS][kStages];  // chunk landed
-  int4* const seqs = reinterpret_cast<int4*>(smem + K::WARPS * K::RING);  // [batch + 1]
+  // each warp's unit, kept here while its groups take the registers: its place; its first list entry
+  // and the one behind its groups
+  __shared__ int4 unit_place[K::WARPS];
+  __shared__ uint2 unit_span[K::WARPS];
+  SeqWork* const seqs = reinterpret_cast<SeqWork*>(smem + K::WARPS * K::RING);  // [batch]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join kernel waits for this one's end)
@@ -321,10 +309,22 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
   for (int b0 = 0; b0 < p.s.batch; b0 += K::THREADS) {
     const int b = b0 + tid;
     uint32_t w = 0;
-    SeqWork<NB> sw;
+    SeqWork sw;
     if (b < p.s.batch) {
-      sw.load(p, b);
-      w = (uint32_t)p.c.hkv * sw.nrb * sw.ng;
+      const int first = p.s.cu ? __ldg(p.s.cu + b) : p.b0 + b, last = p.s.cu ? __ldg(p.s.cu + b + 1) : first + 1;
+      const int len = __ldg(p.s.lengths + b);
+      const long long most = (long long)p.s.max_pages << p.c.page_shift;
+      sw.tok0 = max(first, 0);
+      sw.n = max(0, min(min(last - first, p.max_tokens), p.s.n_tokens - sw.tok0));
+      if (sw.n > 0 && len < 0) raise(p.c.status, DEC_ERR_ARG);
+      if (sw.n > 0 && (p.causal ? (long long)len + sw.n : len) > most) raise(p.c.status, DEC_ERR_CAPACITY);
+      sw.len = len < 0 ? -sw.n : (int)min((long long)len, most);
+      // (a unit without positions still writes its rows)
+      const int held = p.causal ? sw.len + sw.n : sw.len;
+      sw.ng = max(1, min(p.s.max_pages << (p.c.page_shift - 4), (held + kGroup - 1) / kGroup));
+      sw.inv = reciprocal(sw.ng + kUnitCost);
+      sw.nrb = (sw.n * p.group + K::ROWS - 1) / K::ROWS;
+      w = (uint32_t)p.c.hkv * sw.nrb * (sw.ng + kUnitCost);
     }
     uint32_t x = w;
 #pragma unroll
@@ -342,7 +342,10 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
       before += i < warp ? y : 0u;
       all += y;
     }
-    if (b < p.s.batch) seqs[b] = make_int4((int)(before + x - w), sw.tok0, sw.n, sw.len);
+    if (b < p.s.batch) {
+      sw.pre = before + x - w;
+      seqs[b] = sw;
+    }
     base = all;
   }
   __syncthreads();
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
     int a = 0, z = p.s.batch;
     while (z - a > 1) {
       const int m = (a + z) >> 1;
-      if ((uint32_t)seqs[m].x <= f) a = m;
+      if (seqs[m].pre <= f) a = m;
       else z = m;
     }
     return a;
@@ -373,36 +376,42 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
 
   // ---- the copies: 32 entries' group indices at a time, one per lane, and each lane copies its own
   // (one bulk copy a group: a group is contiguous)
-  uint32_t vb = lo, pf = lo;  // first entry of the lanes' window; next entry to copy
-  int vg = -1, vrem = 0;      // its group in the cache (-1: nothing to copy), entries left of its unit
-  auto window = [&](uint32_t f0) {
-    vb = f0;
-    const uint32_t f = f0 + lane;
+  uint32_t pf = lo;    // next entry to copy
+  int vg, vrem;        // group in the cache of entry (the 32 that pf is in) + lane (-1: nothing to copy),
+                       // groups left of its unit
+  auto look = [&](uint32_t f) {
     vg = -1;
     vrem = 0;
-    if (f < hi) {
-      const int b = seq_at(f);
-      SeqWork<NB> sw;
-      sw.get(p, seqs[b]);
-      const uint32_t r = f - sw.pre;
-      const int u = (int)(r / (uint32_t)sw.ng), gr = (int)(r - (uint32_t)u * sw.ng);
-      vrem = sw.ng - gr;
-      const int pos = gr * kGroup;
-      if (pos < (p.causal ? sw.len + sw.n : sw.len)) {
-        const int e = pos >> p.c.page_shift;
-        const int page = __ldg(p.s.table + b * p.s.table_stride + e);
-        const int gpp = 1 << (p.c.page_shift - 4);
-        if ((unsigned)page < (unsigned)p.c.n_pages) vg = (page * p.c.hkv + over(u, sw.nrb)) * gpp + (gr & (gpp - 1));
-        else raise(p.c.status, DEC_ERR_ARG);
-      }
+    if (f >= hi) return;
+    const int b = seq_at(f);
+    const SeqWork sw = seqs[b];
+    const uint32_t r = f - sw.pre, per = sw.ng + kUnitCost;
+    const int u = (int)fast_div(r, per, sw.inv), gr = (int)(r - (uint32_t)u * per);
+    vrem = sw.ng - gr;
+    const int pos = gr * kGroup;
+    if (vrem > 0 && pos < (p.causal ? sw.len + sw.n : sw.len)) {
+      const int page = __ldg(p.s.table + b * p.s.table_stride + (pos >> p.c.page_shift));
+      const int gpp = 1 << (p.c.page_shift - 4);
+      if ((unsigned)page < (unsigned)p.c.n_pages) vg = (page * p.c.hkv + over(u, sw.nrb)) * gpp + (gr & (gpp - 1));
+      else raise(p.c.status, DEC_ERR_ARG);
     }
   };
   int pstage = 0;
+  bool fresh = true;  // pf has come to the next 32
   auto prefetch = [&]() {  // the next chunk, if there is one
-    if (pf >= hi) return;
-    if (pf + CH > vb + 32) window(pf);
-    const int at = (int)(pf - vb);
-    const int n = min(min(CH, __shfl_sync(0xffffffffu, vrem, at)), (int)(hi - pf));
+    int at, rem;
+    for (;;) {
+      if (pf >= hi) return;
+      at = (int)((pf - lo) & 31u);
+      if (fresh) look(pf - at + lane);
+      fresh = false;
+      rem = __shfl_sync(0xffffffffu, vrem, at);
+      if (rem > 0) break;
+      fresh = at + rem + kUnitCost >= 32;
+      pf += rem + kUnitCost;  // to the next unit
+    }
+    // (chunks end with the unit, the warp's part of the list, and the 32 entries)
+    const int n = min(min(CH, rem), min((int)(hi - pf), 32 - at));
     const bool copies = lane >= at && lane < at + n && vg >= 0;
     const uint32_t who = __ballot_sync(0xffffffffu, copies);
     uint64_t* const bar = bars[warp] + pstage;
@@ -410,17 +419,69 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
     __syncwarp();
     if (copies)
       bulk_copy(ring + (pstage * CH + lane - at) * K::GB, p.c.pages + (size_t)vg * K::GB, K::GB, bar);
+    fresh = at + n == 32;
     pf += n;
     pstage = pstage == kStages - 1 ? 0 : pstage + 1;
   };
 
   float acc[NB][KS][4];
   float m[NB][2], l[NB][2], sc[NB][2];
-  int seen[NB][2];
+  int seen[NB][2], smin, smax;
   uint32_t qf[NB][KS][2];
 
+  // ---- the unit that an entry belongs to, and its rows' queries (loaded ahead of their use)
+  uint32_t w[NB][KS * 2];  // the lane's HD / 4 values from t HD / 4 on of rows g, two a word
+  auto open_unit = [&](uint32_t f) {  // -> the unit's first group from entry f on
+    SeqWork sw = seqs[seq_at(f)];
+    const uint32_t per = sw.ng + kUnitCost;
+    int u = (int)fast_div(f - sw.pre, per, sw.inv);
+    uint32_t uid = sw.pre + (uint32_t)u * per;
+    if (f >= uid + sw.ng) {  // behind a unit's groups: the next unit, in the next sequence at its last
+      f = uid + per;
+      if (f >= hi) return f;
+      sw = seqs[seq_at(f)];
+      u = (int)fast_div(f - sw.pre, sw.ng + kUnitCost, sw.inv);
+      uid = f;
+    }
+    const int h = over(u, sw.nrb), row0 = (u - h * sw.nrb) * K::ROWS, rows = sw.n * p.group;
+    if (lane == 0) {
+      unit_place[warp] = make_int4(sw.tok0, h * p.group, row0, rows);
+      unit_span[warp] = make_uint2(uid, uid + sw.ng);
+    }
+    // positions that rows 2t, 2t + 1 see
+    smin = 0x7FFFFFFF;
+    smax = 0;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int rr = row0 + nb * 8 + 2 * t + i;
+        const int x = max(0, p.causal ? sw.len + (int)fast_div(rr, p.group, p.ginv) + 1 : sw.len);
+        seen[nb][i] = rr < rows ? x : 0;
+        smin = min(smin, rr < rows ? x : 0x7FFFFFFF);
+        smax = max(smax, seen[nb][i]);
+      }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      smin = min(smin, __shfl_xor_sync(0xffffffffu, smin, o));
+      smax = max(smax, __shfl_xor_sync(0xffffffffu, smax, o));
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = row0 + nb * 8 + g, tj = (int)fast_div(row, p.group, p.ginv);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.p) + (long long)(sw.tok0 + tj) * p.q.ts +
+                                                        (h * p.group + row - tj * p.group) * p.q.hs + t * (HD / 4));
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) {
+        const uint4 x = row < rows ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        w[nb][4 * i] = x.x; w[nb][4 * i + 1] = x.y; w[nb][4 * i + 2] = x.z; w[nb][4 * i + 3] = x.w;
+      }
+    }
+    return f;
+  };
+
+  uint32_t f = lo < hi ? open_unit(lo) : hi;
   if (lo < hi) {
-    window(lo);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) prefetch();
   }
@@ -428,34 +489,15 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
   uint32_t cphase = 0;
   bool dead = false;
   const Magic magic = p.magic;
-  for (uint32_t f = lo; f < hi && !dead;) {
-    // ---- a unit: its rows' queries as the second operand of S^T, halved down to magnitude 1 .. 2
-    const int b = seq_at(f);
-    SeqWork<NB> sw;
-    sw.get(p, seqs[b]);
-    const int u = (int)((f - sw.pre) / (uint32_t)sw.ng);
-    const uint32_t uid = sw.pre + (uint32_t)u * sw.ng;  // where the unit starts: its name
-    const int h = over(u, sw.nrb), row0 = (u - h * sw.nrb) * K::ROWS, rows = sw.n * p.group;
-    int smin = 0x7FFFFFFF, smax = 0;
+  while (f < hi && !dead) {
+    // ---- a unit: its queries as the second operand of S^T, scaled to magnitude 1 .. 2
+    __syncwarp();
+    const uint32_t uid = unit_span[warp].x, fend = min(hi, unit_span[warp].y);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int row = row0 + nb * 8 + g;
-      uint32_t w[KS * 2];  // HD / 4 values from t HD / 4 on, two a word
-#pragma unroll
-      for (int i = 0; i < KS * 2; ++i) w[i] = 0;
-      if (row < rows) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q.p) + (sw.tok0 + row / p.group) * p.q.ts +
-            (h * p.group + row % p.group) * p.q.hs + t * (HD / 4));
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i) {
-          const uint4 x = __ldg(src + i);
-          w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
-        }
-      }
       uint32_t mag = 0;
 #pragma unroll
-      for (int i = 0; i < KS * 2; ++i) mag = max(mag, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+      for (int i = 0; i < KS * 2; ++i) mag = max(mag, max((w[nb][i] << 16) & 0x7FFFFFFFu, w[nb][i] & 0x7FFF0000u));
       mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
       mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
       // a power of two that leaves the row's largest value in 1 .. 2: bf16 values down to 2^-17 of it
@@ -463,7 +505,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
       const int e = mag == 0 || mag >= 0x7F800000u ? 0 : min(126, max(-126, (int)(mag >> 23) - 127));
       const float down = __int_as_float((127 - e) << 23);
       auto val = [&](int i) {  // value i of the lane's HD / 4
-        return down * __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+        return down * __uint_as_float((i & 1) ? (w[nb][i >> 1] & 0xFFFF0000u) : (w[nb][i >> 1] << 16));
       };
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
@@ -475,12 +517,6 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         sc[nb][i] = __shfl_sync(0xffffffffu, up, (2 * t + i) * 4);
-        const int rr = row0 + nb * 8 + 2 * t + i;
-        seen[nb][i] = rr < rows ? (p.causal ? max(0, sw.len + rr / p.group + 1) : max(0, sw.len)) : 0;
-        if (rr < rows) {
-          smin = min(smin, seen[nb][i]);
-          smax = max(smax, seen[nb][i]);
-        }
         m[nb][i] = -INFINITY;
         l[nb][i] = 0.f;
       }
@@ -489,12 +525,6 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nb][s][i] = 0.f;
     }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      smin = min(smin, __shfl_xor_sync(0xffffffffu, smin, o));
-      smax = max(smax, __shfl_xor_sync(0xffffffffu, smax, o));
-    }
-    const uint32_t fend = min(hi, uid + (uint32_t)sw.ng);
 
     // ---- its groups, a chunk at a time: with every group there and seen by every row, or not
     auto chunk = [&](auto edge, const uint8_t* buf, int pos0, int n) {
@@ -657,8 +687,8 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
         }
       }
     };
-    for (uint32_t f0 = f; f0 < fend; f0 += CH) {
-      const int n = min(CH, (int)(fend - f0));
+    for (uint32_t f0 = f; f0 < fend;) {
+      const int n = min(min(CH, (int)(fend - f0)), 32 - (int)((f0 - lo) & 31u));
       const int pos0 = (int)(f0 - uid) * kGroup;
       prefetch();
       if (!bar_wait(bars[warp] + cstage, cphase)) {
@@ -675,6 +705,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
       if (n < CH || pos0 + CH * kGroup > smin) chunk(std::true_type(), buf, pos0, n);
       else chunk(std::false_type(), buf, pos0, n);
       __syncwarp();  // (the next copy goes where this chunk lay)
+      f0 += n;
     }
 
     // ---- the unit, or this warp's part of it
@@ -684,19 +715,19 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], o);
-    const bool whole = f == uid && fend == uid + (uint32_t)sw.ng;
-    const bool last = fend == hi;
+    const uint32_t u0 = uid, u1 = unit_span[warp].y;
+    const int4 place = unit_place[warp];
+    __syncwarp();
+    const bool whole = f == u0 && fend == u1, last = fend == hi;
+    f = fend == u1 ? fend + kUnitCost : fend;
+    f = f < hi ? open_unit(f) : hi;  // (the next unit's queries are on their way during the stores)
     float* part = nullptr;
     if (!whole) {
       const int e = 2 * warp + (last ? 1 : 0);
-      if (last) {
-        part = reinterpret_cast<float*>(ring);
-      } else {
-        part = p.wparts + ((size_t)cta * K::WARPS + warp) * K::PART;
-      }
+      part = last ? reinterpret_cast<float*>(ring) : p.wparts + ((size_t)cta * K::WARPS + warp) * K::PART;
       if (lane == 0) {
-        ent_unit[e] = make_uint2(uid, uid + (uint32_t)sw.ng);
-        ent_place[e] = make_int4(sw.tok0, h * p.group, row0, rows);
+        ent_unit[e] = make_uint2(u0, u1);
+        ent_place[e] = place;
       }
     }
 #pragma unroll
@@ -704,24 +735,24 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int rr = nb * 8 + 2 * t + i;
+        if (place.z + rr >= place.w) continue;
         if (whole) {
-          if (row0 + rr < rows) {
-            const float inv = l[nb][i] == 0.f ? 0.f : 8.0f / l[nb][i];
-            const long long tok = sw.tok0 + (row0 + rr) / p.group;
-            const int head = h * p.group + (row0 + rr) % p.group;
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + g * (HD / 8));
+          const float inv = l[nb][i] == 0.f ? 0.f : 8.0f / l[nb][i];
+          const int tj = (int)fast_div(place.z + rr, p.group, p.ginv);
+          const long long tok = place.x + tj;
+          const int head = place.y + place.z + rr - tj * p.group;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + g * (HD / 8));
 #pragma unroll
-            for (int k = 0; k < KS; k += 4) {
-              float x[8];
+          for (int k = 0; k < KS; k += 4) {
+            float x[8];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                x[2 * j] = acc[nb][k + j][i] * inv;
-                x[2 * j + 1] = acc[nb][k + j][2 + i] * inv;
-              }
-              dst[k / 4] = pack8_bf16(x);
+            for (int j = 0; j < 4; ++j) {
+              x[2 * j] = acc[nb][k + j][i] * inv;
+              x[2 * j + 1] = acc[nb][k + j][2 + i] * inv;
             }
-            if (p.lse && g == 0) p.lse[tok * p.hq + head] = (m[nb][i] - kPShift + log2f(l[nb][i])) * 0.6931471805599453f;
+            dst[k / 4] = pack8_bf16(x);
           }
+          if (p.lse && g == 0) p.lse[tok * p.hq + head] = (m[nb][i] - kPShift + log2f(l[nb][i])) * 0.6931471805599453f;
         } else {
 #pragma unroll
           for (int k = 0; k < KS; k += 2)
@@ -733,7 +764,6 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
           }
         }
       }
-    f = fend;
   }
 
   // ---- the CTA's unfinished units: one warp per (unit, row), the parts in the list's order
@@ -771,8 +801,9 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
       float me[4], le[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        me[r] = mp[r0 + r];
-        le[r] = mp[K::ROWS + r0 + r];
+        // (parts hold no more than the unit's rows)
+        me[r] = place.z + r0 + r < place.w ? mp[r0 + r] : -INFINITY;
+        le[r] = place.z + r0 + r < place.w ? mp[K::ROWS + r0 + r] : 0.f;
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) j[r].weigh(has ? me[r] : -INFINITY, has ? le[r] : 0.f);
@@ -780,7 +811,10 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
         const int e = __ffs(x) - 1;
         const float* part = part_of(e) + r0 * HD;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) j[r].add(part + r * HD, __shfl_sync(0xffffffffu, j[r].w, e), lane);
+        for (int r = 0; r < 4; ++r) {
+          const float wt = __shfl_sync(0xffffffffu, j[r].w, e);
+          if (place.z + r0 + r < place.w) j[r].add(part + r * HD, wt, lane);
+        }
       }
       if (!cont && !open) {
 #pragma unroll
@@ -790,6 +824,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
         float* dst = p.parts + ((size_t)cta * 2 + (cont ? 0 : 1)) * K::PART;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
+          if (place.z + r0 + r >= place.w) continue;
           j[r].keep(dst + (r0 + r) * HD, lane);
           if (lane == 0) {
             dst[K::ROWS * HD + r0 + r] = j[r].M;
