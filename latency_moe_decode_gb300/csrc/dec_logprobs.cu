@@ -1,17 +1,20 @@
 // Log-probabilities of rows of logits (dec_logprobs of dec.h).
 //
 // One pass over the row, which is read once from memory:
-//  - every thread keeps a running maximum m, s = sum 2^t and u = sum 2^t t with t = (x - m) log2(e)
-//    of its own elements, so nothing is exchanged while the row streams; joined at the end,
-//    lse = M + ln S and the entropy is ln 2 (log2 S - U / S);
+//  - every thread keeps a reference m, s = sum 2^t and u = sum 2^t t with t = (x - m) log2(e) of its own
+//    elements, so nothing is exchanged while the row streams. The reference is the maximum of the
+//    thread's first elements and follows only what passes it by more than 40 (fp32 holds 2^58 times
+//    a vocabulary): following every new maximum costs a warp a rescale at almost every vector. Joined
+//    at the row's maximum M, lse = M + ln S and the entropy is ln 2 (log2 S - U / S);
 //  - the target's rank is counted on the way: elements before the target's id need x >= x_target,
 //    which is x > the next smaller number, so both sides are one comparison with their own bound;
 //  - the alternatives come from a bound: of 32 groups of threads, each knows its largest element, and
 //    the n-th largest of those 32 leaves at least n elements at or above it, for ordinary rows
-//    n to 3.5 n. Threads whose maximum reaches the bound look through their elements again (from
-//    L2), and the few candidates are ranked against each other.
-// What bounds it: at many rows the read of the logits; 8 instructions an element for bf16 stay below
-// it. At few rows latency: a row is then shared by a cluster of up to 8 CTAs.
+//    n to 3.5 n. Threads whose maximum reaches the bound look at its vector again, and through all
+//    theirs where their second largest vector reaches it too; the few candidates are ranked against
+//    each other.
+// What bounds it: at many rows the instructions (about 9 an element for bf16, where the read of the
+// logits leaves time for 11); at few rows latency: a row is then shared by a cluster of up to 8 CTAs.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -36,9 +39,9 @@ struct Params {
   int32_t *rank, *top_ids;
 };
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCand = 2048;     // candidates kept; more (long runs of equal logits) take the slow way
+constexpr int kCand = 2560;     // candidates kept; more (long runs of equal logits) take the slow way
+constexpr int kItems = 512;     // vectors to look at again
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr float kL2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -65,68 +68,122 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
-// A row as vectors of 16 bytes: vector k holds elements k V - shift .. k V - shift + V - 1, of which
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t r) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
+  return f;
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A row as vectors of 32 bytes: vector k holds elements k V - shift .. k V - shift + V - 1, of which
 // those outside the row read as -infinity.
+struct Vec {
+  uint32_t w[8];
+};
 template <bool BF16>
 struct Row {
-  static constexpr int V = BF16 ? 8 : 4;
-  const char* at;  // the 16-byte boundary at or below the row's first element
+  static constexpr int V = BF16 ? 16 : 8, E = BF16 ? 2 : 4;
+  const char* at;  // the 32-byte boundary at or below the row's first element
   int shift, vocab, vectors;
   __device__ __forceinline__ Row(const Params& p, int r) {
-    const char* first = static_cast<const char*>(p.x) + (long long)r * p.stride * (BF16 ? 2 : 4);
-    shift = (int)((reinterpret_cast<uintptr_t>(first) & 15u) / (BF16 ? 2 : 4));
-    at = first - shift * (BF16 ? 2 : 4);
+    const char* first = static_cast<const char*>(p.x) + (long long)r * p.stride * E;
+    shift = (int)((reinterpret_cast<uintptr_t>(first) & 31u) / E);
+    at = first - shift * E;
     vocab = p.vocab;
     vectors = (int)(((long long)shift + vocab + V - 1) / V);
   }
   __device__ __forceinline__ int base(int k) const { return k * V - shift; }
   __device__ __forceinline__ float one(int i) const {
-    const char* q = at + (long long)(i + shift) * (BF16 ? 2 : 4);
+    const char* q = at + ((long long)i + shift) * E;
     return BF16 ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(q)) : *reinterpret_cast<const float*>(q);
   }
-  __device__ __forceinline__ uint4 whole(int k) const { return __ldg(reinterpret_cast<const uint4*>(at) + k); }
+  __device__ __forceinline__ Vec whole(int k) const {
+    Vec v;
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+        : "l"(at + (long long)k * 32));
+    return v;
+  }
   // the first or last vector where the row begins or ends inside it
   __device__ __forceinline__ bool partial(int k) const { return base(k) < 0 || base(k) + V > vocab; }
-  __device__ __forceinline__ uint4 edge(int k) const { return edge_of(at, shift, vocab, k); }
-  __device__ __noinline__ static uint4 edge_of(const char* at, int shift, int vocab, int k) {
+  __device__ __forceinline__ Vec edge(int k) const { return edge_of(at, shift, vocab, k); }
+  __device__ __noinline__ static Vec edge_of(const char* at, int shift, int vocab, int k) {
     const int b = k * V - shift;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.w[i] = 0u;
     for (int i = 0; i < V; ++i) {
       uint32_t x = BF16 ? 0xFF80u : 0xFF800000u;
       if (b + i >= 0 && b + i < vocab)
         x = BF16 ? reinterpret_cast<const uint16_t*>(at)[(long long)k * V + i]
                  : reinterpret_cast<const uint32_t*>(at)[(long long)k * V + i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j == (BF16 ? i / 2 : i)) w[j] |= BF16 && (i & 1) ? x << 16 : x;
+      for (int j = 0; j < 8; ++j)
+        if (j == (BF16 ? i / 2 : i)) v.w[j] |= BF16 && (i & 1) ? x << 16 : x;
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return v;
   }
-  __device__ __forceinline__ static void unpack(const uint4& u, float (&x)[V]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  __device__ __forceinline__ static float element(const Vec& v, int i) {
+    if (!BF16) return __uint_as_float(v.w[i % 8]);
+    const uint32_t w = v.w[(i / 2) % 8];
+    return __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16);
+  }
+  // every element at least `low` (low within 1.1e4)
+  __device__ __forceinline__ static void raise(Vec& v, float low) {
+    const __nv_bfloat162 l = __float2bfloat162_rn(low);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       if (BF16) {
-        x[(2 * i) % V] = __uint_as_float(w[i] << 16);
-        x[(2 * i + 1) % V] = __uint_as_float(w[i] & 0xFFFF0000u);
+        __nv_bfloat162 h = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&v.w[i]), l);
+        v.w[i] = *reinterpret_cast<uint32_t*>(&h);
       } else {
-        x[i % V] = __uint_as_float(w[i]);
+        v.w[i] = __float_as_uint(fmaxf(__uint_as_float(v.w[i]), low));
       }
     }
   }
-  // the largest of a vector; NaN if one of them is
-  __device__ __forceinline__ static float largest(const uint4& u) {
+  __device__ __noinline__ static Vec without_nan(Vec v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (BF16) {
+        if ((v.w[i] & 0x7FFFu) > 0x7F80u) v.w[i] = (v.w[i] & 0xFFFF0000u) | 0xFF80u;
+        if ((v.w[i] & 0x7FFF0000u) > 0x7F800000u) v.w[i] = (v.w[i] & 0xFFFFu) | 0xFF800000u;
+      } else if ((v.w[i] & 0x7FFFFFFFu) > 0x7F800000u) {
+        v.w[i] = 0xFF800000u;
+      }
+    }
+    return v;
+  }
+  // the largest element; NaN if one of them is
+  __device__ __forceinline__ static float largest(const Vec& v) {
     if (BF16) {
-      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-      const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+      __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&v.w[0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&v.w[i]));
       return max_nan(__low2float(m), __high2float(m));
     }
-    return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
-                   max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+    float m = __uint_as_float(v.w[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_nan(m, __uint_as_float(v.w[i]));
+    return m;
   }
 };
 
-// A row's sums over some of its elements: maximum, sum of 2^t and of 2^t t, t = (x - m) log2(e).
+// A row's sums over some of its elements: reference, sum of 2^t and of 2^t t, t = (x - m) log2(e).
 struct Sums {
   float m, s, u;
   __device__ __forceinline__ void raise(float to) {  // (to > m)
@@ -136,11 +193,17 @@ struct Sums {
     s *= f;
     m = to;
   }
-  __device__ __forceinline__ void join(Sums o) {
-    if (o.m > m) raise(o.m);
-    else if (m > o.m) o.raise(m);
-    s += o.s;
-    u += o.u;
+  // the warp's joined sums, in every lane
+  __device__ __forceinline__ void join_warp() {
+    float to = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+    if (to > m) raise(to);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      u += __shfl_xor_sync(0xffffffffu, u, o);
+    }
   }
 };
 
@@ -149,15 +212,19 @@ struct Shared {
   int rank[kMaxCluster * kWarps], bad[kMaxCluster * kWarps];
   unsigned long long group[kMaxCluster * 32];
   unsigned long long bound;  // of the candidates
-  int n;                     // candidates found
+  int n, items;              // candidates found; vectors to look at again
+  float M, ls;               // the row's reference and log of its sum; whether it has a NaN or infinity
+  int any;
   unsigned long long cand[kCand];
   unsigned long long best[kWarps];
+  int item[kItems];
 };
 
 // CTAS CTAs (a cluster) share a row. Everything joined lies in the first one's shared memory.
 template <bool BF16, int CTAS>
-__global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const Params p) {
-  constexpr int V = Row<BF16>::V;
+__global__ void __launch_bounds__(kThreads, 5) logprobs_kernel(const Params p) {
+  constexpr int V = Row<BF16>::V, T = kThreads, W = kWarps;
+  static_assert(CTAS * 32 <= T, "one thread per group of threads");
   __shared__ Shared sh;
   const int r = blockIdx.x / CTAS, part = blockIdx.x % CTAS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -183,52 +250,69 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const Params p) {
 
   // ---- the row
   Sums a{-INFINITY, 0.f, 0.f};
-  int first = INT_MAX, ahead = 0, bad = 0;
-  auto take = [&](const uint4& u, int k) {
-    float x[V];
-    Row<BF16>::unpack(u, x);
-    float mx = Row<BF16>::largest(u);
+  float z = 0.f, low = 0.f;     // m log2(e), and what lies so far below m that it counts nothing
+  float best = -INFINITY, second = -INFINITY;  // the largest vectors' maxima
+  int first = INT_MAX, ahead = 0, bad = 0;     // the largest vector's first element
+  __nv_bfloat162 above2 = __float2bfloat162_rn(above), from2 = __float2bfloat162_rn(from);
+  __nv_bfloat162 count2 = __float2bfloat162_rn(0.f);  // (whole numbers up to 256 are exact)
+  auto take = [&](Vec v, int k) {
+    float mx = Row<BF16>::largest(v);
     if (!(mx < INFINITY)) {  // (rare) NaN orders as -infinity
       bad = 1;
-      mx = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        x[i] = x[i] != x[i] ? -INFINITY : x[i];
-        mx = fmaxf(mx, x[i]);
-      }
+      v = Row<BF16>::without_nan(v);
+      mx = Row<BF16>::largest(v);
     }
     const int b = row.base(k);
-    if (mx > a.m) {
+    second = fmaxf(second, fminf(mx, best));
+    first = mx > best || first == INT_MAX ? b : first;
+    best = fmaxf(best, mx);
+    if (has) {
+      if (b <= t && t < b + V) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) ahead += Row<BF16>::element(v, i) > (b + i < t ? from : above) ? 1 : 0;
+      } else if (BF16) {
+        const __nv_bfloat162 th = b > t ? above2 : from2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) count2 = __hadd2(count2, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&v.w[i]), th));
+      } else {
+        const float th = b > t ? above : from;
+#pragma unroll
+        for (int i = 0; i < V; ++i) ahead += Row<BF16>::element(v, i) > th ? 1 : 0;
+      }
+    }
+    if (mx > a.m + 40.f) {
       a.raise(mx);
-      first = b;
+      z = mx * kL2E;
+      low = mx - 170.f;
     }
-    if (first == INT_MAX) first = b;
-    if (b + V <= t || b > t) {
-      const float th = b > t ? above : from;
+    if (fabsf(a.m) < 1e4f) {
+      Row<BF16>::raise(v, low);  // (2^-150 and less is 0, and 0 x -170 no NaN)
+      const uint64_t l2 = pair(kL2E, kL2E), z2 = pair(-z, -z);
+      uint64_t s = pair(a.s, 0.f), w = pair(a.u, 0.f);
 #pragma unroll
-      for (int i = 0; i < V; ++i) ahead += x[i] > th ? 1 : 0;
-    } else {
+      for (int i = 0; i < V; i += 2) {
+        const uint64_t e = fma2(pair(Row<BF16>::element(v, i), Row<BF16>::element(v, i + 1)), l2, z2);
+        const float2 f = halves(e);
+        const uint64_t y = pair(ex2(f.x), ex2(f.y));
+        s = add2(s, y);
+        w = fma2(y, e, w);
+      }
+      const float2 s1 = halves(s), w1_ = halves(w);
+      a.s = s1.x + s1.y;
+      a.u = w1_.x + w1_.y;
+    } else if (a.m != -INFINITY) {  // (rare: m log2(e) may overflow, m - 170 may be m)
+#pragma unroll 1
+      for (int i = 0; i < V; ++i) {
+        const uint32_t x = BF16 ? (i & 1 ? v.w[0] & 0xFFFF0000u : v.w[0] << 16) : v.w[0];
+        const float e = fmaxf((__uint_as_float(x) - a.m) * kL2E, -256.f), y = ex2(e);
+        a.s += y;
+        a.u = fmaf(y, e, a.u);
+        if (!BF16 || (i & 1)) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) ahead += x[i] > (b + i < t ? from : above) ? 1 : 0;
+          for (int j = 0; j < 7; ++j) v.w[j] = v.w[j + 1];
+        }
+      }
     }
-    const float z = a.m == -INFINITY ? 0.f : a.m * kL2E;
-    if (!(fabsf(z) < 1e38f)) {  // (rare: a maximum near the type's lowest or largest value, z overflows)
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = (x[i] - a.m) * kL2E;
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = fmaf(x[i], kL2E, -z);
-    }
-    float s = 0.f, w = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float e = fmaxf(x[i], -256.f);  // (2^-256 is 0, and 0 x -256 no NaN)
-      const float y = ex2(e);
-      s += y;
-      w = fmaf(y, e, w);
-    }
-    a.s += s;
-    a.u += w;
   };
   // whole vectors, then the row's first and last where they are not (threads 0 and 1 of their CTA)
   constexpr int U = 2;  // vectors in flight
@@ -236,81 +320,90 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const Params p) {
   const int w1 = part == CTAS - 1 && row.partial(row.vectors - 1) ? row.vectors - 1 : v1;
   const int ek = tid == 0 && w0 != v0 ? 0 : tid == 1 && w1 != v1 && (row.vectors > 1 || w0 == v0) ? row.vectors - 1 : -1;
   int k = w0 + tid;
-  for (; k + (U - 1) * kThreads < w1; k += U * kThreads) {
-    uint4 u[U];
+  while (k < w1) {
+    // (counts in bf16: 8 a vector and half, to 29 vectors)
+    for (int i = 0; i < 28 / U && k + (U - 1) * T < w1; ++i, k += U * T) {
+      Vec v[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) u[i] = row.whole(k + i * kThreads);
+      for (int j = 0; j < U; ++j) v[j] = row.whole(k + j * T);
 #pragma unroll
-    for (int i = 0; i < U; ++i) take(u[i], k + i * kThreads);
+      for (int j = 0; j < U; ++j) take(v[j], k + j * T);
+    }
+    if (k + (U - 1) * T >= w1 && k < w1) {
+      static_assert(U <= 2, "one vector is left at most");
+      take(row.whole(k), k);
+      k += T;
+    }
+    if (BF16) {
+      ahead += (int)(__low2float(count2) + __high2float(count2));
+      count2 = __float2bfloat162_rn(0.f);
+    }
   }
-#pragma unroll 1
-  for (; k < w1; k += kThreads) take(row.whole(k), k);
-  if (ek >= 0) take(row.edge(ek), ek);
-  const float mine = a.m;
+  if (ek >= 0) {
+    take(row.edge(ek), ek);
+    if (BF16) ahead += (int)(__low2float(count2) + __high2float(count2));
+  }
 
-  // ---- join: the warps' sums, and the largest element of every 8 threads
-  unsigned long long gk = first == INT_MAX ? 0ull : key_of(mine, first + V - 1);  // (a bound takes the whole vector)
+  // ---- join: the warps' sums, and the largest element of every T / 32 threads
+  unsigned long long gk = first == INT_MAX ? 0ull : key_of(best, first + V - 1);  // (a bound takes the whole vector)
+  if (p.top > 0) {
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) gk = max(gk, __shfl_xor_sync(0xffffffffu, gk, o));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    b.u = __shfl_xor_sync(0xffffffffu, a.u, o);
-    a.join(b);
-    ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
-    bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+    for (int o = 1; o < T / 32; o <<= 1) gk = max(gk, __shfl_xor_sync(0xffffffffu, gk, o));
   }
+  a.join_warp();
+  ahead = __reduce_add_sync(0xffffffffu, ahead);
+  bad = __any_sync(0xffffffffu, bad);
   if (CTAS > 1) sync();  // (the first CTA has begun)
   if (lane == 0) {
-    home->sums[part * kWarps + warp] = a;
-    home->rank[part * kWarps + warp] = ahead;
-    home->bad[part * kWarps + warp] = bad;
+    home->sums[part * W + warp] = a;
+    home->rank[part * W + warp] = ahead;
+    home->bad[part * W + warp] = bad;
   }
-  if ((lane & 7) == 0) home->group[part * 32 + warp * 4 + (lane >> 3)] = gk;
-  if (part == 0 && tid == 0) sh.n = 0;
+  if (tid % (T / 32) == 0) home->group[part * 32 + tid / (T / 32)] = gk;
+  if (tid == 0) sh.n = sh.items = 0;
   sync();
-  if (part == 0 && tid < CTAS * 32 && p.top > 0) {
-    // the top_n-th largest of the groups' largest: at least top_n elements are at or above it
-    const unsigned long long g = sh.group[tid];
-    int before = 0;
+  if (part == 0 && p.top > 0) {
+    // the top_n-th largest of the groups' largest: at least top_n elements are at or above it (8 lanes
+    // a group: what follows the row's last element is latency, so it is spread over the threads)
+#pragma unroll 1
+    for (int i = tid / 8; i < CTAS * 32; i += T / 8) {
+      const unsigned long long g = sh.group[i];
+      int before = 0;
 #pragma unroll 4
-    for (int j = 0; j < CTAS * 32; ++j) {
-      const unsigned long long o = sh.group[j];
-      before += o > g || (o == g && j < tid) ? 1 : 0;
-    }
-    if (before == p.top - 1) sh.bound = g;
-  }
-  float M = 0.f, ls = 0.f;
-  int any = 0;
-  if (part == 0) {
-    // (every warp of the first CTA: the alternatives need the sum too)
-    Sums b = lane < CTAS * kWarps ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f};
-    int rk = lane < CTAS * kWarps ? sh.rank[lane] : 0;
-    any = lane < CTAS * kWarps ? sh.bad[lane] : 0;
-    if (CTAS * kWarps > 32) {
-      b.join(sh.sums[lane + 32]);
-      rk += sh.rank[lane + 32];
-      any |= sh.bad[lane + 32];
-    }
+      for (int j = tid % 8; j < CTAS * 32; j += 8) {
+        const unsigned long long o = sh.group[j];
+        before += o > g || (o == g && j < i) ? 1 : 0;
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      Sums c;
-      c.m = __shfl_xor_sync(0xffffffffu, b.m, o);
-      c.s = __shfl_xor_sync(0xffffffffu, b.s, o);
-      c.u = __shfl_xor_sync(0xffffffffu, b.u, o);
-      b.join(c);
-      rk += __shfl_xor_sync(0xffffffffu, rk, o);
-      any |= __shfl_xor_sync(0xffffffffu, any, o);
+      for (int o = 1; o < 8; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+      if (before == p.top - 1) sh.bound = g;
     }
-    M = b.m;
-    ls = logf(b.s);
-    if (tid == 0) {
-      const float y = any ? NAN : xt == -INFINITY ? -INFINITY : (xt - M) - ls;
+  }
+  if (part == 0 && warp == W - 1) {
+    Sums b = lane < CTAS * W ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f};
+    int rk = lane < CTAS * W ? sh.rank[lane] : 0;
+    int any = lane < CTAS * W ? sh.bad[lane] : 0;
+    if (CTAS * W > 32) {
+      Sums c = sh.sums[(lane + 32) % (CTAS * W)];
+      if (c.m > b.m) b.raise(c.m);
+      else if (b.m > c.m) c.raise(b.m);
+      b.s += c.s;
+      b.u += c.u;
+      rk += sh.rank[(lane + 32) % (CTAS * W)];
+      any |= sh.bad[(lane + 32) % (CTAS * W)];
+    }
+    b.join_warp();
+    rk = __reduce_add_sync(0xffffffffu, rk);
+    any = __any_sync(0xffffffffu, any);
+    if (lane == 0) {
+      const float ls = logf(b.s);
+      const float y = any ? NAN : xt == -INFINITY ? -INFINITY : (xt - b.m) - ls;
       if (p.logprob) p.logprob[r] = has ? y : NAN;
       if (p.rank) p.rank[r] = !has ? -1 : rk + (lowest ? t : 0);
-      if (p.entropy) p.entropy[r] = any ? NAN : M == -INFINITY ? 0.f : kLn2 * (log2f(b.s) - b.u / b.s);
+      if (p.entropy) p.entropy[r] = any ? NAN : b.m == -INFINITY ? 0.f : kLn2 * (log2f(b.s) - b.u / b.s);
+      sh.M = b.m;
+      sh.ls = ls;
+      sh.any = any;
     }
   }
   if (p.top == 0) return;
@@ -318,51 +411,66 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const Params p) {
   // ---- the alternatives
   sync();
   const unsigned long long bound = home->bound;
-  if (first != INT_MAX && key_of(mine, 0) >= bound) {
-    const float least = bound ? value_of(bound) : -INFINITY;  // (0: fewer groups than alternatives, take all)
-    auto pick = [&](const uint4& u, int kk) {
-      if (Row<BF16>::largest(u) < least) return;
-      float x[V];
-      Row<BF16>::unpack(u, x);
-      const int b = row.base(kk);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float y = x[j] != x[j] ? -INFINITY : x[j];
-        if (!(y >= least) || b + j < 0 || b + j >= p.vocab) continue;
-        const unsigned long long key = key_of(y, b + j);
-        if (key < bound) continue;
-        const int at = atomicAdd(&home->n, 1);
-        if (at < kCand) home->cand[at] = key;
-      }
+  const float least = bound ? value_of(bound) : -INFINITY;  // (0: fewer groups than alternatives, take all)
+  auto offer = [&](float x, int id) {
+    const float y = x != x ? -INFINITY : x;
+    // (of the -infinities only ids below top_n can be among the first top_n)
+    if (!(y >= least) || id < 0 || id >= p.vocab || (y == -INFINITY && id >= p.top)) return;
+    const unsigned long long key = key_of(y, id);
+    if (key < bound) return;
+    const int at = atomicAdd(&home->n, 1);
+    if (at < kCand) home->cand[at] = key;
+  };
+  // the vectors to look at go to a list that all threads share, a few elements each
+  if (first != INT_MAX && key_of(best, 0) >= bound) {
+    const bool more = key_of(second, 0) >= bound;
+    const int n = more ? (w1 > w0 + tid ? (w1 - w0 - tid + T - 1) / T : 0) + (ek >= 0 ? 1 : 0) : 1;
+    int i = atomicAdd(&sh.items, n);
+    auto put = [&](int k) {
+      if (i < kItems) sh.item[i] = k;
+      else  // (more than the list holds)
+        for (int j = 0; j < V; ++j)
+          if (row.base(k) + j >= 0 && row.base(k) + j < p.vocab) offer(row.one(row.base(k) + j), row.base(k) + j);
+      ++i;
     };
-    k = w0 + tid;
+    if (!more) {
+      put((first + row.shift) / V);
+    } else {
+      if (ek >= 0) put(ek);
 #pragma unroll 1
-    for (; k + (U - 1) * kThreads < w1; k += U * kThreads) {
-      uint4 u[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) u[i] = row.whole(k + i * kThreads);
-#pragma unroll 1
-      for (int i = 0; i < U; ++i) pick(i == 0 ? u[0] : u[1], k + i * kThreads);
+      for (k = w0 + tid; k < w1; k += T) put(k);
     }
+  }
+  __syncthreads();
 #pragma unroll 1
-    for (; k < w1; k += kThreads) pick(row.whole(k), k);
-    if (ek >= 0) pick(row.edge(ek), ek);
+  for (int i = tid; i < min(sh.items, kItems) * 8; i += T) {
+    const int id = row.base(sh.item[i / 8]) + i % 8 * (V / 8);
+    float x[V / 8];
+#pragma unroll
+    for (int j = 0; j < V / 8; ++j) x[j] = id + j >= 0 && id + j < p.vocab ? row.one(id + j) : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < V / 8; ++j) offer(x[j], id + j);
   }
   sync();
   if (part != 0) return;
   const int n = sh.n;
+  const float M = sh.M, ls = sh.ls;
+  const int any = sh.any;
   auto put = [&](int at, unsigned long long key) {
     const float y = value_of(key);
     if (p.top_ids) p.top_ids[(long long)r * p.top + at] = id_of(key);
     if (p.top_lp) p.top_lp[(long long)r * p.top + at] = any ? NAN : y == -INFINITY ? -INFINITY : (y - M) - ls;
   };
-  if (n <= kThreads) {
+  if (n <= T) {
     // each candidate's place is the number ahead of it (the order they were found in plays no part)
-    if (tid < n) {
-      const unsigned long long key = sh.cand[tid];
+#pragma unroll 1
+    for (int i = tid / 8; i < (n + 3 & ~3); i += T / 8) {
+      const unsigned long long key = i < n ? sh.cand[i] : 0ull;
       int at = 0;
-      for (int i = 0; i < n; ++i) at += sh.cand[i] > key ? 1 : 0;
-      if (at < p.top) put(at, key);
+      for (int j = tid % 8; j < n; j += 8) at += sh.cand[j] > key ? 1 : 0;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) at += __shfl_xor_sync(0xffffffffu, at, o);
+      if (tid % 8 == 0 && i < n && at < p.top) put(at, key);
     }
     return;
   }
@@ -372,12 +480,12 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const Params p) {
   for (int i = 0; i < p.top; ++i) {
     unsigned long long best = 0;
     if (n <= kCand) {
-      for (int j = tid; j < n; j += kThreads) {
+      for (int j = tid; j < n; j += T) {
         const unsigned long long key = sh.cand[j];
         if (key < last) best = max(best, key);
       }
     } else {
-      for (int j = tid; j < p.vocab; j += kThreads) {
+      for (int j = tid; j < p.vocab; j += T) {
         const float y = row.one(j);
         const unsigned long long key = key_of(y != y ? -INFINITY : y, j);
         if (key < last) best = max(best, key);
@@ -389,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_kernel(const Params p) {
     if (lane == 0) sh.best[warp] = best;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kWarps; ++j) best = max(best, sh.best[j]);
+    for (int j = 0; j < W; ++j) best = max(best, sh.best[j]);
     if (tid == 0) put(i, best);
     last = best;
   }
