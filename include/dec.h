@@ -492,6 +492,73 @@ typedef struct {
 } dec_logprobs_args;
 dec_status dec_logprobs(const dec_logprobs_args* args, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+   The engine over these operators. Conventions are the engine's again (errors in
+   dec_last_error(), stream == NULL is the engine's stream, work ordered after its earlier work). */
+
+/* One decode step of `batch` sequences whose keys and values live in paged 4-bit caches, one cache
+   per layer, in place of the engine's own bf16 cache (which it neither reads nor writes; an engine
+   used only this way can have max_ctx 1 and a rotation table of its caller's). Token b stands at
+   position lengths[b] of seqs, is appended there in every layer, and attends to positions 0 ..
+   lengths[b]. lengths are the caller's: add 1 before the next step.
+     caches       host array [n_layers] of the engine's KV heads and head_dim
+     seqs         cu_tokens NULL, n_tokens == batch <= max_batch
+     rope         device fp32 [rope_len][head_dim / 2][2] (as dec_kvq_append's, full heads, half
+                  split); NULL: the engine's table of max_ctx positions
+     the others   as dec_step_args'
+   The step runs in n_layers + 1 cooperative launches (the wide kernel cut at each layer's attention)
+   and the cache's append and attention launches between them; nothing is synchronised. The first
+   call of an engine allocates its buffers for these steps (make it before a stream capture begins).
+   Page ids, lengths and table bounds that are wrong are recorded in the caches' status words.
+   Errors: DEC_ERR_ARG, DEC_ERR_UNSUPPORTED (an engine without the wide kernels: max_batch below
+   dec_info.wide_min_batch, or a shape they do not take), DEC_ERR_POISONED, DEC_ERR_OOM,
+   DEC_ERR_CUDA. */
+typedef struct {
+  const int32_t* tokens;
+  const void* hidden_in;
+  int32_t batch;
+  const dec_kvq_cache* caches;
+  const dec_kvq_seqs* seqs;
+  const float* rope;
+  int32_t rope_len;
+  float* logits;
+  int32_t* next_tokens;
+  void* hidden_out;
+  void* stream;
+} dec_step_kvq_args;
+dec_status dec_step_kvq(dec_engine* eng, const dec_step_kvq_args* args);
+
+/* Move a sequence between the engine's bf16 cache and pages: store writes positions 0 .. length - 1
+   of slot seq into the pages of `table` (device int32 [max_pages], page p holding positions p *
+   page_tokens on) of every layer's cache; load reads `length` positions back into a slot and sets
+   its length. Keys are stored as the engine holds them, rotated. Both synchronise (and report what
+   the kernels found wrong in a status word only through the caches). */
+dec_status dec_kvq_store(dec_engine* eng, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
+                         int32_t max_pages);
+dec_status dec_kvq_load(dec_engine* eng, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
+                        int32_t max_pages, int32_t length);
+
+/* Score a text: append tokens[0 .. n - 1] (device int32) to slot seq as dec_prefill_kv's token mode
+   does (launches of up to DEC_MAX_STEP_TOKENS positions) and give, after each position i, the
+   log-probability and rank of targets[i] (device int32 [n], usually tokens[i + 1]; may be NULL), the
+   entropy and the top_n ids, as dec_logprobs (outputs device arrays of n rows, each may be NULL).
+   Queued on `stream`, nothing is synchronised. Requires vocab > 0. Errors: DEC_ERR_ARG,
+   DEC_ERR_CAPACITY, DEC_ERR_POISONED, DEC_ERR_CUDA. */
+typedef struct {
+  int32_t seq;
+  const int32_t* tokens;
+  int32_t n;
+  const int32_t* targets;
+  float* logprob;
+  int32_t* rank;
+  float* entropy;
+  int32_t top_n;
+  int32_t* top_ids;
+  float* top_logprobs;
+  void* stream;
+} dec_score_args;
+dec_status dec_score(dec_engine* eng, const dec_score_args* args);
+
 #ifdef __cplusplus
 }
 #endif

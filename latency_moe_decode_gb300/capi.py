@@ -91,6 +91,19 @@ class DecLogprobsArgs(C.Structure):
                 ("entropy", C.c_void_p), ("top_n", C.c_int32), ("top_ids", C.c_void_p), ("top_logprobs", C.c_void_p)]
 
 
+class DecStepKvqArgs(C.Structure):
+    _fields_ = [("tokens", C.c_void_p), ("hidden_in", C.c_void_p), ("batch", C.c_int32),
+                ("caches", C.POINTER(DecKvqCache)), ("seqs", C.POINTER(DecKvqSeqs)), ("rope", C.c_void_p),
+                ("rope_len", C.c_int32), ("logits", C.c_void_p), ("next_tokens", C.c_void_p),
+                ("hidden_out", C.c_void_p), ("stream", C.c_void_p)]
+
+
+class DecScoreArgs(C.Structure):
+    _fields_ = [("seq", C.c_int32), ("tokens", C.c_void_p), ("n", C.c_int32), ("targets", C.c_void_p),
+                ("logprob", C.c_void_p), ("rank", C.c_void_p), ("entropy", C.c_void_p), ("top_n", C.c_int32),
+                ("top_ids", C.c_void_p), ("top_logprobs", C.c_void_p), ("stream", C.c_void_p)]
+
+
 DEC_BF16, DEC_F32 = 0, 1
 DEC_MAX_TOP = 32  # include/dec.h
 
@@ -130,6 +143,10 @@ PROTOTYPES = {
     "dec_kvq_attention": (C.c_int, [C.POINTER(DecKvqCache), C.POINTER(DecKvqSeqs), C.POINTER(DecKvqAttentionArgs),
                                     C.c_void_p]),
     "dec_logprobs": (C.c_int, [C.POINTER(DecLogprobsArgs), C.c_void_p]),
+    "dec_step_kvq": (C.c_int, [C.c_void_p, C.POINTER(DecStepKvqArgs)]),
+    "dec_kvq_store": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(DecKvqCache), C.c_void_p, C.c_int32]),
+    "dec_kvq_load": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(DecKvqCache), C.c_void_p, C.c_int32, C.c_int32]),
+    "dec_score": (C.c_int, [C.c_void_p, C.POINTER(DecScoreArgs)]),
 }
 
 _lib = None

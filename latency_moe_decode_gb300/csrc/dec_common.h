@@ -172,6 +172,11 @@ struct WideParams {
   uint16_t* xmid;     // [MB][d] x + attention output projection
   int nch;            // attention chunks per (sequence, KV head)
   int hmax;           // expert slots pbh / exh hold (at least U + n_shared)
+  // steps over a 4-bit cache (wide_segment_kernel): the segment, the q/k/v sums that a segment ends
+  // with, [token][(hq + 2 hkv) hd], and the attention output that the next one begins with
+  int seg;
+  float* qkv;
+  const uint16_t* attn;  // bf16 [token][hq hd]
 };
 
 }  // namespace dec

@@ -14,6 +14,7 @@
 
 #include "dec.h"
 #include "dec_kernel.cuh"
+#include "dec_ops.h"
 #include "dec_wide_host.h"
 
 using namespace dec;
@@ -164,6 +165,15 @@ struct dec_engine {
   int32_t* d_hist = nullptr;
   int32_t* d_accepted = nullptr;  // verify steps: the accepted draft count
   int64_t launches = 0, weight_bytes = 0, kv_bytes = 0, ws_bytes = 0;
+  // steps over 4-bit caches, allocated by the first one: a grid barrier per segment, a layer's q/k/v
+  // sums, rotated queries and attention output, the attention operator's workspace; and the small
+  // index arrays of dec_kvq_store / dec_kvq_load
+  unsigned* kvq_bar = nullptr;
+  float* kvq_qkv = nullptr;
+  uint16_t *kvq_q = nullptr, *kvq_o = nullptr;
+  uint8_t* kvq_ws = nullptr;
+  int64_t kvq_ws_bytes = 0;
+  int32_t* kvq_idx = nullptr;
   uint8_t* arena = nullptr;  // all repacked weight tiles (one allocation the kernel bounds-checks)
   size_t arena_size = 0, arena_used = 0;
 };
@@ -1199,6 +1209,220 @@ dec_status dec_generate(dec_engine* e, const int32_t* first, int32_t batch, int3
   DEC_CUDA(cudaStreamSynchronize(s));
   if (dec_status qs = quiesce(e)) return qs;
   return check_device_status(e);
+}
+
+}  // extern "C"
+
+namespace {
+
+// An operator's failure as the engine's.
+dec_status op_failed(dec_engine* e, dec_status s) { return fail(e, s, dec_op_error()); }
+
+dec_status check_caches(dec_engine* e, const dec_kvq_cache* caches) {
+  const dec_model_cfg& c = e->cfg;
+  if (!caches) return fail(e, DEC_ERR_ARG, "caches: NULL");
+  for (int l = 0; l < c.n_layers; ++l)
+    if (caches[l].n_kv_heads != c.n_kv_heads || caches[l].head_dim != c.head_dim)
+      return fail(e, DEC_ERR_ARG, "caches: KV heads and head_dim must be the engine's, in every layer");
+  return DEC_OK;
+}
+
+// Buffers of the steps over 4-bit caches.
+dec_status kvq_buffers(dec_engine* e, const dec_kvq_cache* any) {
+  if (e->kvq_ws) return DEC_OK;
+  const dec_model_cfg& c = e->cfg;
+  const size_t B = c.max_batch, qd = (size_t)c.n_heads * c.head_dim;
+  dec_status st;
+  if (!e->kvq_bar && (st = dalloc(e, &e->kvq_bar, sizeof(unsigned) * 32 * (c.n_layers + 1), &e->ws_bytes)) != DEC_OK) return st;
+  if (!e->kvq_qkv && (st = dalloc(e, &e->kvq_qkv, sizeof(float) * B * (qd + 2 * c.n_kv_heads * c.head_dim), &e->ws_bytes)) != DEC_OK)
+    return st;
+  if (!e->kvq_q && (st = dalloc(e, &e->kvq_q, 2 * B * qd, &e->ws_bytes)) != DEC_OK) return st;
+  if (!e->kvq_o && (st = dalloc(e, &e->kvq_o, 2 * B * qd, &e->ws_bytes)) != DEC_OK) return st;
+  const int64_t need = dec_kvq_attention_workspace(any, c.n_heads, c.max_batch, 1);
+  if (need < 0) return fail(e, DEC_ERR_UNSUPPORTED, "caches: no attention for this shape");
+  if ((st = dalloc(e, &e->kvq_ws, (size_t)need, &e->ws_bytes)) != DEC_OK) return st;
+  e->kvq_ws_bytes = need;
+  return DEC_OK;
+}
+
+// Positions [0, n) of a slot as rows, and the sequence they make: store (to pages) or load (from them).
+dec_status kvq_move(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, const int32_t* table, int32_t max_pages,
+                    int32_t n, bool store) {
+  const dec_model_cfg& c = e->cfg;
+  if (n == 0) return DEC_OK;
+  if (!table || max_pages < 1) return fail(e, DEC_ERR_ARG, "page table missing");
+  for (int l = 0; l < c.n_layers; ++l)
+    if ((long long)max_pages * caches[l].page_tokens < n) return fail(e, DEC_ERR_CAPACITY, "the page table is too short");
+  if (!e->kvq_idx)
+    if (dec_status st = dalloc(e, &e->kvq_idx, sizeof(int32_t) * 4, &e->ws_bytes)) return st;
+  if (dec_status os = order_on(e, e->stream)) return os;
+  const int32_t idx[4] = {0, n, 0, 0};  // cu_tokens, lengths
+  DEC_CUDA(cudaMemcpyAsync(e->kvq_idx, idx, sizeof idx, cudaMemcpyHostToDevice, e->stream));
+  dec_kvq_seqs sq{};
+  sq.batch = 1;
+  sq.n_tokens = n;
+  sq.cu_tokens = e->kvq_idx;
+  sq.lengths = e->kvq_idx + 2;
+  sq.table = table;
+  sq.max_pages = max_pages;
+  sq.table_stride = max_pages;
+  dec_status st = DEC_OK;
+  for (int l = 0; l < c.n_layers && st == DEC_OK; ++l) {
+    const size_t at = ((size_t)l * c.max_batch + seq) * c.n_kv_heads * c.max_ctx * c.head_dim;
+    const dec_rows k{e->base.kc + at, c.head_dim, (int64_t)c.max_ctx * c.head_dim};
+    const dec_rows v{e->base.vc + at, c.head_dim, (int64_t)c.max_ctx * c.head_dim};
+    if (store) {
+      dec_kvq_append_args a{};
+      a.dtype = DEC_BF16;
+      a.k = k;
+      a.v = v;
+      st = dec_kvq_append(&caches[l], &sq, &a, e->stream);
+    } else {
+      st = dec_kvq_gather(&caches[l], &sq, &k, &v, e->stream);
+    }
+  }
+  DEC_CUDA(cudaStreamSynchronize(e->stream));
+  return st == DEC_OK ? DEC_OK : op_failed(e, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+dec_status dec_step_kvq(dec_engine* e, const dec_step_kvq_args* a) {
+  if (!e || !a) return DEC_ERR_ARG;
+  if (e->poisoned) return fail(e, DEC_ERR_POISONED, "engine poisoned");
+  if (dec_status ds = check_device(e)) return ds;
+  const dec_model_cfg& c = e->cfg;
+  if (a->batch == 0) return DEC_OK;
+  if (a->batch < 0 || a->batch > c.max_batch) return fail(e, DEC_ERR_ARG, "batch out of range");
+  if (!a->tokens && !a->hidden_in) return fail(e, DEC_ERR_ARG, "need tokens or hidden_in");
+  if (a->tokens && c.vocab == 0) return fail(e, DEC_ERR_ARG, "tokens given to a headless stack");
+  if ((a->logits || a->next_tokens) && c.vocab == 0) return fail(e, DEC_ERR_ARG, "no LM head");
+  if ((a->hidden_in && !aligned16(a->hidden_in)) || (a->hidden_out && !aligned16(a->hidden_out)))
+    return fail(e, DEC_ERR_ARG, "hidden_in and hidden_out must be 16-byte aligned");
+  if (!a->seqs || a->seqs->cu_tokens || a->seqs->batch != a->batch || a->seqs->n_tokens != a->batch)
+    return fail(e, DEC_ERR_ARG, "seqs: one row per sequence, as many as the batch");
+  if (!a->seqs->lengths || !a->seqs->table || a->seqs->max_pages < 1)
+    return fail(e, DEC_ERR_ARG, "seqs: lengths and table are needed");
+  if ((a->rope != nullptr) != (a->rope_len > 0)) return fail(e, DEC_ERR_ARG, "rope and rope_len go together");
+  if (dec_status cs = check_caches(e, a->caches)) return cs;
+  const int wi = a->batch <= 16 ? 0 : a->batch <= 32 ? 1 : 2;
+  wide::WideKernelFn kern = e->wkern[wi] ? wide::segment_kernel_for(32 << wi, e->hd, e->group) : nullptr;
+  if (!kern) return fail(e, DEC_ERR_UNSUPPORTED, "steps over 4-bit caches need the wide kernels (max_batch)");
+  if (dec_status bs = kvq_buffers(e, a->caches)) return bs;
+  cudaStream_t s = a->stream ? static_cast<cudaStream_t>(a->stream) : e->stream;
+  if (dec_status os = order_on(e, s)) return os;
+  DEC_CUDA(cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, e->wsmem[wi]));
+  DEC_CUDA(cudaMemsetAsync(e->kvq_bar, 0, sizeof(unsigned) * 32 * (c.n_layers + 1), s));
+
+  KParams p = e->wbase;
+  p.B = a->batch;
+  p.seq0 = 0;
+  p.mpos = 0;
+  p.accepted = nullptr;
+  p.tokens = a->tokens;
+  p.hidden_in = static_cast<const uint16_t*>(a->hidden_in);
+  p.logits = a->logits;
+  p.next_tokens = a->next_tokens;
+  p.hidden_out = static_cast<uint16_t*>(a->hidden_out);
+  p.nsteps = 1;
+  p.ring = e->wring[wi];
+  p.inflight = std::min(p.ring, e->winflight);
+  WideParams wp = e->wp;
+  wp.nch = 1;
+  wp.qkv = e->kvq_qkv;
+  wp.attn = e->kvq_o;
+
+  const int64_t hd = c.head_dim, row = (int64_t)(c.n_heads + 2 * c.n_kv_heads) * hd, qd = (int64_t)c.n_heads * hd;
+  dec_kvq_append_args ap{};
+  ap.dtype = DEC_F32;
+  ap.n_heads = c.n_heads;
+  ap.q = dec_rows{e->kvq_qkv, row, hd};
+  ap.k = dec_rows{e->kvq_qkv + qd, row, hd};
+  ap.v = dec_rows{e->kvq_qkv + qd + (int64_t)c.n_kv_heads * hd, row, hd};
+  ap.q_out = dec_rows{e->kvq_q, qd, hd};
+  ap.rope = a->rope ? a->rope : reinterpret_cast<const float*>(e->base.rope);
+  ap.rope_len = a->rope ? a->rope_len : c.max_ctx;
+  ap.rotary_dim = c.head_dim;
+  dec_kvq_attention_args at{};
+  at.n_heads = c.n_heads;
+  at.q = ap.q_out;
+  at.out = dec_rows{e->kvq_o, qd, hd};
+  at.causal = 1;
+  at.max_tokens = 1;
+  at.workspace = e->kvq_ws;
+  at.workspace_bytes = e->kvq_ws_bytes;
+
+  for (int seg = 0; seg <= c.n_layers; ++seg) {
+    if (seg > 0) {
+      if (dec_status st = dec_kvq_append(&a->caches[seg - 1], a->seqs, &ap, s)) return op_failed(e, st);
+      if (dec_status st = dec_kvq_attention(&a->caches[seg - 1], a->seqs, &at, s)) return op_failed(e, st);
+    }
+    wp.seg = seg;
+    wp.bar = e->kvq_bar + 32 * seg;
+    void* args[] = {&p, &wp};
+    DEC_CUDA(cudaLaunchCooperativeKernel((const void*)kern, dim3(e->grid), dim3(kThreads), args, (size_t)e->wsmem[wi], s));
+    e->launches += 1;
+  }
+  return DEC_OK;
+}
+
+dec_status dec_kvq_store(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
+                         int32_t max_pages) {
+  if (!e) return DEC_ERR_ARG;
+  if (e->poisoned) return fail(e, DEC_ERR_POISONED, "engine poisoned");
+  if (dec_status ds = check_device(e)) return ds;
+  if (seq < 0 || seq >= e->cfg.max_batch) return fail(e, DEC_ERR_ARG, "seq out of range");
+  if (dec_status cs = check_caches(e, caches)) return cs;
+  return kvq_move(e, seq, caches, table, max_pages, e->lengths[seq], true);
+}
+
+dec_status dec_kvq_load(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
+                        int32_t max_pages, int32_t length) {
+  if (!e) return DEC_ERR_ARG;
+  if (e->poisoned) return fail(e, DEC_ERR_POISONED, "engine poisoned");
+  if (dec_status ds = check_device(e)) return ds;
+  if (seq < 0 || seq >= e->cfg.max_batch || length < 0) return fail(e, DEC_ERR_ARG, "seq or length out of range");
+  if (length > e->cfg.max_ctx) return fail(e, DEC_ERR_CAPACITY, "load longer than max_ctx");
+  if (dec_status cs = check_caches(e, caches)) return cs;
+  if (dec_status st = kvq_move(e, seq, caches, table, max_pages, length, false)) return st;
+  return dec_set_length(e, seq, length);
+}
+
+dec_status dec_score(dec_engine* e, const dec_score_args* a) {
+  if (!e || !a) return DEC_ERR_ARG;
+  if (e->poisoned) return fail(e, DEC_ERR_POISONED, "engine poisoned");
+  if (dec_status ds = check_device(e)) return ds;
+  const dec_model_cfg& c = e->cfg;
+  if (a->n < 0 || a->seq < 0 || a->seq >= c.max_batch) return fail(e, DEC_ERR_ARG, "score: seq or n out of range");
+  if (c.vocab == 0) return fail(e, DEC_ERR_ARG, "score needs an embedding and an LM head");
+  if (a->top_n < 0 || a->top_n > DEC_MAX_TOP || a->top_n > c.vocab) return fail(e, DEC_ERR_ARG, "score: top_n");
+  if ((a->logprob || a->rank) && !a->targets) return fail(e, DEC_ERR_ARG, "score: logprob and rank need targets");
+  if (a->n == 0) return DEC_OK;
+  if (!a->tokens) return fail(e, DEC_ERR_ARG, "score: tokens missing");
+  if (e->lengths[a->seq] + (long long)a->n > c.max_ctx) return fail(e, DEC_ERR_CAPACITY, "sequence full");
+  cudaStream_t s = a->stream ? static_cast<cudaStream_t>(a->stream) : e->stream;
+  for (int i = 0; i < a->n; i += DEC_MAX_STEP_TOKENS) {
+    const int n = std::min(DEC_MAX_STEP_TOKENS, a->n - i);
+    // (without a logits buffer the step leaves them in the engine's own)
+    if (dec_status st = launch_step(e, n, a->seq, true, a->tokens + i, nullptr, nullptr, nullptr, nullptr, nullptr, s)) return st;
+    dec_logprobs_args l{};
+    l.logits = e->base.logits_ws;
+    l.dtype = DEC_F32;
+    l.rows = n;
+    l.vocab = c.vocab;
+    l.row_stride = c.vocab;
+    l.targets = a->targets ? a->targets + i : nullptr;
+    l.logprob = a->logprob ? a->logprob + i : nullptr;
+    l.rank = a->rank ? a->rank + i : nullptr;
+    l.entropy = a->entropy ? a->entropy + i : nullptr;
+    l.top_n = a->top_n;
+    l.top_ids = a->top_ids ? a->top_ids + (size_t)i * a->top_n : nullptr;
+    l.top_logprobs = a->top_logprobs ? a->top_logprobs + (size_t)i * a->top_n : nullptr;
+    if (dec_status st = dec_logprobs(&l, s)) return op_failed(e, st);
+  }
+  return DEC_OK;
 }
 
 dec_status dec_set_length(dec_engine* e, int32_t seq, int32_t length) {

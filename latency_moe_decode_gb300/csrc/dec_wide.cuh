@@ -626,6 +626,30 @@ struct WProducer {
       p.trace[kWaitTrace + 1] = tw_rel;
     }
   }
+
+  // One segment (wide_segment_kernel): the second half of layer seg - 1, then the q/k/v stage of
+  // layer seg or the LM head.
+  __device__ void run_segment() {
+    int elist[kMaxExperts];
+    pol_stream = l2_policy(true);
+    pol_near = l2_policy(false);
+    const int l = w.seg - 1;
+    if (!wait_bar(1)) return;
+    if (l >= 0) {
+      issue_gemv(K_O, l, 0, elist);
+      if (wait_bar(3)) {
+        if (!p.dense) issue_gemv(K_ROUTER, l, 0, elist);
+        if (p.dense || p.nsh) issue_gemv(K_SHGU, l, 0, elist);
+        int U = 0;
+        if (!p.dense && routing(U, elist) && wait_bar(6)) issue_gemv(K_RTGU, l, U, elist);
+        if (wait_bar(8)) issue_gemv(K_D, l, U, elist);
+      }
+    }
+    if (w.seg < p.L || p.V > 0) {
+      if (l < 0 || wait_bar(10)) issue_gemv(w.seg < p.L ? K_QKV : K_LM, w.seg < p.L ? w.seg : 0, 0, elist);
+    }
+    drain();
+  }
 };
 
 // ---------------------------------------------------------------------------------------------
@@ -757,6 +781,39 @@ struct WMma {
       ++gseq;
     }
     if (twx) tw_mstage[dk] += gtimer() - cs;
+  }
+
+  // wait until the last products have been written, so that TMEM may be freed
+  __device__ void finish() {
+    if (gseq > 0) {
+      const unsigned last = gseq - 1;
+      const unsigned long long t0 = gtimer();
+      while (!mbar_try_wait(&m->tfull[last % kNGW], (last / kNGW) & 1) && gtimer() - t0 < p.timeout_ns) {
+      }
+    }
+  }
+
+  // (see WProducer::run_segment)
+  __device__ void run_segment() {
+    if (!mbar_wait(&m->tm_ready, 0, p, 50)) dead = true;
+    tc_fence_after();
+    tmem = m->tmem_base;
+    if (w.seg > 0) {
+      gemv(K_O, 0);
+      if (!p.dense) gemv(K_ROUTER, 0);
+      if (p.dense || p.nsh) gemv(K_SHGU, 0);
+      int U = 0;
+      if (!p.dense) {
+        if (!dead && !mbar_wait(&m->rt_bar, 0, p, 51)) dead = true;
+        U = min(max(m->U, 0), w.hmax - p.nsh);
+        gemv(K_RTGU, U);
+      }
+      gemv(K_D, U);
+    }
+    if (w.seg < p.L) gemv(K_QKV, 0);
+    else if (p.V > 0) gemv(K_LM, 0);
+    finish();
+    mbar_arrive(&m->mma_done);
   }
 
   __device__ void run() {
@@ -1548,6 +1605,43 @@ struct WConsumer {
     }
   }
 
+  // ---- steps over a 4-bit cache: what lies between this kernel and the cache's own
+
+  // A layer's q/k/v of every token, summed from the partials: warp unit (token b, row block rb).
+  __device__ void qkv_out() {
+    const WGeo gq = wgeo(p, K_QKV, 0, gridDim.x);
+    const size_t pst = (size_t)p.MB * kTileRows;
+    const int rows = (p.hq + 2 * p.hkv) * HD, nw = gridDim.x * kConsumerWarps;
+#pragma unroll 1
+    for (int wu = blockIdx.x * kConsumerWarps + warp; wu < p.B * p.n_rb_qkv && !dead; wu += nw) {
+      const int b = wu / p.n_rb_qkv, rb = wu % p.n_rb_qkv, row = rb * kTileRows + lane * 4;
+      const int nc = n_contrib(rb * gq.kbs, gq.kbs, gq.T, gridDim.x);
+      const float* src = p.part_qkv + ((size_t)rb * gq.S * p.MB + b) * kTileRows + lane * 4;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int c = 0; c < nc; ++c) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(src + (size_t)c * pst));
+        s.x += a.x;
+        s.y += a.y;
+        s.z += a.z;
+        s.w += a.w;
+      }
+      if (row < rows) *reinterpret_cast<float4*>(w.qkv + (size_t)b * rows + row) = s;
+    }
+  }
+
+  // The attention output of every token as B blocks: warp unit (token b, k block kb).
+  __device__ void attn_pack() {
+    const int nw = gridDim.x * kConsumerWarps;
+#pragma unroll 1
+    for (int wu = blockIdx.x * kConsumerWarps + warp; wu < p.B * p.kb_o && !dead; wu += nw) {
+      const int b = wu / p.kb_o, kb = wu % p.kb_o;
+      const uint2 u = __ldcg(reinterpret_cast<const uint2*>(w.attn + (size_t)b * p.hq * HD + kb * kTileK + lane * 4));
+      const float f[4] = {bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y)};
+      pack4(w.pbo + (size_t)kb * PBS, w.exo + (size_t)kb * kWideMax + b, b, lane * 4, f);
+    }
+  }
+
   // ---- per-token phases (one CTA per token)
 
   __device__ const uint16_t* layer_in(int l, int t) const {
@@ -1902,6 +1996,69 @@ struct WConsumer {
 
   // ---- the step
 
+  // One segment (wide_segment_kernel; see WProducer::run_segment): its barriers are 1 (the input), 2 ..
+  // 10 (the layer's second half), and then the q/k/v stage's or the LM head's.
+  __device__ void run_segment() {
+    if (warp == 0) tmem_alloc(&m->tmem_base, kTmemCols);
+    tc_fence_before();
+    cons_sync();
+    tc_fence_after();
+    tmem = m->tmem_base;
+    if (tid == 0) mbar_arrive(&m->tm_ready);
+    const int l = w.seg - 1;
+    if (l < 0) input_pack();
+    else attn_pack();
+    gbar();
+    if (l >= 0) {
+      gemv(K_O, 0);
+      gbar();
+      xmid_pack(l);
+      gbar();
+      if (!p.dense) gemv(K_ROUTER, 0);
+      if (p.dense || p.nsh) gemv(K_SHGU, 0);
+      gbar();
+      if (!p.dense) route_tokens(l);
+      gbar();
+      local_routing();
+      const int U = m->U;
+      gather(U);
+      gbar();
+      if (!p.dense) gemv(K_RTGU, U);
+      gbar();
+      swiglu_pack(U);
+      gbar();
+      gemv(K_D, U);
+      gbar();
+      layer_out(l, U);
+      gbar();
+    }
+    if (w.seg < p.L) {
+      gemv(K_QKV, 0);
+      gbar();
+      qkv_out();
+    } else if (p.V > 0) {
+      gemv(K_LM, 0);
+      gbar();
+      lm_final();
+      gbar();
+      if (blockIdx.x == 0 && tid < p.B && !dead) {
+        const unsigned long long key = atomicExch(p.amax + tid, 0ull);
+        if (p.next_tokens) p.next_tokens[tid] = (int)(0xFFFFFFFFu - (unsigned)(key & 0xFFFFFFFFull));
+      }
+    }
+    // TMEM is freed once the MMA warp has finished (bounded wait)
+    if (warp == 0) {
+      if (lane == 0) {
+        const unsigned long long t0 = gtimer();
+        while (!mbar_try_wait(&m->mma_done, 0) && gtimer() - t0 < p.timeout_ns) {
+        }
+      }
+      __syncwarp();
+      tc_fence_after();
+      tmem_free(tmem, kTmemCols);
+    }
+  }
+
   __device__ void stamp_layer(int l) {
     if (blockIdx.x == 0 && tid == 0) p.layer_ts[l] = gtimer();
   }
@@ -2052,6 +2209,68 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   WConsumer<NR, HD, G> cons(p, w, ring, full, empty, red, m, reinterpret_cast<float4*>(smem + L.acc_off));
   cons.run();
+}
+
+// A step whose history is in a paged 4-bit cache: the layers' attention runs in the cache's own
+// kernels, so the step is cut at each of them into segments 0 .. n_layers, one launch each, with the
+// same roles, stages and buffers as a whole step's. Segment s ends with the q/k/v sums of layer s (the
+// last one with the logits) and begins with the attention output of layer s - 1.
+template <int NR, int HD, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    wide_segment_kernel(const __grid_constant__ KParams p, const __grid_constant__ WideParams w) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const WLayout L = wlayout(p.ring, NR, HD, G);
+  uint8_t* ring = smem + L.ring_off;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.full_off);
+  uint64_t* empty = reinterpret_cast<uint64_t*>(smem + L.empty_off);
+  uint64_t* mempty = reinterpret_cast<uint64_t*>(smem + L.mempty_off);
+  float* red = reinterpret_cast<float*>(smem + L.red_off);
+  WMisc* m = reinterpret_cast<WMisc*>(smem + L.misc_off);
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    for (int s = 0; s < p.ring; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kConsumerWarps);
+      mbar_init(&mempty[s], 1);
+    }
+    mbar_init(&m->rt_bar, 1);
+    mbar_init(&m->mma_done, 1);
+    mbar_init(&m->tm_ready, 1);
+    mbar_init(&m->sbar, 1);
+    mbar_init(&m->obar, 1);
+    m->stages_begun = 0;
+    for (int i = 0; i < kNGW; ++i) {
+      mbar_init(&m->tfull[i], 2);  // MMA commit + the MMA thread's release of the block scales
+      mbar_init(&m->tempty[i], kConsumerWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid < kWideMax) {
+    int tok = 0;
+    if (tid < p.B) {
+      if (p.tokens) {
+        tok = p.tokens[tid];
+        if (tok < 0 || tok >= p.V) {
+          raise_err(p, kDevBadArg, 2);
+          tok = 0;
+        }
+      }
+    }
+    m->tok[tid] = tok;
+  }
+  __syncthreads();
+  if (tid >= kConsumerWarps * 32) {
+    if (tid == kConsumerWarps * 32) {
+      WProducer<NR, HD, G> prod(p, w, ring, full, empty, mempty, m);
+      prod.run_segment();
+    } else if (tid == (kConsumerWarps + 1) * 32) {
+      WMma<NR, HD, G> mma(p, w, ring, full, mempty, m);
+      mma.run_segment();
+    }
+    return;
+  }
+  WConsumer<NR, HD, G> cons(p, w, ring, full, empty, red, m, reinterpret_cast<float4*>(smem + L.acc_off));
+  cons.run_segment();
 }
 
 }  // namespace wide

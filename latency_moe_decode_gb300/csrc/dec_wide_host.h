@@ -9,6 +9,8 @@ using WideKernelFn = void (*)(const KParams, const WideParams);
 
 // the kernel for B operand blocks of nr rows (steps of up to nr / 2 tokens), or null
 WideKernelFn kernel_for(int nr, int hd, int group);
+// the same for one segment of a step over a 4-bit cache (dec_step_kvq.cu)
+WideKernelFn segment_kernel_for(int nr, int hd, int group);
 // dynamic shared memory of a kernel with `ring` slots
 int smem_bytes(int ring, int nr, int hd, int group);
 // partial-sum slots per output row block, and tiles, of GEMV stage `kind` with U routed experts

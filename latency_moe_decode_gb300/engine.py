@@ -6,13 +6,14 @@ engine's CUDA kernels behind include/dec.h.
 from __future__ import annotations
 
 import ctypes as C
-from typing import Dict, Optional
+from typing import Dict, List, Optional
 
 import numpy as np
 import torch
 
-from . import capi
-from .capi import DecCtx, DecError, DecFp8Mat, DecInfo, DecLayerWeights, DecModelCfg, DecStepArgs, DecWeights
+from . import capi, ops
+from .capi import (DecCtx, DecError, DecFp8Mat, DecInfo, DecKvqCache, DecLayerWeights, DecModelCfg, DecScoreArgs,
+                   DecStepArgs, DecStepKvqArgs, DecWeights)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -177,6 +178,75 @@ class Engine:
         self._check(self.lib.dec_generate_device(self.h, first.data_ptr(), first.numel(), out.shape[0], out.data_ptr(),
                                                  _stream_ptr(stream if stream is not None else torch.cuda.current_stream())),
                     "dec_generate_device")
+
+    # ---- paged 4-bit caches (ops.KvqCache, one per layer)
+    def kvq_caches(self, n_pages: int, page_tokens: int = 64) -> List[ops.KvqCache]:
+        """Caches of n_pages pages for every layer, with one status word between them."""
+        c = self.cfg
+        first = ops.KvqCache(n_pages, c.n_kv_heads, c.head_dim, page_tokens)
+        return [first] + [ops.KvqCache(n_pages, c.n_kv_heads, c.head_dim, page_tokens, status=first.status)
+                          for _ in range(c.n_layers - 1)]
+
+    def _caches(self, caches):
+        if len(caches) != self.cfg.n_layers:
+            raise ValueError(f"{self.cfg.n_layers} caches are needed, one per layer")
+        return (DecKvqCache * len(caches))(*[k.c for k in caches])
+
+    @staticmethod
+    def _table(caches, table: torch.Tensor) -> torch.Tensor:
+        if table.dtype != torch.int32 or table.dim() != 1 or not table.is_contiguous() or table.device != caches[0].device:
+            raise ValueError("table must be a contiguous int32 vector of page ids on the caches' device")
+        return table
+
+    def kvq_store(self, seq: int, caches: List[ops.KvqCache], table: torch.Tensor):
+        """Write slot seq's positions into the pages of `table` (device int32 [pages]) of every cache."""
+        arr, t = self._caches(caches), self._table(caches, table)
+        self._check(self.lib.dec_kvq_store(self.h, seq, arr, t.data_ptr(), t.numel()), "dec_kvq_store")
+
+    def kvq_load(self, seq: int, caches: List[ops.KvqCache], table: torch.Tensor, length: int):
+        """Read `length` positions back into slot seq."""
+        arr, t = self._caches(caches), self._table(caches, table)
+        self._check(self.lib.dec_kvq_load(self.h, seq, arr, t.data_ptr(), t.numel(), length), "dec_kvq_load")
+
+    def step_kvq(self, caches: List[ops.KvqCache], lengths: torch.Tensor, table: torch.Tensor,
+                 tokens: Optional[torch.Tensor] = None, hidden: Optional[torch.Tensor] = None,
+                 rope: Optional[torch.Tensor] = None, logits: Optional[torch.Tensor] = None,
+                 next_tokens: Optional[torch.Tensor] = None, hidden_out: Optional[torch.Tensor] = None, stream=None):
+        """One decode step of lengths.shape[0] sequences over the caches (dec_step_kvq): token b is
+        appended at position lengths[b] of the pages table[b]. The caller adds 1 to lengths."""
+        s = caches[0]._seqs(lengths, table, None, lengths.shape[0])
+        if rope is not None and (rope.dtype != torch.float32 or not rope.is_contiguous() or
+                                 tuple(rope.shape[1:]) != (self.cfg.head_dim // 2, 2) or rope.device != caches[0].device):
+            raise ValueError("rope must be contiguous float32 [positions, head_dim / 2, 2] on the caches' device")
+        arr = self._caches(caches)
+        a = DecStepKvqArgs(_ptr(tokens), _ptr(hidden), lengths.shape[0], arr, C.pointer(s), _ptr(rope),
+                           0 if rope is None else rope.shape[0], _ptr(logits), _ptr(next_tokens), _ptr(hidden_out),
+                           _stream_ptr(stream if stream is not None else torch.cuda.current_stream()))
+        self._check(self.lib.dec_step_kvq(self.h, C.byref(a)), "dec_step_kvq")
+
+    def score(self, tokens: torch.Tensor, seq: int = 0, targets: Optional[torch.Tensor] = None, top_n: int = 0,
+              stream=None) -> ops.LogProbs:
+        """Append tokens (device int32 [n]) to slot seq and return, after each position, the
+        log-probability and rank of its target, the entropy and the top_n alternatives. targets:
+        device int32 [n]; default: each next token (the last row's is -1: logprob NaN, rank -1)."""
+        stream = stream if stream is not None else torch.cuda.current_stream()
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+            t = tokens.to(torch.int32).contiguous()
+            n, dev = t.numel(), t.device
+            if targets is None:
+                targets = torch.cat([t[1:], t.new_full((1,), -1)]) if n else t
+            targets = targets.to(torch.int32).contiguous()
+            if targets.numel() != n or not t.is_cuda or targets.device != dev:
+                raise ValueError("tokens and targets must be device vectors of one length")
+            f32 = dict(dtype=torch.float32, device=dev)
+            lp, ent = torch.empty(n, **f32), torch.empty(n, **f32)
+            rank = torch.empty(n, dtype=torch.int32, device=dev)
+            ids = torch.empty(n, top_n, dtype=torch.int32, device=dev) if top_n > 0 else None
+            tlp = torch.empty(n, top_n, **f32) if top_n > 0 else None
+            a = DecScoreArgs(seq, t.data_ptr(), n, targets.data_ptr(), lp.data_ptr(), rank.data_ptr(), ent.data_ptr(),
+                             top_n, _ptr(ids), _ptr(tlp), _stream_ptr(stream))
+            self._check(self.lib.dec_score(self.h, C.byref(a)), "dec_score")
+        return ops.LogProbs(lp, rank, ent, ids, tlp)
 
     def set_length(self, seq: int, length: int):
         self._check(self.lib.dec_set_length(self.h, seq, length), "dec_set_length")

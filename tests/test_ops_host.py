@@ -133,7 +133,8 @@ def test_struct_sizes_match_the_header(lib, tmp_path):
     import subprocess
     names = {"dec_kvq_cache": DecKvqCache, "dec_kvq_seqs": DecKvqSeqs, "dec_rows": DecRows,
              "dec_kvq_append_args": DecKvqAppendArgs, "dec_kvq_attention_args": DecKvqAttentionArgs,
-             "dec_logprobs_args": DecLogprobsArgs}
+             "dec_logprobs_args": DecLogprobsArgs, "dec_step_kvq_args": capi.DecStepKvqArgs,
+             "dec_score_args": capi.DecScoreArgs}
     src = tmp_path / "s.c"
     src.write_text('#include <stdio.h>\n#include "dec.h"\nint main(void) {' +
                    "".join(f'printf("%d\\n", (int)sizeof({n}));' for n in names) + "return 0; }")
@@ -141,3 +142,10 @@ def test_struct_sizes_match_the_header(lib, tmp_path):
     subprocess.run(["gcc", "-I", os.path.join(root, "include"), "-o", str(tmp_path / "s"), str(src)], check=True)
     got = subprocess.run([str(tmp_path / "s")], check=True, capture_output=True, text=True).stdout.split()
     assert [int(x) for x in got] == [C.sizeof(t) for t in names.values()]
+
+
+def test_engine_entry_points_reject_null(lib):
+    assert lib.dec_step_kvq(None, None) == ARG
+    assert lib.dec_kvq_store(None, 0, None, None, 0) == ARG
+    assert lib.dec_kvq_load(None, 0, None, None, 0, 0) == ARG
+    assert lib.dec_score(None, None) == ARG
