@@ -73,14 +73,18 @@ class DecRows(C.Structure):
     _fields_ = [("p", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
 
 
+def _row_fields(*names):
+    """dec_rows members field by field (the same layout; one constructor call instead of one a member)."""
+    return [(n + f, t) for n in names for f, t in (("", C.c_void_p), ("_token_stride", C.c_int64), ("_head_stride", C.c_int64))]
+
+
 class DecKvqAppendArgs(C.Structure):
-    _fields_ = [("dtype", C.c_int), ("n_heads", C.c_int32), ("q", DecRows), ("k", DecRows), ("v", DecRows),
-                ("q_out", DecRows), ("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("eps", C.c_float),
+    _fields_ = [("dtype", C.c_int), ("n_heads", C.c_int32), *_row_fields("q", "k", "v", "q_out"), ("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("eps", C.c_float),
                 ("rope", C.c_void_p), ("rope_len", C.c_int32), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32)]
 
 
 class DecKvqAttentionArgs(C.Structure):
-    _fields_ = [("n_heads", C.c_int32), ("q", DecRows), ("out", DecRows), ("lse", C.c_void_p), ("scale", C.c_float),
+    _fields_ = [("n_heads", C.c_int32), *_row_fields("q", "out"), ("lse", C.c_void_p), ("scale", C.c_float),
                 ("causal", C.c_int32), ("max_tokens", C.c_int32), ("workspace", C.c_void_p),
                 ("workspace_bytes", C.c_int64)]
 

@@ -35,16 +35,23 @@ def _r(**kw):
     return DecRows(**d)
 
 
+def _flat(d):
+    """dec_rows members as the structures' own fields."""
+    return {k2: v2 for k, v in d.items() for k2, v2 in (
+        [(k, v.p), (k + "_token_stride", v.token_stride), (k + "_head_stride", v.head_stride)]
+        if isinstance(v, DecRows) else [(k, v)])}
+
+
 def _append(**kw):
     d = dict(dtype=0, n_heads=8, q=_r(), k=_r(), v=_r(), q_out=_r(), eps=1e-6)
     d.update(kw)
-    return DecKvqAppendArgs(**d)
+    return DecKvqAppendArgs(**_flat(d))
 
 
 def _attn(**kw):
     d = dict(n_heads=8, q=_r(), out=_r(), max_tokens=1, causal=1)
     d.update(kw)
-    return DecKvqAttentionArgs(**d)
+    return DecKvqAttentionArgs(**_flat(d))
 
 
 def test_page_bytes(lib):
