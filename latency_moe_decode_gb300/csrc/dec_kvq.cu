@@ -251,13 +251,19 @@ dec_status dec_kvq_append(const dec_kvq_cache* c, const dec_kvq_seqs* s, const d
   p.rot = a->rotary_dim;
   p.inter = a->interleaved != 0;
   p.eps = a->eps;
-  const long long rows = (long long)s->n_tokens * (a->n_heads + 2 * c->n_kv_heads);
-  const long long grid = (rows * (c->head_dim / 8) + 255) / 256;
-  if (grid > INT_MAX) return op_fail(DEC_ERR_UNSUPPORTED, "append: too many rows");
   const bool f32 = a->dtype == DEC_F32;
-  auto* k = c->head_dim == 128 ? (f32 ? append_kernel<128, true> : append_kernel<128, false>)
-                               : (f32 ? append_kernel<64, true> : append_kernel<64, false>);
-  k<<<(unsigned)grid, 256, 0, op_stream(stream)>>>(p);
+  const cudaStream_t cs = op_stream(stream);
+  auto go = [&](auto* few, auto* many) {
+    if (s->n_tokens <= 4 * op_sms()) few<<<(unsigned)s->n_tokens, 256, 0, cs>>>(p);
+    else many<<<(unsigned)s->n_tokens, 128, 0, cs>>>(p);
+  };
+  if (c->head_dim == 128) {
+    if (f32) go(append_kernel<128, true, 256>, append_kernel<128, true, 128>);
+    else go(append_kernel<128, false, 256>, append_kernel<128, false, 128>);
+  } else {
+    if (f32) go(append_kernel<64, true, 256>, append_kernel<64, true, 128>);
+    else go(append_kernel<64, false, 256>, append_kernel<64, false, 128>);
+  }
   return launched("append");
 }
 
@@ -275,10 +281,8 @@ dec_status dec_kvq_gather(const dec_kvq_cache* c, const dec_kvq_seqs* s, const d
   p.s = seqs_of(s);
   p.k = rows_of(*k_out);
   p.v = rows_of(*v_out);
-  const long long grid = ((long long)s->n_tokens * 2 * c->n_kv_heads * (c->head_dim / 8) + 255) / 256;
-  if (grid > INT_MAX) return op_fail(DEC_ERR_UNSUPPORTED, "gather: too many rows");
   auto* k = c->head_dim == 128 ? gather_kernel<128> : gather_kernel<64>;
-  k<<<(unsigned)grid, 256, 0, op_stream(stream)>>>(p);
+  k<<<(unsigned)s->n_tokens, 64, 0, op_stream(stream)>>>(p);
   return launched("gather");
 }
 
