@@ -10,6 +10,7 @@
 
 #include "dec_kvq.cuh"
 #include "dec_kvq_attn.cuh"
+#include "dec_kvq_prompt.cuh"
 #include "dec_ops.h"
 
 namespace dec {
@@ -130,6 +131,12 @@ dec_status launched(const char* what) {
   return ce == cudaSuccess ? DEC_OK : op_cuda(ce, what);
 }
 
+// The prompt kernel takes calls whose longest sequence has at least this many query rows.
+#ifndef KVQ_PROMPT
+#define KVQ_PROMPT 64
+#endif
+constexpr int kPromptRows = KVQ_PROMPT;
+
 // The attention kernel's dynamic shared memory limit, raised once per device. The join kernel asks for
 // the same division of the SM's memory, so that none is redivided between the two.
 template <class F>
@@ -147,25 +154,44 @@ dec_status raise_smem(F* k, F* join, int bytes, std::atomic<unsigned long long>&
   return DEC_OK;
 }
 
-// Query rows per unit: 8 as long as they hold the longest sequence's rows, else 16.
-int blocks_of(int n_heads, int hkv, int max_tokens) { return (long long)max_tokens * (n_heads / hkv) <= 8 ? 1 : 2; }
-
-template <int HD, int NB>
-int64_t workspace_of(int sms) {
-  using K = AttnCfg<HD, NB>;
-  return (int64_t)sms * ((2 + K::WARPS) * K::PART * 4 + 32);
+// Which kernel takes a call, by the longest sequence's query rows: 0 and 1, the streaming one with 8 and
+// 16 rows a unit; 2, the one for prompts.
+int kernel_of(int n_heads, int hkv, int max_tokens) {
+  const long long rows = (long long)max_tokens * (n_heads / hkv);
+  return rows <= 8 ? 0 : rows < kPromptRows ? 1 : 2;
 }
 
+// A kernel's launch: its function, the one that joins its parts, and their sizes.
+struct Variant {
+  void (*kernel)(const AttnParams);
+  void (*join)(const AttnParams);
+  int threads, smem, rows, part, wparts;  // parts in floats; a CTA's parts of its warps
+};
 template <int HD, int NB>
-dec_status launch_attention(AttnParams p, int batch, uint8_t* ws, cudaStream_t stream) {
+Variant streaming() {
   using K = AttnCfg<HD, NB>;
-  static std::atomic<unsigned long long> done{0};
-  if (dec_status st = raise_smem(attention_kernel<HD, NB>, join_kernel<HD, NB>, K::smem(), done)) return st;
+  return Variant{attention_kernel<HD, NB>, join_kernel<HD, K::ROWS>, K::THREADS, K::smem(), K::ROWS, K::PART, K::WARPS * K::PART};
+}
+template <int HD>
+Variant prompt() {
+  using C = PromptCfg<HD>;
+  return Variant{prompt_kernel<HD>, join_kernel<HD, C::ROWS>, C::THREADS, C::smem(), C::ROWS, C::PART, 0};
+}
+Variant variant_of(int hd, int kind) {
+  if (hd == 128) return kind == 0 ? streaming<128, 1>() : kind == 1 ? streaming<128, 2>() : prompt<128>();
+  return kind == 0 ? streaming<64, 1>() : kind == 1 ? streaming<64, 2>() : prompt<64>();
+}
+int64_t workspace_of(const Variant& v, int sms) { return (int64_t)sms * (32 + 4ll * (2 * v.part + v.wparts)); }
+
+dec_status launch_attention(AttnParams p, int hd, int kind, int batch, uint8_t* ws, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done[2][3];
+  const Variant v = variant_of(hd, kind);
+  if (dec_status st = raise_smem(v.kernel, v.join, v.smem, done[hd == 128][kind])) return st;
   const int sms = op_sms();
   if (sms < 1) return op_fail(DEC_ERR_CUDA, "attention: no device");
   p.meta = reinterpret_cast<int4*>(ws);
   p.parts = reinterpret_cast<float*>(ws + (size_t)sms * 32);
-  p.wparts = p.parts + (size_t)sms * 2 * K::PART;
+  p.wparts = p.parts + (size_t)sms * 2 * v.part;
   p.min_groups = kMinGroups;
   p.magic = Magic{0x64006400u, 0x54005400u};
   const Seqs all = p.s;
@@ -175,19 +201,19 @@ dec_status launch_attention(AttnParams p, int batch, uint8_t* ws, cudaStream_t s
     p.s.table = all.table + b * all.table_stride;
     if (all.cu) p.s.cu = all.cu + b;
     p.b0 = b;
-    attention_kernel<HD, NB><<<sms, K::THREADS, K::smem(), stream>>>(p);
+    v.kernel<<<sms, v.threads, v.smem, stream>>>(p);
     cudaError_t ce = cudaGetLastError();
     if (ce != cudaSuccess) return op_cuda(ce, "attention");
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sms);
-    cfg.blockDim = dim3(K::ROWS * 32);
+    cfg.gridDim = dim3(sms, v.rows / 8);
+    cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    ce = cudaLaunchKernelEx(&cfg, join_kernel<HD, NB>, p);
+    ce = cudaLaunchKernelEx(&cfg, v.join, p);
     if (ce != cudaSuccess) return op_cuda(ce, "attention (join)");
   }
   return DEC_OK;
@@ -292,9 +318,7 @@ int64_t dec_kvq_attention_workspace(const dec_kvq_cache* c, int32_t n_heads, int
   if (dec_kvq_page_bytes(c->page_tokens, c->n_kv_heads, c->head_dim) == 0) return -1;
   const int sms = op_sms();
   if (sms < 1) return -1;
-  const bool wide = blocks_of(n_heads, c->n_kv_heads, max_tokens) == 2;
-  if (c->head_dim == 128) return wide ? workspace_of<128, 2>(sms) : workspace_of<128, 1>(sms);
-  return wide ? workspace_of<64, 2>(sms) : workspace_of<64, 1>(sms);
+  return workspace_of(variant_of(c->head_dim, kernel_of(n_heads, c->n_kv_heads, max_tokens)), sms);
 }
 
 dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec_kvq_attention_args* a,
@@ -330,18 +354,14 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
   p.causal = a->causal != 0;
   p.max_tokens = a->max_tokens;
   const int max_tokens = std::min(a->max_tokens, s->n_tokens);
-  const bool wide = blocks_of(a->n_heads, c->n_kv_heads, max_tokens) == 2;
+  const int kind = kernel_of(a->n_heads, c->n_kv_heads, max_tokens);
   if (a->workspace_bytes < dec_kvq_attention_workspace(c, a->n_heads, s->batch, max_tokens))
     return op_fail(DEC_ERR_ARG, "attention: workspace too small");
-  // entries of the kernel's list of groups, at most: 32-bit
-  const long long units = (long long)c->n_kv_heads * ((long long)s->n_tokens * p.group / (wide ? 16 : 8) + s->batch);
+  // entries of the kernels' list, at most: 32-bit
+  const long long units = (long long)c->n_kv_heads * ((long long)s->n_tokens * p.group / 8 + s->batch);
   if (units * ((long long)s->max_pages * c->page_tokens / kGroup + 1 + kUnitCost) >= (1LL << 32) - 64)
     return op_fail(DEC_ERR_UNSUPPORTED, "attention: too much work for one call");
-  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-  cudaStream_t st = op_stream(stream);
-  if (c->head_dim == 128)
-    return wide ? launch_attention<128, 2>(p, s->batch, ws, st) : launch_attention<128, 1>(p, s->batch, ws, st);
-  return wide ? launch_attention<64, 2>(p, s->batch, ws, st) : launch_attention<64, 1>(p, s->batch, ws, st);
+  return launch_attention(p, c->head_dim, kind, s->batch, static_cast<uint8_t*>(a->workspace), op_stream(stream));
 }
 
 }  // extern "C"

@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "dec_kvq.cuh"
+#include "dec_prims.cuh"
 
 namespace dec {
 namespace kvq {
@@ -29,6 +30,7 @@ constexpr int kStages = 3;       // chunks of a warp's ring
 constexpr int kMaxSeqs = 256;    // sequences of one launch (their table lies in shared memory)
 constexpr int kUnitCost = 2;     // what beginning and ending a unit costs, in groups' time
 constexpr int kMinGroups = 8;    // groups a CTA takes at least
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 15.0f;  // probabilities are kept times 2^15: f16 then reaches 2^-39 of the largest
 
 
@@ -76,31 +78,22 @@ struct AttnParams {
   int4* meta;     // [CTA][2]: unit continued (1) and finished here (2), unit left open | the open unit's place
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void bar_init(uint64_t* b) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(b)) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* b) {
-  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
-               "l"(src), "r"(bytes), "r"(smem_addr(b))
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(b))
                : "memory");
 }
-// Wait for the barrier's phase; false after about a second (a copy always ends: this only keeps a
-// mistake from holding the GPU).
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
-  for (int i = 0; i < (1 << 23); ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(b)), "r"(parity)
-        : "memory");
-    if (ok) return true;
+// Wait for the barrier's phase; false after a second (copies and products always end: this only keeps
+// a mistake from holding the GPU).
+static __device__ __noinline__ bool bar_wait_long(uint64_t* b, uint32_t parity) {
+  const unsigned long long t0 = gtimer();
+  for (unsigned i = 1;; ++i) {
+    if (mbar_try_wait(b, parity)) return true;
+    if ((i & 63u) == 0 && gtimer() - t0 > 1000000000ull) return false;
   }
-  return false;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
+  return mbar_try_wait(b, parity) || bar_wait_long(b, parity);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -151,6 +144,69 @@ __device__ __forceinline__ uint32_t fast_div(uint32_t x, uint32_t d, uint32_t in
 // (no division for the common single row block)
 __device__ __forceinline__ int over(int a, int d) { return d == 1 ? a : a / d; }
 __host__ __device__ inline uint32_t reciprocal(uint32_t d) { return 0xFFFFFFFFu / d; }
+
+// The list's table in shared memory, by the whole CTA: units of ROWS query rows, entries of POS positions.
+// Returns the number of entries.
+template <int THREADS, int ROWS, int POS, int COST>
+__device__ uint32_t build_list(const AttnParams& p, SeqWork* seqs, uint32_t* scan) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t base = 0;
+  for (int b0 = 0; b0 < p.s.batch; b0 += THREADS) {
+    const int b = b0 + tid;
+    uint32_t w = 0;
+    SeqWork sw;
+    if (b < p.s.batch) {
+      const int first = p.s.cu ? __ldg(p.s.cu + b) : p.b0 + b, last = p.s.cu ? __ldg(p.s.cu + b + 1) : first + 1;
+      const int len = __ldg(p.s.lengths + b);
+      const long long most = (long long)p.s.max_pages << p.c.page_shift;
+      sw.tok0 = max(first, 0);
+      sw.n = max(0, min(min(last - first, p.max_tokens), p.s.n_tokens - sw.tok0));
+      if (sw.n > 0 && len < 0) raise(p.c.status, DEC_ERR_ARG);
+      if (sw.n > 0 && (p.causal ? (long long)len + sw.n : len) > most) raise(p.c.status, DEC_ERR_CAPACITY);
+      sw.len = len < 0 ? -sw.n : (int)min((long long)len, most);
+      // (a unit without positions still writes its rows)
+      const int held = (int)min(most, (long long)(p.causal ? sw.len + sw.n : sw.len));
+      sw.ng = max(1, (held + POS - 1) / POS);
+      sw.inv = reciprocal(sw.ng + COST);
+      sw.nrb = (sw.n * p.group + ROWS - 1) / ROWS;
+      w = (uint32_t)p.c.hkv * sw.nrb * (sw.ng + COST);
+    }
+    uint32_t x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    uint32_t before = base, all = base;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+      const uint32_t y = scan[i];
+      before += i < warp ? y : 0u;
+      all += y;
+    }
+    if (b < p.s.batch) {
+      sw.pre = before + x - w;
+      seqs[b] = sw;
+    }
+    base = all;
+  }
+  __syncthreads();
+  return base;
+}
+
+// the sequence that entry f of the list belongs to
+__device__ __forceinline__ int seq_of_entry(const SeqWork* seqs, int batch, uint32_t f) {
+  int a = 0, z = batch;
+  while (z - a > 1) {
+    const int m = (a + z) >> 1;
+    if (seqs[m].pre <= f) a = m;
+    else z = m;
+  }
+  return a;
+}
 
 // The operands of O^T's products with a group's values (vw: the lane's words of positions 2t, 2t + 1,
 // 2t + 8, 2t + 9; bytes: their scales): put(k, a0..a3) for 16 values of the head at a time, of which
@@ -274,7 +330,7 @@ struct Joined {
         reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + lane * V);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) dst[i] = __floats2bfloat162_rn(a[2 * i] * inv, a[2 * i + 1] * inv);
-    if (p.lse && lane == 0) p.lse[tok * p.hq + head] = (M - kPShift + log2f(L)) * 0.6931471805599453f;
+    if (p.lse && lane == 0) p.lse[tok * p.hq + head] = (M - kPShift + log2f(L)) * kLn2;
   }
 };
 
@@ -302,54 +358,10 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
   static_assert(2 * K::WARPS <= 32, "one entry per lane in the join");
   if (tid < 32) ent_unit[tid] = make_uint2(0u, 0u);
   if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) bar_init(bars[warp] + i);
+    for (int i = 0; i < kStages; ++i) mbar_init(bars[warp] + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  uint32_t base = 0;
-  for (int b0 = 0; b0 < p.s.batch; b0 += K::THREADS) {
-    const int b = b0 + tid;
-    uint32_t w = 0;
-    SeqWork sw;
-    if (b < p.s.batch) {
-      const int first = p.s.cu ? __ldg(p.s.cu + b) : p.b0 + b, last = p.s.cu ? __ldg(p.s.cu + b + 1) : first + 1;
-      const int len = __ldg(p.s.lengths + b);
-      const long long most = (long long)p.s.max_pages << p.c.page_shift;
-      sw.tok0 = max(first, 0);
-      sw.n = max(0, min(min(last - first, p.max_tokens), p.s.n_tokens - sw.tok0));
-      if (sw.n > 0 && len < 0) raise(p.c.status, DEC_ERR_ARG);
-      if (sw.n > 0 && (p.causal ? (long long)len + sw.n : len) > most) raise(p.c.status, DEC_ERR_CAPACITY);
-      sw.len = len < 0 ? -sw.n : (int)min((long long)len, most);
-      // (a unit without positions still writes its rows)
-      const int held = p.causal ? sw.len + sw.n : sw.len;
-      sw.ng = max(1, min(p.s.max_pages << (p.c.page_shift - 4), (held + kGroup - 1) / kGroup));
-      sw.inv = reciprocal(sw.ng + kUnitCost);
-      sw.nrb = (sw.n * p.group + K::ROWS - 1) / K::ROWS;
-      w = (uint32_t)p.c.hkv * sw.nrb * (sw.ng + kUnitCost);
-    }
-    uint32_t x = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) sh_scan[warp] = x;
-    __syncthreads();
-    uint32_t before = base, all = base;
-#pragma unroll
-    for (int i = 0; i < K::WARPS; ++i) {
-      const uint32_t y = sh_scan[i];
-      before += i < warp ? y : 0u;
-      all += y;
-    }
-    if (b < p.s.batch) {
-      sw.pre = before + x - w;
-      seqs[b] = sw;
-    }
-    base = all;
-  }
-  __syncthreads();
-  const uint32_t W = base;
+  const uint32_t W = build_list<K::THREADS, K::ROWS, kGroup, kUnitCost>(p, seqs, sh_scan);
   const int ctas = (int)min((uint32_t)gridDim.x, (W + p.min_groups - 1) / p.min_groups);
   const int cta = blockIdx.x;
   if (tid == 0) p.meta[2 * cta] = make_int4(0, 0, 0, 0);  // (before the barrier that the join's marks come after)
@@ -361,17 +373,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
   const uint32_t lo = clo + (uint32_t)((unsigned long long)(chi - clo) * warp / K::WARPS);
   const uint32_t hi = clo + (uint32_t)((unsigned long long)(chi - clo) * (warp + 1) / K::WARPS);
 
-  // the sequence that entry f of the list belongs to
-  auto seq_at = [&](uint32_t f) {
-    int a = 0, z = p.s.batch;
-    while (z - a > 1) {
-      const int m = (a + z) >> 1;
-      if (seqs[m].pre <= f) a = m;
-      else z = m;
-    }
-    return a;
-  };
-
+  auto seq_at = [&](uint32_t f) { return seq_of_entry(seqs, p.s.batch, f); };
   uint8_t* const ring = smem + warp * K::RING;
 
   // ---- the copies: 32 entries' group indices at a time, one per lane, and each lane copies its own
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
     const bool copies = lane >= at && lane < at + n && vg >= 0;
     const uint32_t who = __ballot_sync(0xffffffffu, copies);
     uint64_t* const bar = bars[warp] + pstage;
-    if (lane == 0) bar_expect(bar, __popc(who) * K::GB);
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(who) * K::GB);
     __syncwarp();
     if (copies)
       bulk_copy(ring + (pstage * CH + lane - at) * K::GB, p.c.pages + (size_t)vg * K::GB, K::GB, bar);
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
             }
             dst[k / 4] = pack8_bf16(x);
           }
-          if (p.lse && g == 0) p.lse[tok * p.hq + head] = (m[nb][i] - kPShift + log2f(l[nb][i])) * 0.6931471805599453f;
+          if (p.lse && g == 0) p.lse[tok * p.hq + head] = (m[nb][i] - kPShift + log2f(l[nb][i])) * kLn2;
         } else {
 #pragma unroll
           for (int k = 0; k < KS; k += 2)
@@ -836,13 +838,13 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
   }
 }
 
-// Units that more than one CTA worked on: warp r of block c joins row r of the unit that CTA c left
+// Units that more than one CTA worked on: warp r of block (c, y) joins row 8 y + r of the unit that CTA c left
 // open with the parts of the CTAs that continued it.
-template <int HD, int NB>
-__global__ void __launch_bounds__(AttnCfg<HD, NB>::ROWS * 32) join_kernel(const AttnParams p) {
-  using K = AttnCfg<HD, NB>;
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(256) join_kernel(const AttnParams p) {
+  constexpr int PART = ROWS * HD + 2 * ROWS;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched before the attention kernel has ended)
-  const int c = blockIdx.x, lane = threadIdx.x & 31, row = threadIdx.x >> 5, ctas = gridDim.x;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5), ctas = gridDim.x;
   if (!p.meta[2 * c].y) return;
   const int4 place = p.meta[2 * c + 1];
   if (place.z + row >= place.w) return;
@@ -860,14 +862,14 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::ROWS * 32) join_kernel(const 
     n += z + (__shfl_sync(0xffffffffu, f, z) & 1);
     break;
   }
-  auto part_of = [&](int i) { return p.parts + ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * K::PART; };
+  auto part_of = [&](int i) { return p.parts + ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * PART; };
   Joined<HD> all;
   all.weigh(-INFINITY, 0.f);
   for (int b = 0; b < n; b += 32) {
     float me = -INFINITY, le = 0.f;
     if (b + lane < n) {
-      me = part_of(b + lane)[K::ROWS * HD + row];
-      le = part_of(b + lane)[K::ROWS * HD + K::ROWS + row];
+      me = part_of(b + lane)[ROWS * HD + row];
+      le = part_of(b + lane)[ROWS * HD + ROWS + row];
     }
     Joined<HD> j;
     j.weigh(me, le);

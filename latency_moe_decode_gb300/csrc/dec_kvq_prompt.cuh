@@ -1,0 +1,482 @@
+// Attention over the paged 4-bit cache for many query rows (prompt chunks).
+//
+// Work that the tensor cores bound: 4 hd flops per (query row, position), each position's codes
+// turned into operands once per 128 query rows. A CTA takes a stretch of (unit, tile of 128
+// positions) entries, a unit being (sequence, KV head, 128 query rows), with a role for each warp:
+//  - one copies the tiles' codes (bulk copies, three tiles ahead);
+//  - eight turn them into f16 in the 128-byte swizzled layout that the MMAs read. A word of codes
+//    gives pairs (i, i + 4), and nothing puts them in order: the queries are staged in the same
+//    order, and the outputs' columns are put right when they are written;
+//  - one thread issues S = Q K^T (128 x 128 x hd, two S buffers in tensor memory) and O += P V
+//    (128 x hd x 128, V read MN-major), the next tile's S before this tile's O;
+//  - four hold one query row a thread: maximum, exponentials, P as f16 into shared memory. The
+//    reference of the exponentials follows the maximum only when that passes it by 2^8 (O lies in
+//    tensor memory, and rescaling it costs as much as the exponentials).
+#pragma once
+#include "dec_kvq_attn.cuh"
+
+namespace dec {
+namespace kvq {
+
+constexpr int kTile = 128;           // positions per tile
+constexpr int kPromptStages = 3;     // tiles of codes in the ring
+constexpr int kPromptCost = 1;       // a unit's fixed cost, in tiles' time
+constexpr float kPromptShift = 7.0f; // P is kept times 2^7 (at most 2^15 with the reference's slack of 2^8)
+
+template <int HD>
+struct PromptCfg {
+  static constexpr int ROWS = 128;
+  static constexpr int THREADS = 14 * 32;  // 4 softmax, 8 decode, MMA, copy
+  static constexpr int HP = HD / 64;       // 64-value parts of a head
+  static constexpr int OPERAND = HP * 16384;
+  static constexpr int RAW = kTile / kGroup * group_bytes(HD);
+  static constexpr int Q = 0, K = OPERAND, V = 3 * OPERAND, P = 4 * OPERAND, RING = P + 32768;
+  static constexpr int TABLE = RING + kPromptStages * RAW;
+  static constexpr int PART = ROWS * HD + 2 * ROWS;
+  static constexpr int smem() { return TABLE + kMaxSeqs * (int)sizeof(SeqWork) + 1024; }
+};
+
+struct PromptBars {
+  uint64_t raw_full[kPromptStages], raw_empty[kPromptStages];
+  uint64_t k_full[2], k_empty[2], v_full, s_full[2], s_empty[2], p_full, pv_done, q_full;
+};
+
+// Instruction descriptor of kind::f16 with f16 A (K-major) and B and an fp32 D of shape M x N; B K-major
+// or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&d)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "f"(d[0]), "f"(d[1]), "f"(d[2]), "f"(d[3]), "f"(d[4]), "f"(d[5]), "f"(d[6]), "f"(d[7]), "f"(d[8]), "f"(d[9]),
+      "f"(d[10]), "f"(d[11]), "f"(d[12]), "f"(d[13]), "f"(d[14]), "f"(d[15]), "f"(d[16]), "f"(d[17]), "f"(d[18]),
+      "f"(d[19]), "f"(d[20]), "f"(d[21]), "f"(d[22]), "f"(d[23]), "f"(d[24]), "f"(d[25]), "f"(d[26]), "f"(d[27]),
+      "f"(d[28]), "f"(d[29]), "f"(d[30]), "f"(d[31])
+      : "memory");
+}
+
+// A CTA's stretch of one unit, as every role walks them.
+struct Stretch {
+  SeqWork sw;
+  uint32_t uid;  // the unit's first entry
+  int h, row0, t0, t1;  // KV head, first query row, tiles [t0, t1) (none where no row sees them)
+  int smin, smax;       // positions that every row, and that some row sees
+  uint32_t next;        // entry to go on from
+  __device__ __forceinline__ bool find(const AttnParams& p, const SeqWork* seqs, uint32_t f, uint32_t end) {
+    for (;;) {
+      if (f >= end) return false;
+      sw = seqs[seq_of_entry(seqs, p.s.batch, f)];
+      const uint32_t per = sw.ng + kPromptCost;
+      const int u = (int)fast_div(f - sw.pre, per, sw.inv);
+      uid = sw.pre + (uint32_t)u * per;
+      if (f >= uid + sw.ng) {  // behind the unit's tiles
+        f = uid + per;
+        continue;
+      }
+      h = over(u, sw.nrb);
+      row0 = (u - h * sw.nrb) * 128;
+      const int last = min(row0 + 128, sw.n * p.group) - 1;
+      smin = max(0, p.causal ? sw.len + (int)fast_div(row0, p.group, p.ginv) + 1 : sw.len);
+      smax = max(0, p.causal ? sw.len + (int)fast_div(last, p.group, p.ginv) + 1 : sw.len);
+      t0 = (int)(f - uid);
+      const uint32_t stop = min(end, uid + sw.ng);
+      t1 = min((int)(stop - uid), (smax + kTile - 1) / kTile);
+      next = stop;
+      return true;
+    }
+  }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const AttnParams p) {
+  using C = PromptCfg<HD>;
+  extern __shared__ uint8_t dyn[];
+  __shared__ PromptBars bars;
+  __shared__ uint32_t sh_scan[C::THREADS / 32], tmem_base;
+  __shared__ int nan_from[HD / kBlock];  // the first position with a NaN run of values, where rows differ in what they see
+  uint8_t* const smem = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+  SeqWork* const seqs = reinterpret_cast<SeqWork*>(smem + C::TABLE);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the join kernel waits for this one's end)
+  if (tid == 0) {
+    for (int i = 0; i < kPromptStages; ++i) {
+      mbar_init(&bars.raw_full[i], 1);
+      mbar_init(&bars.raw_empty[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.k_full[i], 8);
+      mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.s_empty[i], 4);
+    }
+    mbar_init(&bars.v_full, 8);
+    mbar_init(&bars.p_full, 4);
+    mbar_init(&bars.pv_done, 1);
+    mbar_init(&bars.q_full, 4);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) tmem_alloc(&tmem_base, 512);
+  tc_fence_before();
+  const uint32_t W = build_list<C::THREADS, C::ROWS, kTile, kPromptCost>(p, seqs, sh_scan);
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;  // S at columns 0 and 128, O at 256
+  const int cta = blockIdx.x, ctas = (int)min((uint32_t)gridDim.x, W);
+  uint32_t clo = 0, chi = 0;
+  if (cta < ctas) {
+    clo = (uint32_t)((unsigned long long)W * cta / ctas);
+    chi = (uint32_t)((unsigned long long)W * (cta + 1) / ctas);
+  }
+  bool ok = true;  // (false after a wait that ran out: the role stops, and so do the others in time)
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    if (ok && !bar_wait(b, parity)) {
+      ok = false;
+      raise(p.c.status, DEC_ERR_TIMEOUT);
+    }
+    return ok;
+  };
+  Stretch s;
+
+  if (warp == 13) {
+    // ---- copies: lane i the tile's group i
+    int n = 0;
+    for (uint32_t f = clo; ok && s.find(p, seqs, f, chi); f = s.next) {
+      const int b = seq_of_entry(seqs, p.s.batch, f), gpp = 1 << (p.c.page_shift - 4);
+      for (int t = s.t0; t < s.t1 && ok; ++t, ++n) {
+        const int st = n % kPromptStages, pos = t * kTile + lane * kGroup;
+        int gi = -1;
+        if (lane < kTile / kGroup && pos < s.smax) {
+          const int page = pos >> p.c.page_shift < p.s.max_pages ? __ldg(p.s.table + b * p.s.table_stride + (pos >> p.c.page_shift)) : -1;
+          if ((unsigned)page < (unsigned)p.c.n_pages) gi = (page * p.c.hkv + s.h) * gpp + ((pos >> 4) & (gpp - 1));
+          else raise(p.c.status, DEC_ERR_ARG);
+        }
+        if (n >= kPromptStages && !wait(&bars.raw_empty[st], (n / kPromptStages - 1) & 1)) break;
+        const uint32_t who = __ballot_sync(0xffffffffu, gi >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[st], __popc(who) * group_bytes(HD));
+        __syncwarp();
+        if (gi >= 0)
+          bulk_copy(smem + C::RING + st * C::RAW + lane * group_bytes(HD), p.c.pages + (size_t)gi * group_bytes(HD),
+                    group_bytes(HD), &bars.raw_full[st]);
+      }
+    }
+    for (int i = max(0, n - kPromptStages); i < n; ++i) bar_wait(&bars.raw_full[i % kPromptStages], (i / kPromptStages) & 1);
+  } else if (warp == 12) {
+    // ---- products
+    if (lane == 0) {
+      constexpr uint32_t kIdS = idesc_f16_f32(128, 128, false), kIdO = idesc_f16_f32(128, HD, true);
+      int n = 0, seg = 0;  // tiles, stretches so far
+      auto scores = [&](int i) {  // of tile i
+        if (!wait(&bars.k_full[i & 1], (i >> 1) & 1)) return;
+        if (i >= 2 && !wait(&bars.s_empty[i & 1], ((i >> 1) - 1) & 1)) return;
+        tc_fence_after();
+        const uint8_t* k = smem + C::K + (i & 1) * C::OPERAND;
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d) {
+          const int at = (d >> 2) * 16384 + (d & 3) * 32;
+          mma_bf16(tmem + (i & 1) * 128, smem_desc_sw128(smem + C::Q + at, 16, 1024), smem_desc_sw128(k + at, 16, 1024), kIdS,
+                   d > 0 ? 1u : 0u);
+        }
+        mma_commit(&bars.s_full[i & 1]);
+        mma_commit(&bars.k_empty[i & 1]);
+      };
+      for (uint32_t f = clo; ok && s.find(p, seqs, f, chi); f = s.next) {
+        const int tiles = s.t1 - s.t0;
+        if (tiles <= 0) continue;
+        if (!wait(&bars.q_full, seg & 1)) break;
+        ++seg;
+        tc_fence_after();
+        scores(n);
+        for (int i = 0; i < tiles && ok; ++i, ++n) {
+          if (i + 1 < tiles) scores(n + 1);
+          if (!wait(&bars.v_full, n & 1) || !wait(&bars.p_full, n & 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int d = 0; d < kTile / 16; ++d)
+            mma_bf16(tmem + 256, smem_desc_sw128(smem + C::P + (d >> 2) * 16384 + (d & 3) * 32, 16, 1024),
+                     smem_desc_sw128(smem + C::V + d * 2048, 16384, 1024), kIdO, i > 0 || d > 0 ? 1u : 0u);
+          mma_commit(&bars.pv_done);
+        }
+      }
+      if (n > 0) bar_wait(&bars.pv_done, (n - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---- codes to operands: 16 bytes of codes (four words) at a time, in an order that spreads the
+    // 16-byte stores of eight lanes over all banks
+    const int dt = tid - 128;
+    const Magic magic = p.magic;
+    int n = 0, seg = 0;
+    auto put = [&](uint8_t* base, int pos, int j, uint32_t w, const Scale2& sc) {
+      uint32_t a, b, c, d;
+      sc.decode(w, magic, a, b);
+      sc.decode(w >> 8, magic, c, d);
+      *reinterpret_cast<uint4*>(base + (j >> 3) * 16384 + pos * 128 + (((j & 7) ^ (pos & 7)) << 4)) = make_uint4(a, b, c, d);
+    };
+    for (uint32_t f = clo; ok && s.find(p, seqs, f, chi); f = s.next) {
+      for (int t = s.t0; t < s.t1 && ok; ++t, ++n) {
+        const int st = n % kPromptStages;
+        const uint8_t* raw = smem + C::RING + st * C::RAW;
+        if (!wait(&bars.raw_full[st], (n / kPromptStages) & 1)) break;
+        if (n >= 2 && !wait(&bars.k_empty[n & 1], ((n >> 1) - 1) & 1)) break;
+        uint8_t* const k = smem + C::K + (n & 1) * C::OPERAND;
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) {
+          // lane bits: t's low bit, g's two low bits, t's high bit, g's high bit
+          const int x = lane, tq = (x & 1) | ((x >> 3) & 1) << 1, g = ((x >> 1) & 3) | ((x >> 4) & 1) << 2;
+          const int grp = dt >> 5;  // one group a warp
+          const uint8_t* gp = raw + grp * group_bytes(HD);
+          if (HD == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(gp + i * 512 + (g * 4 + tq) * 16);
+            const uint32_t sb = *reinterpret_cast<const uint16_t*>(gp + 2 * code_bytes(HD) + (g * 4 + tq) * 4 + i * 2);
+            const int pos = grp * 16 + g + 8 * i;
+            Scale2 s0, s1;
+            s0.set(__byte_perm(sb, 0, 0x4040));
+            s1.set(__byte_perm(sb, 0, 0x4141));
+            put(k, pos, 4 * tq, u.x, s0);
+            put(k, pos, 4 * tq + 1, u.y, s0);
+            put(k, pos, 4 * tq + 2, u.z, s1);
+            put(k, pos, 4 * tq + 3, u.w, s1);
+          } else {
+            const uint4 u = *reinterpret_cast<const uint4*>(gp + (g * 4 + tq) * 16);
+            const uint32_t sb = *reinterpret_cast<const uint16_t*>(gp + 2 * code_bytes(HD) + (g * 4 + tq) * 2);
+            const int pos = grp * 16 + g;
+            Scale2 s0, s1;
+            s0.set(__byte_perm(sb, 0, 0x4040));
+            s1.set(__byte_perm(sb, 0, 0x4141));
+            put(k, pos, 2 * tq, u.x, s0);
+            put(k, pos, 2 * tq + 1, u.y, s0);
+            put(k, pos + 8, 2 * tq, u.z, s1);
+            put(k, pos + 8, 2 * tq + 1, u.w, s1);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.k_full[n & 1]);
+        if (t == s.t0 && !wait(&bars.q_full, seg++ & 1)) break;  // (the stretch's nan_from is set)
+        if (n >= 1 && !wait(&bars.pv_done, (n - 1) & 1)) break;
+        uint8_t* const v = smem + C::V;
+        const bool edge = (t + 1) * kTile > s.smin;
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) {
+          // lane bits: the run's two low bits, t's low bit, t's high bit, the run's high bit
+          const int x = lane, gv = (x & 3) | ((x >> 4) & 1) << 2, tq = (x >> 2) & 3;
+          const int grp = dt >> 5;
+          const uint8_t* gp = raw + grp * group_bytes(HD) + code_bytes(HD);
+          const uint4 u = *reinterpret_cast<const uint4*>(gp + (HD == 128 ? i * 512 : 0) + (gv * 4 + tq) * 16);
+          const int lo = grp * 16 + 2 * tq;  // the lane's first position
+          uint32_t sb;
+          if (HD == 128) sb = *reinterpret_cast<const uint16_t*>(gp + code_bytes(HD) + scale_bytes(HD) + (gv * 4 + tq) * 4 + i * 2);
+          else sb = *reinterpret_cast<const uint32_t*>(gp + code_bytes(HD) + scale_bytes(HD) + ((gv >> 1) * 4 + tq) * 4);
+          if (edge) {
+            // what no row sees counts nothing (scale 0); a run of NaNs that only some rows see is
+            // noted, and put into their outputs at the end (0 x NaN is NaN: P cannot leave it out)
+#pragma unroll
+            for (int y = 0; y < (HD == 128 ? 2 : 4); ++y) {
+              const int pos = t * kTile + lo + (y & 1) + (HD == 128 ? 8 * i : 8 * (y >> 1));
+              const bool bad = ((sb >> (8 * y)) & 255u) == 255u;
+              if (bad && pos < s.smax) atomicMin(&nan_from[HD == 128 ? gv : gv >> 1], pos);
+              if (bad || pos >= s.smax) sb &= ~(255u << (8 * y));
+            }
+          }
+          Scale2 s0, s1;
+          if (HD == 128) {
+            s0.set(__byte_perm(sb, 0, 0x4040));
+            s1.set(__byte_perm(sb, 0, 0x4141));
+            const int pos = lo + 8 * i, odd = tq & 1;  // (odd t: the second position first)
+            put(v, pos + odd, 2 * gv, odd ? u.z : u.x, odd ? s1 : s0);
+            put(v, pos + odd, 2 * gv + 1, odd ? u.w : u.y, odd ? s1 : s0);
+            put(v, pos + 1 - odd, 2 * gv, odd ? u.x : u.z, odd ? s0 : s1);
+            put(v, pos + 1 - odd, 2 * gv + 1, odd ? u.y : u.w, odd ? s0 : s1);
+          } else {
+            s0.set(__byte_perm(sb, 0, 0x4040));
+            s1.set(__byte_perm(sb, 0, 0x4141));
+            put(v, lo, gv, u.x, s0);
+            put(v, lo + 1, gv, u.y, s1);
+            s0.set(__byte_perm(sb, 0, 0x4242));
+            s1.set(__byte_perm(sb, 0, 0x4343));
+            put(v, lo + 8, gv, u.z, s0);
+            put(v, lo + 9, gv, u.w, s1);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars.v_full);
+          mbar_arrive(&bars.raw_empty[st]);
+        }
+      }
+    }
+  } else {
+    // ---- one query row a thread
+    const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
+    int n = 0;
+    int4 meta = make_int4(0, 0, 0, 0), mplace = make_int4(0, 0, 0, 0);
+    for (uint32_t f = clo; ok && s.find(p, seqs, f, chi); f = s.next) {
+      const int row = s.row0 + tid, rows = s.sw.n * p.group, tj = (int)fast_div(row, p.group, p.ginv);
+      const bool live = row < rows;
+      const long long tok = s.sw.tok0 + tj;
+      const int head = s.h * p.group + row - tj * p.group;
+      const int seen = live ? max(0, p.causal ? s.sw.len + tj + 1 : s.sw.len) : 0;
+      if (tid < HD / kBlock) nan_from[tid] = 0x7FFFFFFF;
+      // queries, scaled by a power of two to magnitude 1 .. 2 (f16 then holds bf16 values down to 2^-17
+      // of the largest exactly), in the order in which a word of codes gives its values
+      float sc;
+      {
+        uint4 u[HD / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.p) + tok * p.q.ts + head * p.q.hs);
+        uint32_t mag = 0;
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) {
+          u[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) mag = max(mag, max((w[y] << 16) & 0x7FFFFFFFu, w[y] & 0x7FFF0000u));
+        }
+        const int e = mag == 0 || mag >= 0x7F800000u ? 0 : min(126, max(-126, (int)(mag >> 23) - 127));
+        const float down = __int_as_float((127 - e) << 23);
+        sc = fmaxf(p.scale * __int_as_float((127 + e) << 23), 1e-37f);
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) {
+          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+          auto val = [&](int y) { return down * __uint_as_float((y & 1) ? w[y >> 1] & 0xFFFF0000u : w[y >> 1] << 16); };
+          uint4 o;
+          o.x = h2u(__floats2half2_rn(val(0), val(4)));
+          o.y = h2u(__floats2half2_rn(val(1), val(5)));
+          o.z = h2u(__floats2half2_rn(val(2), val(6)));
+          o.w = h2u(__floats2half2_rn(val(3), val(7)));
+          *reinterpret_cast<uint4*>(smem + C::Q + (i >> 3) * 16384 + tid * 128 + (((i & 7) ^ (tid & 7)) << 4)) = o;
+        }
+      }
+      const int tiles = s.t1 - s.t0;
+      if (tiles > 0) {
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // (nan_from, too)
+        if (lane == 0) mbar_arrive(&bars.q_full);
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < tiles && ok; ++i, ++n) {
+        const uint32_t ts = tl + (n & 1) * 128;
+        const int pos0 = (s.t0 + i) * kTile;
+        const bool edge = pos0 + kTile > s.smin;
+        if (!wait(&bars.s_full[n & 1], (n >> 1) & 1)) break;
+        tc_fence_after();
+        float x[32], mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(ts + c * 32, x);
+#pragma unroll
+          for (int y = 0; y < 32; ++y) mx = fmaxf(mx, edge && pos0 + c * 32 + y >= seen ? -INFINITY : x[y]);
+        }
+        mx *= sc;
+        const float was = m;
+        if (m == -INFINITY || mx > m + 8.f) m = fmaxf(m, mx);
+        // the products so far are done before their operands, or O, are written again
+        if (n > 0 && !wait(&bars.pv_done, (n - 1) & 1)) break;
+        if (i > 0 && __any_sync(0xffffffffu, m != was)) {
+          const float fo = m == was ? 1.f : was == -INFINITY ? 0.f : ex2(was - m);
+          l *= fo;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) {
+            tmem_ld32(tl + 256 + c * 32, x);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) x[y] *= fo;
+            tmem_st32(tl + 256 + c * 32, x);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        const float z = (m == -INFINITY ? 0.f : m) - kPromptShift;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(ts + c * 32, x);
+#pragma unroll
+          for (int y = 0; y < 32; ++y) {
+            x[y] = ex2(fmaf(x[y], sc, -z));
+            if (edge && pos0 + c * 32 + y >= seen) x[y] = 0.f;
+            l += x[y];
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            uint4 o;
+            o.x = h2u(__floats2half2_rn(x[8 * y], x[8 * y + 1]));
+            o.y = h2u(__floats2half2_rn(x[8 * y + 2], x[8 * y + 3]));
+            o.z = h2u(__floats2half2_rn(x[8 * y + 4], x[8 * y + 5]));
+            o.w = h2u(__floats2half2_rn(x[8 * y + 6], x[8 * y + 7]));
+            const int ch = (c & 1) * 4 + y;
+            *reinterpret_cast<uint4*>(smem + C::P + (c >> 1) * 16384 + tid * 128 + ((ch ^ (tid & 7)) << 4)) = o;
+          }
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars.s_empty[n & 1]);
+          mbar_arrive(&bars.p_full);
+        }
+      }
+      if (!ok) break;
+      // ---- the rows' outputs, or this CTA's part of them
+      if (tiles > 0 && !wait(&bars.pv_done, (n - 1) & 1)) break;
+      tc_fence_after();
+      const uint32_t u1 = s.uid + (uint32_t)s.sw.ng;
+      const bool cont = s.uid < clo, open = u1 > chi;
+      float* const part = p.parts + ((size_t)cta * 2 + (cont ? 0 : 1)) * C::PART;
+      const float inv = l == 0.f ? 0.f : 8.0f / l;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
+        float x[32];
+        if (tiles > 0) {
+          tmem_ld32(tl + 256 + c * 32, x);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) x[y] = 0.f;
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {  // a run of 16 values
+          const bool nan = tiles > 0 && nan_from[2 * c + y] < seen;
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            float o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[(k >> 1) + 4 * (k & 1)] = nan ? NAN : x[16 * y + 8 * z + k];
+            if (live && !cont && !open) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] *= inv;
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + c * 32 + y * 16 + z * 8) =
+                  pack8_bf16(o);
+            } else if (live) {
+              float4* d = reinterpret_cast<float4*>(part + tid * HD + c * 32 + y * 16 + z * 8);
+              d[0] = make_float4(o[0], o[1], o[2], o[3]);
+              d[1] = make_float4(o[4], o[5], o[6], o[7]);
+            }
+          }
+        }
+      }
+      if (live && !cont && !open) {
+        if (p.lse) p.lse[tok * p.hq + head] = (m - kPromptShift + log2f(l)) * kLn2;
+      } else if (live) {
+        part[128 * HD + tid] = m + (kPShift - kPromptShift);  // (the join takes sums as kept times 2^kPShift)
+        part[128 * HD + 128 + tid] = l;
+      }
+      if (cont) meta.x = open ? 1 : 3;
+      else if (open) {
+        meta.y = 1;
+        mplace = make_int4(s.sw.tok0, s.h * p.group, s.row0, rows);
+      }
+      tc_fence_before();
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // (nan_from is set anew)
+    }
+    if (tid == 0) {
+      p.meta[2 * cta] = meta;
+      p.meta[2 * cta + 1] = mplace;
+    }
+  }
+  __syncthreads();
+  if (warp == 12) tmem_free(tmem, 512);
+}
+
+}  // namespace kvq
+}  // namespace dec

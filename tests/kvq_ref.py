@@ -42,9 +42,9 @@ def norm_rotate(x, w, eps, table, pos, interleaved):
     return x
 
 
-def attend(q, k, v, scale, seen):
+def attend(q, k, v, scale, seen, kept=2.0 ** -29):
     """q [hq, hd], k, v [positions, hkv, hd]: out, lse, and per (head, d) what sizes the error bounds:
-    sum_p p |v| + 2^-29 sum_p |v| / sum_p e^(s - max) (out_bounds takes 2^-11 of it) and max over the
+    sum_p p |v| + kept sum_p |v| / sum_p e^(s - max) (out_bounds takes 2^-11 of it) and max over the
     seen positions of scale * sum_d |q k|."""
     hq, hd = q.shape
     out, lse = np.zeros((hq, hd)), np.full(hq, -np.inf)
@@ -59,7 +59,7 @@ def attend(q, k, v, scale, seen):
         e = np.exp(s - m)
         p = e / e.sum()
         out[h], lse[h] = p @ vv, m + np.log(e.sum())
-        mass[h] = p @ np.abs(vv) + 2.0 ** -29 * np.abs(vv).sum(0) / e.sum()
+        mass[h] = p @ np.abs(vv) + kept * np.abs(vv).sum(0) / e.sum()
         big[h] = (np.abs(kk) @ np.abs(q[h])).max() * scale
     return out, lse, mass, big
 
@@ -72,7 +72,9 @@ def out_bounds(out, lse, mass, big, hd, seen):
     over `seen` terms; the output rounds to bf16. Rounding to 11 bits is 2^-11 of a term as long as f16
     has them: terms e^(s - max) are kept times 2^15, and f16's subnormal step is 2^-24, so a term is off
     by half a step, 2^-25 / 2^15 = 2^-40 (of the largest term, 1, before the division by the sum), at
-    least; times |v| and summed that is 2^-11 of `mass`'s second part, 2^-29 sum |v| / sum e^(s - max)."""
+    least; times |v| and summed that is 2^-11 of `mass`'s second part, 2^-29 sum |v| / sum e^(s - max).
+    The kernel for prompts (64 query rows and more) keeps terms times 2^7 and lets the maximum lead its
+    reference by 2^8, so the largest term is kept as 2^7 at least: 2^-25 / 2^7 = 2^-32, kept = 2^-21."""
     d = hd * 2.0 ** -23 * big + 2.0 ** -14 / hd * big * 2.0 ** -9 + 2.0 ** -21 * (big + 1)
     n = 2.0 ** -23 * (np.sqrt(seen) * 8 + 32)
     ob = 2.0 ** -8 * np.abs(out) + mass * (2.0 ** -11 + 2 * d[:, None] + n) + 1e-30

@@ -163,6 +163,13 @@ ATTN = [
     (64, 4, 2, 64, False, [5, 1, 4], [0, 1, 301]),
     (64, 8, 1, 256, True, [9], [250]),
     (64, 3, 3, 32, True, [70], [0]),
+    # more query rows than a stretch of the kernel for prompts, parts of tiles, several CTAs a unit
+    (128, 8, 2, 16, True, [200, 1, 33], [700, 0, 2000]),
+    (128, 4, 1, 64, True, [16], [127]),
+    (128, 4, 4, 32, True, [129, 64], [0, 128]),
+    (64, 8, 2, 64, False, [64, 40, 3], [0, 500, 129]),
+    (64, 2, 1, 16, True, [300], [40]),
+    (128, 16, 1, 256, False, [9, 2], [1, 1000]),
 ]
 
 
@@ -182,7 +189,8 @@ def _check(out, lse, q, k, v, new, lens, causal, scale, hd, first=0):
         held = l + m if causal else l
         for j in range(m):
             seen = l + j + 1 if causal else l
-            o, s, mass, big = ref.attend(q[row], k[at:at + held], v[at:at + held], scale, seen)
+            kept = 2.0 ** (-21 if max(new) * q.shape[1] // k.shape[1] >= 64 else -29)
+            o, s, mass, big = ref.attend(q[row], k[at:at + held], v[at:at + held], scale, seen, kept)
             ob, lb = ref.out_bounds(o, s, mass, big, hd, max(seen, 1))
             assert (np.abs(out[row] - o) <= ob).all(), (row, np.max(np.abs(out[row] - o) / ob))
             if seen <= 0:
