@@ -9,15 +9,20 @@
 //    order, and the outputs' columns are put right when they are written;
 //  - one thread issues S = Q K^T (128 x 128 x hd, two S buffers in tensor memory) and O += P V
 //    (128 x hd x 128, V read MN-major), the next tile's S before this tile's O;
-//  - four hold one query row a thread: maximum, exponentials, P as f16 into shared memory. The
-//    reference of the exponentials follows the maximum only when that passes it by 2^8 (O lies in
-//    tensor memory, and rescaling it costs as much as the exponentials).
+//  - eight hold half a query row a thread: its 64 scores stay in registers from the maximum (joined
+//    with the other half's) through the exponentials to P, f16 in shared memory. The reference of the
+//    exponentials follows the maximum only when that passes it by 2^8 (O lies in tensor memory, and
+//    rescaling it costs as much as the exponentials). With whole rows and two reads of the scores, four
+//    warps took 6.7 k cycles a tile for this; the exponentials' own floor is 1 k.
 #pragma once
 #include "dec_kvq_attn.cuh"
 
 namespace dec {
 namespace kvq {
 
+#ifndef KVQ_DW
+#define KVQ_DW 4
+#endif
 constexpr int kTile = 128;           // positions per tile
 constexpr int kPromptStages = 3;     // tiles of codes in the ring
 constexpr int kPromptCost = 1;       // a unit's fixed cost, in tiles' time
@@ -26,7 +31,8 @@ constexpr float kPromptShift = 7.0f; // P is kept times 2^7 (at most 2^15 with t
 template <int HD>
 struct PromptCfg {
   static constexpr int ROWS = 128;
-  static constexpr int THREADS = 14 * 32;  // 4 softmax, 8 decode, MMA, copy
+  static constexpr int DW = KVQ_DW;                    // warps that decode
+  static constexpr int THREADS = (8 + DW + 2) * 32;  // 8 softmax, DW decode, MMA, copy
   static constexpr int HP = HD / 64;       // 64-value parts of a head
   static constexpr int OPERAND = HP * 16384;
   static constexpr int RAW = kTile / kGroup * group_bytes(HD);
@@ -96,6 +102,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
   extern __shared__ uint8_t dyn[];
   __shared__ PromptBars bars;
   __shared__ uint32_t sh_scan[C::THREADS / 32], tmem_base;
+  __shared__ float xm[2][2][128], xl[2][128];  // rows' maxima and sums, of each half
   __shared__ int nan_from[HD / kBlock];  // the first position with a NaN run of values, where rows differ in what they see
   uint8_t* const smem = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
   SeqWork* const seqs = reinterpret_cast<SeqWork*>(smem + C::TABLE);
@@ -105,21 +112,21 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
   if (tid == 0) {
     for (int i = 0; i < kPromptStages; ++i) {
       mbar_init(&bars.raw_full[i], 1);
-      mbar_init(&bars.raw_empty[i], 8);
+      mbar_init(&bars.raw_empty[i], C::DW);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.k_full[i], 8);
+      mbar_init(&bars.k_full[i], C::DW);
       mbar_init(&bars.k_empty[i], 1);
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.s_empty[i], 4);
+      mbar_init(&bars.s_empty[i], 8);
     }
-    mbar_init(&bars.v_full, 8);
-    mbar_init(&bars.p_full, 4);
+    mbar_init(&bars.v_full, C::DW);
+    mbar_init(&bars.p_full, 8);
     mbar_init(&bars.pv_done, 1);
-    mbar_init(&bars.q_full, 4);
+    mbar_init(&bars.q_full, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) tmem_alloc(&tmem_base, 512);
+  if (warp == 8 + C::DW) tmem_alloc(&tmem_base, 512);
   tc_fence_before();
   const uint32_t W = build_list<C::THREADS, C::ROWS, kTile, kPromptCost>(p, seqs, sh_scan);
   tc_fence_after();
@@ -130,22 +137,21 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
     clo = (uint32_t)((unsigned long long)W * cta / ctas);
     chi = (uint32_t)((unsigned long long)W * (cta + 1) / ctas);
   }
-  bool ok = true;  // (false after a wait that ran out: the role stops, and so do the others in time)
+  bool ok = true;  // (false after a wait that ran out: the thread waits no more and runs to its end)
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (ok && !bar_wait(b, parity)) {
       ok = false;
       raise(p.c.status, DEC_ERR_TIMEOUT);
     }
-    return ok;
   };
   Stretch s;
 
-  if (warp == 13) {
+  if (warp == 9 + C::DW) {
     // ---- copies: lane i the tile's group i
     int n = 0;
-    for (uint32_t f = clo; ok && s.find(p, seqs, f, chi); f = s.next) {
+    for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
       const int b = seq_of_entry(seqs, p.s.batch, f), gpp = 1 << (p.c.page_shift - 4);
-      for (int t = s.t0; t < s.t1 && ok; ++t, ++n) {
+      for (int t = s.t0; t < s.t1; ++t, ++n) {
         const int st = n % kPromptStages, pos = t * kTile + lane * kGroup;
         int gi = -1;
         if (lane < kTile / kGroup && pos < s.smax) {
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
           if ((unsigned)page < (unsigned)p.c.n_pages) gi = (page * p.c.hkv + s.h) * gpp + ((pos >> 4) & (gpp - 1));
           else raise(p.c.status, DEC_ERR_ARG);
         }
-        if (n >= kPromptStages && !wait(&bars.raw_empty[st], (n / kPromptStages - 1) & 1)) break;
+        if (n >= kPromptStages) wait(&bars.raw_empty[st], (n / kPromptStages - 1) & 1);
         const uint32_t who = __ballot_sync(0xffffffffu, gi >= 0);
         if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[st], __popc(who) * group_bytes(HD));
         __syncwarp();
@@ -163,14 +169,14 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
       }
     }
     for (int i = max(0, n - kPromptStages); i < n; ++i) bar_wait(&bars.raw_full[i % kPromptStages], (i / kPromptStages) & 1);
-  } else if (warp == 12) {
+  } else if (warp == 8 + C::DW) {
     // ---- products
     if (lane == 0) {
       constexpr uint32_t kIdS = idesc_f16_f32(128, 128, false), kIdO = idesc_f16_f32(128, HD, true);
       int n = 0, seg = 0;  // tiles, stretches so far
       auto scores = [&](int i) {  // of tile i
-        if (!wait(&bars.k_full[i & 1], (i >> 1) & 1)) return;
-        if (i >= 2 && !wait(&bars.s_empty[i & 1], ((i >> 1) - 1) & 1)) return;
+        wait(&bars.k_full[i & 1], (i >> 1) & 1);
+        if (i >= 2) wait(&bars.s_empty[i & 1], ((i >> 1) - 1) & 1);
         tc_fence_after();
         const uint8_t* k = smem + C::K + (i & 1) * C::OPERAND;
 #pragma unroll
@@ -182,16 +188,17 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         mma_commit(&bars.s_full[i & 1]);
         mma_commit(&bars.k_empty[i & 1]);
       };
-      for (uint32_t f = clo; ok && s.find(p, seqs, f, chi); f = s.next) {
+      for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
         const int tiles = s.t1 - s.t0;
         if (tiles <= 0) continue;
-        if (!wait(&bars.q_full, seg & 1)) break;
+        wait(&bars.q_full, seg & 1);
         ++seg;
         tc_fence_after();
         scores(n);
-        for (int i = 0; i < tiles && ok; ++i, ++n) {
+        for (int i = 0; i < tiles; ++i, ++n) {
           if (i + 1 < tiles) scores(n + 1);
-          if (!wait(&bars.v_full, n & 1) || !wait(&bars.p_full, n & 1)) break;
+          wait(&bars.v_full, n & 1);
+          wait(&bars.p_full, n & 1);
           tc_fence_after();
 #pragma unroll
           for (int d = 0; d < kTile / 16; ++d)
@@ -203,10 +210,10 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
       if (n > 0) bar_wait(&bars.pv_done, (n - 1) & 1);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // ---- codes to operands: 16 bytes of codes (four words) at a time, in an order that spreads the
     // 16-byte stores of eight lanes over all banks
-    const int dt = tid - 128;
+    constexpr int GW = 8 / C::DW;  // groups of a tile a warp
     const Magic magic = p.magic;
     int n = 0, seg = 0;
     auto put = [&](uint8_t* base, int pos, int j, uint32_t w, const Scale2& sc) {
@@ -215,91 +222,100 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
       sc.decode(w >> 8, magic, c, d);
       *reinterpret_cast<uint4*>(base + (j >> 3) * 16384 + pos * 128 + (((j & 7) ^ (pos & 7)) << 4)) = make_uint4(a, b, c, d);
     };
-    for (uint32_t f = clo; ok && s.find(p, seqs, f, chi); f = s.next) {
-      for (int t = s.t0; t < s.t1 && ok; ++t, ++n) {
-        const int st = n % kPromptStages;
-        const uint8_t* raw = smem + C::RING + st * C::RAW;
-        if (!wait(&bars.raw_full[st], (n / kPromptStages) & 1)) break;
-        if (n >= 2 && !wait(&bars.k_empty[n & 1], ((n >> 1) - 1) & 1)) break;
-        uint8_t* const k = smem + C::K + (n & 1) * C::OPERAND;
+    auto keys = [&](int i) {  // of tile i
+      const int st = i % kPromptStages;
+      wait(&bars.raw_full[st], (i / kPromptStages) & 1);
+      if (i >= 2) wait(&bars.k_empty[i & 1], ((i >> 1) - 1) & 1);
+      uint8_t* const k = smem + C::K + (i & 1) * C::OPERAND;
+      // lane bits: t's low bit, g's two low bits, t's high bit, g's high bit
+      const int tq = (lane & 1) | ((lane >> 3) & 1) << 1, g = ((lane >> 1) & 3) | ((lane >> 4) & 1) << 2;
 #pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {
-          // lane bits: t's low bit, g's two low bits, t's high bit, g's high bit
-          const int x = lane, tq = (x & 1) | ((x >> 3) & 1) << 1, g = ((x >> 1) & 3) | ((x >> 4) & 1) << 2;
-          const int grp = dt >> 5;  // one group a warp
-          const uint8_t* gp = raw + grp * group_bytes(HD);
-          if (HD == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(gp + i * 512 + (g * 4 + tq) * 16);
-            const uint32_t sb = *reinterpret_cast<const uint16_t*>(gp + 2 * code_bytes(HD) + (g * 4 + tq) * 4 + i * 2);
-            const int pos = grp * 16 + g + 8 * i;
-            Scale2 s0, s1;
-            s0.set(__byte_perm(sb, 0, 0x4040));
-            s1.set(__byte_perm(sb, 0, 0x4141));
-            put(k, pos, 4 * tq, u.x, s0);
-            put(k, pos, 4 * tq + 1, u.y, s0);
-            put(k, pos, 4 * tq + 2, u.z, s1);
-            put(k, pos, 4 * tq + 3, u.w, s1);
-          } else {
-            const uint4 u = *reinterpret_cast<const uint4*>(gp + (g * 4 + tq) * 16);
-            const uint32_t sb = *reinterpret_cast<const uint16_t*>(gp + 2 * code_bytes(HD) + (g * 4 + tq) * 2);
-            const int pos = grp * 16 + g;
-            Scale2 s0, s1;
-            s0.set(__byte_perm(sb, 0, 0x4040));
-            s1.set(__byte_perm(sb, 0, 0x4141));
-            put(k, pos, 2 * tq, u.x, s0);
-            put(k, pos, 2 * tq + 1, u.y, s0);
-            put(k, pos + 8, 2 * tq, u.z, s1);
-            put(k, pos + 8, 2 * tq + 1, u.w, s1);
+      for (int gw = 0; gw < GW; ++gw) {
+      const int grp = (warp - 8) * GW + gw;
+      const uint8_t* const gp = smem + C::RING + st * C::RAW + grp * group_bytes(HD);
+      uint4 u[HD / 64];
+#pragma unroll
+      for (int y = 0; y < HD / 64; ++y) u[y] = *reinterpret_cast<const uint4*>(gp + y * 512 + (g * 4 + tq) * 16);
+      if (HD == 128) {
+        const uint32_t sb = *reinterpret_cast<const uint32_t*>(gp + 2 * code_bytes(HD) + (g * 4 + tq) * 4);
+#pragma unroll
+        for (int y = 0; y < HD / 64; ++y) {
+          const int pos = grp * 16 + g + 8 * y;
+          Scale2 s0, s1;
+          s0.set(__byte_perm(sb, 0, y ? 0x4242 : 0x4040));
+          s1.set(__byte_perm(sb, 0, y ? 0x4343 : 0x4141));
+          put(k, pos, 4 * tq, u[y].x, s0);
+          put(k, pos, 4 * tq + 1, u[y].y, s0);
+          put(k, pos, 4 * tq + 2, u[y].z, s1);
+          put(k, pos, 4 * tq + 3, u[y].w, s1);
+        }
+      } else {
+        const uint32_t sb = *reinterpret_cast<const uint16_t*>(gp + 2 * code_bytes(HD) + (g * 4 + tq) * 2);
+        const int pos = grp * 16 + g;
+        Scale2 s0, s1;
+        s0.set(__byte_perm(sb, 0, 0x4040));
+        s1.set(__byte_perm(sb, 0, 0x4141));
+        put(k, pos, 2 * tq, u[0].x, s0);
+        put(k, pos, 2 * tq + 1, u[0].y, s0);
+        put(k, pos + 8, 2 * tq, u[0].z, s1);
+        put(k, pos + 8, 2 * tq + 1, u[0].w, s1);
+      }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.k_full[i & 1]);
+    };
+    for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
+      if (s.t0 < s.t1) {
+        keys(n);
+        wait(&bars.q_full, seg++ & 1);  // (the stretch's nan_from is set)
+      }
+      for (int t = s.t0; t < s.t1; ++t, ++n) {
+        const int st = n % kPromptStages;
+        if (t + 1 < s.t1) keys(n + 1);  // (the next tile's scores wait for nothing else)
+        uint8_t* const v = smem + C::V;
+        // lane bits: the run's two low bits, t's low bit, t's high bit, the run's high bit
+        const int gv = (lane & 3) | ((lane >> 4) & 1) << 2, tq = (lane >> 2) & 3;
+        if (n >= 1) wait(&bars.pv_done, (n - 1) & 1);
+#pragma unroll
+        for (int gw = 0; gw < GW; ++gw) {
+        const int grp = (warp - 8) * GW + gw;
+        const uint8_t* const gp = smem + C::RING + st * C::RAW + grp * group_bytes(HD) + code_bytes(HD);
+        const int lo = grp * 16 + 2 * tq;  // the lane's first position
+        uint4 u[HD / 64];
+#pragma unroll
+        for (int y = 0; y < HD / 64; ++y) u[y] = *reinterpret_cast<const uint4*>(gp + y * 512 + (gv * 4 + tq) * 16);
+        // scales of positions lo, lo + 1, lo + 8, lo + 9
+        uint32_t sb = *reinterpret_cast<const uint32_t*>(gp + code_bytes(HD) + scale_bytes(HD) +
+                                                         ((HD == 128 ? gv : gv >> 1) * 4 + tq) * 4);
+        if ((t + 1) * kTile > s.smin) {
+          // what no row sees counts nothing (scale 0); a run of NaNs that only some rows see is noted,
+          // and put into their outputs at the end (0 x NaN is NaN: P cannot leave it out)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int pos = t * kTile + lo + (y & 1) + 8 * (y >> 1);
+            const bool bad = ((sb >> (8 * y)) & 255u) == 255u;
+            if (bad && pos < s.smax) atomicMin(&nan_from[HD == 128 ? gv : gv >> 1], pos);
+            if (bad || pos >= s.smax) sb &= ~(255u << (8 * y));
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.k_full[n & 1]);
-        if (t == s.t0 && !wait(&bars.q_full, seg++ & 1)) break;  // (the stretch's nan_from is set)
-        if (n >= 1 && !wait(&bars.pv_done, (n - 1) & 1)) break;
-        uint8_t* const v = smem + C::V;
-        const bool edge = (t + 1) * kTile > s.smin;
 #pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {
-          // lane bits: the run's two low bits, t's low bit, t's high bit, the run's high bit
-          const int x = lane, gv = (x & 3) | ((x >> 4) & 1) << 2, tq = (x >> 2) & 3;
-          const int grp = dt >> 5;
-          const uint8_t* gp = raw + grp * group_bytes(HD) + code_bytes(HD);
-          const uint4 u = *reinterpret_cast<const uint4*>(gp + (HD == 128 ? i * 512 : 0) + (gv * 4 + tq) * 16);
-          const int lo = grp * 16 + 2 * tq;  // the lane's first position
-          uint32_t sb;
-          if (HD == 128) sb = *reinterpret_cast<const uint16_t*>(gp + code_bytes(HD) + scale_bytes(HD) + (gv * 4 + tq) * 4 + i * 2);
-          else sb = *reinterpret_cast<const uint32_t*>(gp + code_bytes(HD) + scale_bytes(HD) + ((gv >> 1) * 4 + tq) * 4);
-          if (edge) {
-            // what no row sees counts nothing (scale 0); a run of NaNs that only some rows see is
-            // noted, and put into their outputs at the end (0 x NaN is NaN: P cannot leave it out)
-#pragma unroll
-            for (int y = 0; y < (HD == 128 ? 2 : 4); ++y) {
-              const int pos = t * kTile + lo + (y & 1) + (HD == 128 ? 8 * i : 8 * (y >> 1));
-              const bool bad = ((sb >> (8 * y)) & 255u) == 255u;
-              if (bad && pos < s.smax) atomicMin(&nan_from[HD == 128 ? gv : gv >> 1], pos);
-              if (bad || pos >= s.smax) sb &= ~(255u << (8 * y));
-            }
-          }
+        for (int y = 0; y < 2; ++y) {
           Scale2 s0, s1;
+          s0.set(__byte_perm(sb, 0, y ? 0x4242 : 0x4040));
+          s1.set(__byte_perm(sb, 0, y ? 0x4343 : 0x4141));
           if (HD == 128) {
-            s0.set(__byte_perm(sb, 0, 0x4040));
-            s1.set(__byte_perm(sb, 0, 0x4141));
-            const int pos = lo + 8 * i, odd = tq & 1;  // (odd t: the second position first)
-            put(v, pos + odd, 2 * gv, odd ? u.z : u.x, odd ? s1 : s0);
-            put(v, pos + odd, 2 * gv + 1, odd ? u.w : u.y, odd ? s1 : s0);
-            put(v, pos + 1 - odd, 2 * gv, odd ? u.x : u.z, odd ? s0 : s1);
-            put(v, pos + 1 - odd, 2 * gv + 1, odd ? u.y : u.w, odd ? s0 : s1);
+            const uint4 x = u[y % (HD / 64)];
+            const int pos = lo + 8 * y, odd = tq & 1;  // (odd t: the second position first)
+            put(v, pos + odd, 2 * gv, odd ? x.z : x.x, odd ? s1 : s0);
+            put(v, pos + odd, 2 * gv + 1, odd ? x.w : x.y, odd ? s1 : s0);
+            put(v, pos + 1 - odd, 2 * gv, odd ? x.x : x.z, odd ? s0 : s1);
+            put(v, pos + 1 - odd, 2 * gv + 1, odd ? x.y : x.w, odd ? s0 : s1);
           } else {
-            s0.set(__byte_perm(sb, 0, 0x4040));
-            s1.set(__byte_perm(sb, 0, 0x4141));
-            put(v, lo, gv, u.x, s0);
-            put(v, lo + 1, gv, u.y, s1);
-            s0.set(__byte_perm(sb, 0, 0x4242));
-            s1.set(__byte_perm(sb, 0, 0x4343));
-            put(v, lo + 8, gv, u.z, s0);
-            put(v, lo + 9, gv, u.w, s1);
+            put(v, lo + 8 * y, gv, y ? u[0].z : u[0].x, s0);
+            put(v, lo + 8 * y + 1, gv, y ? u[0].w : u[0].y, s1);
           }
+        }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -310,12 +326,15 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
       }
     }
   } else {
-    // ---- one query row a thread
-    const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
+    // ---- half a query row a thread: columns 64 half .. + 63 of S, HD / 2 half .. of O
+    const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16), to = tl + 256 + half * (HD / 2);
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory"); };  // (both halves' warps)
+    auto all_sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     int n = 0;
     int4 meta = make_int4(0, 0, 0, 0), mplace = make_int4(0, 0, 0, 0);
-    for (uint32_t f = clo; ok && s.find(p, seqs, f, chi); f = s.next) {
-      const int row = s.row0 + tid, rows = s.sw.n * p.group, tj = (int)fast_div(row, p.group, p.ginv);
+    for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
+      const int row = s.row0 + r, rows = s.sw.n * p.group, tj = (int)fast_div(row, p.group, p.ginv);
       const bool live = row < rows;
       const long long tok = s.sw.tok0 + tj;
       const int head = s.h * p.group + row - tj * p.group;
@@ -325,141 +344,151 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
       // of the largest exactly), in the order in which a word of codes gives its values
       float sc;
       {
-        uint4 u[HD / 8];
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.p) + tok * p.q.ts + head * p.q.hs);
+        uint4 u[HD / 16];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.p) + tok * p.q.ts + head * p.q.hs) +
+                           half * (HD / 16);
         uint32_t mag = 0;
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
-          u[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < HD / 16; ++i) u[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) {
           const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
           for (int y = 0; y < 4; ++y) mag = max(mag, max((w[y] << 16) & 0x7FFFFFFFu, w[y] & 0x7FFF0000u));
         }
+        xm[0][half][r] = __uint_as_float(mag);
+        pair_sync();
+        mag = max(mag, __float_as_uint(xm[0][half ^ 1][r]));
         const int e = mag == 0 || mag >= 0x7F800000u ? 0 : min(126, max(-126, (int)(mag >> 23) - 127));
         const float down = __int_as_float((127 - e) << 23);
         sc = fmaxf(p.scale * __int_as_float((127 + e) << 23), 1e-37f);
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
+        for (int i = 0; i < HD / 16; ++i) {
           const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
           auto val = [&](int y) { return down * __uint_as_float((y & 1) ? w[y >> 1] & 0xFFFF0000u : w[y >> 1] << 16); };
-          uint4 o;
-          o.x = h2u(__floats2half2_rn(val(0), val(4)));
-          o.y = h2u(__floats2half2_rn(val(1), val(5)));
-          o.z = h2u(__floats2half2_rn(val(2), val(6)));
-          o.w = h2u(__floats2half2_rn(val(3), val(7)));
-          *reinterpret_cast<uint4*>(smem + C::Q + (i >> 3) * 16384 + tid * 128 + (((i & 7) ^ (tid & 7)) << 4)) = o;
+          const int ch = half * (HD / 16) + i;
+          *reinterpret_cast<uint4*>(smem + C::Q + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+              make_uint4(h2u(__floats2half2_rn(val(0), val(4))), h2u(__floats2half2_rn(val(1), val(5))),
+                         h2u(__floats2half2_rn(val(2), val(6))), h2u(__floats2half2_rn(val(3), val(7))));
         }
       }
       const int tiles = s.t1 - s.t0;
-      if (tiles > 0) {
-        fence_proxy_async_smem();
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // (nan_from, too)
-        if (lane == 0) mbar_arrive(&bars.q_full);
-      }
+      fence_proxy_async_smem();
+      all_sync();  // (nan_from, and xm before the first tile's maxima)
+      if (tiles > 0 && lane == 0) mbar_arrive(&bars.q_full);
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < tiles && ok; ++i, ++n) {
-        const uint32_t ts = tl + (n & 1) * 128;
-        const int pos0 = (s.t0 + i) * kTile;
-        const bool edge = pos0 + kTile > s.smin;
-        if (!wait(&bars.s_full[n & 1], (n >> 1) & 1)) break;
+      for (int i = 0; i < tiles; ++i, ++n) {
+        const uint32_t ts = tl + (n & 1) * 128 + half * 64;
+        const int pos0 = (s.t0 + i) * kTile + half * 64;
+        wait(&bars.s_full[n & 1], (n >> 1) & 1);
         tc_fence_after();
-        float x[32], mx = -INFINITY;
+        float x[2][32];
+        tmem_ld32(ts, x[0]);
+        tmem_ld32(ts + 32, x[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.s_empty[n & 1]);
+        if ((s.t0 + i + 1) * kTile > s.smin) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(ts + c * 32, x);
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int y = 0; y < 32; ++y) mx = fmaxf(mx, edge && pos0 + c * 32 + y >= seen ? -INFINITY : x[y]);
+            for (int y = 0; y < 32; ++y)
+              if (pos0 + c * 32 + y >= seen) x[c][y] = -INFINITY;
         }
-        mx *= sc;
+        float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+        for (int y = 0; y < 32; y += 2) {
+          mx = fmaxf(mx, fmaxf(x[0][y], x[0][y + 1]));
+          my = fmaxf(my, fmaxf(x[1][y], x[1][y + 1]));
+        }
+        mx = fmaxf(mx, my);
+        xm[n & 1][half][r] = mx;
+        pair_sync();
+        mx = fmaxf(mx, xm[n & 1][half ^ 1][r]) * sc;
         const float was = m;
         if (m == -INFINITY || mx > m + 8.f) m = fmaxf(m, mx);
+        const float z = (m == -INFINITY ? 0.f : m) - kPromptShift;
+        uint32_t ph[32];
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) {
+            const float a = ex2(fmaf(x[c][y], sc, -z)), b = ex2(fmaf(x[c][y + 1], sc, -z));
+            l0 += a;
+            l1 += b;
+            ph[c * 16 + y / 2] = h2u(__floats2half2_rn(a, b));
+          }
         // the products so far are done before their operands, or O, are written again
-        if (n > 0 && !wait(&bars.pv_done, (n - 1) & 1)) break;
+        if (n > 0) wait(&bars.pv_done, (n - 1) & 1);
         if (i > 0 && __any_sync(0xffffffffu, m != was)) {
           const float fo = m == was ? 1.f : was == -INFINITY ? 0.f : ex2(was - m);
           l *= fo;
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < HD / 32; ++c) {
-            tmem_ld32(tl + 256 + c * 32, x);
+          for (int c = 0; c < HD / 64; ++c) {
+            float o[32];
+            tmem_ld32(to + c * 32, o);
 #pragma unroll
-            for (int y = 0; y < 32; ++y) x[y] *= fo;
-            tmem_st32(tl + 256 + c * 32, x);
+            for (int y = 0; y < 32; ++y) o[y] *= fo;
+            tmem_st32(to + c * 32, o);
           }
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
         }
-        const float z = (m == -INFINITY ? 0.f : m) - kPromptShift;
+        l += l0 + l1;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(ts + c * 32, x);
-#pragma unroll
-          for (int y = 0; y < 32; ++y) {
-            x[y] = ex2(fmaf(x[y], sc, -z));
-            if (edge && pos0 + c * 32 + y >= seen) x[y] = 0.f;
-            l += x[y];
-          }
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            uint4 o;
-            o.x = h2u(__floats2half2_rn(x[8 * y], x[8 * y + 1]));
-            o.y = h2u(__floats2half2_rn(x[8 * y + 2], x[8 * y + 3]));
-            o.z = h2u(__floats2half2_rn(x[8 * y + 4], x[8 * y + 5]));
-            o.w = h2u(__floats2half2_rn(x[8 * y + 6], x[8 * y + 7]));
-            const int ch = (c & 1) * 4 + y;
-            *reinterpret_cast<uint4*>(smem + C::P + (c >> 1) * 16384 + tid * 128 + ((ch ^ (tid & 7)) << 4)) = o;
-          }
-        }
-        tc_fence_before();
+        for (int y = 0; y < 8; ++y)
+          *reinterpret_cast<uint4*>(smem + C::P + half * 16384 + r * 128 + ((y ^ (r & 7)) << 4)) =
+              make_uint4(ph[4 * y], ph[4 * y + 1], ph[4 * y + 2], ph[4 * y + 3]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars.s_empty[n & 1]);
-          mbar_arrive(&bars.p_full);
-        }
+        if (lane == 0) mbar_arrive(&bars.p_full);
       }
-      if (!ok) break;
       // ---- the rows' outputs, or this CTA's part of them
-      if (tiles > 0 && !wait(&bars.pv_done, (n - 1) & 1)) break;
+      if (tiles > 0) wait(&bars.pv_done, (n - 1) & 1);
       tc_fence_after();
+      xl[half][r] = l;
+      pair_sync();
+      l += xl[half ^ 1][r];
       const uint32_t u1 = s.uid + (uint32_t)s.sw.ng;
       const bool cont = s.uid < clo, open = u1 > chi;
       float* const part = p.parts + ((size_t)cta * 2 + (cont ? 0 : 1)) * C::PART;
       const float inv = l == 0.f ? 0.f : 8.0f / l;
 #pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
+      for (int c = 0; c < HD / 64; ++c) {
         float x[32];
         if (tiles > 0) {
-          tmem_ld32(tl + 256 + c * 32, x);
+          tmem_ld32(to + c * 32, x);
         } else {
 #pragma unroll
           for (int y = 0; y < 32; ++y) x[y] = 0.f;
         }
+        const int col = half * (HD / 2) + c * 32;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {  // a run of 16 values
-          const bool nan = tiles > 0 && nan_from[2 * c + y] < seen;
+        for (int y = 0; y < 4; ++y) {
+          const bool nan = tiles > 0 && nan_from[(col >> 4) + (y >> 1)] < seen;  // (a run of 16 values)
+          float o[8];
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            float o[8];
+          for (int k = 0; k < 8; ++k) o[(k >> 1) + 4 * (k & 1)] = nan ? NAN : x[8 * y + k];
+          if (live && !cont && !open) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[(k >> 1) + 4 * (k & 1)] = nan ? NAN : x[16 * y + 8 * z + k];
-            if (live && !cont && !open) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] *= inv;
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + c * 32 + y * 16 + z * 8) =
-                  pack8_bf16(o);
-            } else if (live) {
-              float4* d = reinterpret_cast<float4*>(part + tid * HD + c * 32 + y * 16 + z * 8);
-              d[0] = make_float4(o[0], o[1], o[2], o[3]);
-              d[1] = make_float4(o[4], o[5], o[6], o[7]);
-            }
+            for (int k = 0; k < 8; ++k) o[k] *= inv;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o.p) + tok * p.o.ts + head * p.o.hs + col + y * 8) = pack8_bf16(o);
+          } else if (live) {
+            float4* d = reinterpret_cast<float4*>(part + r * HD + col + y * 8);
+            d[0] = make_float4(o[0], o[1], o[2], o[3]);
+            d[1] = make_float4(o[4], o[5], o[6], o[7]);
           }
         }
       }
-      if (live && !cont && !open) {
-        if (p.lse) p.lse[tok * p.hq + head] = (m - kPromptShift + log2f(l)) * kLn2;
-      } else if (live) {
-        part[128 * HD + tid] = m + (kPShift - kPromptShift);  // (the join takes sums as kept times 2^kPShift)
-        part[128 * HD + 128 + tid] = l;
+      if (half == 0 && live) {
+        if (!cont && !open) {
+          if (p.lse) p.lse[tok * p.hq + head] = (m - kPromptShift + log2f(l)) * kLn2;
+        } else {
+          part[128 * HD + r] = m + (kPShift - kPromptShift);  // (the join takes sums as kept times 2^kPShift)
+          part[128 * HD + 128 + r] = l;
+        }
       }
       if (cont) meta.x = open ? 1 : 3;
       else if (open) {
@@ -467,7 +496,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         mplace = make_int4(s.sw.tok0, s.h * p.group, s.row0, rows);
       }
       tc_fence_before();
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // (nan_from is set anew)
+      all_sync();  // (nan_from is set anew)
     }
     if (tid == 0) {
       p.meta[2 * cta] = meta;
@@ -475,7 +504,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
     }
   }
   __syncthreads();
-  if (warp == 12) tmem_free(tmem, 512);
+  if (warp == 8 + C::DW) tmem_free(tmem, 512);
 }
 
 }  // namespace kvq
