@@ -3,14 +3,16 @@
 // Work that the tensor cores bound: 4 hd flops per (query row, position), each position's codes
 // turned into operands once per 128 query rows. A CTA takes a stretch of (unit, tile of 128
 // positions) entries, a unit being (sequence, KV head, 128 query rows), with a role for each warp:
-//  - one copies the tiles' codes (bulk copies, three tiles ahead);
-//  - eight turn them into f16 in the 128-byte swizzled layout that the MMAs read. A word of codes
+//  - one copies the tiles' codes (bulk copies, four tiles ahead);
+//  - four turn them into f16 in the 128-byte swizzled layout that the MMAs read. A word of codes
 //    gives pairs (i, i + 4), and nothing puts them in order: the queries are staged in the same
 //    order, and the outputs' columns are put right when they are written;
 //  - one thread issues S = Q K^T (128 x 128 x hd, two S buffers in tensor memory) and O += P V
-//    (128 x hd x 128, V read MN-major), the next tile's S before this tile's O;
+//    (128 x hd x 128, V read MN-major), the next tile's S before this tile's O. Q and P are A operands
+//    in tensor memory: shared memory then carries the codes, K and V only (with all four there its
+//    bandwidth held a tile to 2.9 k cycles);
 //  - eight hold half a query row a thread: its 64 scores stay in registers from the maximum (joined
-//    with the other half's) through the exponentials to P, f16 in shared memory. The reference of the
+//    with the other half's) through the exponentials to P, f16 in tensor memory. The reference of the
 //    exponentials follows the maximum only when that passes it by 2^8 (O lies in tensor memory, and
 //    rescaling it costs as much as the exponentials). With whole rows and two reads of the scores, four
 //    warps took 6.7 k cycles a tile for this; the exponentials' own floor is 1 k.
@@ -20,23 +22,23 @@
 namespace dec {
 namespace kvq {
 
-#ifndef KVQ_DW
-#define KVQ_DW 4
-#endif
 constexpr int kTile = 128;           // positions per tile
-constexpr int kPromptStages = 3;     // tiles of codes in the ring
+constexpr int kPromptStages = 4;     // tiles of codes in the ring
 constexpr int kPromptCost = 1;       // a unit's fixed cost, in tiles' time
+constexpr int kSplitCost = 8;
 constexpr float kPromptShift = 7.0f; // P is kept times 2^7 (at most 2^15 with the reference's slack of 2^8)
 
 template <int HD>
 struct PromptCfg {
   static constexpr int ROWS = 128;
-  static constexpr int DW = KVQ_DW;                    // warps that decode
+  static constexpr int DW = 4;                         // warps that decode
   static constexpr int THREADS = (8 + DW + 2) * 32;  // 8 softmax, DW decode, MMA, copy
   static constexpr int HP = HD / 64;       // 64-value parts of a head
   static constexpr int OPERAND = HP * 16384;
   static constexpr int RAW = kTile / kGroup * group_bytes(HD);
-  static constexpr int Q = 0, K = OPERAND, V = 3 * OPERAND, P = 4 * OPERAND, RING = P + 32768;
+  static constexpr int K = 0, V = 2 * OPERAND, RING = 4 * OPERAND;
+  // tensor memory columns: two S, O, Q and P (two f16 a column)
+  static constexpr int TS = 0, TO = 256, TQ = 384, TP = 448;
   static constexpr int TABLE = RING + kPromptStages * RAW;
   static constexpr int PART = ROWS * HD + 2 * ROWS;
   static constexpr int smem() { return TABLE + kMaxSeqs * (int)sizeof(SeqWork) + 1024; }
@@ -44,7 +46,7 @@ struct PromptCfg {
 
 struct PromptBars {
   uint64_t raw_full[kPromptStages], raw_empty[kPromptStages];
-  uint64_t k_full[2], k_empty[2], v_full, s_full[2], s_empty[2], p_full, pv_done, q_full;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full, pv_done, q_full;
 };
 
 // Instruction descriptor of kind::f16 with f16 A (K-major) and B and an fp32 D of shape M x N; B K-major
@@ -64,17 +66,39 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&d)[32]) 
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* d) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+          taddr),
+      "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]), "r"(d[4]), "r"(d[5]), "r"(d[6]), "r"(d[7]), "r"(d[8]), "r"(d[9]),
+      "r"(d[10]), "r"(d[11]), "r"(d[12]), "r"(d[13]), "r"(d[14]), "r"(d[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B^T for one K = 16 slice of f16 operands: row r of A in lane r, two values a
+// column.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // A CTA's stretch of one unit, as every role walks them.
 struct Stretch {
   SeqWork sw;
   uint32_t uid;  // the unit's first entry
-  int h, row0, t0, t1;  // KV head, first query row, tiles [t0, t1) (none where no row sees them)
+  int b, h, row0, t0, t1;  // sequence, KV head, first query row, tiles [t0, t1) (none where no row sees them)
   int smin, smax;       // positions that every row, and that some row sees
   uint32_t next;        // entry to go on from
   __device__ __forceinline__ bool find(const AttnParams& p, const SeqWork* seqs, uint32_t f, uint32_t end) {
     for (;;) {
       if (f >= end) return false;
-      sw = seqs[seq_of_entry(seqs, p.s.batch, f)];
+      b = seq_of_entry(seqs, p.s.batch, f);
+      sw = seqs[b];
       const uint32_t per = sw.ng + kPromptCost;
       const int u = (int)fast_div(f - sw.pre, per, sw.inv);
       uid = sw.pre + (uint32_t)u * per;
@@ -117,10 +141,11 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.k_full[i], C::DW);
       mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_full[i], C::DW);
+      mbar_init(&bars.v_empty[i], 1);
       mbar_init(&bars.s_full[i], 1);
       mbar_init(&bars.s_empty[i], 8);
     }
-    mbar_init(&bars.v_full, C::DW);
     mbar_init(&bars.p_full, 8);
     mbar_init(&bars.pv_done, 1);
     mbar_init(&bars.q_full, 8);
@@ -128,10 +153,21 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
   }
   if (warp == 8 + C::DW) tmem_alloc(&tmem_base, 512);
   tc_fence_before();
+  __shared__ uint32_t units, longest;
+  if (tid == 0) units = longest = 0;
   const uint32_t W = build_list<C::THREADS, C::ROWS, kTile, kPromptCost>(p, seqs, sh_scan);
+  for (int b = tid; b < p.s.batch; b += C::THREADS) {
+    if (seqs[b].nrb == 0) continue;
+    atomicAdd(&units, (uint32_t)p.c.hkv * seqs[b].nrb);
+    atomicMax(&longest, (uint32_t)seqs[b].ng + kPromptCost);
+  }
+  __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base;  // S at columns 0 and 128, O at 256
-  const int cta = blockIdx.x, ctas = (int)min((uint32_t)gridDim.x, W);
+  const uint32_t tmem = tmem_base;
+  // A CTA a unit where that takes no longer than an even cut, whose parts have to be written and joined
+  // (about kSplitCost tiles' time); with units of one length the cut then falls between them.
+  const int cta = blockIdx.x;
+  const int ctas = (int)(units <= gridDim.x && longest <= W / gridDim.x + kSplitCost ? units : min((uint32_t)gridDim.x, W));
   uint32_t clo = 0, chi = 0;
   if (cta < ctas) {
     clo = (uint32_t)((unsigned long long)W * cta / ctas);
@@ -150,12 +186,12 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
     // ---- copies: lane i the tile's group i
     int n = 0;
     for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
-      const int b = seq_of_entry(seqs, p.s.batch, f), gpp = 1 << (p.c.page_shift - 4);
+      const int gpp = 1 << (p.c.page_shift - 4);
       for (int t = s.t0; t < s.t1; ++t, ++n) {
         const int st = n % kPromptStages, pos = t * kTile + lane * kGroup;
         int gi = -1;
         if (lane < kTile / kGroup && pos < s.smax) {
-          const int page = pos >> p.c.page_shift < p.s.max_pages ? __ldg(p.s.table + b * p.s.table_stride + (pos >> p.c.page_shift)) : -1;
+          const int page = pos >> p.c.page_shift < p.s.max_pages ? __ldg(p.s.table + s.b * p.s.table_stride + (pos >> p.c.page_shift)) : -1;
           if ((unsigned)page < (unsigned)p.c.n_pages) gi = (page * p.c.hkv + s.h) * gpp + ((pos >> 4) & (gpp - 1));
           else raise(p.c.status, DEC_ERR_ARG);
         }
@@ -182,8 +218,8 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
 #pragma unroll
         for (int d = 0; d < HD / 16; ++d) {
           const int at = (d >> 2) * 16384 + (d & 3) * 32;
-          mma_bf16(tmem + (i & 1) * 128, smem_desc_sw128(smem + C::Q + at, 16, 1024), smem_desc_sw128(k + at, 16, 1024), kIdS,
-                   d > 0 ? 1u : 0u);
+          mma_f16_ts(tmem + C::TS + (i & 1) * 128, tmem + C::TQ + d * 8, smem_desc_sw128(k + at, 16, 1024), kIdS,
+                     d > 0 ? 1u : 0u);
         }
         mma_commit(&bars.s_full[i & 1]);
         mma_commit(&bars.k_empty[i & 1]);
@@ -197,14 +233,16 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         scores(n);
         for (int i = 0; i < tiles; ++i, ++n) {
           if (i + 1 < tiles) scores(n + 1);
-          wait(&bars.v_full, n & 1);
+          wait(&bars.v_full[n & 1], (n >> 1) & 1);
           wait(&bars.p_full, n & 1);
           tc_fence_after();
 #pragma unroll
           for (int d = 0; d < kTile / 16; ++d)
-            mma_bf16(tmem + 256, smem_desc_sw128(smem + C::P + (d >> 2) * 16384 + (d & 3) * 32, 16, 1024),
-                     smem_desc_sw128(smem + C::V + d * 2048, 16384, 1024), kIdO, i > 0 || d > 0 ? 1u : 0u);
+            mma_f16_ts(tmem + C::TO, tmem + C::TP + d * 8,
+                       smem_desc_sw128(smem + C::V + (n & 1) * C::OPERAND + d * 2048, 16384, 1024), kIdO,
+                       i > 0 || d > 0 ? 1u : 0u);
           mma_commit(&bars.pv_done);
+          mma_commit(&bars.v_empty[n & 1]);
         }
       }
       if (n > 0) bar_wait(&bars.pv_done, (n - 1) & 1);
@@ -273,10 +311,10 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
       for (int t = s.t0; t < s.t1; ++t, ++n) {
         const int st = n % kPromptStages;
         if (t + 1 < s.t1) keys(n + 1);  // (the next tile's scores wait for nothing else)
-        uint8_t* const v = smem + C::V;
+        uint8_t* const v = smem + C::V + (n & 1) * C::OPERAND;
         // lane bits: the run's two low bits, t's low bit, t's high bit, the run's high bit
         const int gv = (lane & 3) | ((lane >> 4) & 1) << 2, tq = (lane >> 2) & 3;
-        if (n >= 1) wait(&bars.pv_done, (n - 1) & 1);
+        if (n >= 2) wait(&bars.v_empty[n & 1], ((n >> 1) - 1) & 1);
 #pragma unroll
         for (int gw = 0; gw < GW; ++gw) {
         const int grp = (warp - 8) * GW + gw;
@@ -320,7 +358,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bars.v_full);
+          mbar_arrive(&bars.v_full[n & 1]);
           mbar_arrive(&bars.raw_empty[st]);
         }
       }
@@ -328,7 +366,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
   } else {
     // ---- half a query row a thread: columns 64 half .. + 63 of S, HD / 2 half .. of O
     const int half = warp >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16), to = tl + 256 + half * (HD / 2);
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16), to = tl + C::TO + half * (HD / 2);
     auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3)) : "memory"); };  // (both halves' warps)
     auto all_sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     int n = 0;
@@ -362,23 +400,25 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         const int e = mag == 0 || mag >= 0x7F800000u ? 0 : min(126, max(-126, (int)(mag >> 23) - 127));
         const float down = __int_as_float((127 - e) << 23);
         sc = fmaxf(p.scale * __int_as_float((127 + e) << 23), 1e-37f);
+        uint32_t qh[HD / 4];
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i) {
           const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
           auto val = [&](int y) { return down * __uint_as_float((y & 1) ? w[y >> 1] & 0xFFFF0000u : w[y >> 1] << 16); };
-          const int ch = half * (HD / 16) + i;
-          *reinterpret_cast<uint4*>(smem + C::Q + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
-              make_uint4(h2u(__floats2half2_rn(val(0), val(4))), h2u(__floats2half2_rn(val(1), val(5))),
-                         h2u(__floats2half2_rn(val(2), val(6))), h2u(__floats2half2_rn(val(3), val(7))));
+#pragma unroll
+          for (int y = 0; y < 4; ++y) qh[4 * i + y] = h2u(__floats2half2_rn(val(y), val(y + 4)));
         }
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) tmem_st16(tl + C::TQ + half * (HD / 4) + 16 * i, qh + 16 * i);
+        tmem_st_wait();
+        tc_fence_before();
       }
       const int tiles = s.t1 - s.t0;
-      fence_proxy_async_smem();
       all_sync();  // (nan_from, and xm before the first tile's maxima)
       if (tiles > 0 && lane == 0) mbar_arrive(&bars.q_full);
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < tiles; ++i, ++n) {
-        const uint32_t ts = tl + (n & 1) * 128 + half * 64;
+        const uint32_t ts = tl + C::TS + (n & 1) * 128 + half * 64;
         const int pos0 = (s.t0 + i) * kTile + half * 64;
         wait(&bars.s_full[n & 1], (n >> 1) & 1);
         tc_fence_after();
@@ -433,15 +473,12 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
             for (int y = 0; y < 32; ++y) o[y] *= fo;
             tmem_st32(to + c * 32, o);
           }
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-          tc_fence_before();
         }
         l += l0 + l1;
-#pragma unroll
-        for (int y = 0; y < 8; ++y)
-          *reinterpret_cast<uint4*>(smem + C::P + half * 16384 + r * 128 + ((y ^ (r & 7)) << 4)) =
-              make_uint4(ph[4 * y], ph[4 * y + 1], ph[4 * y + 2], ph[4 * y + 3]);
-        fence_proxy_async_smem();
+        tmem_st16(tl + C::TP + half * 32, ph);
+        tmem_st16(tl + C::TP + half * 32 + 16, ph + 16);
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full);
       }
