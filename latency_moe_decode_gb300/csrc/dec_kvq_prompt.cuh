@@ -251,58 +251,65 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
   } else if (warp >= 8) {
     // ---- codes to operands: 16 bytes of codes (four words) at a time, in an order that spreads the
     // 16-byte stores of eight lanes over all banks
+    // Chunk c (16 bytes) of row r of an operand lies at r 128 + ((c ^ r % 8) << 4): with a lane's first
+    // address a, the others are a ^ (constant << 4) and a + constant rows.
     constexpr int GW = 8 / C::DW;  // groups of a tile a warp
     const Magic magic = p.magic;
+    const uint32_t sm = smem_u32(smem);
     int n = 0, seg = 0;
-    auto put = [&](uint8_t* base, int pos, int j, uint32_t w, const Scale2& sc) {
+    auto put = [&](uint32_t at, uint32_t w, const Scale2& sc) {
       uint32_t a, b, c, d;
       sc.decode(w, magic, a, b);
       sc.decode(w >> 8, magic, c, d);
-      *reinterpret_cast<uint4*>(base + (j >> 3) * 16384 + pos * 128 + (((j & 7) ^ (pos & 7)) << 4)) = make_uint4(a, b, c, d);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
     };
+    // keys: lane bits t's low bit, g's two low bits, t's high bit, g's high bit
+    const int kt = (lane & 1) | ((lane >> 3) & 1) << 1, kg = ((lane >> 1) & 3) | ((lane >> 4) & 1) << 2;
+    const int kc = kt * (HD / 32);  // the lane's first chunk
+    const uint32_t ka = sm + C::K + ((warp - 8) * GW * 16 + kg) * 128 + (kc >> 3) * 16384 + (((kc & 7) ^ kg) << 4);
     auto keys = [&](int i) {  // of tile i
       const int st = i % kPromptStages;
       wait(&bars.raw_full[st], (i / kPromptStages) & 1);
       if (i >= 2) wait(&bars.k_empty[i & 1], ((i >> 1) - 1) & 1);
-      uint8_t* const k = smem + C::K + (i & 1) * C::OPERAND;
-      // lane bits: t's low bit, g's two low bits, t's high bit, g's high bit
-      const int tq = (lane & 1) | ((lane >> 3) & 1) << 1, g = ((lane >> 1) & 3) | ((lane >> 4) & 1) << 2;
+      const uint32_t to = ka + (i & 1) * C::OPERAND;
 #pragma unroll
       for (int gw = 0; gw < GW; ++gw) {
-      const int grp = (warp - 8) * GW + gw;
-      const uint8_t* const gp = smem + C::RING + st * C::RAW + grp * group_bytes(HD);
-      uint4 u[HD / 64];
+        const uint8_t* const gp = smem + C::RING + st * C::RAW + ((warp - 8) * GW + gw) * group_bytes(HD);
+        const uint32_t at = to + gw * 2048;
+        uint4 u[HD / 64];
 #pragma unroll
-      for (int y = 0; y < HD / 64; ++y) u[y] = *reinterpret_cast<const uint4*>(gp + y * 512 + (g * 4 + tq) * 16);
-      if (HD == 128) {
-        const uint32_t sb = *reinterpret_cast<const uint32_t*>(gp + 2 * code_bytes(HD) + (g * 4 + tq) * 4);
-#pragma unroll
-        for (int y = 0; y < HD / 64; ++y) {
-          const int pos = grp * 16 + g + 8 * y;
-          Scale2 s0, s1;
-          s0.set(__byte_perm(sb, 0, y ? 0x4242 : 0x4040));
-          s1.set(__byte_perm(sb, 0, y ? 0x4343 : 0x4141));
-          put(k, pos, 4 * tq, u[y].x, s0);
-          put(k, pos, 4 * tq + 1, u[y].y, s0);
-          put(k, pos, 4 * tq + 2, u[y].z, s1);
-          put(k, pos, 4 * tq + 3, u[y].w, s1);
-        }
-      } else {
-        const uint32_t sb = *reinterpret_cast<const uint16_t*>(gp + 2 * code_bytes(HD) + (g * 4 + tq) * 2);
-        const int pos = grp * 16 + g;
+        for (int y = 0; y < HD / 64; ++y) u[y] = *reinterpret_cast<const uint4*>(gp + y * 512 + (kg * 4 + kt) * 16);
         Scale2 s0, s1;
-        s0.set(__byte_perm(sb, 0, 0x4040));
-        s1.set(__byte_perm(sb, 0, 0x4141));
-        put(k, pos, 2 * tq, u[0].x, s0);
-        put(k, pos, 2 * tq + 1, u[0].y, s0);
-        put(k, pos + 8, 2 * tq, u[0].z, s1);
-        put(k, pos + 8, 2 * tq + 1, u[0].w, s1);
-      }
+        if (HD == 128) {
+          const uint32_t sb = *reinterpret_cast<const uint32_t*>(gp + 2 * code_bytes(HD) + (kg * 4 + kt) * 4);
+#pragma unroll
+          for (int y = 0; y < HD / 64; ++y) {
+            s0.set(__byte_perm(sb, 0, y ? 0x4242 : 0x4040));
+            s1.set(__byte_perm(sb, 0, y ? 0x4343 : 0x4141));
+            put(at + y * 1024, u[y].x, s0);
+            put((at ^ 16) + y * 1024, u[y].y, s0);
+            put((at ^ 32) + y * 1024, u[y].z, s1);
+            put((at ^ 48) + y * 1024, u[y].w, s1);
+          }
+        } else {
+          const uint32_t sb = *reinterpret_cast<const uint16_t*>(gp + 2 * code_bytes(HD) + (kg * 4 + kt) * 2);
+          s0.set(__byte_perm(sb, 0, 0x4040));
+          s1.set(__byte_perm(sb, 0, 0x4141));
+          put(at, u[0].x, s0);
+          put(at ^ 16, u[0].y, s0);
+          put(at + 1024, u[0].z, s1);
+          put((at ^ 16) + 1024, u[0].w, s1);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.k_full[i & 1]);
     };
+    // values: lane bits the run's two low bits, t's low bit, t's high bit, the run's high bit; lanes of odd
+    // t (hd 128) take their second position first
+    const int vg = (lane & 3) | ((lane >> 4) & 1) << 2, vt = (lane >> 2) & 3, odd = HD == 128 ? vt & 1 : 0;
+    const int vc = vg * (HD / 64), vr = 2 * vt + odd;  // the lane's first chunk and row
+    const uint32_t va = sm + C::V + ((warp - 8) * GW * 16 + vr) * 128 + (vc >> 3) * 16384 + (((vc & 7) ^ vr) << 4);
     for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
       if (s.t0 < s.t1) {
         keys(n);
@@ -311,49 +318,52 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
       for (int t = s.t0; t < s.t1; ++t, ++n) {
         const int st = n % kPromptStages;
         if (t + 1 < s.t1) keys(n + 1);  // (the next tile's scores wait for nothing else)
-        uint8_t* const v = smem + C::V + (n & 1) * C::OPERAND;
-        // lane bits: the run's two low bits, t's low bit, t's high bit, the run's high bit
-        const int gv = (lane & 3) | ((lane >> 4) & 1) << 2, tq = (lane >> 2) & 3;
         if (n >= 2) wait(&bars.v_empty[n & 1], ((n >> 1) - 1) & 1);
+        const uint32_t to = va + (n & 1) * C::OPERAND;
 #pragma unroll
         for (int gw = 0; gw < GW; ++gw) {
-        const int grp = (warp - 8) * GW + gw;
-        const uint8_t* const gp = smem + C::RING + st * C::RAW + grp * group_bytes(HD) + code_bytes(HD);
-        const int lo = grp * 16 + 2 * tq;  // the lane's first position
-        uint4 u[HD / 64];
+          const int grp = (warp - 8) * GW + gw;
+          const uint8_t* const gp = smem + C::RING + st * C::RAW + grp * group_bytes(HD) + code_bytes(HD);
+          const uint32_t at = to + gw * 2048;
+          uint4 u[HD / 64];
 #pragma unroll
-        for (int y = 0; y < HD / 64; ++y) u[y] = *reinterpret_cast<const uint4*>(gp + y * 512 + (gv * 4 + tq) * 16);
-        // scales of positions lo, lo + 1, lo + 8, lo + 9
-        uint32_t sb = *reinterpret_cast<const uint32_t*>(gp + code_bytes(HD) + scale_bytes(HD) +
-                                                         ((HD == 128 ? gv : gv >> 1) * 4 + tq) * 4);
-        if ((t + 1) * kTile > s.smin) {
-          // what no row sees counts nothing (scale 0); a run of NaNs that only some rows see is noted,
-          // and put into their outputs at the end (0 x NaN is NaN: P cannot leave it out)
+          for (int y = 0; y < HD / 64; ++y) u[y] = *reinterpret_cast<const uint4*>(gp + y * 512 + (vg * 4 + vt) * 16);
+          // scales of positions 2t, 2t + 1, 2t + 8, 2t + 9
+          uint32_t sb = *reinterpret_cast<const uint32_t*>(gp + code_bytes(HD) + scale_bytes(HD) +
+                                                           ((HD == 128 ? vg : vg >> 1) * 4 + vt) * 4);
+          if ((t + 1) * kTile > s.smin) {
+            // what no row sees counts nothing (scale 0); a run of NaNs that only some rows see is noted,
+            // and put into their outputs at the end (0 x NaN is NaN: P cannot leave it out)
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int pos = t * kTile + lo + (y & 1) + 8 * (y >> 1);
-            const bool bad = ((sb >> (8 * y)) & 255u) == 255u;
-            if (bad && pos < s.smax) atomicMin(&nan_from[HD == 128 ? gv : gv >> 1], pos);
-            if (bad || pos >= s.smax) sb &= ~(255u << (8 * y));
+            for (int y = 0; y < 4; ++y) {
+              const int pos = t * kTile + grp * 16 + 2 * vt + (y & 1) + 8 * (y >> 1);
+              const bool bad = ((sb >> (8 * y)) & 255u) == 255u;
+              if (bad && pos < s.smax) atomicMin(&nan_from[HD == 128 ? vg : vg >> 1], pos);
+              if (bad || pos >= s.smax) sb &= ~(255u << (8 * y));
+            }
           }
-        }
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
           Scale2 s0, s1;
-          s0.set(__byte_perm(sb, 0, y ? 0x4242 : 0x4040));
-          s1.set(__byte_perm(sb, 0, y ? 0x4343 : 0x4141));
           if (HD == 128) {
-            const uint4 x = u[y % (HD / 64)];
-            const int pos = lo + 8 * y, odd = tq & 1;  // (odd t: the second position first)
-            put(v, pos + odd, 2 * gv, odd ? x.z : x.x, odd ? s1 : s0);
-            put(v, pos + odd, 2 * gv + 1, odd ? x.w : x.y, odd ? s1 : s0);
-            put(v, pos + 1 - odd, 2 * gv, odd ? x.x : x.z, odd ? s0 : s1);
-            put(v, pos + 1 - odd, 2 * gv + 1, odd ? x.y : x.w, odd ? s0 : s1);
+            sb = odd ? __byte_perm(sb, 0, 0x2301) : sb;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint4 x = u[y % (HD / 64)];
+              s0.set(__byte_perm(sb, 0, y ? 0x4242 : 0x4040));
+              s1.set(__byte_perm(sb, 0, y ? 0x4343 : 0x4141));
+              put(at + y * 1024, odd ? x.z : x.x, s0);
+              put((at ^ 16) + y * 1024, odd ? x.w : x.y, s0);
+              put((at ^ 144) + y * 1024, odd ? x.x : x.z, s1);  // (the row's last bit flips: 128, and the chunk's)
+              put((at ^ 128) + y * 1024, odd ? x.y : x.w, s1);
+            }
           } else {
-            put(v, lo + 8 * y, gv, y ? u[0].z : u[0].x, s0);
-            put(v, lo + 8 * y + 1, gv, y ? u[0].w : u[0].y, s1);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              s0.set(__byte_perm(sb, 0, y ? 0x4242 : 0x4040));
+              s1.set(__byte_perm(sb, 0, y ? 0x4343 : 0x4141));
+              put(at + y * 1024, y ? u[0].z : u[0].x, s0);
+              put((at ^ 144) + y * 1024, y ? u[0].w : u[0].y, s1);
+            }
           }
-        }
         }
         fence_proxy_async_smem();
         __syncwarp();
