@@ -365,8 +365,9 @@ const char* dec_op_error(void);
    infinity or NaN is held as NaNs.
    status (device int32, may be NULL; zero it once) receives DEC_ERR_ARG when a kernel meets a
    page id outside 0 .. n_pages - 1 or a negative position, and DEC_ERR_CAPACITY when a position
-   lies beyond the page table or the rotation table (the first one met stays). The kernel skips
-   such a row or such positions and touches nothing out of range. */
+   lies beyond the page table or the rotation table (the first one met stays), and DEC_ERR_TIMEOUT
+   if a kernel gave up waiting for its own copies. The kernel skips such a row or such positions
+   and touches nothing out of range. */
 typedef struct {
   void* pages;
   int32_t n_pages;
@@ -380,8 +381,8 @@ typedef struct {
    cu_tokens[b] .. cu_tokens[b + 1] - 1 (device int32 [batch + 1]; NULL: one row per sequence and
    n_tokens == batch). Its row j stands at position lengths[b] + j (device int32 [batch]), and
    position p is in page table[b * table_stride + p / page_tokens] (device int32; max_pages
-   entries of each row are valid). cu_tokens must ascend. Rows before cu_tokens[0] or from cu_tokens[batch] on belong to
-   no sequence: outputs leave them as they were. */
+   entries of each row are valid). cu_tokens must ascend. Rows before cu_tokens[0] or from
+   cu_tokens[batch] on belong to no sequence: outputs leave them as they were. */
 typedef struct {
   int32_t batch;
   int32_t n_tokens;
@@ -447,7 +448,10 @@ dec_status dec_kvq_gather(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, 
      workspace  16-byte aligned device memory of dec_kvq_attention_workspace() bytes; its content
                 is of no interest before or after the call
    A row with no position gives out = 0 and lse = -infinity. Scores, softmax statistics and the
-   output sum are fp32; queries enter the products exactly (bf16), probabilities with 11 bits. */
+   output sum are fp32; queries enter the products exactly (values below 2^-17 of their head's
+   largest: to 2^-25 of it), probabilities with 11 bits. Rows that meet a bad page or a position
+   beyond the page table hold nothing of use, the other sequences' are right. A call of 2^31 query
+   rows or of a page table of 2^31 positions is DEC_ERR_UNSUPPORTED. */
 typedef struct {
   int32_t n_heads;
   dec_rows q, out;

@@ -131,11 +131,13 @@ dec_status launched(const char* what) {
   return ce == cudaSuccess ? DEC_OK : op_cuda(ce, what);
 }
 
-// The prompt kernel takes calls whose longest sequence has at least this many query rows.
-#ifndef KVQ_PROMPT
-#define KVQ_PROMPT 64
-#endif
-constexpr int kPromptRows = KVQ_PROMPT;
+// The prompt kernel takes calls whose longest sequence has more query rows per KV head than this: the
+// streaming one's time grows with every 16 rows, the prompt kernel's with every 128. Streaming against
+// prompt kernel, us: hd 128, 8 KV heads, 17 .. 32 rows, one sequence on 8 k 23.6 / 20.3, on 64 k 53.6 /
+// 52.0, 16 on 2 k 42.3 / 34.5, 64 on 1 k 85.5 / 85.7; 16 rows, on 64 k 37.3 / 52.0, 64 on 1 k 52.0 / 91.9.
+// hd 64 (half the decoding for as many exponentials), 48 rows, one on 8 k 20.8 / 16.6, on 64 k 50.7 / 41.8,
+// 64 on 1 k 67.4 / 63.0; 32 rows, on 64 k 38.4 / 41.8, 64 on 1 k 47.9 / 63.0.
+constexpr int prompt_above(int hd) { return hd == 128 ? 16 : 32; }
 
 // The attention kernel's dynamic shared memory limit, raised once per device. The join kernel asks for
 // the same division of the SM's memory, so that none is redivided between the two.
@@ -156,9 +158,9 @@ dec_status raise_smem(F* k, F* join, int bytes, std::atomic<unsigned long long>&
 
 // Which kernel takes a call, by the longest sequence's query rows: 0 and 1, the streaming one with 8 and
 // 16 rows a unit; 2, the one for prompts.
-int kernel_of(int n_heads, int hkv, int max_tokens) {
+int kernel_of(int hd, int n_heads, int hkv, int max_tokens) {
   const long long rows = (long long)max_tokens * (n_heads / hkv);
-  return rows <= 8 ? 0 : rows < kPromptRows ? 1 : 2;
+  return rows <= 8 ? 0 : rows <= prompt_above(hd) ? 1 : 2;
 }
 
 // A kernel's launch: its function, the one that joins its parts, and their sizes.
@@ -318,7 +320,7 @@ int64_t dec_kvq_attention_workspace(const dec_kvq_cache* c, int32_t n_heads, int
   if (dec_kvq_page_bytes(c->page_tokens, c->n_kv_heads, c->head_dim) == 0) return -1;
   const int sms = op_sms();
   if (sms < 1) return -1;
-  return workspace_of(variant_of(c->head_dim, kernel_of(n_heads, c->n_kv_heads, max_tokens)), sms);
+  return workspace_of(variant_of(c->head_dim, kernel_of(c->head_dim, n_heads, c->n_kv_heads, max_tokens)), sms);
 }
 
 dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec_kvq_attention_args* a,
@@ -354,12 +356,12 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
   p.causal = a->causal != 0;
   p.max_tokens = a->max_tokens;
   const int max_tokens = std::min(a->max_tokens, s->n_tokens);
-  const int kind = kernel_of(a->n_heads, c->n_kv_heads, max_tokens);
+  const int kind = kernel_of(c->head_dim, a->n_heads, c->n_kv_heads, max_tokens);
   if (a->workspace_bytes < dec_kvq_attention_workspace(c, a->n_heads, s->batch, max_tokens))
     return op_fail(DEC_ERR_ARG, "attention: workspace too small");
-  // entries of the kernels' list, at most: 32-bit
+  // entries of the kernels' lists, at most: 32-bit
   const long long units = (long long)c->n_kv_heads * ((long long)s->n_tokens * p.group / 8 + s->batch);
-  if (units * ((long long)s->max_pages * c->page_tokens / kGroup + 1 + kUnitCost) >= (1LL << 32) - 64)
+  if (units * ((long long)s->max_pages * c->page_tokens / kGroup + 1 + std::max(kUnitCost, kPromptCost)) >= (1LL << 32) - 64)
     return op_fail(DEC_ERR_UNSUPPORTED, "attention: too much work for one call");
   return launch_attention(p, c->head_dim, kind, s->batch, static_cast<uint8_t*>(a->workspace), op_stream(stream));
 }

@@ -4,8 +4,9 @@
 // turned into operands once per 128 query rows. A CTA takes a stretch of (unit, tile of 128
 // positions) entries, a unit being (sequence, KV head, 128 query rows), with a role for each warp:
 //  - one copies the tiles' codes (bulk copies, four tiles ahead);
-//  - four turn them into f16 in the 128-byte swizzled layout that the MMAs read. A word of codes
-//    gives pairs (i, i + 4), and nothing puts them in order: the queries are staged in the same
+//  - six turn them into f16 in the 128-byte swizzled layout that the MMAs read, half a group at a time
+//    (four warps: 2.5 k cycles a tile, more than any other role; with these six, 16 warps fill the
+//    registers). A word of codes gives pairs (i, i + 4), and nothing puts them in order: the queries are staged in the same
 //    order, and the outputs' columns are put right when they are written;
 //  - one thread issues S = Q K^T (128 x 128 x hd, two S buffers in tensor memory) and O += P V
 //    (128 x hd x 128, V read MN-major), the next tile's S before this tile's O. Q and P are A operands
@@ -24,15 +25,15 @@ namespace kvq {
 
 constexpr int kTile = 128;           // positions per tile
 constexpr int kPromptStages = 4;     // tiles of codes in the ring
-constexpr int kPromptCost = 1;       // a unit's fixed cost, in tiles' time
-constexpr int kSplitCost = 8;
+constexpr int kPromptCost = 5;       // a unit's fixed cost, in tiles' time (1: 128 sequences of 8 rows on 300, 88 us; 5: 78)
+constexpr int kSplitCost = 8;        // what parts that have to be joined cost, in tiles' time
 constexpr float kPromptShift = 7.0f; // P is kept times 2^7 (at most 2^15 with the reference's slack of 2^8)
 
 template <int HD>
 struct PromptCfg {
   static constexpr int ROWS = 128;
-  static constexpr int DW = 4;                         // warps that decode
-  static constexpr int THREADS = (8 + DW + 2) * 32;  // 8 softmax, DW decode, MMA, copy
+  static constexpr int DW = 6;                         // warps that decode
+  static constexpr int THREADS = (8 + DW + 2) * 32;  // 8 softmax, DW decode, MMA, copy: 128 registers each
   static constexpr int HP = HD / 64;       // 64-value parts of a head
   static constexpr int OPERAND = HP * 16384;
   static constexpr int RAW = kTile / kGroup * group_bytes(HD);
@@ -253,7 +254,9 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
     // 16-byte stores of eight lanes over all banks
     // Chunk c (16 bytes) of row r of an operand lies at r 128 + ((c ^ r % 8) << 4): with a lane's first
     // address a, the others are a ^ (constant << 4) and a + constant rows.
-    constexpr int GW = 8 / C::DW;  // groups of a tile a warp
+    // Half a group (8 positions) at a time, the warps in turn; those with fewer of a tile's keys have more
+    // of its values.
+    const int kw = warp - 8, vw = kw >= 4 ? kw - 4 : kw + 2;
     const Magic magic = p.magic;
     const uint32_t sm = smem_u32(smem);
     int n = 0, seg = 0;
@@ -266,39 +269,35 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
     // keys: lane bits t's low bit, g's two low bits, t's high bit, g's high bit
     const int kt = (lane & 1) | ((lane >> 3) & 1) << 1, kg = ((lane >> 1) & 3) | ((lane >> 4) & 1) << 2;
     const int kc = kt * (HD / 32);  // the lane's first chunk
-    const uint32_t ka = sm + C::K + ((warp - 8) * GW * 16 + kg) * 128 + (kc >> 3) * 16384 + (((kc & 7) ^ kg) << 4);
+    const uint32_t ka = sm + C::K + kg * 128 + (kc >> 3) * 16384 + (((kc & 7) ^ kg) << 4);
     auto keys = [&](int i) {  // of tile i
       const int st = i % kPromptStages;
       wait(&bars.raw_full[st], (i / kPromptStages) & 1);
       if (i >= 2) wait(&bars.k_empty[i & 1], ((i >> 1) - 1) & 1);
+      const uint8_t* const from = smem + C::RING + st * C::RAW;
       const uint32_t to = ka + (i & 1) * C::OPERAND;
 #pragma unroll
-      for (int gw = 0; gw < GW; ++gw) {
-        const uint8_t* const gp = smem + C::RING + st * C::RAW + ((warp - 8) * GW + gw) * group_bytes(HD);
-        const uint32_t at = to + gw * 2048;
-        uint4 u[HD / 64];
-#pragma unroll
-        for (int y = 0; y < HD / 64; ++y) u[y] = *reinterpret_cast<const uint4*>(gp + y * 512 + (kg * 4 + kt) * 16);
+      for (int x = 0; x < (16 + C::DW - 1) / C::DW; ++x) {
+        const int hg = kw + x * C::DW, y = hg & 1;
+        if (hg >= 16) break;
+        const uint8_t* const gp = from + (hg >> 1) * group_bytes(HD);
+        const uint32_t at = to + hg * 1024;
         Scale2 s0, s1;
         if (HD == 128) {
-          const uint32_t sb = *reinterpret_cast<const uint32_t*>(gp + 2 * code_bytes(HD) + (kg * 4 + kt) * 4);
-#pragma unroll
-          for (int y = 0; y < HD / 64; ++y) {
-            s0.set(__byte_perm(sb, 0, y ? 0x4242 : 0x4040));
-            s1.set(__byte_perm(sb, 0, y ? 0x4343 : 0x4141));
-            put(at + y * 1024, u[y].x, s0);
-            put((at ^ 16) + y * 1024, u[y].y, s0);
-            put((at ^ 32) + y * 1024, u[y].z, s1);
-            put((at ^ 48) + y * 1024, u[y].w, s1);
-          }
-        } else {
-          const uint32_t sb = *reinterpret_cast<const uint16_t*>(gp + 2 * code_bytes(HD) + (kg * 4 + kt) * 2);
+          const uint4 u = *reinterpret_cast<const uint4*>(gp + y * 512 + (kg * 4 + kt) * 16);
+          const uint32_t sb = *reinterpret_cast<const uint16_t*>(gp + 2 * code_bytes(HD) + (kg * 4 + kt) * 4 + y * 2);
           s0.set(__byte_perm(sb, 0, 0x4040));
           s1.set(__byte_perm(sb, 0, 0x4141));
-          put(at, u[0].x, s0);
-          put(at ^ 16, u[0].y, s0);
-          put(at + 1024, u[0].z, s1);
-          put((at ^ 16) + 1024, u[0].w, s1);
+          put(at, u.x, s0);
+          put(at ^ 16, u.y, s0);
+          put(at ^ 32, u.z, s1);
+          put(at ^ 48, u.w, s1);
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(gp + (kg * 4 + kt) * 16 + y * 8);
+          const uint32_t sb = gp[2 * code_bytes(HD) + (kg * 4 + kt) * 2 + y];
+          s0.set(__byte_perm(sb, 0, 0x4040));
+          put(at, u.x, s0);
+          put(at ^ 16, u.y, s0);
         }
       }
       fence_proxy_async_smem();
@@ -309,7 +308,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
     // t (hd 128) take their second position first
     const int vg = (lane & 3) | ((lane >> 4) & 1) << 2, vt = (lane >> 2) & 3, odd = HD == 128 ? vt & 1 : 0;
     const int vc = vg * (HD / 64), vr = 2 * vt + odd;  // the lane's first chunk and row
-    const uint32_t va = sm + C::V + ((warp - 8) * GW * 16 + vr) * 128 + (vc >> 3) * 16384 + (((vc & 7) ^ vr) << 4);
+    const uint32_t va = sm + C::V + vr * 128 + (vc >> 3) * 16384 + (((vc & 7) ^ vr) << 4);
     for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
       if (s.t0 < s.t1) {
         keys(n);
@@ -319,50 +318,43 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         const int st = n % kPromptStages;
         if (t + 1 < s.t1) keys(n + 1);  // (the next tile's scores wait for nothing else)
         if (n >= 2) wait(&bars.v_empty[n & 1], ((n >> 1) - 1) & 1);
+        const uint8_t* const from = smem + C::RING + st * C::RAW + code_bytes(HD);
         const uint32_t to = va + (n & 1) * C::OPERAND;
 #pragma unroll
-        for (int gw = 0; gw < GW; ++gw) {
-          const int grp = (warp - 8) * GW + gw;
-          const uint8_t* const gp = smem + C::RING + st * C::RAW + grp * group_bytes(HD) + code_bytes(HD);
-          const uint32_t at = to + gw * 2048;
-          uint4 u[HD / 64];
-#pragma unroll
-          for (int y = 0; y < HD / 64; ++y) u[y] = *reinterpret_cast<const uint4*>(gp + y * 512 + (vg * 4 + vt) * 16);
-          // scales of positions 2t, 2t + 1, 2t + 8, 2t + 9
-          uint32_t sb = *reinterpret_cast<const uint32_t*>(gp + code_bytes(HD) + scale_bytes(HD) +
-                                                           ((HD == 128 ? vg : vg >> 1) * 4 + vt) * 4);
+        for (int x = 0; x < (16 + C::DW - 1) / C::DW; ++x) {
+          const int hg = vw + x * C::DW, y = hg & 1;
+          if (hg >= 16) break;
+          const uint8_t* const gp = from + (hg >> 1) * group_bytes(HD);
+          const uint32_t at = to + hg * 1024;
+          // scales of positions 2t and 2t + 1 of the half
+          uint32_t sb = *reinterpret_cast<const uint16_t*>(gp + code_bytes(HD) + scale_bytes(HD) +
+                                                           ((HD == 128 ? vg : vg >> 1) * 4 + vt) * 4 + y * 2);
           if ((t + 1) * kTile > s.smin) {
             // what no row sees counts nothing (scale 0); a run of NaNs that only some rows see is noted,
             // and put into their outputs at the end (0 x NaN is NaN: P cannot leave it out)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int pos = t * kTile + grp * 16 + 2 * vt + (y & 1) + 8 * (y >> 1);
-              const bool bad = ((sb >> (8 * y)) & 255u) == 255u;
+            for (int e = 0; e < 2; ++e) {
+              const int pos = t * kTile + hg * 8 + 2 * vt + e;
+              const bool bad = ((sb >> (8 * e)) & 255u) == 255u;
               if (bad && pos < s.smax) atomicMin(&nan_from[HD == 128 ? vg : vg >> 1], pos);
-              if (bad || pos >= s.smax) sb &= ~(255u << (8 * y));
+              if (bad || pos >= s.smax) sb &= ~(255u << (8 * e));
             }
           }
           Scale2 s0, s1;
           if (HD == 128) {
-            sb = odd ? __byte_perm(sb, 0, 0x2301) : sb;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint4 x = u[y % (HD / 64)];
-              s0.set(__byte_perm(sb, 0, y ? 0x4242 : 0x4040));
-              s1.set(__byte_perm(sb, 0, y ? 0x4343 : 0x4141));
-              put(at + y * 1024, odd ? x.z : x.x, s0);
-              put((at ^ 16) + y * 1024, odd ? x.w : x.y, s0);
-              put((at ^ 144) + y * 1024, odd ? x.x : x.z, s1);  // (the row's last bit flips: 128, and the chunk's)
-              put((at ^ 128) + y * 1024, odd ? x.y : x.w, s1);
-            }
+            const uint4 u = *reinterpret_cast<const uint4*>(gp + y * 512 + (vg * 4 + vt) * 16);
+            s0.set(__byte_perm(sb, 0, odd ? 0x4141 : 0x4040));
+            s1.set(__byte_perm(sb, 0, odd ? 0x4040 : 0x4141));
+            put(at, odd ? u.z : u.x, s0);
+            put(at ^ 16, odd ? u.w : u.y, s0);
+            put(at ^ 144, odd ? u.x : u.z, s1);  // (the row's last bit flips: 128, and the chunk's)
+            put(at ^ 128, odd ? u.y : u.w, s1);
           } else {
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              s0.set(__byte_perm(sb, 0, y ? 0x4242 : 0x4040));
-              s1.set(__byte_perm(sb, 0, y ? 0x4343 : 0x4141));
-              put(at + y * 1024, y ? u[0].z : u[0].x, s0);
-              put((at ^ 144) + y * 1024, y ? u[0].w : u[0].y, s1);
-            }
+            const uint2 u = *reinterpret_cast<const uint2*>(gp + (vg * 4 + vt) * 16 + y * 8);
+            s0.set(__byte_perm(sb, 0, 0x4040));
+            s1.set(__byte_perm(sb, 0, 0x4141));
+            put(at, u.x, s0);
+            put(at ^ 144, u.y, s1);
           }
         }
         fence_proxy_async_smem();

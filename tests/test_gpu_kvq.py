@@ -170,6 +170,16 @@ ATTN = [
     (64, 8, 2, 64, False, [64, 40, 3], [0, 500, 129]),
     (64, 2, 1, 16, True, [300], [40]),
     (128, 16, 1, 256, False, [9, 2], [1, 1000]),
+    # rows about which another kernel takes the call
+    (128, 8, 2, 64, True, [2, 1], [30, 7]),
+    (128, 8, 2, 64, True, [3, 2], [200, 31]),
+    (128, 8, 2, 32, True, [4, 1], [127, 600]),
+    (128, 8, 2, 32, True, [5, 1, 0, 2], [127, 600, 3, 0]),
+    (64, 8, 2, 64, True, [8, 3], [500, 1]),
+    (64, 8, 2, 64, True, [9, 3], [500, 1]),
+    # prompts whose sequences see nothing
+    (128, 4, 1, 16, False, [30, 20, 10], [0, 0, 0]),
+    (64, 4, 1, 16, False, [30, 1, 10], [0, 9, 0]),
 ]
 
 
@@ -189,7 +199,8 @@ def _check(out, lse, q, k, v, new, lens, causal, scale, hd, first=0):
         held = l + m if causal else l
         for j in range(m):
             seen = l + j + 1 if causal else l
-            kept = 2.0 ** (-21 if max(new) * q.shape[1] // k.shape[1] >= 64 else -29)
+            # (the kernel for prompts, from this many query rows on, keeps probabilities down to 2^-21)
+            kept = 2.0 ** (-21 if max(new) * q.shape[1] // k.shape[1] > (16 if hd == 128 else 32) else -29)
             o, s, mass, big = ref.attend(q[row], k[at:at + held], v[at:at + held], scale, seen, kept)
             ob, lb = ref.out_bounds(o, s, mass, big, hd, max(seen, 1))
             assert (np.abs(out[row] - o) <= ob).all(), (row, np.max(np.abs(out[row] - o) / ob))
@@ -232,9 +243,7 @@ def test_attention_leaves_rows_of_no_sequence_and_takes_strides():
     out = torch.full((n, 10, 64), 5.0, dtype=BF, device="cuda")
     got = cache.attention(wide[:, 2:10], _ints(lens), table, cu_tokens=_cu(new, first), max_tokens=3, out=out[:, 1:9])
     cache.check()
-    dummy = np.full((n, 8), np.nan)
-    at = 0
-    row = first
+    at, row = 0, first
     for m, l in zip(new, lens):
         for j in range(m):
             o, s, mass, big = ref.attend(_np(q[row]), k[at:at + l + m], v[at:at + l + m], 0.125, l + j + 1)
@@ -242,7 +251,6 @@ def test_attention_leaves_rows_of_no_sequence_and_takes_strides():
             row += 1
         at += l + m
     assert (out[0] == 5).all() and (out[row:] == 5).all() and (out[:, 0] == 5).all() and (out[:, 9] == 5).all()
-    assert dummy.shape == (n, 8)
 
 
 def test_attention_ignores_what_lies_behind_a_sequence():
@@ -388,6 +396,79 @@ def test_two_streams_at_once_and_repeats_agree():
                 got.append(cache.attention(q, ln, table, return_lse=True))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l in got)
+
+
+def _prompts(m, hd=128, hq=8, hkv=2, seed=61):
+    """Three sequences of m, 1 and 2 m new tokens, which each of the kernels takes for some m."""
+    new, lens = [m, 1, 2 * m], [300, 20, 0]
+    cache, table, k, v, g = _filled([l + n for l, n in zip(lens, new)], hkv, hd, 16, seed)
+    q = _rnd(g, sum(new), hq, hd).cuda()
+    return cache, table, q, dict(lengths=_ints(lens), table=table, cu_tokens=_cu(new), max_tokens=2 * m)
+
+
+@pytest.mark.parametrize("m", [1, 2, 25])
+def test_streams_graphs_and_outputs_over_the_queries_agree(m):
+    cache, table, q, kw = _prompts(m)
+    want = cache.attention(q, return_lse=True, **kw)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(3)], []
+    for _ in range(8):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(cache.attention(q, return_lse=True, **kw))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l in got)
+    graph, held = torch.cuda.CUDAGraph(), q.clone()
+    with torch.cuda.graph(graph):
+        cache.attention(held, out=held, **kw)  # (capture does not run it)
+        twice = cache.attention(q, **kw)
+    for _ in range(3):
+        held.copy_(q)
+        graph.replay()
+        assert torch.equal(held, want[0]) and torch.equal(twice, want[0])
+    cache.check()
+
+
+@pytest.mark.parametrize("m", [2, 4, 25])
+def test_rows_beyond_max_tokens_are_left(m):
+    cache, table, q, kw = _prompts(m)
+    want = cache.attention(q, **kw)
+    out = torch.full_like(q, 3.0)
+    cache.attention(q, out=out, **{**kw, "max_tokens": m})
+    assert (out[2 * m + 1:] == 3.0).all()
+    # (another bound may choose another kernel. Values up to 4.5; probabilities to 2^-11 of themselves and
+    # their sum, outputs to 2^-8: 2 (2 4.5 2^-11 + 4.5 2^-8) = 0.044)
+    assert (out[:2 * m + 1].float() - want[:2 * m + 1].float()).abs().max() < 0.05
+    cache.check()
+
+
+def test_prompts_of_many_sequences():
+    """More sequences than one launch of the kernel for prompts lists, some without rows."""
+    b = 300
+    new, lens = [(i * 5) % 7 for i in range(b)], [(i * 11) % 40 for i in range(b)]
+    cache, table, k, v, g = _filled([l + n for l, n in zip(lens, new)], 1, 128, 16, 62)
+    q = _rnd(g, sum(new), 4, 128)
+    out, lse = cache.attention(q.cuda(), _ints(lens), table, cu_tokens=_cu(new), max_tokens=6, return_lse=True)
+    cache.check()
+    _check(_np(out), _np(lse), _np(q), k, v, new, lens, True, 128 ** -0.5, 128)
+
+
+def test_bad_pages_of_a_prompt_are_reported():
+    from latency_moe_decode_gb300.capi import DecError
+    cache, table, q, kw = _prompts(25)
+    want = cache.attention(q, **kw)
+    wrong = table.clone()
+    wrong[0, 3], wrong[0, 7] = cache.n_pages, -5
+    for bad, code in ((dict(table=wrong), -1), (dict(lengths=_ints([300, 20, 2 ** 31 - 60])), -8),
+                      (dict(lengths=_ints([-3, 20, 0])), -1), (dict(table=table[:, :2]), -8)):
+        out = cache.attention(q, **{**kw, **bad})
+        with pytest.raises(DecError) as e:
+            cache.check()
+        assert e.value.status == code
+        if "table" in bad and bad["table"] is wrong:
+            assert torch.equal(out[25:], want[25:])  # the other sequences'
+    assert torch.equal(cache.attention(q, **kw), want)
+    cache.check()
 
 
 def test_bad_device_data_is_reported_and_touches_nothing():
