@@ -60,22 +60,37 @@ __device__ __forceinline__ float scale_of(int b) {
   return 8.0f * __half2float(__ushort_as_half((unsigned short)(b << 7)));
 }
 
+// Keys that come out of the norm and the rotation have gone through some 16 fp32 roundings (the sum of
+// squares, halved by the root; the root; two products; the rotation), which leave a standard deviation of
+// about 1.5 x 2^-24 of the pair's larger value: one code in a million would be the neighbour of what the
+// formula gives. Where that error, or that of fp32 values as they are, may have made the choice (CHECK,
+// near), the row is made anew with twice the bits (settle_row). kNear is five deviations, for values up to
+// 8 codes: one row in 1000 is made anew; a bound on all roundings at once would take three times as many.
+constexpr float kNear = 0x1p-18f;
+
 // The scale byte of a run whose largest magnitude has the bits `mag`: max / 7 (and / 8) rounded to
 // 3 mantissa bits.
-__device__ __forceinline__ int scale_byte(uint32_t mag) {
+template <bool CHECK>
+__device__ __forceinline__ int scale_byte(uint32_t mag, bool& near) {
   if (mag >= 0x7F800000u) return kScaleNan;
   const float m = __uint_as_float(mag), q = m * (1.0f / 7.0f);
   const float w = fminf(fmaf(fmaf(-q, 7.0f, m), 1.0f / 7.0f, q) * 0.125f, 60.0f);  // (see code_word)
-  if (w < 6.103515625e-05f) return __float2int_rn(w * 131072.0f);  // below 2^-14: steps of 2^-17
   uint32_t u = __float_as_uint(w);
+  if (w < 6.103515625e-05f) {  // below 2^-14: steps of 2^-17
+    const float v = w * 131072.0f;
+    if (CHECK) near |= fabsf(v - floorf(v) - 0.5f) <= 0x1p-17f;
+    return __float2int_rn(v);
+  }
+  if (CHECK) near |= (u & 0xFFFFFu) - (0x80000u - 8u) <= 16u;
   u += 0x7FFFFu + ((u >> 20) & 1u);
   return (int)(u >> 20) - (112 << 3);
 }
 
 // Eight values as a word of codes at scale s (0: an empty or NaN run, every code 0).
-__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float s) {
+template <bool CHECK>
+__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float s, bool& near) {
   if (!(s > 0.f)) return 0x88888888u;
-  float inv, c[8];
+  float inv, c[8], d = 0.f;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -84,12 +99,15 @@ __device__ __forceinline__ uint32_t code_word(const float (&x)[8], float s) {
     // fall on either side of it).
     const float q = x[i] * inv, r = fmaf(-q, s, x[i]);
     const float y = fminf(fmaxf(fmaf(r, inv, q), -8.f), 7.f);
-    c[i] = (y + 12582912.f) - 12582904.f;  // to the nearest whole number, ties to even; + 8
+    c[i] = (y + 12582912.f) - 12582912.f;  // to the nearest whole number, ties to even
+    if (CHECK) d = fmaxf(d, fabsf(y - c[i]));
   }
-  // four codes make a whole number below 2^16, which 2^23 leaves in the low mantissa bits
+  if (CHECK) near |= d >= 0.5f - kNear;
+  // four codes + 8 make a whole number below 2^16, which 2^23 leaves in the low mantissa bits
   const float lo = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]);
   const float hi = fmaf(fmaf(fmaf(c[7], 16.f, c[6]), 16.f, c[5]), 16.f, c[4]);
-  return __byte_perm(__float_as_uint(lo + 8388608.f), __float_as_uint(hi + 8388608.f), 0x5410);
+  constexpr float k8 = 8388608.f + 8.f * (1 + 16 + 256 + 4096);
+  return __byte_perm(__float_as_uint(lo + k8), __float_as_uint(hi + k8), 0x5410);
 }
 
 struct Seqs {
@@ -208,6 +226,105 @@ struct Raw {
   }
 };
 
+// The unevaluated sum of two floats, about 46 bits (64-bit arithmetic runs at a hundredth of fp32's rate
+// here: one row settled in it took 12 us).
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two renorm(float h, float l) {  // |l| below |h|
+  const float s = h + l;
+  return Two{s, l - (s - h)};
+}
+__device__ __forceinline__ Two add(const Two& a, const Two& b) {
+  const float s = a.h + b.h, t = s - a.h;
+  return renorm(s, (a.h - (s - t)) + (b.h - t) + (a.l + b.l));
+}
+__device__ __forceinline__ Two mul(float a, float b) {
+  const float h = a * b;
+  return Two{h, fmaf(a, b, -h)};
+}
+__device__ __forceinline__ Two mul(const Two& a, float b) {
+  const float h = a.h * b;
+  return renorm(h, fmaf(a.l, b, fmaf(a.h, b, -h)));
+}
+__device__ __forceinline__ Two shfl_xor(const Two& a, int m) {
+  return Two{__shfl_xor_sync(0xffffffffu, a.h, m), __shfl_xor_sync(0xffffffffu, a.l, m)};
+}
+
+// 32 values of a row of keys or values anew, by a warp, from value d0 on: norm (nw: its weights, or null),
+// rotation (rot values, by the angles at `ang`), scales and codes with 46 bits. Latency is all of it: the
+// loads are asked for at once, the row's parts go to as many warps.
+template <int HD, bool F32>
+__device__ __noinline__ void settle_row(const void* x, const uint16_t* nw, float eps, const float2* ang, int rot, bool inter,
+                                        bool key, int pp, int d0, uint8_t* at) {
+  const int lane = threadIdx.x & 31, half = rot / 2, d = d0 + lane;
+  auto value = [&](int i) {
+    return F32 ? static_cast<const float*>(x)[i] : __uint_as_float((uint32_t) static_cast<const uint16_t*>(x)[i] << 16);
+  };
+  // its pair's other value, and the angle
+  const bool first = inter ? !(d & 1) : d < half, turned = d < rot;
+  const int o = !turned ? d : inter ? d ^ 1 : first ? d + half : d - half;
+  float all[HD / 32];
+#pragma unroll
+  for (int i = 0; i < HD / 32; ++i) all[i] = value(i * 32 + lane);
+  const float a = value(d), b = value(o);
+  const float wa = nw ? __uint_as_float((uint32_t)nw[d] << 16) : 1.f, wb = nw ? __uint_as_float((uint32_t)nw[o] << 16) : 1.f;
+  const float2 turn = turned ? __ldg(ang + (inter ? d >> 1 : first ? d : o)) : make_float2(1.f, 0.f);
+  Two inv{1.f, 0.f};
+  if (nw) {
+    Two m = mul(all[0], all[0]);
+#pragma unroll
+    for (int i = 1; i < HD / 32; ++i) m = add(m, mul(all[i], all[i]));
+#pragma unroll 1
+    for (int i = 16; i > 0; i >>= 1) m = add(m, shfl_xor(m, i));
+    m = add(Two{m.h * (1.0f / HD), m.l * (1.0f / HD)}, Two{eps, 0.f});
+    // 1 / sqrt(m) = r (1 + e / 2 + 3 e^2 / 8 ..), e = 1 - m r^2
+    const float r = rsqrtf(m.h);
+    const Two rr = mul(r, r);
+    const float e = fmaf(-m.h, rr.h, 1.f) - fmaf(m.h, rr.l, m.l * rr.h);
+    inv = renorm(r, r * e * fmaf(0.375f, e, 0.5f));
+  }
+  auto normed = [&](float y, float w) {
+    const Two u = mul(y, w), v = mul(u, inv.h);
+    return renorm(v.h, fmaf(u.h, inv.l, v.l));
+  };
+  Two v = normed(a, wa);
+  if (turned) v = add(mul(v, turn.x), mul(normed(b, wb), first ? -turn.y : turn.y));
+  // the run's largest magnitude: 16 lanes
+  Two m{fabsf(v.h), v.h < 0.f ? -v.l : v.l};
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const Two y = shfl_xor(m, o);
+    if (m.h == m.h && (!(y.h <= m.h) || (y.h == m.h && y.l > m.l))) m = y;  // (a NaN stays)
+  }
+  bool unused = false;
+  int sb = m.h <= 3.4028235e38f ? scale_byte<false>(__float_as_uint(m.h), unused) : kScaleNan;
+  if (sb != kScaleNan) {
+    // 7 times the middle to the scale above and to the one below
+    const float up = sb < kScaleMax ? (m.h - 3.5f * (scale_of(sb) + scale_of(sb + 1))) + m.l : -1.f;
+    const float down = sb > 0 ? (m.h - 3.5f * (scale_of(sb) + scale_of(sb - 1))) + m.l : 1.f;
+    if (up > 0.f || (up == 0.f && (sb & 1))) ++sb;
+    else if (down < 0.f || (down == 0.f && (sb & 1))) --sb;
+  }
+  int code = 8;
+  if (sb != 0 && sb != kScaleNan) {
+    const float s = scale_of(sb);
+    float c, inv_s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv_s) : "f"(s));
+    c = rintf(v.h * inv_s);  // (one off at most)
+    const float e = fmaf(-c, s, v.h), over = (e - 0.5f * s) + v.l, under = (e + 0.5f * s) + v.l;
+    const bool odd = (int)c & 1;
+    if (over > 0.f || (over == 0.f && odd)) c += 1.f;
+    else if (under < 0.f || (under == 0.f && odd)) c -= 1.f;
+    code = (int)fminf(fmaxf(c, -8.f), 7.f) + 8;
+  }
+  uint32_t word = (uint32_t)code << (4 * (lane & 7));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+  if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(at + (key ? k_word<HD>(pp, d >> 3) : v_word<HD>(pp, d >> 3))) = word;
+  if ((lane & 15) == 0) at[key ? k_scale<HD>(pp, d >> 4) : v_scale<HD>(pp, d >> 4)] = (uint8_t)sb;
+}
+
 // One CTA per token: HD / 8 lanes a row (head), eight values a lane, query heads first, then key and
 // value heads. Norm and rotation exchange values by shuffles inside the row, a scale's run is two
 // lanes. What bounds it: for prompts the bytes of the rows (the token's angles and norm weights are
@@ -218,6 +335,8 @@ struct Raw {
 template <int HD, bool F32, int T>
 __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
   constexpr int LPR = HD / 8, SLOTS = T / LPR, R = 3;
+  __shared__ uint32_t todo[64];  // a bit a row of keys (1024 at most), and of values
+  bool any = false;
   const int tok = blockIdx.x, l = threadIdx.x % LPR, slot = threadIdx.x / LPR;
   const int per_tok = p.hq + 2 * p.c.hkv;
   Raw<F32> raw[R];
@@ -231,6 +350,8 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
     }
   };
   fetch(0);
+  if (threadIdx.x < 64) todo[threadIdx.x] = 0;
+  __syncthreads();
   int j = 0;
   const int b = seq_of_warp(p.s, tok, j);
   if (b < 0) return;
@@ -297,6 +418,7 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
           for (int k = 0; k < 8; ++k) x[k] = x[k] * inv * w[k];
         }
       }
+      const bool keys = (p.kn || turns) && __any_sync(0xffffffffu, kind == 1 && in);  // (some, with roundings behind them)
       if (turns) {
         if (p.inter) {
           if (mine && kind < 2) {
@@ -322,15 +444,41 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) mag = max(mag, __float_as_uint(x[k]) & 0x7FFFFFFFu);
       mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+      int sb;
+      uint32_t word;
+      bool near = false;
+      if (keys || F32) {  // (bf16 values as they are lie on a middle or well beside it, fp32 ones may be just beside)
+        sb = scale_byte<true>(mag, near);
+        word = code_word<true>(x, sb == kScaleNan ? 0.f : scale_of(sb), near);
+        if (near && in && kind > 0 && !(kind == 1 && far) && (F32 || kind == 1)) {
+          atomicOr(&todo[(kind - 1) * 32 + (h >> 5)], 1u << (h & 31));
+          any = true;
+        }
+      } else {
+        sb = scale_byte<false>(mag, near);
+        word = code_word<false>(x, sb == kScaleNan ? 0.f : scale_of(sb), near);
+      }
       if (in && grp && (kind == 2 || (kind == 1 && !far))) {
         uint8_t* const at = grp + (size_t)h * gpp * group_bytes(HD);
-        const int sb = scale_byte(mag);
-        *reinterpret_cast<uint32_t*>(at + (kind == 1 ? k_word<HD>(pp, l) : v_word<HD>(pp, l))) =
-            code_word(x, sb == kScaleNan ? 0.f : scale_of(sb));
+        *reinterpret_cast<uint32_t*>(at + (kind == 1 ? k_word<HD>(pp, l) : v_word<HD>(pp, l))) = word;
         if ((l & 1) == 0) at[kind == 1 ? k_scale<HD>(pp, l >> 1) : v_scale<HD>(pp, l >> 1)] = (uint8_t)sb;
       }
     }
   }
+  if (!__syncthreads_or(any) || !grp) return;
+  // ---- rows with a choice left open: 32 values a warp
+  constexpr int PARTS = HD / 32;
+  const int warp = threadIdx.x / 32;
+  for (int i = 0, n = 0, words = (p.c.hkv + 31) / 32; i < 2 * words; ++i)
+    for (uint32_t m = todo[i < words ? i : 32 + i - words]; m; m &= m - 1, ++n) {
+      if (n % (T / 32 / PARTS) != warp / PARTS) continue;
+      const bool key = i < words;
+      const int h = (key ? i : i - words) * 32 + __ffs(m) - 1;
+      const Rows& in = key ? p.k : p.v;
+      settle_row<HD, F32>(static_cast<const char*>(in.p) + (tok * in.ts + h * in.hs) * (F32 ? 4 : 2), key ? p.kn : nullptr,
+                          p.eps, reinterpret_cast<const float2*>(p.rope + (long long)pos * p.rot), key && turns ? p.rot : 0,
+                          p.inter != 0, key, pp, warp % PARTS * 32, grp + (size_t)h * gpp * group_bytes(HD));
+    }
 }
 
 // Eight values of a word of codes at scale byte sb, as bf16: (code + 8) enters the low mantissa bits of

@@ -96,6 +96,60 @@ def test_append_and_gather(hd, hq, hkv, page, dtype, norm, rot, inter, new, lens
     assert changed <= n * hkv * 2 * (hd // 2 + hd // 16)
 
 
+@pytest.mark.parametrize("hd,dtype,norm,rot,inter", [(128, BF, True, 128, False), (128, F32, True, 64, True),
+                                                     (64, BF, False, 64, False), (64, F32, False, 0, False)])
+def test_codes_are_those_of_the_formula(hd, dtype, norm, rot, inter):
+    """Millions of values, so that some fall within fp32's error of the border between two codes or scales: every
+    one is held as the formula in 64 bits says. (An empty row and one with a NaN among them.)"""
+    from latency_moe_decode_gb300 import ops
+    n, hkv = 2 ** 18 // hd, 8
+    g = torch.Generator().manual_seed(hd)
+    k, v = (_rnd(g, n, hkv, hd, dtype=dtype, scale=2.0) for _ in range(2))
+    k[3, 1], v[5, 2, 20] = 0, float("nan")
+    k[7, 3, 1] *= 1e4
+    kn = (1 + 0.2 * torch.randn(hd, generator=g)).to(BF) if norm else None
+    rope = ops.rope_table(n, rot, 1e6) if rot else None
+    cache, table = _cache([n], hkv, hd, 64)
+    cache.append(k.cuda(), v.cuda(), _ints([0]), table, cu_tokens=_cu([n]), k_norm=None if kn is None else kn.cuda(),
+                 rope=rope, interleaved=inter)
+    gk, gv = (_np(t) for t in cache.gather(_ints([0]), table, n, cu_tokens=_cu([n])))
+    cache.check()
+    want = ref.norm_rotate(_np(k), None if kn is None else _np(kn), 1e-6, None if rope is None else _np(rope), np.arange(n),
+                           inter)
+    for got, x in ((gk, want), (gv, _np(v))):
+        held = ref.store(x)[0]
+        wrong = ~((got == held) | (np.isnan(got) & np.isnan(held)))
+        assert not wrong.any(), (wrong.sum(), got[wrong][:4], held[wrong][:4])
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_on_the_border_between_codes(hd, dtype):
+    """Keys (rotated by nothing: cos 1, sin 0) and values with runs on a middle between two codes, or between two
+    scales, and just beside it, next to runs of zeros, tiny ones, NaNs and infinities."""
+    n, hkv = 64, 40
+    x = torch.zeros(n, hkv, hd)
+    x[..., :16] = (torch.arange(16) - 7.5).clamp(-6.5, 6.5)
+    x[..., 15] = 7
+    x[:, ::2, 5] = 7 * 17 / 16              # between scales 1 and 1.125
+    x[:, ::3, 16 + 3] = float("nan")
+    x[:, 1::3, 32:48] = 2.0 ** -15 * torch.arange(16)
+    x[:, 2::5, -1] = float("inf")
+    x[:, 1::5, -2] = -1e5
+    if dtype == F32:
+        step = torch.arange(n)[:, None, None] - n // 2
+        x[..., :16] *= 1 + 2.0 ** -23 * step
+    x = x.to(dtype)
+    rope = torch.tensor([1.0, 0.0]).repeat(n, hd // 2, 1).cuda()
+    cache, table = _cache([n], hkv, hd, 16)
+    cache.append(x.cuda(), x.cuda(), _ints([0]), table, cu_tokens=_cu([n]), rope=rope)
+    with np.errstate(invalid="ignore"):  # (0 times what is not finite)
+        turned = ref.norm_rotate(_np(x), None, 0.0, _np(rope), np.arange(n), False)
+    for got, want in zip(cache.gather(_ints([0]), table, n, cu_tokens=_cu([n])), (turned, _np(x))):
+        assert np.array_equal(_np(got), ref.store(want)[0], equal_nan=True)
+    cache.check()
+
+
 def test_append_takes_strides_and_leaves_other_rows():
     """q, k, v as slices of one projection, q_out a slice of a wider buffer, rows before the first and
     behind the last sequence, an empty sequence between two."""
