@@ -146,22 +146,14 @@ __device__ __forceinline__ uint8_t* group_at(const Cache& c, const Seqs& s, int 
   return c.pages + (((size_t)page * c.hkv + h) * gpp + ((pos >> 4) & (gpp - 1))) * group_bytes(HD);
 }
 
-// Eight consecutive values of a row in fp32.
-template <bool F32>
-__device__ __forceinline__ void load8(const void* p, long long at, float (&x)[8]) {
-  if (F32) {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 a = f[0], b = f[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive bf16 values in fp32.
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
 __device__ __forceinline__ uint4 pack8_bf16(const float (&x)[8]) {
@@ -227,7 +219,7 @@ struct Raw {
 };
 
 // The unevaluated sum of two floats, about 46 bits (64-bit arithmetic runs at a hundredth of fp32's rate
-// here: one row settled in it took 12 us).
+// here: a row settled in it took 12 us, and takes 2 like this).
 struct Two {
   float h, l;
 };
@@ -327,11 +319,14 @@ __device__ __noinline__ void settle_row(const void* x, const uint16_t* nw, float
 
 // One CTA per token: HD / 8 lanes a row (head), eight values a lane, query heads first, then key and
 // value heads. Norm and rotation exchange values by shuffles inside the row, a scale's run is two
-// lanes. What bounds it: for prompts the bytes of the rows (the token's angles and norm weights are
-// read once for all its heads, the rows ahead of the position that they wait for); for single tokens
-// the chain bounds -> length -> page, 2 to 3 us.
-// CTAs of 256 threads while they leave SMs empty, of 128 beyond: what precedes the rows costs every
-// warp alike (8 k tokens of 32 + 16 heads of 128: 77 us with 256 and IEEE quotients and roots).
+// lanes. What bounds it: for prompts the instructions (310 a warp for two rows, issue slots
+// 75 to 80 % full; the bytes would take half the time; packed fp32 pairs changed nothing). The token's
+// angles and norm weights are read once for all its heads, the rows ahead of the position that they wait
+// for. For single tokens the chain bounds -> length -> page, 2 to 3 us.
+// CTAs of 256 threads while the SMs hold them all at once (four each), of 128 beyond: what precedes the
+// rows costs every warp alike. 256 against 128 threads, 32 + 16 heads of 128: one token 4.2 us against
+// 5.7, 304 5.1 / 6.4, 608 8.6 / 8.6, 1216 13.6 / 12.4 (8 k tokens: 59; with 256 and IEEE quotients 77. Of the
+// 59, looking for choices left open takes 3, settling them 1).
 template <int HD, bool F32, int T>
 __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
   constexpr int LPR = HD / 8, SLOTS = T / LPR, R = 3;
@@ -413,7 +408,7 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
           float inv = rsqrtf(m);
           inv = inv * fmaf(-0.5f * m * inv, inv, 1.5f);  // (one step: to the last place or two)
           float w[8];
-          load8<false>(nw, l * 8, w);
+          load8(nw + l * 8, w);
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[k] = x[k] * inv * w[k];
         }

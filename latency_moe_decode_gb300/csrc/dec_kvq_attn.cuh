@@ -17,6 +17,9 @@
 //    movmatrix; the running maximum and sum stay in fp32 registers;
 //  - what a warp leaves unfinished of a unit is joined per CTA in shared memory, and what a CTA
 //    leaves unfinished by a second small kernel, both in a fixed order.
+// Measured (32 query, 8 KV heads of 128, one row a sequence): 16 sequences of 32 k 81 us (4.5 TB/s; ALU pipe 51 %, issue slots 60 %); 64 of 2 k and one of 64 k 29 us, of which 14 are
+// the stream and 15 are fixed: list and page table 3, a unit's queries 3, the first chunk's code and
+// data 3, joins 6. Cutting the joins' dependent loads to one round did not shorten them.
 #pragma once
 #include <type_traits>
 
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t sh_scan[K::WARPS];
   // what the warps leave unfinished, in the list's order: two entries a warp (a unit it found begun, a
-  // unit it left open). First and last + 1 list entry of the unit; its place (see Place)
+  // unit it left open). First and last + 1 list entry of the unit; its place
   __shared__ uint2 ent_unit[32];
   __shared__ int4 ent_place[32];
   __shared__ uint64_t bars[K::WARPS][kStages];  // chunk landed

@@ -17,6 +17,9 @@
 //    exponentials follows the maximum only when that passes it by 2^8 (O lies in tensor memory, and
 //    rescaling it costs as much as the exponentials). With whole rows and two reads of the scores, four
 //    warps took 6.7 k cycles a tile for this; the exponentials' own floor is 1 k.
+// Measured (32 query, 8 KV heads of 128): 2 chunks of 256 rows on 4 k 59 us, 580 TFLOP/s; 2048 rows on 2 k
+// 185 us. A tile takes 2.7 k cycles, 1 k of them on the tensor cores: decoding and exponentials take turns
+// at the same issue slots, 1.8 k each. A unit's begin and end take 10 k cycles more.
 #pragma once
 #include "dec_kvq_attn.cuh"
 
