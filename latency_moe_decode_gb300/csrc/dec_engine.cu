@@ -1221,9 +1221,14 @@ dec_status op_failed(dec_engine* e, dec_status s) { return fail(e, s, dec_op_err
 dec_status check_caches(dec_engine* e, const dec_kvq_cache* caches) {
   const dec_model_cfg& c = e->cfg;
   if (!caches) return fail(e, DEC_ERR_ARG, "caches: NULL");
-  for (int l = 0; l < c.n_layers; ++l)
+  for (int l = 0; l < c.n_layers; ++l) {
     if (caches[l].n_kv_heads != c.n_kv_heads || caches[l].head_dim != c.head_dim)
       return fail(e, DEC_ERR_ARG, "caches: KV heads and head_dim must be the engine's, in every layer");
+    // (what the operators would refuse layer by layer, before anything is queued)
+    if (!caches[l].pages || !aligned16(caches[l].pages) || caches[l].n_pages < 1 ||
+        dec_kvq_page_bytes(caches[l].page_tokens, c.n_kv_heads, c.head_dim) == 0)
+      return fail(e, DEC_ERR_ARG, "caches: pages missing or misaligned, or a page size there is not");
+  }
   return DEC_OK;
 }
 
@@ -1303,7 +1308,7 @@ dec_status dec_step_kvq(dec_engine* e, const dec_step_kvq_args* a) {
     return fail(e, DEC_ERR_ARG, "hidden_in and hidden_out must be 16-byte aligned");
   if (!a->seqs || a->seqs->cu_tokens || a->seqs->batch != a->batch || a->seqs->n_tokens != a->batch)
     return fail(e, DEC_ERR_ARG, "seqs: one row per sequence, as many as the batch");
-  if (!a->seqs->lengths || !a->seqs->table || a->seqs->max_pages < 1)
+  if (!a->seqs->lengths || !a->seqs->table || a->seqs->max_pages < 1 || a->seqs->table_stride < 0)
     return fail(e, DEC_ERR_ARG, "seqs: lengths and table are needed");
   if ((a->rope != nullptr) != (a->rope_len > 0)) return fail(e, DEC_ERR_ARG, "rope and rope_len go together");
   if (dec_status cs = check_caches(e, a->caches)) return cs;

@@ -359,9 +359,10 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
   const int kind = kernel_of(c->head_dim, a->n_heads, c->n_kv_heads, max_tokens);
   if (a->workspace_bytes < dec_kvq_attention_workspace(c, a->n_heads, s->batch, max_tokens))
     return op_fail(DEC_ERR_ARG, "attention: workspace too small");
-  // entries of the kernels' lists, at most: 32-bit
-  const long long units = (long long)c->n_kv_heads * ((long long)s->n_tokens * p.group / 8 + s->batch);
-  if (units * ((long long)s->max_pages * c->page_tokens / kGroup + 1 + std::max(kUnitCost, kPromptCost)) >= (1LL << 32) - 64)
+  // entries of the kernel's list, at most: 32-bit
+  const int rows = kind == 0 ? 8 : kind == 1 ? 16 : 128, positions = kind == 2 ? kTile : kGroup;
+  const long long units = (long long)c->n_kv_heads * ((long long)s->n_tokens * p.group / rows + s->batch);
+  if (units * ((long long)s->max_pages * c->page_tokens / positions + 1 + std::max(kUnitCost, kPromptCost)) >= (1LL << 32) - 64)
     return op_fail(DEC_ERR_UNSUPPORTED, "attention: too much work for one call");
   return launch_attention(p, c->head_dim, kind, s->batch, static_cast<uint8_t*>(a->workspace), op_stream(stream));
 }

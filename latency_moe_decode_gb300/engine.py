@@ -218,8 +218,13 @@ class Engine:
         if rope is not None and (rope.dtype != torch.float32 or not rope.is_contiguous() or
                                  tuple(rope.shape[1:]) != (self.cfg.head_dim // 2, 2) or rope.device != caches[0].device):
             raise ValueError("rope must be contiguous float32 [positions, head_dim / 2, 2] on the caches' device")
-        arr = self._caches(caches)
-        a = DecStepKvqArgs(_ptr(tokens), _ptr(hidden), lengths.shape[0], arr, C.pointer(s), _ptr(rope),
+        arr, n, c = self._caches(caches), lengths.shape[0], self.cfg
+        for name, t, dtype, per in (("tokens", tokens, torch.int32, 1), ("hidden", hidden, torch.bfloat16, c.hidden),
+                                    ("logits", logits, torch.float32, c.vocab), ("next_tokens", next_tokens, torch.int32, 1),
+                                    ("hidden_out", hidden_out, torch.bfloat16, c.hidden)):
+            if t is not None and (t.dtype != dtype or t.numel() < n * per or not t.is_contiguous() or t.device != caches[0].device):
+                raise ValueError(f"{name} must be contiguous {dtype} of {n} rows on {caches[0].device}")
+        a = DecStepKvqArgs(_ptr(tokens), _ptr(hidden), n, arr, C.pointer(s), _ptr(rope),
                            0 if rope is None else rope.shape[0], _ptr(logits), _ptr(next_tokens), _ptr(hidden_out),
                            _stream_ptr(stream if stream is not None else torch.cuda.current_stream()))
         self._check(self.lib.dec_step_kvq(self.h, C.byref(a)), "dec_step_kvq")

@@ -47,7 +47,7 @@ def _readable(t: torch.Tensor) -> torch.Tensor:
     per = 16 // t.element_size()
     s0, s1, s2 = t.stride()
     if s2 != 1 or s0 % per or s1 % per or t.data_ptr() % 16:
-        t = t.clone() if t.is_contiguous() else t.contiguous()
+        t = t.clone(memory_format=torch.contiguous_format)
     return t
 
 
@@ -250,6 +250,8 @@ def logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, top_n
     if dt is None or len(shape) != 2 or not logits.is_cuda:
         raise ValueError("logits must be bfloat16 or float32 [rows, vocab] on a CUDA device")
     rows, vocab = shape
+    if rows >= 2 ** 31 or vocab >= 2 ** 31:
+        raise ValueError("logits: 2^31 rows or ids")
     s0, s1 = logits.stride()
     if s1 != 1 and vocab > 1:
         logits = logits.contiguous()

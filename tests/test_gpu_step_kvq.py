@@ -227,6 +227,9 @@ def test_refusals_of_steps_over_caches():
     for bad in (lambda: eng.step_kvq(caches[:1], _ints(lens), table, tokens=tok),
                 lambda: eng.step_kvq(other, _ints(lens), table, tokens=tok),
                 lambda: eng.step_kvq(caches, _ints(lens), table),
+                lambda: eng.step_kvq(caches, _ints(lens), table, tokens=tok[:4]),
+                lambda: eng.step_kvq(caches, _ints(lens), table, tokens=tok.long()),
+                lambda: eng.step_kvq(caches, _ints(lens), table, tokens=tok, next_tokens=tok[:3]),
                 lambda: eng.step_kvq(caches, _ints(lens * 6), table.repeat(6, 1), tokens=tok.repeat(6)),
                 lambda: eng.step_kvq(caches, _ints(lens), table, tokens=tok, rope=torch.zeros(4, 8, 2, device="cuda")),
                 lambda: eng.kvq_store(99, caches, table[0].contiguous()),
@@ -234,6 +237,18 @@ def test_refusals_of_steps_over_caches():
                 lambda: eng.kvq_load(0, caches, table[0].contiguous(), 10000)):
         with pytest.raises((DecError, ValueError)):
             bad()
+    # a bad cache of the last layer is refused before anything is queued
+    import ctypes as C
+    from latency_moe_decode_gb300.capi import DecKvqCache, DecStepKvqArgs
+    pages = [k.pages.clone() for k in caches]
+    for field, value in (("pages", None), ("pages", caches[0].c.pages + 8), ("n_pages", 0), ("page_tokens", 24)):
+        arr = (DecKvqCache * len(caches))(*[k.c for k in caches])
+        setattr(arr[len(caches) - 1], field, value)
+        a = DecStepKvqArgs(tok.data_ptr(), None, 5, arr, C.pointer(caches[0]._seqs(_ints(lens), table, None, 5)), None, 0, None,
+                           None, None, None)
+        assert eng.lib.dec_step_kvq(eng.h, C.byref(a)) == -1
+    torch.cuda.synchronize()
+    assert all(torch.equal(k.pages, p) for k, p in zip(caches, pages))
     small = _engine(_models(DENSE, 3)[1], max_ctx=16, max_batch=1)  # no wide kernels
     with pytest.raises(DecError) as e:
         small.step_kvq(caches, _ints([0]), table[:1], tokens=_ints([1]))

@@ -112,6 +112,18 @@ def test_nothing_to_do(lib):
     assert lib.dec_op_error() == b""
 
 
+def test_readable_copies_odd_strides():
+    import torch
+    from latency_moe_decode_gb300 import ops
+    b = torch.arange(5000).to(torch.bfloat16)
+    for t in (torch.as_strided(b, (1, 8, 128), (1027, 128, 1)), torch.as_strided(b, (2, 8, 128), (1027, 128, 1)),
+              b[1:1025].view(1, 8, 128), torch.as_strided(b, (2, 4, 128), (1024, 256, 2))):
+        r = ops._readable(t)
+        assert torch.equal(r, t) and all(x % 8 == 0 for x in r.stride()[:2]) and r.stride(2) == 1 and r.data_ptr() % 16 == 0
+    t = b[:2048].view(2, 8, 128)
+    assert ops._readable(t) is t
+
+
 def test_workspace_sizes(lib):
     w = lib.dec_kvq_attention_workspace
     for bad in (dict(head_dim=96), dict(page_tokens=3), dict(n_kv_heads=0)):
