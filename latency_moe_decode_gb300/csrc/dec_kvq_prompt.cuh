@@ -21,6 +21,7 @@
 // 185 us. A tile takes 2.7 k cycles, 1 k of them on the tensor cores: decoding and exponentials take turns
 // at the same issue slots, 1.8 k each. A unit's begin and end take 10 k cycles more.
 #pragma once
+#include "dec_f32x2.cuh"
 #include "dec_kvq_attn.cuh"
 
 namespace dec {
@@ -454,14 +455,14 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         if (m == -INFINITY || mx > m + 8.f) m = fmaxf(m, mx);
         const float z = (m == -INFINITY ? 0.f : m) - kPromptShift;
         uint32_t ph[32];
-        float l0 = 0.f, l1 = 0.f;
+        uint64_t l2 = 0;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int y = 0; y < 32; y += 2) {
-            const float a = ex2(fmaf(x[c][y], sc, -z)), b = ex2(fmaf(x[c][y + 1], sc, -z));
-            l0 += a;
-            l1 += b;
+            const float2 t = halves(fma2(pair(x[c][y], x[c][y + 1]), pair(sc, sc), pair(-z, -z)));
+            const float a = ex2(t.x), b = ex2(t.y);
+            l2 = add2(l2, pair(a, b));
             ph[c * 16 + y / 2] = h2u(__floats2half2_rn(a, b));
           }
         // the products so far are done before their operands, or O, are written again
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
             tmem_st32(to + c * 32, o);
           }
         }
-        l += l0 + l1;
+        l += halves(l2).x + halves(l2).y;
         tmem_st16(tl + C::TP + half * 32, ph);
         tmem_st16(tl + C::TP + half * 32 + 16, ph + 16);
         tmem_st_wait();
