@@ -319,13 +319,13 @@ __device__ __noinline__ void settle_row(const void* x, const uint16_t* nw, float
 
 // One CTA per token: HD / 8 lanes a row (head), eight values a lane, query heads first, then key and
 // value heads. Norm and rotation exchange values by shuffles inside the row, a scale's run is two
-// lanes. What bounds it: for prompts the instructions (310 a warp for two rows, issue slots
+// lanes. What bounds it: for prompts the instructions (270 a warp for two rows, issue slots
 // 75 to 80 % full; the bytes would take half the time; packed fp32 pairs changed nothing). The token's
 // angles and norm weights are read once for all its heads, the rows ahead of the position that they wait
 // for. For single tokens the chain bounds -> length -> page, 2 to 3 us.
 // CTAs of 256 threads while the SMs hold them all at once (four each), of 128 beyond: what precedes the
 // rows costs every warp alike. 256 against 128 threads, 32 + 16 heads of 128: one token 4.2 us against
-// 5.7, 304 5.1 / 6.4, 608 8.6 / 8.6, 1216 13.6 / 12.4 (8 k tokens: 59; with 256 and IEEE quotients 77. Of the
+// 5.7, 304 5.1 / 6.4, 608 8.6 / 8.6, 1216 13.6 / 12.4 (9.3 k tokens: 59; with 256 and IEEE quotients 77. Of the
 // 59, looking for choices left open takes 3, settling them 1).
 template <int HD, bool F32, int T>
 __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {

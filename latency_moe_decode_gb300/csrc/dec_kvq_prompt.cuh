@@ -17,9 +17,10 @@
 //    exponentials follows the maximum only when that passes it by 2^8 (O lies in tensor memory, and
 //    rescaling it costs as much as the exponentials). With whole rows and two reads of the scores, four
 //    warps took 6.7 k cycles a tile for this; the exponentials' own floor is 1 k.
-// Measured (32 query, 8 KV heads of 128): 2 chunks of 256 rows on 4 k 59 us, 580 TFLOP/s; 2048 rows on 2 k
-// 185 us. A tile takes 2.7 k cycles, 1 k of them on the tensor cores: decoding and exponentials take turns
-// at the same issue slots, 1.8 k each. A unit's begin and end take 10 k cycles more.
+// Measured (32 query, 8 KV heads of 128): 2 chunks of 256 rows on 4 k 58 us, 600 TFLOP/s; 2048 rows on 2 k
+// 180 us. A tile takes 2.6 k cycles, 1 k of them on the tensor cores; softmax is busy for 1.8 k (0.9 k of
+// exponentials in all warps at once), decoding for 2 k; issue slots are 60 % full. Issuing whichever of the
+// next scores and the outputs is ready first changed nothing. A unit's begin and end take 10 k cycles more.
 #pragma once
 #include "dec_f32x2.cuh"
 #include "dec_kvq_attn.cuh"

@@ -73,7 +73,7 @@ def out_bounds(out, lse, mass, big, hd, seen):
     has them: terms e^(s - max) are kept times 2^15, and f16's subnormal step is 2^-24, so a term is off
     by half a step, 2^-25 / 2^15 = 2^-40 (of the largest term, 1, before the division by the sum), at
     least; times |v| and summed that is 2^-11 of `mass`'s second part, 2^-29 sum |v| / sum e^(s - max).
-    The kernel for prompts (64 query rows and more) keeps terms times 2^7 and lets the maximum lead its
+    The kernel for prompts (calls of many query rows) keeps terms times 2^7 and lets the maximum lead its
     reference by 2^8, so the largest term is kept as 2^7 at least: 2^-25 / 2^7 = 2^-32, kept = 2^-21."""
     d = hd * 2.0 ** -23 * big + 2.0 ** -14 / hd * big * 2.0 ** -9 + 2.0 ** -21 * (big + 1)
     n = 2.0 ** -23 * (np.sqrt(seen) * 8 + 32)
