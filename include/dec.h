@@ -415,8 +415,10 @@ int64_t dec_kvq_page_bytes(int32_t page_tokens, int32_t n_kv_heads, int32_t head
                 head are rotated: pair i is (i, i + rotary_dim / 2), or with interleaved != 0
                 (2i, 2i + 1): (a, b) -> (a cos - b sin, a sin + b cos)
      q_out      bf16 rows (may be q.p itself when that is bf16 with the same strides)
-   Everything is computed in fp32 and rounded once, to bf16 or to the cache's codes. The same
-   position must not be appended twice in one call. */
+   Everything is computed in fp32 and rounded once, to bf16 or to the cache's codes; keys whose fp32
+   value is too near the border between two codes or scales to tell are computed again with twice
+   the bits. Inputs above 1e18 overflow the norm's squares. The same position must not be
+   appended twice in one call. */
 typedef struct {
   dec_dtype dtype;
   int32_t n_heads;
