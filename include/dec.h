@@ -452,7 +452,8 @@ dec_status dec_kvq_gather(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, 
    A row with no position gives out = 0 and lse = -infinity. Scores, softmax statistics and the
    output sum are fp32; queries enter the products exactly (values below 2^-17 of their head's
    largest: to 2^-25 of it), probabilities with 11 bits. Rows that meet a bad page or a position
-   beyond the page table hold nothing of use, the other sequences' are right. A call of 2^31 query
+   beyond the page table hold nothing of use, the other sequences' are right. A call repeated
+   gives the same bits; a sequence in another batch may be cut and joined elsewhere. A call of 2^31 query
    rows or of a page table of 2^31 positions is DEC_ERR_UNSUPPORTED. */
 typedef struct {
   int32_t n_heads;
@@ -480,7 +481,9 @@ int64_t dec_kvq_attention_workspace(const dec_kvq_cache* cache, int32_t n_heads,
                   top_n <= DEC_MAX_TOP, <= vocab) and their log-probabilities
    Each output may be NULL (logprob and rank need targets). Logits of -infinity have probability
    0; a row with nothing else gives log-probabilities of -infinity and entropy 0. A row with a
-   NaN or +infinity gives NaN log-probabilities and entropy; a NaN orders as -infinity. */
+   NaN or +infinity gives NaN log-probabilities and entropy; a NaN orders as -infinity. Sums are
+   fp32: a call repeated gives the same bits, a row in a call of other sizes or at another
+   alignment may be summed in another order. */
 #define DEC_MAX_TOP 32
 typedef struct {
   const void* logits;

@@ -8,8 +8,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdec.so")
 SOURCES = ["dec_engine.cu", "dec_wide.cu", "dec_kvq.cu", "dec_logprobs.cu", "dec_step_kvq.cu"]
-HEADERS = ["dec_common.h", "dec_prims.cuh", "dec_kernel.cuh", "dec_wide.cuh", "dec_wide_host.h", "dec_kvq.cuh", "dec_kvq_attn.cuh", "dec_kvq_prompt.cuh",
-           "dec_f32x2.cuh", "dec_ops.h"]
+HEADERS = ["dec_common.h", "dec_prims.cuh", "dec_kernel.cuh", "dec_wide.cuh", "dec_wide_host.h", "dec_kvq.cuh", "dec_kvq_attn.cuh",
+           "dec_kvq_prompt.cuh", "dec_f32x2.cuh", "dec_ops.h"]
 
 
 def nvcc() -> str:

@@ -79,7 +79,8 @@ def _row_fields(*names):
 
 
 class DecKvqAppendArgs(C.Structure):
-    _fields_ = [("dtype", C.c_int), ("n_heads", C.c_int32), *_row_fields("q", "k", "v", "q_out"), ("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("eps", C.c_float),
+    _fields_ = [("dtype", C.c_int), ("n_heads", C.c_int32), *_row_fields("q", "k", "v", "q_out"),
+                ("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("eps", C.c_float),
                 ("rope", C.c_void_p), ("rope_len", C.c_int32), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32)]
 
 

@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
   const int other = mine && !p.inter ? (first ? l + half / 8 : l - half / 8) : l;
   float cs[8], sn[8];
   if (mine) {
-    const float4* t = reinterpret_cast<const float4*>(p.rope + (long long)pos * p.rot + (p.inter ? l * 8 : 2 * (first ? l * 8 : l * 8 - half)));
+    const float4* t = reinterpret_cast<const float4*>(p.rope + (long long)pos * p.rot +
+                                                      (p.inter ? l * 8 : 2 * (first ? l * 8 : l * 8 - half)));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (p.inter && i >= 2) break;

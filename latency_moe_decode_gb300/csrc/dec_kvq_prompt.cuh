@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         const int st = n % kPromptStages, pos = t * kTile + lane * kGroup;
         int gi = -1;
         if (lane < kTile / kGroup && pos < s.smax) {
-          const int page = pos >> p.c.page_shift < p.s.max_pages ? __ldg(p.s.table + s.b * p.s.table_stride + (pos >> p.c.page_shift)) : -1;
+          const int e = pos >> p.c.page_shift;
+          const int page = e < p.s.max_pages ? __ldg(p.s.table + s.b * p.s.table_stride + e) : -1;
           if ((unsigned)page < (unsigned)p.c.n_pages) gi = (page * p.c.hkv + s.h) * gpp + ((pos >> 4) & (gpp - 1));
           else raise(p.c.status, DEC_ERR_ARG);
         }

@@ -452,6 +452,29 @@ def test_two_streams_at_once_and_repeats_agree():
     assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l in got)
 
 
+@pytest.mark.parametrize("m", [1, 3, 30])
+def test_pages_beyond_four_gigabytes(m):
+    """Pages at the end of a pool of 5.9 GB hold and give what pages at the start of a small one do."""
+    from latency_moe_decode_gb300 import ops
+    g = torch.Generator().manual_seed(71)
+    hkv, hq, hd, page, lens = 8, 32, 128, 256, [700, 3]
+    far = ops.KvqCache(20000, hkv, hd, page)
+    near = ops.KvqCache(6, hkv, hd, page)
+    tables = _ints([[19999, 14570, 19998], [19997, 14569, 14568]]), _ints([[0, 1, 2], [3, 4, 5]])
+    k, v = (_rnd(g, sum(lens), hkv, hd).cuda() for _ in range(2))
+    kn, vn = (_rnd(g, 2 * m, hkv, hd).cuda() for _ in range(2))
+    q = _rnd(g, 2 * m, hq, hd).cuda()
+    got = []
+    for cache, table in zip((far, near), tables):
+        cache.append(k, v, _ints([0, 0]), table, cu_tokens=_cu(lens))
+        cache.append(kn, vn, _ints(lens), table, cu_tokens=_cu([m, m]))
+        got.append((*cache.attention(q, _ints(lens), table, cu_tokens=_cu([m, m]), max_tokens=m, return_lse=True),
+                    *cache.gather(_ints([0, 0]), table, sum(lens), cu_tokens=_cu(lens))))
+        cache.check()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert got[0][0].abs().sum() > 0
+
+
 def _prompts(m, hd=128, hq=8, hkv=2, seed=61):
     """Three sequences of m, 1 and 2 m new tokens, which each of the kernels takes for some m."""
     new, lens = [m, 1, 2 * m], [300, 20, 0]

@@ -36,9 +36,10 @@ def _close(got, want, tol):
     assert (np.abs(got[fin] - want[fin]) <= np.broadcast_to(tol, want.shape)[fin]).all()
 
 
-def _check(x, t, n):
+def _check(x, t, n, r=None):
     from latency_moe_decode_gb300 import ops
-    r = ops.logprobs(x, None if t is None else torch.from_numpy(t).cuda(), top_n=n)
+    if r is None:
+        r = ops.logprobs(x, None if t is None else torch.from_numpy(t).cuda(), top_n=n)
     tt = np.zeros(len(x), np.int32) if t is None else t
     mine, rank, ent, ids, tops, lse = _ref(x, tt, n)
     # sums of up to `vocab` fp32 terms by chains of at most a few hundred, exponentials of arguments
@@ -108,6 +109,21 @@ def test_strided_and_unaligned_rows(dtype):
     t = _targets(g, 6, 2999)
     for x in (big[:, 1:3000], big[:, :2999], big[::2, 2:], big[:, ::3][:, :900]):
         _check(x, np.minimum(t, x.shape[1] - 1)[:len(x)], 7)
+
+
+def test_rows_beyond_32_bit_offsets():
+    from latency_moe_decode_gb300 import ops
+    g = torch.Generator().manual_seed(5)
+    rows, vocab = 70000, 32001  # 2.2 thousand million elements
+    x = torch.zeros(rows, vocab, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = (3 * torch.randn(3, vocab, generator=g)).to(torch.bfloat16).cuda()
+    t = torch.full((rows,), 7, dtype=torch.int32, device="cuda")
+    r = ops.logprobs(x, t, top_n=4)
+    # (against the 64-bit form: a copy of the rows elsewhere is summed in another order, since a thread's
+    # vectors are the row's aligned ones)
+    _check(x[-3:], t[-3:].cpu().numpy(), 4, ops.LogProbs(*(a[-3:] for a in r)))
+    assert (r.rank[:-3] == 7).all() and (r.top_ids[:-3] == torch.arange(4, device="cuda")).all()
+    assert (r.logprob[:-3] + np.log(vocab)).abs().max().item() < 2.0 ** -24 * (16 + np.log(vocab) * 4 + np.sqrt(vocab))
 
 
 def test_captured_and_on_two_streams():
