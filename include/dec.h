@@ -540,8 +540,16 @@ dec_status dec_step_kvq(dec_engine* eng, const dec_step_kvq_args* args);
 /* Move a sequence between the engine's bf16 cache and pages: store writes positions 0 .. length - 1
    of slot seq into the pages of `table` (device int32 [max_pages], page p holding positions p *
    page_tokens on) of every layer's cache; load reads `length` positions back into a slot and sets
-   its length. Keys are stored as the engine holds them, rotated. Both synchronise (and report what
-   the kernels found wrong in a status word only through the caches). */
+   its length. Keys are stored as the engine holds them, rotated. Queued on `stream`, behind what the
+   caller has queued there on the pages and the table; synchronised before return (what the
+   kernels found wrong is reported only in the caches' status words). Without a stream they are queued on
+   the engine's own: nothing of the caller's is waited for then, so the table has to be written and
+   other work on the pages done before the call. */
+dec_status dec_kvq_store_ex(dec_engine* eng, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
+                            int32_t max_pages, void* stream);
+dec_status dec_kvq_load_ex(dec_engine* eng, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
+                           int32_t max_pages, int32_t length, void* stream);
+/* The same with stream = NULL. */
 dec_status dec_kvq_store(dec_engine* eng, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
                          int32_t max_pages);
 dec_status dec_kvq_load(dec_engine* eng, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,

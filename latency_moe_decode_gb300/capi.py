@@ -151,6 +151,9 @@ PROTOTYPES = {
     "dec_step_kvq": (C.c_int, [C.c_void_p, C.POINTER(DecStepKvqArgs)]),
     "dec_kvq_store": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(DecKvqCache), C.c_void_p, C.c_int32]),
     "dec_kvq_load": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(DecKvqCache), C.c_void_p, C.c_int32, C.c_int32]),
+    "dec_kvq_store_ex": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(DecKvqCache), C.c_void_p, C.c_int32, C.c_void_p]),
+    "dec_kvq_load_ex": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(DecKvqCache), C.c_void_p, C.c_int32, C.c_int32,
+                                  C.c_void_p]),
     "dec_score": (C.c_int, [C.c_void_p, C.POINTER(DecScoreArgs)]),
 }
 

@@ -1250,9 +1250,10 @@ dec_status kvq_buffers(dec_engine* e, const dec_kvq_cache* any) {
   return DEC_OK;
 }
 
-// Positions [0, n) of a slot as rows, and the sequence they make: store (to pages) or load (from them).
+// Positions [0, n) of a slot as rows, and the sequence they make: store (to pages) or load (from them), on
+// stream s: that is where the caller's own work on the pages and the table is queued.
 dec_status kvq_move(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, const int32_t* table, int32_t max_pages,
-                    int32_t n, bool store) {
+                    int32_t n, bool store, cudaStream_t s) {
   const dec_model_cfg& c = e->cfg;
   if (n == 0) return DEC_OK;
   if (!table || max_pages < 1) return fail(e, DEC_ERR_ARG, "page table missing");
@@ -1260,9 +1261,9 @@ dec_status kvq_move(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, con
     if ((long long)max_pages * caches[l].page_tokens < n) return fail(e, DEC_ERR_CAPACITY, "the page table is too short");
   if (!e->kvq_idx)
     if (dec_status st = dalloc(e, &e->kvq_idx, sizeof(int32_t) * 4, &e->ws_bytes)) return st;
-  if (dec_status os = order_on(e, e->stream)) return os;
+  if (dec_status os = order_on(e, s)) return os;
   const int32_t idx[4] = {0, n, 0, 0};  // cu_tokens, lengths
-  DEC_CUDA(cudaMemcpyAsync(e->kvq_idx, idx, sizeof idx, cudaMemcpyHostToDevice, e->stream));
+  DEC_CUDA(cudaMemcpyAsync(e->kvq_idx, idx, sizeof idx, cudaMemcpyHostToDevice, s));
   dec_kvq_seqs sq{};
   sq.batch = 1;
   sq.n_tokens = n;
@@ -1281,12 +1282,12 @@ dec_status kvq_move(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, con
       a.dtype = DEC_BF16;
       a.k = k;
       a.v = v;
-      st = dec_kvq_append(&caches[l], &sq, &a, e->stream);
+      st = dec_kvq_append(&caches[l], &sq, &a, s);
     } else {
-      st = dec_kvq_gather(&caches[l], &sq, &k, &v, e->stream);
+      st = dec_kvq_gather(&caches[l], &sq, &k, &v, s);
     }
   }
-  DEC_CUDA(cudaStreamSynchronize(e->stream));
+  DEC_CUDA(cudaStreamSynchronize(s));
   return st == DEC_OK ? DEC_OK : op_failed(e, st);
 }
 
@@ -1373,26 +1374,39 @@ dec_status dec_step_kvq(dec_engine* e, const dec_step_kvq_args* a) {
   return DEC_OK;
 }
 
-dec_status dec_kvq_store(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
-                         int32_t max_pages) {
+dec_status dec_kvq_store_ex(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
+                            int32_t max_pages, void* stream) {
   if (!e) return DEC_ERR_ARG;
   if (e->poisoned) return fail(e, DEC_ERR_POISONED, "engine poisoned");
   if (dec_status ds = check_device(e)) return ds;
   if (seq < 0 || seq >= e->cfg.max_batch) return fail(e, DEC_ERR_ARG, "seq out of range");
   if (dec_status cs = check_caches(e, caches)) return cs;
-  return kvq_move(e, seq, caches, table, max_pages, e->lengths[seq], true);
+  return kvq_move(e, seq, caches, table, max_pages, e->lengths[seq], true,
+                  stream ? static_cast<cudaStream_t>(stream) : e->stream);
 }
 
-dec_status dec_kvq_load(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
-                        int32_t max_pages, int32_t length) {
+dec_status dec_kvq_store(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
+                         int32_t max_pages) {
+  return dec_kvq_store_ex(e, seq, caches, table, max_pages, nullptr);
+}
+
+dec_status dec_kvq_load_ex(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
+                           int32_t max_pages, int32_t length, void* stream) {
   if (!e) return DEC_ERR_ARG;
   if (e->poisoned) return fail(e, DEC_ERR_POISONED, "engine poisoned");
   if (dec_status ds = check_device(e)) return ds;
   if (seq < 0 || seq >= e->cfg.max_batch || length < 0) return fail(e, DEC_ERR_ARG, "seq or length out of range");
   if (length > e->cfg.max_ctx) return fail(e, DEC_ERR_CAPACITY, "load longer than max_ctx");
   if (dec_status cs = check_caches(e, caches)) return cs;
-  if (dec_status st = kvq_move(e, seq, caches, table, max_pages, length, false)) return st;
+  if (dec_status st = kvq_move(e, seq, caches, table, max_pages, length, false,
+                               stream ? static_cast<cudaStream_t>(stream) : e->stream))
+    return st;
   return dec_set_length(e, seq, length);
+}
+
+dec_status dec_kvq_load(dec_engine* e, int32_t seq, const dec_kvq_cache* caches, const int32_t* table,
+                        int32_t max_pages, int32_t length) {
+  return dec_kvq_load_ex(e, seq, caches, table, max_pages, length, nullptr);
 }
 
 dec_status dec_score(dec_engine* e, const dec_score_args* a) {

@@ -198,15 +198,20 @@ class Engine:
             raise ValueError("table must be a contiguous int32 vector of page ids on the caches' device")
         return table
 
-    def kvq_store(self, seq: int, caches: List[ops.KvqCache], table: torch.Tensor):
-        """Write slot seq's positions into the pages of `table` (device int32 [pages]) of every cache."""
+    def kvq_store(self, seq: int, caches: List[ops.KvqCache], table: torch.Tensor, stream=None):
+        """Write slot seq's positions into the pages of `table` (device int32 [pages]) of every cache, on
+        `stream` (default: torch's current stream), behind what is queued there; waits for the end."""
         arr, t = self._caches(caches), self._table(caches, table)
-        self._check(self.lib.dec_kvq_store(self.h, seq, arr, t.data_ptr(), t.numel()), "dec_kvq_store")
+        self._check(self.lib.dec_kvq_store_ex(self.h, seq, arr, t.data_ptr(), t.numel(),
+                                              _stream_ptr(stream if stream is not None else torch.cuda.current_stream())),
+                    "dec_kvq_store_ex")
 
-    def kvq_load(self, seq: int, caches: List[ops.KvqCache], table: torch.Tensor, length: int):
-        """Read `length` positions back into slot seq."""
+    def kvq_load(self, seq: int, caches: List[ops.KvqCache], table: torch.Tensor, length: int, stream=None):
+        """Read `length` positions back into slot seq, on `stream` as kvq_store."""
         arr, t = self._caches(caches), self._table(caches, table)
-        self._check(self.lib.dec_kvq_load(self.h, seq, arr, t.data_ptr(), t.numel(), length), "dec_kvq_load")
+        self._check(self.lib.dec_kvq_load_ex(self.h, seq, arr, t.data_ptr(), t.numel(), length,
+                                             _stream_ptr(stream if stream is not None else torch.cuda.current_stream())),
+                    "dec_kvq_load_ex")
 
     def step_kvq(self, caches: List[ops.KvqCache], lengths: torch.Tensor, table: torch.Tensor,
                  tokens: Optional[torch.Tensor] = None, hidden: Optional[torch.Tensor] = None,
