@@ -481,7 +481,9 @@ int64_t dec_kvq_attention_workspace(const dec_kvq_cache* cache, int32_t n_heads,
                   top_n <= DEC_MAX_TOP, <= vocab) and their log-probabilities
    Each output may be NULL (logprob and rank need targets). Logits of -infinity have probability
    0; a row with nothing else gives log-probabilities of -infinity and entropy 0. A row with a
-   NaN or +infinity gives NaN log-probabilities and entropy; a NaN orders as -infinity. Sums are
+   NaN or +infinity gives NaN log-probabilities and entropy; a NaN orders as -infinity.
+   Log-probabilities are at most 0 and entropies at least 0, and their error does not grow with a
+   common offset of the logits. (Rows whose largest logit is 8192 and more in magnitude are read twice.) Sums are
    fp32: a call repeated gives the same bits, a row in a call of other sizes or at another
    alignment may be summed in another order. */
 #define DEC_MAX_TOP 32

@@ -1,11 +1,14 @@
 // Log-probabilities of rows of logits (dec_logprobs of dec.h).
 //
 // One pass over the row, which is read once from memory:
-//  - every thread keeps a reference m, s = sum 2^t and u = sum 2^t t with t = (x - m) log2(e) of its own
-//    elements, so nothing is exchanged while the row streams. The reference is the maximum of the
-//    thread's first elements and follows only what passes it by more than 40 (fp32 holds 2^58 times
-//    a vocabulary): following every new maximum costs a warp a rescale at almost every vector. Joined
-//    at the row's maximum M, lse = M + ln S and the entropy is ln 2 (log2 S - U / S);
+//  - every thread keeps a reference z, s = sum 2^t and u = sum 2^t t with t = x log2(e) - z of its own
+//    elements, so nothing is exchanged while the row streams. z is a multiple of 8 that follows the thread's
+//    maximum, set 8 to 16 above what passes it: one fma gives t with one rounding whatever offset the logits
+//    have, sums are rescaled by powers of two, and seldom (set to the next multiple instead, that cost one row of 32000
+//    0.7 us), and the largest term, which is all there is of a confident row, has t in -16 .. 0. Threads
+//    and CTAs are joined at the largest z. With the row's maximum M, ls = lse - M = ln 2 (log2 S - (M log2(e) - z))
+//    is at least 0, a log-probability (x - M) - ls at most 0, the entropy ln 2 (log2 S - U / S). Rows whose
+//    maximum lies at or beyond +-8192 are summed in a second pass, relative to M itself;
 //  - the target's rank is counted on the way: elements before the target's id need x >= x_target,
 //    which is x > the next smaller number, so both sides are one comparison with their own bound;
 //  - the alternatives come from a bound: of 32 groups of threads, each knows its largest element, and
@@ -46,6 +49,9 @@ constexpr int kItems = 512;     // vectors to look at again
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr float kL2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kStep = 8.f, kRoom = 1.f;  // references are multiples of kStep, set with room for kRoom kSteps more
+constexpr float kFar = 8192.f;    // rows whose maximum reaches this magnitude are summed relative to it
+constexpr float kNone = -32768.f; // the reference of no elements
 
 // The order of (logit, id): larger logit first, then lower id, as an unsigned key; -0 is 0.
 __device__ __forceinline__ unsigned long long key_of(float x, int id) {
@@ -163,27 +169,33 @@ struct Row {
   }
 };
 
-// A row's sums over some of its elements: reference, sum of 2^t and of 2^t t, t = (x - m) log2(e).
+// A row's sums over some of its elements: reference, sum of 2^t and of 2^t t, t = x log2(e) - z; and their
+// maximum.
 struct Sums {
-  float m, s, u;
-  __device__ __forceinline__ void raise(float to) {  // (to > m)
-    const float d = fmaxf((m - to) * kL2E, -256.f);
-    const float f = m == -INFINITY ? 0.f : ex2(d);
-    u = m == -INFINITY ? 0.f : f * fmaf(s, d, u);
+  float z, s, u, m;
+  __device__ __forceinline__ void raise(float to) {  // (to > z)
+    const float d = fmaxf(z - to, -256.f), f = ex2(d);
+    u = f * fmaf(s, d, u);
     s *= f;
-    m = to;
+    z = to;
   }
-  // the warp's joined sums, in every lane
-  __device__ __forceinline__ void join_warp() {
-    float to = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
-    if (to > m) raise(to);
+  __device__ __forceinline__ void add_lanes() {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       s += __shfl_xor_sync(0xffffffffu, s, o);
       u += __shfl_xor_sync(0xffffffffu, u, o);
     }
+  }
+  // the warp's joined sums, in every lane
+  __device__ __forceinline__ void join_warp() {
+    float to = z;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    if (to > z) raise(to);
+    add_lanes();
   }
 };
 
@@ -193,12 +205,41 @@ struct Shared {
   unsigned long long group[kMaxCluster * 32];
   unsigned long long bound;  // of the candidates
   int n, items;              // candidates found; vectors to look at again
-  float M, ls;               // the row's reference and log of its sum; whether it has a NaN or infinity
-  int any;
+  float M, ls;               // the row's maximum, its lse less that; whether it has a NaN or infinity
+  int any, far;              // whether it has to be summed relative to M
   unsigned long long cand[kCand];
   unsigned long long best[kWarps];
   int item[kItems];
 };
+
+// What is written for a row, by one thread: ls = lse - M.
+__device__ __forceinline__ void put_row(const Params& p, int r, bool has, float xt, float M, float ls, float entropy, int any) {
+  const float y = any ? NAN : xt == -INFINITY ? -INFINITY : (xt - M) - ls;
+  if (p.logprob) p.logprob[r] = has ? y : NAN;
+  if (p.entropy) p.entropy[r] = any ? NAN : entropy;
+}
+
+// The sums relative to M of a row without NaN or infinity, by the whole CTA; in thread 0 the row's.
+template <bool BF16>
+__device__ __noinline__ Sums far_sums(const char* first, int vocab, float M, Sums* warps) {
+  const int tid = threadIdx.x;
+  Sums a{0.f, 0.f, 0.f, M};
+#pragma unroll 4
+  for (int i = tid; i < vocab; i += kThreads) {
+    const float x = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(first)[i]) : reinterpret_cast<const float*>(first)[i];
+    const float t = fmaxf((x - M) * kL2E, -256.f), y = ex2(t);
+    a.s += y;
+    a.u = fmaf(y, t, a.u);
+  }
+  a.add_lanes();
+  if (tid % 32 == 0) warps[tid / 32] = a;
+  __syncthreads();
+  for (int i = 1; tid == 0 && i < kWarps; ++i) {
+    a.s += warps[i].s;
+    a.u += warps[i].u;
+  }
+  return a;
+}
 
 // CTAS CTAs (a cluster) share a row. Everything joined lies in the first one's shared memory.
 template <bool BF16, int CTAS>
@@ -229,8 +270,8 @@ __global__ void __launch_bounds__(kThreads, 5) logprobs_kernel(const Params p) {
   }
 
   // ---- the row
-  Sums a{-INFINITY, 0.f, 0.f};
-  float z = 0.f, low = 0.f;     // m log2(e), and what lies so far below m that it counts nothing
+  Sums a{kNone, 0.f, 0.f, -INFINITY};
+  float top = -kFar - 256.f, low = 0.f;  // the reference as a logit, and what lies so far below that it counts nothing
   float best = -INFINITY, second = -INFINITY;  // the largest vectors' maxima
   int first = INT_MAX, ahead = 0, bad = 0;     // the largest vector's first element
   __nv_bfloat162 above2 = __float2bfloat162_rn(above), from2 = __float2bfloat162_rn(from);
@@ -260,14 +301,14 @@ __global__ void __launch_bounds__(kThreads, 5) logprobs_kernel(const Params p) {
         for (int i = 0; i < V; ++i) ahead += Row<BF16>::element(v, i) > th ? 1 : 0;
       }
     }
-    if (mx > a.m + 40.f) {
-      a.raise(mx);
-      z = mx * kL2E;
-      low = mx - 170.f;
+    if (mx > top) {
+      a.raise(kStep * ceilf(fmaf(fminf(mx, kFar), kL2E / kStep, kRoom)));
+      top = a.z * kLn2;
+      low = top - 130.f;
     }
-    if (fabsf(a.m) < 1e4f) {
-      Row<BF16>::raise(v, low);  // (2^-150 and less is 0, and 0 x -170 no NaN)
-      const uint64_t l2 = pair(kL2E, kL2E), z2 = pair(-z, -z);
+    if (a.z != kNone) {  // (vectors below -8448 alone add nothing to a row with a maximum above -8192)
+      Row<BF16>::raise(v, low);  // (2^-180 is 0, and 0 x -180 no NaN)
+      const uint64_t l2 = pair(kL2E, kL2E), z2 = pair(-a.z, -a.z);
       uint64_t s = pair(a.s, 0.f), w = pair(a.u, 0.f);
 #pragma unroll
       for (int i = 0; i < V; i += 2) {
@@ -280,18 +321,6 @@ __global__ void __launch_bounds__(kThreads, 5) logprobs_kernel(const Params p) {
       const float2 s1 = halves(s), w1_ = halves(w);
       a.s = s1.x + s1.y;
       a.u = w1_.x + w1_.y;
-    } else if (a.m != -INFINITY) {  // (rare: m log2(e) may overflow, m - 170 may be m)
-#pragma unroll 1
-      for (int i = 0; i < V; ++i) {
-        const uint32_t x = BF16 ? (i & 1 ? v.w[0] & 0xFFFF0000u : v.w[0] << 16) : v.w[0];
-        const float e = fmaxf((__uint_as_float(x) - a.m) * kL2E, -256.f), y = ex2(e);
-        a.s += y;
-        a.u = fmaf(y, e, a.u);
-        if (!BF16 || (i & 1)) {
-#pragma unroll
-          for (int j = 0; j < 7; ++j) v.w[j] = v.w[j + 1];
-        }
-      }
     }
   };
   // whole vectors, then the row's first and last where they are not (threads 0 and 1 of their CTA)
@@ -330,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 5) logprobs_kernel(const Params p) {
 #pragma unroll
     for (int o = 1; o < T / 32; o <<= 1) gk = max(gk, __shfl_xor_sync(0xffffffffu, gk, o));
   }
+  a.m = best;
   a.join_warp();
   ahead = __reduce_add_sync(0xffffffffu, ahead);
   bad = __any_sync(0xffffffffu, bad);
@@ -360,15 +390,16 @@ __global__ void __launch_bounds__(kThreads, 5) logprobs_kernel(const Params p) {
     }
   }
   if (part == 0 && warp == W - 1) {
-    Sums b = lane < CTAS * W ? sh.sums[lane] : Sums{-INFINITY, 0.f, 0.f};
+    Sums b = lane < CTAS * W ? sh.sums[lane] : Sums{kNone, 0.f, 0.f, -INFINITY};
     int rk = lane < CTAS * W ? sh.rank[lane] : 0;
     int any = lane < CTAS * W ? sh.bad[lane] : 0;
     if (CTAS * W > 32) {
       Sums c = sh.sums[(lane + 32) % (CTAS * W)];
-      if (c.m > b.m) b.raise(c.m);
-      else if (b.m > c.m) c.raise(b.m);
+      if (c.z > b.z) b.raise(c.z);
+      else if (b.z > c.z) c.raise(b.z);
       b.s += c.s;
       b.u += c.u;
+      b.m = fmaxf(b.m, c.m);
       rk += sh.rank[(lane + 32) % (CTAS * W)];
       any |= sh.bad[(lane + 32) % (CTAS * W)];
     }
@@ -376,20 +407,38 @@ __global__ void __launch_bounds__(kThreads, 5) logprobs_kernel(const Params p) {
     rk = __reduce_add_sync(0xffffffffu, rk);
     any = __any_sync(0xffffffffu, any);
     if (lane == 0) {
-      const float ls = logf(b.s);
-      const float y = any ? NAN : xt == -INFINITY ? -INFINITY : (xt - b.m) - ls;
-      if (p.logprob) p.logprob[r] = has ? y : NAN;
+      const bool none = b.m == -INFINITY, far = !any && !none && !(fabsf(b.m) < kFar);
+      // the sum relative to the whole number next to the maximum (a power of two apart: the logarithm and what
+      // it is compared with stay near 0 for a confident row)
+      const float c = any || none || far ? 0.f : rintf(b.m * kL2E);
+      const float s = b.s * ex2(b.z - c);
+      const float ls = none ? 0.f : fmaxf(kLn2 * (log2f(s) - fmaf(b.m, kL2E, -c)), 0.f);
       if (p.rank) p.rank[r] = !has ? -1 : rk + (lowest ? t : 0);
-      if (p.entropy) p.entropy[r] = any ? NAN : b.m == -INFINITY ? 0.f : kLn2 * (log2f(b.s) - b.u / b.s);
+      if (!far) put_row(p, r, has, xt, b.m, ls, none ? 0.f : fmaxf(kLn2 * (log2f(b.s) - b.u / b.s), 0.f), any);
       sh.M = b.m;
       sh.ls = ls;
       sh.any = any;
+      sh.far = far;
     }
+  }
+  if (p.top == 0) {
+    if (part != 0) return;
+    __syncthreads();
+  } else {
+    sync();
+  }
+  if (part == 0 && sh.far) {  // (the type's lowest value everywhere, say)
+    const Sums b = far_sums<BF16>(row.at + row.shift * Row<BF16>::E, p.vocab, sh.M, sh.sums);
+    if (tid == 0) {
+      const float l2 = log2f(b.s);
+      sh.ls = fmaxf(kLn2 * l2, 0.f);
+      put_row(p, r, has, xt, b.m, sh.ls, fmaxf(kLn2 * (l2 - b.u / b.s), 0.f), 0);
+    }
+    __syncthreads();
   }
   if (p.top == 0) return;
 
   // ---- the alternatives
-  sync();
   const unsigned long long bound = home->bound;
   const float least = bound ? value_of(bound) : -INFINITY;  // (0: fewer groups than alternatives, take all)
   auto offer = [&](float x, int id) {
