@@ -245,9 +245,7 @@ dec_status dec_kvq_append(const dec_kvq_cache* c, const dec_kvq_seqs* s, const d
   if (dec_status st = check_seqs(s, c)) return st;
   if (!a) return op_fail(DEC_ERR_ARG, "append: NULL arguments");
   if (a->dtype != DEC_BF16 && a->dtype != DEC_F32) return op_fail(DEC_ERR_ARG, "append: unknown dtype");
-  const bool has_q = a->q.p != nullptr;
-  if (a->n_heads < 0 || a->n_heads > 16384 || has_q != (a->n_heads > 0))
-    return op_fail(DEC_ERR_ARG, "append: n_heads goes with q");
+  if (a->n_heads < 0 || a->n_heads > 16384) return op_fail(DEC_ERR_ARG, "append: n_heads out of range");
   if (a->rotary_dim < 0 || a->rotary_dim > c->head_dim || a->rotary_dim % 16)
     return op_fail(DEC_ERR_ARG, "append: rotary_dim must be a multiple of 16 within head_dim");
   if ((a->rotary_dim > 0) != (a->rope != nullptr) || a->rope_len < 0)
@@ -256,7 +254,9 @@ dec_status dec_kvq_append(const dec_kvq_cache* c, const dec_kvq_seqs* s, const d
   if ((a->q_norm && !op_aligned(a->q_norm)) || (a->k_norm && !op_aligned(a->k_norm)))
     return op_fail(DEC_ERR_ARG, "append: norm weights must be 16-byte aligned");
   if (!(a->eps >= 0.f)) return op_fail(DEC_ERR_ARG, "append: eps must not be negative");
-  if (s->batch == 0 || s->n_tokens == 0) return DEC_OK;
+  if (s->batch == 0 || s->n_tokens == 0) return DEC_OK;  // (rows of nothing may lie nowhere)
+  const bool has_q = a->q.p != nullptr;
+  if (has_q != (a->n_heads > 0)) return op_fail(DEC_ERR_ARG, "append: n_heads goes with q");
   if (dec_status st = check_rows(&a->k, a->dtype, "append: k")) return st;
   if (dec_status st = check_rows(&a->v, a->dtype, "append: v")) return st;
   if (has_q) {

@@ -3,7 +3,7 @@ import types
 
 import torch
 
-from latency_moe_decode_gb300 import ops
+from latency_moe_decode_gb300 import build, capi, ops
 from latency_moe_decode_gb300.engine import Engine
 
 
@@ -31,3 +31,20 @@ def test_moving_slots_is_queued_on_the_callers_stream():
     eng.kvq_load(2, [_cache()], table, 33, stream=0)  # (torch's default stream: not the engine's own)
     assert [c[0] for c in calls] == ["dec_kvq_store_ex", "dec_kvq_load_ex"]
     assert calls[0][1][-1] == 4096 and calls[1][1][-2:] == (33, 1)
+
+
+def test_appending_nothing_with_queries_of_no_address():
+    """An empty tensor has no address: rows of nothing are no error, with queries or without."""
+    build.build()
+    lib = capi.lib()
+    cache = capi.DecKvqCache(4096, 4, 64, 2, 128, None)
+    none = dict(dtype=0, k=None, v=None, eps=1e-6)
+    for batch, cu in ((0, None), (2, 4096)):
+        seqs = capi.DecKvqSeqs(batch, 0, cu, 4096, 4096, 4, 4)
+        for heads in (0, 8):
+            assert lib.dec_kvq_append(cache, seqs, capi.DecKvqAppendArgs(n_heads=heads, **none), None) == 0
+        assert lib.dec_kvq_append(cache, seqs, capi.DecKvqAppendArgs(n_heads=-1, **none), None) == -1
+    # with rows, queries still have to be there
+    one = capi.DecKvqSeqs(1, 1, None, 4096, 4096, 4, 4)
+    assert lib.dec_kvq_append(cache, one, capi.DecKvqAppendArgs(n_heads=8, dtype=0, k=4096, v=4096, eps=1e-6), None) == -1
+    assert b"n_heads goes with q" in lib.dec_op_error()
