@@ -367,7 +367,7 @@ const char* dec_op_error(void);
    page id outside 0 .. n_pages - 1 or a negative position, and DEC_ERR_CAPACITY when a position
    lies beyond the page table or the rotation table (the first one met stays), and DEC_ERR_TIMEOUT
    if a kernel gave up waiting for its own copies. The kernel skips such a row or such positions
-   and touches nothing out of range. */
+   and touches nothing out of range (an append whose page is bad still gives the row's queries). */
 typedef struct {
   void* pages;
   int32_t n_pages;

@@ -356,12 +356,11 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
     raise(p.c.status, DEC_ERR_ARG);
     return;
   }
-  const bool turns = p.rot > 0, far = turns && pos >= p.rope_len;  // (beyond the table: keys and queries are skipped)
-  if (far) raise(p.c.status, DEC_ERR_CAPACITY);
+  const bool turns = p.rot > 0, far = turns && pos >= p.rope_len;  // (beyond the table: the row is skipped)
   // the page, and the lane's angles: pairs (8l + i, its partner), or four pairs of neighbours
   const int e = pos >> p.c.page_shift, gpp = 1 << (p.c.page_shift - 4);
   int page = -1;
-  if (e >= p.s.max_pages) raise(p.c.status, DEC_ERR_CAPACITY);
+  if (far || e >= p.s.max_pages) raise(p.c.status, DEC_ERR_CAPACITY);
   else if ((unsigned)(page = __ldg(p.s.table + b * p.s.table_stride + e)) >= (unsigned)p.c.n_pages) {
     raise(p.c.status, DEC_ERR_ARG);
     page = -1;
@@ -446,7 +445,7 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
       if (keys || F32) {  // (bf16 values as they are lie on a middle or well beside it, fp32 ones may be just beside)
         sb = scale_byte<true>(mag, near);
         word = code_word<true>(x, sb == kScaleNan ? 0.f : scale_of(sb), near);
-        if (near && in && kind > 0 && !(kind == 1 && far) && (F32 || kind == 1)) {
+        if (near && in && kind > 0 && (F32 || kind == 1)) {
           atomicOr(&todo[(kind - 1) * 32 + (h >> 5)], 1u << (h & 31));
           any = true;
         }
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
         sb = scale_byte<false>(mag, near);
         word = code_word<false>(x, sb == kScaleNan ? 0.f : scale_of(sb), near);
       }
-      if (in && grp && (kind == 2 || (kind == 1 && !far))) {
+      if (in && grp && kind > 0) {
         uint8_t* const at = grp + (size_t)h * gpp * group_bytes(HD);
         *reinterpret_cast<uint32_t*>(at + (kind == 1 ? k_word<HD>(pp, l) : v_word<HD>(pp, l))) = word;
         if ((l & 1) == 0) at[kind == 1 ? k_scale<HD>(pp, l >> 1) : v_scale<HD>(pp, l >> 1)] = (uint8_t)sb;
