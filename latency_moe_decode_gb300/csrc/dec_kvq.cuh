@@ -66,29 +66,37 @@ __device__ __forceinline__ float scale_of(int b) {
 // formula gives. Where that error, or that of fp32 values as they are, may have made the choice (CHECK,
 // near), the row is made anew with twice the bits (settle_row). kNear is five deviations, for values up to
 // 8 codes: one row in 1000 is made anew; a bound on all roundings at once would take three times as many.
+// A rotation may leave a run much smaller than the values that it was made of, whose roundings it keeps: the
+// larger result of a pair is at least the larger product over the root of 2, so the largest result of the
+// run's pairs, times 1.5 where it is well above the run's own (`big`), widens the search in proportion.
 constexpr float kNear = 0x1p-18f;
 
 // The scale byte of a run whose largest magnitude has the bits `mag`: max / 7 (and / 8) rounded to
 // 3 mantissa bits.
 template <bool CHECK>
-__device__ __forceinline__ int scale_byte(uint32_t mag, bool& near) {
+__device__ __forceinline__ int scale_byte(uint32_t mag, float big, bool& near) {
   if (mag >= 0x7F800000u) return kScaleNan;
   const float m = __uint_as_float(mag), q = m * (1.0f / 7.0f);
   const float w = fminf(fmaf(fmaf(-q, 7.0f, m), 1.0f / 7.0f, q) * 0.125f, 60.0f);  // (see code_word)
   uint32_t u = __float_as_uint(w);
+  float wide = 1.f;
+  if (CHECK) {
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(wide) : "f"(m));
+    wide = fmaxf(big * wide, 1.f);  // (0 x infinity: 1)
+  }
   if (w < 6.103515625e-05f) {  // below 2^-14: steps of 2^-17
     const float v = w * 131072.0f;
-    if (CHECK) near |= fabsf(v - floorf(v) - 0.5f) <= 0x1p-17f;
+    if (CHECK) near |= fabsf(v - floorf(v) - 0.5f) <= 0x1p-17f * wide;
     return __float2int_rn(v);
   }
-  if (CHECK) near |= (u & 0xFFFFFu) - (0x80000u - 8u) <= 16u;
+  if (CHECK) near |= fabsf((float)(u & 0xFFFFFu) - 524288.f) <= 8.f * wide;
   u += 0x7FFFFu + ((u >> 20) & 1u);
   return (int)(u >> 20) - (112 << 3);
 }
 
 // Eight values as a word of codes at scale s (0: an empty or NaN run, every code 0).
 template <bool CHECK>
-__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float s, bool& near) {
+__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float s, float big, bool& near) {
   if (!(s > 0.f)) return 0x88888888u;
   float inv, c[8], d = 0.f;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
@@ -102,7 +110,7 @@ __device__ __forceinline__ uint32_t code_word(const float (&x)[8], float s, bool
     c[i] = (y + 12582912.f) - 12582912.f;  // to the nearest whole number, ties to even
     if (CHECK) d = fmaxf(d, fabsf(y - c[i]));
   }
-  if (CHECK) near |= d >= 0.5f - kNear;
+  if (CHECK) near |= d >= 0.5f - kNear * fmaxf(big * inv * 0.125f, 1.f);
   // four codes + 8 make a whole number below 2^16, which 2^23 leaves in the low mantissa bits
   const float lo = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]);
   const float hi = fmaf(fmaf(fmaf(c[7], 16.f, c[6]), 16.f, c[5]), 16.f, c[4]);
@@ -290,7 +298,7 @@ __device__ __noinline__ void settle_row(const void* x, const uint16_t* nw, float
     if (m.h == m.h && (!(y.h <= m.h) || (y.h == m.h && y.l > m.l))) m = y;  // (a NaN stays)
   }
   bool unused = false;
-  int sb = m.h <= 3.4028235e38f ? scale_byte<false>(__float_as_uint(m.h), unused) : kScaleNan;
+  int sb = m.h <= 3.4028235e38f ? scale_byte<false>(__float_as_uint(m.h), 0.f, unused) : kScaleNan;
   if (sb != kScaleNan) {
     // 7 times the middle to the scale above and to the one below
     const float up = sb < kScaleMax ? (m.h - 3.5f * (scale_of(sb) + scale_of(sb + 1))) + m.l : -1.f;
@@ -438,20 +446,24 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
       uint32_t mag = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) mag = max(mag, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+      uint32_t pair = mag;  // with the pairs' other values
       mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
       int sb;
       uint32_t word;
       bool near = false;
       if (keys || F32) {  // (bf16 values as they are lie on a middle or well beside it, fp32 ones may be just beside)
-        sb = scale_byte<true>(mag, near);
-        word = code_word<true>(x, sb == kScaleNan ? 0.f : scale_of(sb), near);
+        pair = max(pair, __shfl_sync(0xffffffffu, pair, other, LPR));
+        pair = max(pair, __shfl_xor_sync(0xffffffffu, pair, 1));
+        const float big = kind == 1 ? fmaf(1.5f, __uint_as_float(pair), -0.5f * __uint_as_float(mag)) : 0.f;
+        sb = scale_byte<true>(mag, big, near);
+        word = code_word<true>(x, sb == kScaleNan ? 0.f : scale_of(sb), big, near);
         if (near && in && kind > 0 && (F32 || kind == 1)) {
           atomicOr(&todo[(kind - 1) * 32 + (h >> 5)], 1u << (h & 31));
           any = true;
         }
       } else {
-        sb = scale_byte<false>(mag, near);
-        word = code_word<false>(x, sb == kScaleNan ? 0.f : scale_of(sb), near);
+        sb = scale_byte<false>(mag, 0.f, near);
+        word = code_word<false>(x, sb == kScaleNan ? 0.f : scale_of(sb), 0.f, near);
       }
       if (in && grp && kind > 0) {
         uint8_t* const at = grp + (size_t)h * gpp * group_bytes(HD);

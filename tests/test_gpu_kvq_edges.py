@@ -59,3 +59,36 @@ def test_rows_beyond_the_rotation_table_are_not_appended_by_half(dtype, hd, rot,
         with pytest.raises(DecError) as e:
             cache.check()
         assert e.value.status == -8
+
+
+@pytest.mark.parametrize("hd,dtype,norm,rot,inter", [(128, BF, True, 128, False), (128, F32, False, 128, False),
+                                                     (64, BF, False, 32, False), (64, F32, True, 64, True), (128, BF, False, 16, False)])
+@pytest.mark.parametrize("size", [30.0, 300.0, 3e4])
+def test_codes_of_runs_that_a_rotation_leaves_small(hd, dtype, norm, rot, inter, size):
+    """Pairs of large values that turn into one small and one large one: the small one keeps the large ones'
+    roundings, and is held as the formula in 64 bits says all the same. (One pair or all pairs of a run; runs of
+    adjacent pairs hold both values.)"""
+    from latency_moe_decode_gb300 import ops
+    n, hkv = 2 ** 18 // hd, 8
+    g = torch.Generator().manual_seed(hd + rot)
+    k = torch.randn(n, hkv, hd, generator=g)
+    rope = ops.rope_table(n, rot, 1e6)
+    c, s = rope.cpu().unbind(-1)
+    i = torch.arange(rot // 2)
+    a, b = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
+    r = size * (0.5 + torch.rand(n, hkv, rot // 2, generator=g))
+    r[:, ::2] *= (torch.rand(n, hkv // 2, rot // 2, generator=g) < 0.1)  # some heads: a pair of a run now and then
+    k[..., a] += r * s[:, None]
+    k[..., b] += r * c[:, None]  # a cos - b sin: what the rounding to the type and the noise leave
+    k = k.to(dtype)
+    kn = (1 + 0.2 * torch.randn(hd, generator=g)).to(BF) if norm else None
+    if norm:  # (a pair's two weights alike, or the norm undoes the angle)
+        kn[b] = kn[a]
+    cache, table = _cache([n], hkv, hd, 64)
+    cache.append(k.cuda(), k.cuda(), _ints([0]), table, cu_tokens=_cu([n]), k_norm=None if kn is None else kn.cuda(),
+                 rope=rope, interleaved=inter)
+    got = _np(cache.gather(_ints([0]), table, n, cu_tokens=_cu([n]))[0])
+    cache.check()
+    held = ref.store(ref.norm_rotate(_np(k), None if kn is None else _np(kn), 1e-6, _np(rope), np.arange(n), inter))[0]
+    wrong = got != held
+    assert not wrong.any(), (wrong.sum(), got[wrong][:4], held[wrong][:4])
