@@ -325,7 +325,8 @@ dec_status dec_get_trace(dec_engine* eng, uint64_t* host_buf, int32_t n, int32_t
    CTA: host_buf[l] is the %globaltimer time (ns) at which the input of layer l was final, as
    that CTA saw it (l = 0: the step start; l = n_layers: the final norm's input), and
    host_buf[n_layers + 1] the time that CTA finished the step. So host_buf[l + 1] - host_buf[l]
-   is layer l's time on the critical path and the last difference the LM head's tail. Copies
+   is layer l's time on the critical path and the last difference the LM head's tail (in a step over 4-bit
+   caches the launches between included). Copies
    min(n, n_layers + 2) words and returns the count in *n_written. Synchronises with the
    engine's work. */
 dec_status dec_get_layer_times(dec_engine* eng, uint64_t* host_buf, int32_t n, int32_t* n_written);

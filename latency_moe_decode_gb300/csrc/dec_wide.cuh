@@ -2032,6 +2032,7 @@ struct WConsumer {
       layer_out(l, U);
       gbar();
     }
+    stamp_layer(w.seg);
     if (w.seg < p.L) {
       gemv(K_QKV, 0);
       gbar();
@@ -2046,6 +2047,7 @@ struct WConsumer {
         if (p.next_tokens) p.next_tokens[tid] = (int)(0xFFFFFFFFu - (unsigned)(key & 0xFFFFFFFFull));
       }
     }
+    if (w.seg == p.L) stamp_layer(p.L + 1);
     // TMEM is freed once the MMA warp has finished (bounded wait)
     if (warp == 0) {
       if (lane == 0) {
