@@ -92,3 +92,22 @@ def test_codes_of_runs_that_a_rotation_leaves_small(hd, dtype, norm, rot, inter,
     held = ref.store(ref.norm_rotate(_np(k), None if kn is None else _np(kn), 1e-6, _np(rope), np.arange(n), inter))[0]
     wrong = got != held
     assert not wrong.any(), (wrong.sum(), got[wrong][:4], held[wrong][:4])
+
+
+def test_the_public_way_to_the_current_stream(monkeypatch):
+    """The handle that a torch without the short cut would give is the same, on any stream."""
+    from latency_moe_decode_gb300 import ops
+    cache, table, _, _, g = _filled([40], 2, 128, 16, 3)
+    q = _rnd(g, 1, 8, 128).cuda()
+    s = torch.cuda.Stream()
+    want = cache.attention(q, _ints([39]), table)
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.current_stream(), s):
+        with torch.cuda.stream(stream):
+            assert ops._current_raw_stream(0) == ops._raw_stream(0) == stream.cuda_stream
+    monkeypatch.setattr(ops, "_raw_stream", ops._current_raw_stream)
+    ln = _ints([39])
+    torch.cuda.synchronize()
+    got = cache.attention(q, ln, table, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

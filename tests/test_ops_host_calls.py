@@ -1,4 +1,7 @@
 """What the Python bindings hand to the library, without a GPU."""
+import os
+import subprocess
+import sys
 import types
 
 import torch
@@ -48,3 +51,17 @@ def test_appending_nothing_with_queries_of_no_address():
     one = capi.DecKvqSeqs(1, 1, None, 4096, 4096, 4, 4)
     assert lib.dec_kvq_append(cache, one, capi.DecKvqAppendArgs(n_heads=8, dtype=0, k=4096, v=4096, eps=1e-6), None) == -1
     assert b"n_heads goes with q" in lib.dec_op_error()
+
+
+def test_imports_with_a_torch_without_cuda():
+    """A torch built without CUDA lacks the short cut to a stream's handle; importing asks for none of it."""
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'):\n"
+            "    del torch._C._cuda_getCurrentRawStream\n"
+            "from latency_moe_decode_gb300 import engine, ops\n"
+            "torch.cuda.current_stream = lambda i: type('S', (), {'cuda_stream': 40 + i})\n"
+            "print(ops._raw_stream(2))\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split() == ["42"]
