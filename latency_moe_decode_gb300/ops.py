@@ -33,10 +33,14 @@ def _current_raw_stream(index: int) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw_stream)
 
 
-def _on_stream(stream):
-    """A torch stream, or a cudaStream_t, as the current stream: the whole call, its outputs and the
-    copies it makes included, then belongs to it."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+def _on_stream(stream, device: torch.device):
+    """A torch stream, or a cudaStream_t, of the tensors' device as its current stream: the whole call,
+    its outputs and the copies it makes included, then belongs to it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _call(f, index: int, *args) -> int:
@@ -138,7 +142,7 @@ class KvqCache:
         ([n, n_heads, head_dim], of the same type) return it normalised and rotated, in bf16. rope: a
         rope_table() of rotary_dim = 2 * rope.shape[1]."""
         if stream is not None:
-            with _on_stream(stream):
+            with _on_stream(stream, self.device):
                 return self.append(k, v, lengths, table, cu_tokens, q, q_norm, k_norm, eps, rope, interleaved, q_out)
         index, hd, hkv, dtype = self._index, self.head_dim, self.n_kv_heads, k.dtype
         shape = k.shape
@@ -182,7 +186,7 @@ class KvqCache:
                out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """The values the cache holds at the sequences' positions: k, v bf16 [n_tokens, n_kv_heads, head_dim]."""
         if stream is not None:
-            with _on_stream(stream):
+            with _on_stream(stream, self.device):
                 return self.gather(lengths, table, n_tokens, cu_tokens, out)
         hkv, hd = self.n_kv_heads, self.head_dim
         shape = (n_tokens, hkv, hd)
@@ -206,7 +210,7 @@ class KvqCache:
         of one sequence (default: n with cu_tokens, 1 without). Returns out (bf16, shaped as q), or
         (out, lse) with lse fp32 [n, n_heads]."""
         if stream is not None:
-            with _on_stream(stream):
+            with _on_stream(stream, self.device):
                 return self.attention(q, lengths, table, cu_tokens, max_tokens, causal, scale, out, return_lse)
         index, hd, shape = self._index, self.head_dim, q.shape
         if q.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != hd or q.get_device() != index:
@@ -247,8 +251,8 @@ class LogProbs(NamedTuple):
 def logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, top_n: int = 0, stream=None) -> LogProbs:
     """Log-probabilities of `targets` (int32 [rows]) under logits (fp32 or bf16 [rows, vocab]), their
     ranks, the rows' entropies and the top_n likeliest ids with their log-probabilities."""
-    if stream is not None:
-        with _on_stream(stream):
+    if stream is not None and logits.is_cuda:
+        with _on_stream(stream, logits.device):
             return logprobs(logits, targets, top_n)
     dt = _DTYPES.get(logits.dtype)
     shape = logits.shape

@@ -111,3 +111,25 @@ def test_the_public_way_to_the_current_stream(monkeypatch):
     got = cache.attention(q, ln, table, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_raw_streams_through_every_call():
+    from latency_moe_decode_gb300 import ops
+    cache, table, _, _, g = _filled([40], 2, 128, 16, 4)
+    kv, q = _rnd(g, 1, 2, 128).cuda(), _rnd(g, 1, 8, 128).cuda()
+    logits, t = torch.randn(3, 500, generator=g).cuda(), _ints([1, 2, 3])
+    ln = _ints([39])
+
+    def calls(stream):
+        qo = cache.append(kv, kv, ln, table, q=q, stream=stream)
+        got = [qo, *cache.gather(ln, table, 1, stream=stream), cache.attention(q, ln, table, stream=stream)]
+        got += [x for x in ops.logprobs(logits, t, top_n=3, stream=stream)]
+        torch.cuda.synchronize()
+        return got
+
+    s = torch.cuda.Stream()
+    want = calls(None)
+    for stream in (s, s.cuda_stream, 0, torch.cuda.default_stream()):
+        assert all(torch.equal(a, b) for a, b in zip(calls(stream), want))
+    with pytest.raises(ValueError):
+        ops.logprobs(logits.cpu(), stream=s)

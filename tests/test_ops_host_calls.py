@@ -4,6 +4,7 @@ import subprocess
 import sys
 import types
 
+import pytest
 import torch
 
 from latency_moe_decode_gb300 import build, capi, ops
@@ -65,3 +66,23 @@ def test_imports_with_a_torch_without_cuda():
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     assert r.stdout.split() == ["42"]
+
+
+def test_streams_belong_to_the_tensors_device(monkeypatch):
+    """With another device than the tensors' current, a raw handle is a stream of the tensors' device; a torch
+    stream of another device is refused (the call would run unordered with it)."""
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.handle, self.device = handle, torch.device("cuda:0") if device is None else device
+
+    used = []
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", used.append)
+    one = torch.device("cuda:1")
+    ops._on_stream(4096, one)
+    ops._on_stream(Stream(5, one), one)
+    assert [(s.handle, s.device) for s in used] == [(4096, one), (5, one)]
+    with pytest.raises(ValueError):
+        ops._on_stream(Stream(5), one)
+    assert len(used) == 2
