@@ -448,6 +448,8 @@ dec_status dec_kvq_gather(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, 
                 exp(scale q.k) over the row's positions
      scale      0: 1 / sqrt(head_dim)
      max_tokens an upper bound of the rows of one sequence (host); rows beyond it are not computed
+     likely_tokens  how many rows most sequences have (host; 0: max_tokens), where max_tokens is far above it:
+                it chooses among kernels for few and for many rows, each of which takes any number
      workspace  16-byte aligned device memory of dec_kvq_attention_workspace() bytes; its content
                 is of no interest before or after the call
    A row with no position gives out = 0 and lse = -infinity. Scores, softmax statistics and the
@@ -465,6 +467,7 @@ typedef struct {
   int32_t max_tokens;
   void* workspace;
   int64_t workspace_bytes;
+  int32_t likely_tokens;
 } dec_kvq_attention_args;
 dec_status dec_kvq_attention(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, const dec_kvq_attention_args* args,
                              void* stream);

@@ -87,7 +87,7 @@ class DecKvqAppendArgs(C.Structure):
 class DecKvqAttentionArgs(C.Structure):
     _fields_ = [("n_heads", C.c_int32), *_row_fields("q", "out"), ("lse", C.c_void_p), ("scale", C.c_float),
                 ("causal", C.c_int32), ("max_tokens", C.c_int32), ("workspace", C.c_void_p),
-                ("workspace_bytes", C.c_int64)]
+                ("workspace_bytes", C.c_int64), ("likely_tokens", C.c_int32)]
 
 
 class DecLogprobsArgs(C.Structure):

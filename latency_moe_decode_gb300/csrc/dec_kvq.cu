@@ -331,8 +331,8 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
   if (!a) return op_fail(DEC_ERR_ARG, "attention: NULL arguments");
   if (a->n_heads < 1 || a->n_heads > 16384 || a->n_heads % c->n_kv_heads)
     return op_fail(DEC_ERR_ARG, "attention: n_heads must be a multiple of the cache's KV heads");
-  if (a->max_tokens < 0 || !(a->scale >= 0.f) || std::isinf(a->scale))
-    return op_fail(DEC_ERR_ARG, "attention: max_tokens and scale must not be negative, scale finite");
+  if (a->max_tokens < 0 || a->likely_tokens < 0 || !(a->scale >= 0.f) || std::isinf(a->scale))
+    return op_fail(DEC_ERR_ARG, "attention: max_tokens, likely_tokens and scale must not be negative, scale finite");
   if (s->batch == 0 || s->n_tokens == 0 || a->max_tokens == 0) return DEC_OK;
   if (dec_status st = check_rows(&a->q, DEC_BF16, "attention: q")) return st;
   if (dec_status st = check_rows(&a->out, DEC_BF16, "attention: out")) return st;
@@ -356,14 +356,21 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
   p.causal = a->causal != 0;
   p.max_tokens = a->max_tokens;
   const int max_tokens = std::min(a->max_tokens, s->n_tokens);
-  const int kind = kernel_of(c->head_dim, a->n_heads, c->n_kv_heads, max_tokens);
   if (a->workspace_bytes < dec_kvq_attention_workspace(c, a->n_heads, s->batch, max_tokens))
     return op_fail(DEC_ERR_ARG, "attention: workspace too small");
+  // (a kernel for fewer rows needs no more workspace)
+  int kind = kernel_of(c->head_dim, a->n_heads, c->n_kv_heads, max_tokens);
+  const int likely = a->likely_tokens > 0 && a->likely_tokens < max_tokens
+                         ? kernel_of(c->head_dim, a->n_heads, c->n_kv_heads, a->likely_tokens)
+                         : kind;
   // entries of the kernel's list, at most: 32-bit
-  const int rows = kind == 0 ? 8 : kind == 1 ? 16 : 128, positions = kind == 2 ? kTile : kGroup;
-  const long long units = (long long)c->n_kv_heads * ((long long)s->n_tokens * p.group / rows + s->batch);
-  if (units * ((long long)s->max_pages * c->page_tokens / positions + 1 + std::max(kUnitCost, kPromptCost)) >= (1LL << 32) - 64)
-    return op_fail(DEC_ERR_UNSUPPORTED, "attention: too much work for one call");
+  auto fits = [&](int k) {
+    const int rows = k == 0 ? 8 : k == 1 ? 16 : 128, positions = k == 2 ? kTile : kGroup;
+    const long long units = (long long)c->n_kv_heads * ((long long)s->n_tokens * p.group / rows + s->batch);
+    return units * ((long long)s->max_pages * c->page_tokens / positions + 1 + std::max(kUnitCost, kPromptCost)) < (1LL << 32) - 64;
+  };
+  if (fits(likely)) kind = likely;
+  else if (!fits(kind)) return op_fail(DEC_ERR_UNSUPPORTED, "attention: too much work for one call");
   return launch_attention(p, c->head_dim, kind, s->batch, static_cast<uint8_t*>(a->workspace), op_stream(stream));
 }
 

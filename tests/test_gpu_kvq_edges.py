@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import kvq_ref as ref
-from tests.test_gpu_kvq import _cache, _cu, _filled, _ints, _np, _rnd
+from tests.test_gpu_kvq import _cache, _check, _cu, _filled, _ints, _np, _rnd
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -133,3 +133,47 @@ def test_raw_streams_through_every_call():
         assert all(torch.equal(a, b) for a, b in zip(calls(stream), want))
     with pytest.raises(ValueError):
         ops.logprobs(logits.cpu(), stream=s)
+
+
+@pytest.mark.parametrize("hd,hq,hkv", [(128, 8, 2), (64, 8, 1)])
+def test_the_default_bound_takes_decode_batches_to_their_own_kernel(hd, hq, hkv):
+    """cu_tokens without max_tokens: the same bits as with the rows that the sequences have."""
+    for new in ([1] * 40, [2, 1] * 9 + [0], [30, 41, 25]):
+        lens = [(37 * i) % 300 for i in range(len(new))]
+        cache, table, _, _, g = _filled([l + n for l, n in zip(lens, new)], hkv, hd, 16, 8)
+        q = _rnd(g, sum(new), hq, hd).cuda()
+        a = cache.attention(q, _ints(lens), table, cu_tokens=_cu(new), return_lse=True)
+        b = cache.attention(q, _ints(lens), table, cu_tokens=_cu(new), max_tokens=max(new), return_lse=True)
+        cache.check()
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_more_rows_than_were_likely():
+    """Every kernel takes any number of rows: one sequence of many among single tokens; and a call whose rows would
+    not fit the list of the likely kernel goes to the other one."""
+    from latency_moe_decode_gb300 import ops
+    from latency_moe_decode_gb300.capi import DecKvqAttentionArgs
+    hd, hq, hkv = 128, 8, 2
+    new = [1] * 30 + [50] + [1] * 9
+    lens = [(53 * i) % 200 for i in range(len(new))]
+    cache, table, k, v, g = _filled([l + n for l, n in zip(lens, new)], hkv, hd, 16, 9)
+    q = _rnd(g, sum(new), hq, hd)
+    out, lse = cache.attention(q.cuda(), _ints(lens), table, cu_tokens=_cu(new), return_lse=True)
+    cache.check()
+    _check(_np(out), _np(lse), _np(q), k, v, new, lens, True, hd ** -0.5, hd)
+    # rows 3 .. a million belong to no sequence; the table could reach a million positions
+    n = 1 << 20
+    wide = torch.zeros(1, n // 16, dtype=torch.int32, device="cuda")
+    wide[0, :table.shape[1]] = table[30]
+    ln, cu, dev, res = _ints([50]), _cu([3]), q.cuda(), []
+    for rows, likely in ((3, 0), (n, 1)):
+        o = torch.zeros(3, hq, hd, dtype=BF, device="cuda")
+        ws = torch.empty(cache.lib.dec_kvq_attention_workspace(cache.c, hq, 1, rows), dtype=torch.uint8, device="cuda")
+        a = DecKvqAttentionArgs(hq, dev.data_ptr(), hq * hd, hd, o.data_ptr(), hq * hd, hd, None, 0.0, 1, rows, ws.data_ptr(),
+                                ws.numel(), likely)
+        s = cache._seqs(ln, wide, cu, rows)
+        assert cache.lib.dec_kvq_attention(cache.c, s, a, None) == 0, cache.lib.dec_op_error()
+        torch.cuda.synchronize()
+        res.append(o.float())
+    cache.check()
+    assert res[0].abs().sum() > 0 and (res[0] - res[1]).abs().max() < 0.05  # (as bounds of other kernels: 0.044)

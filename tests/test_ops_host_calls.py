@@ -86,3 +86,27 @@ def test_streams_belong_to_the_tensors_device(monkeypatch):
     with pytest.raises(ValueError):
         ops._on_stream(Stream(5), one)
     assert len(used) == 2
+
+
+def test_attention_passes_on_the_likely_rows(monkeypatch):
+    """Without max_tokens the bound is all rows, and the kernel goes by the mean; given, it is what counts."""
+    build.build()
+    calls = []
+    monkeypatch.setattr(ops, "_call", lambda f, index, c, s, a: calls.append((s.batch, a.max_tokens, a.likely_tokens)) or 0)
+    monkeypatch.setattr(ops.KvqCache, "_seqs", lambda self, lengths, table, cu, n: capi.DecKvqSeqs(lengths.numel(), n))
+    cache = object.__new__(ops.KvqCache)
+    cache._index, cache.head_dim, cache.n_kv_heads, cache.device, cache.c = -1, 64, 2, torch.device("cpu"), None
+    cache._ws = {(4, m): 16 for m in (1, 9, 2, 0)}
+    lib = capi.lib()
+    cache.lib = lib
+    cu, lengths = torch.zeros(5, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    q = torch.zeros(9, 4, 64, dtype=torch.bfloat16)
+    cache.attention(q, lengths, None, cu_tokens=cu)
+    cache.attention(q, lengths, None, cu_tokens=cu, max_tokens=2)
+    cache.attention(q[:4], lengths, None)
+    cache.attention(q[:0], lengths[:0], None, cu_tokens=cu[:1])
+    assert [c[1:] for c in calls] == [(9, 3), (2, 0), (1, 1), (0, 0)]
+    a = capi.DecKvqAttentionArgs(n_heads=8, q=4096, q_token_stride=1024, q_head_stride=128, out=4096, out_token_stride=1024,
+                                 out_head_stride=128, max_tokens=1, likely_tokens=-1)
+    seqs, c = capi.DecKvqSeqs(1, 1, None, 4096, 4096, 4, 4), capi.DecKvqCache(4096, 4, 64, 2, 128, None)
+    assert lib.dec_kvq_attention(c, seqs, a, None) == -1 and b"likely_tokens" in lib.dec_op_error()
