@@ -382,7 +382,8 @@ typedef struct {
    cu_tokens[b] .. cu_tokens[b + 1] - 1 (device int32 [batch + 1]; NULL: one row per sequence and
    n_tokens == batch). Its row j stands at position lengths[b] + j (device int32 [batch]), and
    position p is in page table[b * table_stride + p / page_tokens] (device int32; max_pages
-   entries of each row are valid). cu_tokens must ascend. Rows before cu_tokens[0] or from
+   entries of each row are valid). cu_tokens must ascend (the attention computes none of up to 256 neighbouring sequences among which they
+   do not, and records DEC_ERR_ARG). Rows before cu_tokens[0] or from
    cu_tokens[batch] on belong to no sequence: outputs leave them as they were. */
 typedef struct {
   int32_t batch;

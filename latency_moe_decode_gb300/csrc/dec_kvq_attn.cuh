@@ -150,55 +150,57 @@ __device__ __forceinline__ int over(int a, int d) { return d == 1 ? a : a / d; }
 __host__ __device__ inline uint32_t reciprocal(uint32_t d) { return 0xFFFFFFFFu / d; }
 
 // The list's table in shared memory, by the whole CTA: units of ROWS query rows, entries of POS positions.
-// Returns the number of entries.
+// Returns the number of entries. Token bounds that do not ascend leave nothing to do: sequences that share rows
+// could make more entries than the call was checked for.
 template <int THREADS, int ROWS, int POS, int COST>
 __device__ uint32_t build_list(const AttnParams& p, SeqWork* seqs, uint32_t* scan) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t base = 0;
-  for (int b0 = 0; b0 < p.s.batch; b0 += THREADS) {
-    const int b = b0 + tid;
-    uint32_t w = 0;
-    SeqWork sw;
-    if (b < p.s.batch) {
-      const int first = p.s.cu ? __ldg(p.s.cu + b) : p.b0 + b, last = p.s.cu ? __ldg(p.s.cu + b + 1) : first + 1;
-      const int len = __ldg(p.s.lengths + b);
-      const long long most = (long long)p.s.max_pages << p.c.page_shift;
-      sw.tok0 = max(first, 0);
-      sw.n = max(0, min(min(last - first, p.max_tokens), p.s.n_tokens - sw.tok0));
-      if (sw.n > 0 && len < 0) raise(p.c.status, DEC_ERR_ARG);
-      if (sw.n > 0 && (p.causal ? (long long)len + sw.n : len) > most) raise(p.c.status, DEC_ERR_CAPACITY);
-      sw.len = len < 0 ? -sw.n : (int)min((long long)len, most);
-      // (a unit without positions still writes its rows)
-      const int held = (int)min(most, (long long)(p.causal ? sw.len + sw.n : sw.len));
-      sw.ng = max(1, (held + POS - 1) / POS);
-      sw.inv = reciprocal(sw.ng + COST);
-      sw.nrb = (sw.n * p.group + ROWS - 1) / ROWS;
-      w = (uint32_t)p.c.hkv * sw.nrb * (sw.ng + COST);
-    }
-    uint32_t x = w;
+  static_assert(THREADS >= kMaxSeqs, "a thread for every sequence");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = tid;
+  uint32_t w = 0;
+  bool wrong = false;
+  SeqWork sw;
+  if (b < p.s.batch) {
+    const int first = p.s.cu ? __ldg(p.s.cu + b) : p.b0 + b, last = p.s.cu ? __ldg(p.s.cu + b + 1) : first + 1;
+    wrong = first < 0 || last < first;
+    const int len = __ldg(p.s.lengths + b);
+    const long long most = (long long)p.s.max_pages << p.c.page_shift;
+    sw.tok0 = max(first, 0);
+    sw.n = max(0, min(min(last - first, p.max_tokens), p.s.n_tokens - sw.tok0));
+    if (sw.n > 0 && len < 0) raise(p.c.status, DEC_ERR_ARG);
+    if (sw.n > 0 && (p.causal ? (long long)len + sw.n : len) > most) raise(p.c.status, DEC_ERR_CAPACITY);
+    sw.len = len < 0 ? -sw.n : (int)min((long long)len, most);
+    // (a unit without positions still writes its rows)
+    const int held = (int)min(most, (long long)(p.causal ? sw.len + sw.n : sw.len));
+    sw.ng = max(1, (held + POS - 1) / POS);
+    sw.inv = reciprocal(sw.ng + COST);
+    sw.nrb = (sw.n * p.group + ROWS - 1) / ROWS;
+    w = (uint32_t)p.c.hkv * sw.nrb * (sw.ng + COST);
+  }
+  uint32_t x = w;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) scan[warp] = x;
-    __syncthreads();
-    uint32_t before = base, all = base;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) scan[warp] = x;
+  wrong = __syncthreads_or(wrong);
+  uint32_t before = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-      const uint32_t y = scan[i];
-      before += i < warp ? y : 0u;
-      all += y;
-    }
-    if (b < p.s.batch) {
-      sw.pre = before + x - w;
-      seqs[b] = sw;
-    }
-    base = all;
+  for (int i = 0; i < THREADS / 32; ++i) {
+    const uint32_t y = scan[i];
+    before += i < warp ? y : 0u;
+    all += y;
+  }
+  if (wrong) {
+    if (tid == 0) raise(p.c.status, DEC_ERR_ARG);
+    all = sw.nrb = 0;
+  }
+  if (b < p.s.batch) {
+    sw.pre = before + x - w;
+    seqs[b] = sw;
   }
   __syncthreads();
-  return base;
+  return all;
 }
 
 // the sequence that entry f of the list belongs to

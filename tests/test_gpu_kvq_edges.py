@@ -177,3 +177,23 @@ def test_more_rows_than_were_likely():
         res.append(o.float())
     cache.check()
     assert res[0].abs().sum() > 0 and (res[0] - res[1]).abs().max() < 0.05  # (as bounds of other kernels: 0.044)
+
+
+@pytest.mark.parametrize("m", [1, 3, 20])
+@pytest.mark.parametrize("bounds", [[0, 2, 1, 4], [4, 3, 2, 0], [-1, 1, 2, 4], [0, 3, 3, 2]])
+def test_token_bounds_that_do_not_ascend(bounds, m):
+    """Reported, and nothing computed, by each of the kernels (as few, more and many rows choose them)."""
+    from latency_moe_decode_gb300.capi import DecError
+    lens = [30, 5, 90]
+    cache, table, _, _, g = _filled([l + 2 * m for l in lens], 2, 128, 16, 10)
+    q = _rnd(g, 4 * m, 8, 128).cuda()
+    out = torch.full_like(q, 3.0)
+    cu = _ints([b * m for b in bounds])
+    cache.attention(q, _ints(lens), table, cu_tokens=cu, max_tokens=m, out=out)
+    with pytest.raises(DecError) as e:
+        cache.check()
+    assert e.value.status == -1 and (out == 3).all()
+    good = _ints([0, m, 2 * m, 2 * m])
+    cache.attention(q, _ints(lens), table, cu_tokens=good, max_tokens=m, out=out)
+    cache.check()
+    assert (out[:2 * m] != 3).any(-1).all() and (out[2 * m:] == 3).all()
