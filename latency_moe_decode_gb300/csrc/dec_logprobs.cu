@@ -569,7 +569,8 @@ extern "C" dec_status dec_logprobs(const dec_logprobs_args* a, void* stream) {
   if (!a->logits) return op_fail(DEC_ERR_ARG, "logprobs: logits are NULL");
   if (reinterpret_cast<uintptr_t>(a->logits) % (a->dtype == DEC_BF16 ? 2 : 4))
     return op_fail(DEC_ERR_ARG, "logprobs: logits are not aligned to their type");
-  if (a->vocab > INT_MAX - 64 || a->rows > INT_MAX / lp::kMaxCluster)
+  // (ids are counted in 32 bits, up to four steps of a CTA past the row's end)
+  if (a->vocab > INT_MAX - 4 * lp::kThreads || a->rows > INT_MAX / lp::kMaxCluster)
     return op_fail(DEC_ERR_UNSUPPORTED, "logprobs: too many rows or ids");
   if (dec_status st = op_on_device(a->logits, "logprobs: logits")) return st;
   lp::Params p;

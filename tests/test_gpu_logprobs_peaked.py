@@ -85,3 +85,19 @@ def test_rows_of_any_magnitude(vocab, n, dtype):
     lp = _exact(x)[0]
     t = np.where(lp[np.arange(len(t)), t] < -3.4e38, x.argmax(-1).cpu().numpy(), t).astype(np.int32)  # (beyond fp32's range)
     _check(x, t, min(n, 1))
+
+
+@pytest.mark.parametrize("value", [0.0, 9000.0])
+def test_the_longest_rows(value):
+    """2^31 - 1025 equal logits: a second look at the whole row for its alternatives, another for its sums where they lie
+    far from 0."""
+    from latency_moe_decode_gb300 import ops
+    vocab = 2 ** 31 - 1025
+    x = torch.full((1, vocab), value, dtype=BF, device="cuda")
+    x[0, 5] = -torch.inf
+    r = ops.logprobs(x, torch.tensor([vocab - 1], dtype=torch.int32, device="cuda"), top_n=1)
+    want = -np.log(vocab - 1)
+    # every sum is of ones or of one power of two, exact up to 2^24 of them: a thread has 2^20 to 2^23
+    assert abs(r.logprob.item() - want) <= 40 * U * -want and abs(r.top_logprobs.item() - want) <= 40 * U * -want
+    assert abs(r.entropy.item() + want) <= 80 * U * -want
+    assert r.rank.item() == vocab - 2 and r.top_ids.item() == 0

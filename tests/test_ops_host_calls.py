@@ -110,3 +110,11 @@ def test_attention_passes_on_the_likely_rows(monkeypatch):
                                  out_head_stride=128, max_tokens=1, likely_tokens=-1)
     seqs, c = capi.DecKvqSeqs(1, 1, None, 4096, 4096, 4, 4), capi.DecKvqCache(4096, 4, 64, 2, 128, None)
     assert lib.dec_kvq_attention(c, seqs, a, None) == -1 and b"likely_tokens" in lib.dec_op_error()
+
+
+def test_rows_whose_ids_would_pass_32_bits_are_refused():
+    build.build()
+    lib = capi.lib()
+    for vocab, refused in ((2 ** 31 - 1, True), (2 ** 31 - 1024, True), (2 ** 31 - 1025, False)):
+        a = capi.DecLogprobsArgs(logits=4096, dtype=0, rows=1, vocab=vocab, row_stride=vocab, entropy=4096)
+        assert (lib.dec_logprobs(a, None) == -5) == refused
