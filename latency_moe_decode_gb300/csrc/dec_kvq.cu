@@ -83,6 +83,8 @@ dec_status check_seqs(const dec_kvq_seqs* s, const dec_kvq_cache* c) {
     return op_fail(DEC_ERR_ARG, "sequences: without cu_tokens every sequence has one row (n_tokens == batch)");
   if (s->batch == 0 || s->n_tokens == 0) return DEC_OK;
   if (!s->lengths || !s->table || s->max_pages == 0) return op_fail(DEC_ERR_ARG, "sequences: lengths and table are needed");
+  // (sequences are counted in 32 bits, up to a launch's share past the last)
+  if (s->batch > INT_MAX - 4 * kMaxSeqs) return op_fail(DEC_ERR_UNSUPPORTED, "sequences: a batch of 2^31");
   if (s->table_stride < 0) return op_fail(DEC_ERR_ARG, "sequences: negative table_stride");
   if ((long long)s->max_pages * c->page_tokens > INT_MAX - 65536)
     return op_fail(DEC_ERR_UNSUPPORTED, "sequences: a page table of 2^31 positions or more");

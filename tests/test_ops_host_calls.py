@@ -118,3 +118,19 @@ def test_rows_whose_ids_would_pass_32_bits_are_refused():
     for vocab, refused in ((2 ** 31 - 1, True), (2 ** 31 - 1024, True), (2 ** 31 - 1025, False)):
         a = capi.DecLogprobsArgs(logits=4096, dtype=0, rows=1, vocab=vocab, row_stride=vocab, entropy=4096)
         assert (lib.dec_logprobs(a, None) == -5) == refused
+
+
+def test_batches_whose_sequences_would_pass_32_bits_are_refused():
+    build.build()
+    lib = capi.lib()
+    cache = capi.DecKvqCache(4096, 4, 64, 2, 128, None)
+    rows = capi.DecRows(4096, 256, 128)
+    append = capi.DecKvqAppendArgs(dtype=0, k=4096, k_token_stride=256, k_head_stride=128, v=4096, v_token_stride=256,
+                                   v_head_stride=128, eps=1e-6)
+    attend = capi.DecKvqAttentionArgs(n_heads=2, q=4096, q_token_stride=256, q_head_stride=128, out=4096,
+                                      out_token_stride=256, out_head_stride=128, max_tokens=1)
+    for batch, refused in ((2 ** 31 - 1, True), (2 ** 31 - 1024, True), (2 ** 31 - 1025, False)):
+        seqs = capi.DecKvqSeqs(batch, 1, 4096, 4096, 4096, 4, 4)
+        got = [lib.dec_kvq_append(cache, seqs, append, None), lib.dec_kvq_gather(cache, seqs, rows, rows, None)]
+        assert [st == -5 for st in got] == [refused] * 2
+        assert lib.dec_kvq_attention(cache, seqs, attend, None) == (-5 if refused else -1)  # (no workspace)
