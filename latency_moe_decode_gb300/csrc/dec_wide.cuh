@@ -842,12 +842,7 @@ struct WMma {
       ++lay;
     }
     if (p.V > 0) gemv(K_LM, 0);
-    if (gseq > 0) {
-      const unsigned last = gseq - 1;
-      const unsigned long long t0 = gtimer();
-      while (!mbar_try_wait(&m->tfull[last % kNGW], (last / kNGW) & 1) && gtimer() - t0 < p.timeout_ns) {
-      }
-    }
+    finish();
     if (DEC_TRACE && blockIdx.x == 0) {
       p.trace[kWaitTrace + 2] = tw_full;
       p.trace[kWaitTrace + 3] = tw_tmem;
@@ -2149,6 +2144,33 @@ struct WConsumer {
 
 // ---------------------------------------------------------------------------------------------
 
+// The CTA's barriers, by one thread.
+__device__ __forceinline__ void init_bars(int ring, uint64_t* full, uint64_t* empty, uint64_t* mempty, WMisc* m) {
+  for (int s = 0; s < ring; ++s) {
+    mbar_init(&full[s], 1);
+    mbar_init(&empty[s], kConsumerWarps);
+    mbar_init(&mempty[s], 1);
+  }
+  mbar_init(&m->rt_bar, 1);
+  mbar_init(&m->mma_done, 1);
+  mbar_init(&m->tm_ready, 1);
+  mbar_init(&m->sbar, 1);
+  mbar_init(&m->obar, 1);
+  m->stages_begun = 0;
+  for (int i = 0; i < kNGW; ++i) {
+    mbar_init(&m->tfull[i], 2);  // MMA commit + the MMA thread's release of the block scales
+    mbar_init(&m->tempty[i], kConsumerWarps);
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+__device__ __forceinline__ int token_of(const KParams& p, int b) {
+  const int tok = p.tokens[b];
+  if (tok >= 0 && tok < p.V) return tok;
+  raise_err(p, kDevBadArg, 2);
+  return 0;
+}
+
 template <int NR, int HD, int G>
 __global__ void __launch_bounds__(kThreads, 1)
     wide_step_kernel(const __grid_constant__ KParams p, const __grid_constant__ WideParams w) {
@@ -2161,24 +2183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* red = reinterpret_cast<float*>(smem + L.red_off);
   WMisc* m = reinterpret_cast<WMisc*>(smem + L.misc_off);
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    for (int s = 0; s < p.ring; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kConsumerWarps);
-      mbar_init(&mempty[s], 1);
-    }
-    mbar_init(&m->rt_bar, 1);
-    mbar_init(&m->mma_done, 1);
-    mbar_init(&m->tm_ready, 1);
-    mbar_init(&m->sbar, 1);
-    mbar_init(&m->obar, 1);
-    m->stages_begun = 0;
-    for (int i = 0; i < kNGW; ++i) {
-      mbar_init(&m->tfull[i], 2);  // MMA commit + the MMA thread's release of the block scales
-      mbar_init(&m->tempty[i], kConsumerWarps);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
+  if (tid == 0) init_bars(p.ring, full, empty, mempty, m);
   if (tid < kWideMax) {
     int len = 0, tok = 0;
     if (tid < p.B) {
@@ -2187,13 +2192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         raise_err(p, kDevBadArg, 1);
         len = 0;
       }
-      if (p.tokens) {
-        tok = p.tokens[tid];
-        if (tok < 0 || tok >= p.V) {
-          raise_err(p, kDevBadArg, 2);
-          tok = 0;
-        }
-      }
+      if (p.tokens) tok = token_of(p, tid);
     }
     m->len[tid] = len;
     m->tok[tid] = tok;
@@ -2229,36 +2228,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* red = reinterpret_cast<float*>(smem + L.red_off);
   WMisc* m = reinterpret_cast<WMisc*>(smem + L.misc_off);
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    for (int s = 0; s < p.ring; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kConsumerWarps);
-      mbar_init(&mempty[s], 1);
-    }
-    mbar_init(&m->rt_bar, 1);
-    mbar_init(&m->mma_done, 1);
-    mbar_init(&m->tm_ready, 1);
-    mbar_init(&m->sbar, 1);
-    mbar_init(&m->obar, 1);
-    m->stages_begun = 0;
-    for (int i = 0; i < kNGW; ++i) {
-      mbar_init(&m->tfull[i], 2);  // MMA commit + the MMA thread's release of the block scales
-      mbar_init(&m->tempty[i], kConsumerWarps);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
+  if (tid == 0) init_bars(p.ring, full, empty, mempty, m);
   if (tid < kWideMax) {
-    int tok = 0;
-    if (tid < p.B) {
-      if (p.tokens) {
-        tok = p.tokens[tid];
-        if (tok < 0 || tok >= p.V) {
-          raise_err(p, kDevBadArg, 2);
-          tok = 0;
-        }
-      }
-    }
-    m->tok[tid] = tok;
+    m->tok[tid] = tid < p.B && p.tokens ? token_of(p, tid) : 0;
   }
   __syncthreads();
   if (tid >= kConsumerWarps * 32) {
