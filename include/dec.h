@@ -418,8 +418,9 @@ int64_t dec_kvq_page_bytes(int32_t page_tokens, int32_t n_kv_heads, int32_t head
                 (2i, 2i + 1): (a, b) -> (a cos - b sin, a sin + b cos)
      q_out      bf16 rows (may be q.p itself when that is bf16 with the same strides)
    Everything is computed in fp32 and rounded once, to bf16 or to the cache's codes; keys whose fp32
-   value is too near the border between two codes or scales to tell are computed again with twice
-   the bits. Inputs above 1e18 overflow the norm's squares. The same position must not be
+   value lies within five standard deviations of its roundings of the border between two codes or scales are
+   computed again with twice the bits (so a code beside the formula's is not excluded, but would take
+   roundings that all but agree). Inputs above 1e18 overflow the norm's squares. The same position must not be
    appended twice in one call. */
 typedef struct {
   dec_dtype dtype;
@@ -455,7 +456,10 @@ dec_status dec_kvq_gather(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, 
                 is of no interest before or after the call
    A row with no position gives out = 0 and lse = -infinity. Scores, softmax statistics and the
    output sum are fp32; queries enter the products exactly (values below 2^-17 of their head's
-   largest: to 2^-25 of it), probabilities with 11 bits. Rows that meet a bad page or a position
+   largest: to 2^-25 of it). Probabilities enter the second product with 11 bits, down to 2^-29 of the row's
+   largest, and below that to steps of 2^-40 of it; in the kernel for many rows (more than 16 query rows
+   per KV head and sequence, 32 for heads of 64) down to 2^-21 and to steps of 2^-32. Their sum is of
+   fp32 terms. Rows that meet a bad page or a position
    beyond the page table hold nothing of use, the other sequences' are right. A call repeated
    gives the same bits; a sequence in another batch may be cut and joined elsewhere. A call of 2^31 query
    rows or of a page table of 2^31 positions is DEC_ERR_UNSUPPORTED. */
@@ -472,7 +476,8 @@ typedef struct {
 } dec_kvq_attention_args;
 dec_status dec_kvq_attention(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, const dec_kvq_attention_args* args,
                              void* stream);
-/* Workspace bytes for calls with these sizes on the current device (-1 for a refused shape). */
+/* Workspace bytes for calls with these sizes on the current device (-1 for a refused shape); any batch
+   needs the same. */
 int64_t dec_kvq_attention_workspace(const dec_kvq_cache* cache, int32_t n_heads, int32_t batch, int32_t max_tokens);
 
 /* Log-probabilities of rows of logits (fp32 or bf16; row r at logits + r * row_stride elements):

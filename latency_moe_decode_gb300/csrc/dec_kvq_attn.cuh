@@ -18,7 +18,8 @@
 //  - what a warp leaves unfinished of a unit is joined per CTA in shared memory, and what a CTA
 //    leaves unfinished by a second small kernel, both in a fixed order.
 // Measured (32 query, 8 KV heads of 128, one row a sequence): 16 sequences of 8 k to 32 k
-// 81 us (4.5 TB/s; ALU pipe 51 %, issue slots 60 %); 64 of up to 2 k and one of 64 k 29 us, of which 14 are
+// 80 us (4.5 TB/s; issue slots 62 % full, ALU pipe 51 %: neither binds, but scores, maximum, exponentials and
+// values of a chunk are one chain of dependent instructions a warp, four warps a scheduler); 64 of up to 2 k and one of 64 k 29 us, of which 14 are
 // the stream and 15 are fixed: list and page table 3, a unit's queries 3, the first chunk's code and
 // data 3, joins 6. Cutting the joins' dependent loads to one round did not shorten them.
 #pragma once

@@ -16,9 +16,10 @@
 //    n to 3.5 n. Threads whose maximum reaches the bound look at its vector again, and through all
 //    theirs where their second largest vector reaches it too; the few candidates are ranked against
 //    each other.
-// What bounds it: at many rows the instructions (about 9 an element for bf16, where the read of the
-// logits leaves time for 11): 2048 rows of 32000 bf16 41 us, 3.2 TB/s; at few rows latency (one row of
-// 32000 7 us), and for long ones a CTA's rate: a cluster of up to 8 CTAs then shares a row.
+// What bounds it: at many rows the instructions and the waits between a row's parts. 2048 rows of 32000 bf16
+// take 41 us, 3.2 TB/s: 15 instructions a logit, 24 us of full issue slots (they are 66 % full), of which the
+// pass is 9 and the rest follows it row by row, between barriers, while the CTA asks for no more of memory. At few rows
+// latency (one row of 32000 7 us), and for long ones a CTA's rate: a cluster of up to 8 CTAs then shares a row.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
