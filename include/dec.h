@@ -23,6 +23,8 @@
  *    the new stream wait for the old one (an event), so calls of one engine run in call order
  *    whatever streams they are given. Work of other engines and other libraries is never waited
  *    for: no entry point synchronises the whole device.
+ *    Calls without a `stream` argument run on the engine's own stream: what the caller has queued
+ *    elsewhere on their buffers has to be done before (the Python wrapper waits for it).
  *  - Entry points that queue device work require the engine's device to be the current CUDA
  *    device (DEC_ERR_ARG otherwise).
  *  - Every call returns a dec_status. Errors found on the device (a wait that ran out of time,

@@ -104,6 +104,12 @@ class Engine:
         except Exception:
             pass
 
+    @staticmethod
+    def _wait():
+        """Before calls that run on the engine's own stream, which is not ordered after torch's: what is still queued
+        there may be writing their inputs, or be the last use of memory that an output has been given."""
+        torch.cuda.current_stream().synchronize()
+
     # ---- API
     def prefill_tokens(self, tokens: torch.Tensor, seq: int = 0):
         """tokens: device int32 [n_seq, n] (or [n] for one slot)."""
@@ -112,6 +118,7 @@ class Engine:
             t = t[None]
         t = t.contiguous()
         ctx = DecCtx(seq, t.shape[0], t.data_ptr(), t.shape[1], None, None)
+        self._wait()
         self._check(self.lib.dec_prefill_kv(self.h, C.byref(ctx)), "dec_prefill_kv")
 
     def prefill_tokens_noalloc(self, tokens: torch.Tensor, seq: int = 0):
@@ -122,12 +129,14 @@ class Engine:
             raise ValueError("tokens must be a contiguous int32 device tensor")
         t = tokens if tokens.dim() == 2 else tokens[None]
         ctx = DecCtx(seq, t.shape[0], t.data_ptr(), t.shape[1], None, None)
+        self._wait()
         self._check(self.lib.dec_prefill_kv_noalloc(self.h, C.byref(ctx)), "dec_prefill_kv_noalloc")
 
     def prefill_import(self, k: torch.Tensor, v: torch.Tensor, seq: int = 0, n_seq: int = 1):
         """k, v: device bf16 [n_layers, n_kv_heads, n, head_dim]."""
         k, v = k.contiguous(), v.contiguous()
         ctx = DecCtx(seq, n_seq, None, k.shape[2], k.data_ptr(), v.data_ptr())
+        self._wait()
         self._check(self.lib.dec_prefill_kv(self.h, C.byref(ctx)), "dec_prefill_kv")
 
     def step(self, tokens: Optional[torch.Tensor] = None, hidden: Optional[torch.Tensor] = None,
@@ -270,6 +279,7 @@ class Engine:
         c = self.cfg
         k = torch.empty(c.n_kv_heads, n, c.head_dim, dtype=torch.bfloat16, device="cuda")
         v = torch.empty_like(k)
+        self._wait()
         self._check(self.lib.dec_export_kv(self.h, seq, layer, pos0, n, k.data_ptr(), v.data_ptr()), "dec_export_kv")
         return k, v
 

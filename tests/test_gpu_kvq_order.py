@@ -85,3 +85,39 @@ def test_store_follows_the_reads_and_the_table(raw):
             assert np.array_equal(got.double().cpu().numpy(), ref.store(bfv(x[l]))[0].transpose(1, 0, 2))
         assert not c.pages[:c.page_bytes].any()  # page 0, which the table held before it was written
     caches[0].check()
+
+
+def test_slots_filled_and_read_beside_queued_work():
+    """Keys, values and ids that are still being written when a slot is filled from them; a slot read into memory
+    that queued work has used."""
+    eng, plain = (_engine(_models(CFG, 2)[1]) for _ in range(2))
+    k, v = (t.cuda() for t in synth.gen_kv(CFG, N, seed=8))
+    ids = synth.gen_tokens(9, CFG.vocab, seed=3).cuda().to(torch.int32)
+    plain.prefill_import(k, v, seq=1)
+    plain.prefill_tokens(ids, seq=2)
+    plain.prefill_tokens_noalloc(ids, seq=3)
+    late = [torch.zeros_like(t) for t in (k, v, ids)]
+    torch.cuda.synchronize()
+
+    def fill():
+        for t in late:
+            t.zero_()
+        torch.cuda._sleep(BUSY)
+        for t, x in zip(late, (k, v, ids)):
+            t.copy_(x)
+
+    fill()
+    eng.prefill_import(late[0], late[1], seq=1)
+    fill()
+    eng.prefill_tokens(late[2], seq=2)
+    fill()
+    eng.prefill_tokens_noalloc(late[2], seq=3)
+    for seq, n in ((1, N), (2, 9), (3, 9)):
+        for l in range(CFG.n_layers):
+            torch.cuda._sleep(BUSY // 10)
+            used = torch.empty(2, CFG.n_kv_heads, n, CFG.head_dim, dtype=torch.bfloat16, device="cuda")
+            used.fill_(7.0)  # queued; its memory goes to the next outputs
+            del used
+            got = eng.export_kv(seq, l, 0, n)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, plain.export_kv(seq, l, 0, n)))

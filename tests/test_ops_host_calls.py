@@ -134,3 +134,24 @@ def test_batches_whose_sequences_would_pass_32_bits_are_refused():
         got = [lib.dec_kvq_append(cache, seqs, append, None), lib.dec_kvq_gather(cache, seqs, rows, rows, None)]
         assert [st == -5 for st in got] == [refused] * 2
         assert lib.dec_kvq_attention(cache, seqs, attend, None) == (-5 if refused else -1)  # (no workspace)
+
+
+def test_calls_on_the_engines_own_stream_wait_for_torchs(monkeypatch):
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or 0
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(synchronize=lambda: calls.append("wait")))
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: empty(*a, dtype=kw["dtype"]))
+    eng = _engine(Lib())
+    eng.cfg.n_kv_heads, eng.cfg.head_dim = 2, 64
+    t = torch.zeros(5, dtype=torch.int32)
+    kv = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    eng.prefill_tokens(t)
+    eng.prefill_tokens_noalloc(t)
+    eng.prefill_import(kv, kv)
+    eng.export_kv(0, 0, 0, 3)
+    assert calls == ["wait", "dec_prefill_kv", "wait", "dec_prefill_kv_noalloc", "wait", "dec_prefill_kv", "wait", "dec_export_kv"]
