@@ -384,9 +384,9 @@ typedef struct {
    cu_tokens[b] .. cu_tokens[b + 1] - 1 (device int32 [batch + 1]; NULL: one row per sequence and
    n_tokens == batch). Its row j stands at position lengths[b] + j (device int32 [batch]), and
    position p is in page table[b * table_stride + p / page_tokens] (device int32; max_pages
-   entries of each row are valid). cu_tokens must ascend (the attention computes none of up to 256 neighbouring sequences among which they
-   do not, and records DEC_ERR_ARG). Rows before cu_tokens[0] or from
-   cu_tokens[batch] on belong to no sequence: outputs leave them as they were. */
+   entries of each row are valid). cu_tokens must ascend (where they do not, the attention records
+   DEC_ERR_ARG and computes none of the up to 256 neighbouring sequences of a launch). Rows before
+   cu_tokens[0] or from cu_tokens[batch] on belong to no sequence: outputs leave them as they were. */
 typedef struct {
   int32_t batch;
   int32_t n_tokens;

@@ -369,7 +369,8 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
   auto fits = [&](int k) {
     const int rows = k == 0 ? 8 : k == 1 ? 16 : 128, positions = k == 2 ? kTile : kGroup;
     const long long units = (long long)c->n_kv_heads * ((long long)s->n_tokens * p.group / rows + s->batch);
-    return units * ((long long)s->max_pages * c->page_tokens / positions + 1 + std::max(kUnitCost, kPromptCost)) < (1LL << 32) - 64;
+    const long long each = (long long)s->max_pages * c->page_tokens / positions + 1 + std::max(kUnitCost, kPromptCost);
+    return units * each < (1LL << 32) - 64;
   };
   if (fits(likely)) kind = likely;
   else if (!fits(kind)) return op_fail(DEC_ERR_UNSUPPORTED, "attention: too much work for one call");

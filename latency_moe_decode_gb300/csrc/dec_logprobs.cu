@@ -227,7 +227,8 @@ __device__ __noinline__ Sums far_sums(const char* first, int vocab, float M, Sum
   Sums a{0.f, 0.f, 0.f, M};
 #pragma unroll 4
   for (int i = tid; i < vocab; i += kThreads) {
-    const float x = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(first)[i]) : reinterpret_cast<const float*>(first)[i];
+    const float x = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(first)[i])
+                         : reinterpret_cast<const float*>(first)[i];
     const float t = fmaxf((x - M) * kL2E, -256.f), y = ex2(t);
     a.s += y;
     a.u = fmaf(y, t, a.u);
