@@ -14,7 +14,10 @@
 //    has nothing to offer here: 8 columns of queries leave the tensor cores mostly idle, and the
 //    codes would have to be written to shared memory again for tcgen05 to read them;
 //  - probabilities go from the first product's result layout to the second's operand layout by
-//    movmatrix; the running maximum and sum stay in fp32 registers;
+//    movmatrix, rounded to f16 on the way: 11 bits where the bf16 output keeps 8. Two f16 a probability
+//    (22 bits) and a second product took 16 sequences of 8 k to 32 k from 80 to 89 us and left the output's
+//    error against 64 bits at 0.0017. The running maximum, the sum (of unrounded terms) and the output stay in
+//    fp32 registers;
 //  - what a warp leaves unfinished of a unit is joined per CTA in shared memory, and what a CTA
 //    leaves unfinished by a second small kernel, both in a fixed order.
 // Measured (32 query, 8 KV heads of 128, one row a sequence): 16 sequences of 8 k to 32 k

@@ -13,7 +13,8 @@
 //    in tensor memory: shared memory then carries the codes, K and V only (with all four there its
 //    bandwidth held a tile to 2.9 k cycles);
 //  - eight hold half a query row a thread: its 64 scores stay in registers from the maximum (joined
-//    with the other half's) through the exponentials to P, f16 in tensor memory. The reference of the
+//    with the other half's) through the exponentials to P, f16 in tensor memory (11 bits, as in the kernel for
+//    few rows; there is no room for a second half of each). The reference of the
 //    exponentials follows the maximum only when that passes it by 2^8 (O lies in tensor memory, and
 //    rescaling it costs as much as the exponentials). With whole rows and two reads of the scores, four
 //    warps took 6.7 k cycles a tile for this; the exponentials' own floor is 1 k.
