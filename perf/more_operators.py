@@ -443,10 +443,10 @@ def _rotate(x, table, pos):
 def _commit(s):
     seq, j, _, depth = _tree_sees(s)
     _, _, at, off = _where(s["cu"], s["table"], s["page"], s["lengths"], s["n_tokens"])
-    source = j.clone()
+    source = j.long()
     kept = j < s["count"][seq]
-    source[kept] = s["path"][seq[kept], j[kept].long()]
-    row = (s["cu"][seq] + source).long()
+    source[kept] = s["path"][seq[kept], j[kept].long()].long()
+    row = s["cu"][seq] + source
     got = []
     for i, x in enumerate((_rotate(s["k"], s["rope"], s["lengths"][seq] + depth), s["v"])):
         codes, scales = _quantise(x)
