@@ -343,8 +343,8 @@ const char* dec_status_string(dec_status s);
 void dec_destroy(dec_engine* eng);
 
 /* ------------------------------------------------------------------------------------------
-   Operators beside the engine: a paged KV cache held in 4 bits, attention over it, and
-   log-probabilities. They keep no state of their own: the caller owns every buffer. Unlike the
+   Operators beside the engine: a paged KV cache held in 4 bits, attention over it (for trees of drafted
+   tokens too), what keeps it within a bound, log-probabilities, and the verification of drafts. They keep no state of their own: the caller owns every buffer. Unlike the
    engine's entry points they take no engine, so:
     - stream == NULL is the legacy default stream; work is queued on `stream`, nothing is
       synchronised, no call allocates device memory, and every call may be captured into a graph;
@@ -435,6 +435,10 @@ typedef struct {
   int32_t rope_len;
   int32_t rotary_dim;
   int32_t interleaved;
+  const int32_t* positions; /* device [n_tokens], may be NULL: the rotary position of each row, where that is not
+                               where the row stands in the cache (a token of a tree, a sequence that gave positions
+                               up). A negative one is DEC_ERR_ARG, one beyond the rotation table DEC_ERR_CAPACITY, in
+                               status; the row is skipped */
 } dec_kvq_append_args;
 dec_status dec_kvq_append(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, const dec_kvq_append_args* args,
                           void* stream);
@@ -454,6 +458,10 @@ dec_status dec_kvq_gather(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, 
      max_tokens an upper bound of the rows of one sequence (host); rows beyond it are not computed
      likely_tokens  how many rows most sequences have (host; 0: max_tokens), where max_tokens is far above it:
                 it chooses among kernels for few and for many rows, each of which takes any number
+     tree_mask  device, NULL or the sequences' trees (causal != 0): row j of sequence b attends to positions 0 ..
+                lengths[b] - 1 and, of the sequence's own rows, to those i (position lengths[b] + i) whose bit i % 32 of
+                word tree_mask[row * tree_stride + i / 32] is set, i < 32 tree_words. tree_words: 1 .. DEC_MAX_TREE / 32;
+                rows numbered from 32 tree_words on are seen by none. As dec_draft_tree writes them, or any other set
      workspace  16-byte aligned device memory of dec_kvq_attention_workspace() bytes; its content
                 is of no interest before or after the call
    A row with no position gives out = 0 and lse = -infinity. Scores, softmax statistics and the
@@ -465,6 +473,7 @@ dec_status dec_kvq_gather(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, 
    beyond the page table hold nothing of use, the other sequences' are right. A call repeated
    gives the same bits; a sequence in another batch may be cut and joined elsewhere. A call of 2^31 query
    rows or of a page table of 2^31 positions is DEC_ERR_UNSUPPORTED. */
+#define DEC_MAX_TREE 1024 /* rows of one sequence's tree */
 typedef struct {
   int32_t n_heads;
   dec_rows q, out;
@@ -475,12 +484,110 @@ typedef struct {
   void* workspace;
   int64_t workspace_bytes;
   int32_t likely_tokens;
+  const uint32_t* tree_mask;
+  int64_t tree_stride;
+  int32_t tree_words;
 } dec_kvq_attention_args;
 dec_status dec_kvq_attention(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, const dec_kvq_attention_args* args,
                              void* stream);
 /* Workspace bytes for calls with these sizes on the current device (-1 for a refused shape); any batch
    needs the same. */
 int64_t dec_kvq_attention_workspace(const dec_kvq_cache* cache, int32_t n_heads, int32_t batch, int32_t max_tokens);
+
+/* Trees of drafted tokens. Row j of a sequence has the row parents[j] (an index within the sequence, below j) as
+   its parent; row 0 is the sequence's last known token. A row whose parent is not an earlier row begins a path of
+   its own.
+     parents    device int32 [n_tokens]
+     lengths    device int32 [batch]: position of row 0 (NULL: no positions)
+     max_tokens an upper bound of the rows of one sequence (host), at most DEC_MAX_TREE: a sequence's rows beyond it
+                are not computed
+     mask       [n_tokens][mask_stride] words, of which the first (max_tokens + 31) / 32 of each row are written: bit i
+                where row i of the sequence is the row itself or above it
+     positions  device int32 [n_tokens], may be NULL: lengths[b] + how many rows are above the row
+   Rows of no sequence are left as they are. A cu_tokens that does not ascend makes sequences of no rows. */
+typedef struct {
+  int32_t batch;
+  int32_t n_tokens;
+  const int32_t* cu_tokens; /* device [batch + 1] */
+  const int32_t* parents;
+  const int32_t* lengths;
+  int32_t max_tokens;
+  uint32_t* mask;
+  int64_t mask_stride;
+  int32_t* positions;
+} dec_draft_tree_args;
+dec_status dec_draft_tree(const dec_draft_tree_args* args, void* stream);
+
+/* Attention weight that cached positions receive, added up: for every position p that a row of the call attends to
+   (causal and lengths as in dec_kvq_attention) and every KV head h
+     mass_out[p] = decay * mass[p] + sum over the rows that attend to p and the heads of h's group of exp(scale q.k - lse)
+   where mass and mass_out are fp32 [n_pages][n_kv_heads][page_tokens], laid out as the cache's pages (mass_out may be
+   mass). Positions that the call's rows stand at (causal) have had nothing before, and where decay is 0 nothing is
+   read. Positions that no row could attend to are left as they are.
+     q          bf16 rows of n_heads heads, lse device fp32 [n_tokens][n_heads], both as the attention had and gave them;
+                a row whose lse is not finite adds nothing
+     max_tokens an upper bound of the rows of one sequence (host); rows beyond it add nothing
+   Scores and sums are fp32 (as the attention's: queries enter exactly); no sum's order depends on the call's other
+   sequences, and a call repeated gives the same bits. Bad pages are skipped and recorded in the cache's status. */
+typedef struct {
+  int32_t n_heads;
+  dec_rows q;
+  const float* lse;
+  float scale; /* 0: 1 / sqrt(head_dim) */
+  int32_t causal;
+  int32_t max_tokens;
+  float decay;
+  const float* mass; /* may be NULL where decay is 0 */
+  float* mass_out;
+} dec_kvq_mass_args;
+dec_status dec_kvq_mass(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, const dec_kvq_mass_args* args, void* stream);
+
+/* The positions that a cache bounded to `budget` a sequence keeps, for every sequence b and KV head: the first `sinks`
+   and the last `recent` of its lengths[b] positions and, of those between, the ones of the largest mass (equal masses:
+   the lower position first; a NaN orders below everything), budget in all. A sequence of budget positions and fewer
+   keeps all.
+     kept       device int32 [batch][n_kv_heads][budget]: the positions, ascending; -1 behind the last
+     count      device int32 [batch]: how many
+   seqs: n_tokens is of no interest, cu_tokens NULL and n_tokens == batch. Positions in bad pages (recorded in the
+   cache's status) weigh nothing; a sequence whose length is negative (DEC_ERR_ARG) or beyond the page table
+   (DEC_ERR_CAPACITY) keeps none. sinks + recent <= budget. */
+typedef struct {
+  const float* mass; /* fp32 [n_pages][n_kv_heads][page_tokens] */
+  int32_t budget;
+  int32_t sinks;
+  int32_t recent;
+  int32_t* kept;
+  int32_t* count;
+} dec_kvq_heaviest_args;
+dec_status dec_kvq_heaviest(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, const dec_kvq_heaviest_args* args,
+                            void* stream);
+
+/* Move positions as they are held (codes and scales, nothing is rounded again): for every sequence b, KV head h and
+   i < min(count[b], max_count) position lengths[b] + i receives what position lengths[b] + index[i] holds, index being
+   the list at index + b * index_stride + h * head_stride (head_stride 0: one list for all heads).
+     index      device int32. Within a list it ascends and index[i] >= i: positions move down, into room that others
+                have left, or stay. A negative entry moves nothing. A list that does not ascend, or moves up, leaves
+                anything in the sequence's positions
+     count      device int32 [batch]
+     to         device int32, NULL or the page table to write to, in place of seqs' own: [batch][to_stride], to_pages of
+                each row valid. It shares no page with the table that is read
+     mass       NULL, or fp32 [n_pages][n_kv_heads][page_tokens], moved alongside
+   In place (to NULL), positions that stay are not written: pages at a sequence's beginning that others share may be
+   part of it as long as nothing moves in them. Other pages belong to one sequence of the call.
+   seqs: cu_tokens NULL and n_tokens == batch; lengths is where a sequence's moves begin (its committed length; NULL: 0).
+   Pages and positions out of range are skipped and recorded in status. */
+typedef struct {
+  const int32_t* index;
+  int64_t index_stride;
+  int64_t head_stride;
+  const int32_t* count;
+  int32_t max_count;
+  const int32_t* to;
+  int32_t to_pages;
+  int64_t to_stride;
+  float* mass;
+} dec_kvq_move_args;
+dec_status dec_kvq_move(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, const dec_kvq_move_args* args, void* stream);
 
 /* Log-probabilities of rows of logits (fp32 or bf16; row r at logits + r * row_stride elements):
      targets      device int32 [rows], may be NULL; a target outside 0 .. vocab - 1 gives
@@ -515,6 +622,57 @@ typedef struct {
 } dec_logprobs_args;
 dec_status dec_logprobs(const dec_logprobs_args* args, void* stream);
 
+/* Verification of drafted tokens against the target's probabilities, so that the tokens that come out are
+   distributed as the target's own ("vLLM's Kimi K3 Backend Hits 842 Tokens per Second", section "Throughput holds
+   across the tested range": verifying speculative drafts). Sequence b's rows are cu_tokens[b] .. cu_tokens[b + 1] - 1:
+   row 0 its last known token, every other one a draft with a parent as in dec_draft_tree (parents NULL: each row's
+   parent is the row before, a chain). p_j = softmax(logits of row j / temperature[b]) is the target's distribution
+   after row j, q_j the one that the children of row j were drawn from, independently of one another: row j of
+   draft_probs, or (draft_probs NULL) certainty of the child's token. From row 0 on, at row j with p = p_j, its
+   children c in ascending order:
+     uniforms[c] q(tokens[c]) < p(tokens[c]): c is accepted, and it goes on at row c;
+     otherwise p becomes max(p - q, 0) over its sum (where that is 0, p stays) for the next child.
+   Where no child is accepted (or there is none) the next token is the first id, in ascending order, up to which p sums
+   to more than uniforms[row 0] times its whole sum. temperature NULL: 1; one that is not above 0: greedily, p_j and q
+   are certainty of the first of the largest logits, and of the child's token.
+     logits     [n_tokens] rows of vocab, fp32 or bf16, row_stride elements apart; -infinity has probability 0. A row
+                with a NaN or +infinity, or nothing but -infinity, has no distribution: no child of it is accepted, and
+                the next token after it is -1
+     draft_probs  device fp32, prob_stride elements apart, or NULL; read only for rows with children. Not renormalised
+     tokens, parents  device int32 [n_tokens]. A draft outside the vocabulary is refused and changes nothing
+     uniforms   device fp32 [n_tokens], in 0 <= u < 1: row 0's for the next token, a draft's for its acceptance
+     max_tokens an upper bound of the rows of one sequence (host), at most DEC_MAX_TREE; rows beyond it are not looked at
+     path       device int32 [batch][max_tokens]: the accepted rows, 0 first; -1 behind the last (dec_kvq_move's list)
+     count      device int32 [batch]: how many (1 + the accepted drafts; 0 for a sequence of no rows)
+     next_tokens  device int32 [batch] (-1 for a sequence of no rows)
+     workspace  16-byte aligned, of dec_verify_drafts_workspace() bytes
+   Acceptance is decided on fp32 sums where they leave no doubt, and like the next token on sums of some 36 bits where
+   they do. Probabilities below 2^-120 of the row's largest count as 0. A call repeated gives the same. */
+typedef struct {
+  const void* logits;
+  dec_dtype dtype;
+  int32_t vocab;
+  int64_t row_stride;
+  const float* draft_probs;
+  int64_t prob_stride;
+  int32_t batch;
+  int32_t n_tokens;
+  const int32_t* cu_tokens;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const float* uniforms;
+  const float* temperature; /* device [batch] */
+  int32_t max_tokens;
+  int32_t* path;
+  int32_t* count;
+  int32_t* next_tokens;
+  void* workspace;
+  int64_t workspace_bytes;
+} dec_verify_drafts_args;
+dec_status dec_verify_drafts(const dec_verify_drafts_args* args, void* stream);
+/* Workspace bytes for n_tokens rows on any device (-1: negative). */
+int64_t dec_verify_drafts_workspace(int32_t n_tokens);
+
 /* ------------------------------------------------------------------------------------------
    The engine over these operators. Conventions are the engine's again (errors in
    dec_last_error(), stream == NULL is the engine's stream, work ordered after its earlier work). */
@@ -525,13 +683,20 @@ dec_status dec_logprobs(const dec_logprobs_args* args, void* stream);
    position lengths[b] of seqs, is appended there in every layer, and attends to positions 0 ..
    lengths[b]. lengths are the caller's: add 1 before the next step.
      caches       host array [n_layers] of the engine's KV heads and head_dim
-     seqs         cu_tokens NULL, n_tokens == batch <= max_batch
+     seqs         cu_tokens NULL, n_tokens == batch <= max_batch. Or, to verify drafts, several token rows a sequence
+                  (cu_tokens given): batch counts the rows, n_tokens == batch, max_tokens bounds the rows of one
+                  sequence, and row j of sequence b is appended at lengths[b] + j
+     parents      with cu_tokens: NULL (the rows of a sequence follow one another), or device int32 [batch], each row's
+                  parent in its sequence's tree of drafts (dec_draft_tree): the row then attends to positions 0 ..
+                  lengths[b] - 1 and to its own path, and its rotary position goes by its depth. dec_verify_drafts
+                  takes the step's logits, dec_kvq_move its path, once for each layer's cache
      rope         device fp32 [rope_len][head_dim / 2][2] (as dec_kvq_append's, full heads, half
                   split); NULL: the engine's table of max_ctx positions
      the others   as dec_step_args'
    The step runs in n_layers + 1 cooperative launches (the wide kernel cut at each layer's attention)
    and the cache's append and attention launches between them; nothing is synchronised. The first
-   call of an engine allocates its buffers for these steps (make it before a stream capture begins).
+   call of an engine allocates its buffers for these steps, and so does its first one with cu_tokens (make them before
+   a stream capture begins). Rows of no sequence (before cu_tokens[0], behind the last) give nothing of use.
    Page ids, lengths and table bounds that are wrong are recorded in the caches' status words.
    Errors: DEC_ERR_ARG, DEC_ERR_UNSUPPORTED (an engine without the wide kernels: max_batch below
    dec_info.wide_min_batch, or a shape they do not take), DEC_ERR_POISONED, DEC_ERR_OOM,
@@ -548,6 +713,8 @@ typedef struct {
   int32_t* next_tokens;
   void* hidden_out;
   void* stream;
+  const int32_t* parents;
+  int32_t max_tokens;
 } dec_step_kvq_args;
 dec_status dec_step_kvq(dec_engine* eng, const dec_step_kvq_args* args);
 

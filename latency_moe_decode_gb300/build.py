@@ -7,9 +7,10 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdec.so")
-SOURCES = ["dec_engine.cu", "dec_wide.cu", "dec_kvq.cu", "dec_logprobs.cu", "dec_step_kvq.cu"]
+SOURCES = ["dec_engine.cu", "dec_wide.cu", "dec_kvq.cu", "dec_logprobs.cu", "dec_step_kvq.cu", "dec_kvq_keep.cu",
+           "dec_verify.cu"]
 HEADERS = ["dec_common.h", "dec_prims.cuh", "dec_kernel.cuh", "dec_wide.cuh", "dec_wide_host.h", "dec_kvq.cuh", "dec_kvq_attn.cuh",
-           "dec_kvq_prompt.cuh", "dec_f32x2.cuh", "dec_ops.h"]
+           "dec_kvq_prompt.cuh", "dec_kvq_host.h", "dec_kvq_keep.cuh", "dec_f32x2.cuh", "dec_ops.h"]
 
 
 def nvcc() -> str:

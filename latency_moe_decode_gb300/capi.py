@@ -81,13 +81,46 @@ def _row_fields(*names):
 class DecKvqAppendArgs(C.Structure):
     _fields_ = [("dtype", C.c_int), ("n_heads", C.c_int32), *_row_fields("q", "k", "v", "q_out"),
                 ("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("eps", C.c_float),
-                ("rope", C.c_void_p), ("rope_len", C.c_int32), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32)]
+                ("rope", C.c_void_p), ("rope_len", C.c_int32), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("positions", C.c_void_p)]
 
 
 class DecKvqAttentionArgs(C.Structure):
     _fields_ = [("n_heads", C.c_int32), *_row_fields("q", "out"), ("lse", C.c_void_p), ("scale", C.c_float),
                 ("causal", C.c_int32), ("max_tokens", C.c_int32), ("workspace", C.c_void_p),
-                ("workspace_bytes", C.c_int64), ("likely_tokens", C.c_int32)]
+                ("workspace_bytes", C.c_int64), ("likely_tokens", C.c_int32), ("tree_mask", C.c_void_p),
+                ("tree_stride", C.c_int64), ("tree_words", C.c_int32)]
+
+
+class DecDraftTreeArgs(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("n_tokens", C.c_int32), ("cu_tokens", C.c_void_p), ("parents", C.c_void_p),
+                ("lengths", C.c_void_p), ("max_tokens", C.c_int32), ("mask", C.c_void_p), ("mask_stride", C.c_int64),
+                ("positions", C.c_void_p)]
+
+
+class DecKvqMassArgs(C.Structure):
+    _fields_ = [("n_heads", C.c_int32), *_row_fields("q"), ("lse", C.c_void_p), ("scale", C.c_float),
+                ("causal", C.c_int32), ("max_tokens", C.c_int32), ("decay", C.c_float), ("mass", C.c_void_p),
+                ("mass_out", C.c_void_p)]
+
+
+class DecKvqHeaviestArgs(C.Structure):
+    _fields_ = [("mass", C.c_void_p), ("budget", C.c_int32), ("sinks", C.c_int32), ("recent", C.c_int32),
+                ("kept", C.c_void_p), ("count", C.c_void_p)]
+
+
+class DecKvqMoveArgs(C.Structure):
+    _fields_ = [("index", C.c_void_p), ("index_stride", C.c_int64), ("head_stride", C.c_int64), ("count", C.c_void_p),
+                ("max_count", C.c_int32), ("to", C.c_void_p), ("to_pages", C.c_int32), ("to_stride", C.c_int64),
+                ("mass", C.c_void_p)]
+
+
+class DecVerifyDraftsArgs(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("dtype", C.c_int), ("vocab", C.c_int32), ("row_stride", C.c_int64),
+                ("draft_probs", C.c_void_p), ("prob_stride", C.c_int64), ("batch", C.c_int32), ("n_tokens", C.c_int32),
+                ("cu_tokens", C.c_void_p), ("tokens", C.c_void_p), ("parents", C.c_void_p), ("uniforms", C.c_void_p),
+                ("temperature", C.c_void_p), ("max_tokens", C.c_int32), ("path", C.c_void_p), ("count", C.c_void_p),
+                ("next_tokens", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
 
 
 class DecLogprobsArgs(C.Structure):
@@ -100,7 +133,7 @@ class DecStepKvqArgs(C.Structure):
     _fields_ = [("tokens", C.c_void_p), ("hidden_in", C.c_void_p), ("batch", C.c_int32),
                 ("caches", C.POINTER(DecKvqCache)), ("seqs", C.POINTER(DecKvqSeqs)), ("rope", C.c_void_p),
                 ("rope_len", C.c_int32), ("logits", C.c_void_p), ("next_tokens", C.c_void_p),
-                ("hidden_out", C.c_void_p), ("stream", C.c_void_p)]
+                ("hidden_out", C.c_void_p), ("stream", C.c_void_p), ("parents", C.c_void_p), ("max_tokens", C.c_int32)]
 
 
 class DecScoreArgs(C.Structure):
@@ -111,6 +144,7 @@ class DecScoreArgs(C.Structure):
 
 DEC_BF16, DEC_F32 = 0, 1
 DEC_MAX_TOP = 32  # include/dec.h
+DEC_MAX_TREE = 1024
 
 # name -> (restype, argtypes); the exported surface of dec.h
 PROTOTYPES = {
@@ -147,6 +181,13 @@ PROTOTYPES = {
     "dec_kvq_attention_workspace": (C.c_int64, [C.POINTER(DecKvqCache), C.c_int32, C.c_int32, C.c_int32]),
     "dec_kvq_attention": (C.c_int, [C.POINTER(DecKvqCache), C.POINTER(DecKvqSeqs), C.POINTER(DecKvqAttentionArgs),
                                     C.c_void_p]),
+    "dec_draft_tree": (C.c_int, [C.POINTER(DecDraftTreeArgs), C.c_void_p]),
+    "dec_kvq_mass": (C.c_int, [C.POINTER(DecKvqCache), C.POINTER(DecKvqSeqs), C.POINTER(DecKvqMassArgs), C.c_void_p]),
+    "dec_kvq_heaviest": (C.c_int, [C.POINTER(DecKvqCache), C.POINTER(DecKvqSeqs), C.POINTER(DecKvqHeaviestArgs),
+                                   C.c_void_p]),
+    "dec_kvq_move": (C.c_int, [C.POINTER(DecKvqCache), C.POINTER(DecKvqSeqs), C.POINTER(DecKvqMoveArgs), C.c_void_p]),
+    "dec_verify_drafts": (C.c_int, [C.POINTER(DecVerifyDraftsArgs), C.c_void_p]),
+    "dec_verify_drafts_workspace": (C.c_int64, [C.c_int32]),
     "dec_logprobs": (C.c_int, [C.POINTER(DecLogprobsArgs), C.c_void_p]),
     "dec_step_kvq": (C.c_int, [C.c_void_p, C.POINTER(DecStepKvqArgs)]),
     "dec_kvq_store": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(DecKvqCache), C.c_void_p, C.c_int32]),

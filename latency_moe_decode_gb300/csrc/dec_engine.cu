@@ -173,6 +173,11 @@ struct dec_engine {
   uint16_t *kvq_q = nullptr, *kvq_o = nullptr;
   uint8_t* kvq_ws = nullptr;
   int64_t kvq_ws_bytes = 0;
+  // steps of several rows a sequence: the attention's workspace, trees' masks and rotary positions
+  uint8_t* kvq_rows_ws = nullptr;
+  int64_t kvq_rows_ws_bytes = 0;
+  uint32_t* kvq_mask = nullptr;
+  int32_t* kvq_pos = nullptr;
   int32_t* kvq_idx = nullptr;
   uint8_t* arena = nullptr;  // all repacked weight tiles (one allocation the kernel bounds-checks)
   size_t arena_size = 0, arena_used = 0;
@@ -1232,6 +1237,8 @@ dec_status check_caches(dec_engine* e, const dec_kvq_cache* caches) {
   return DEC_OK;
 }
 
+constexpr int kTreeWords = 2;  // of a mask: steps have up to 64 rows
+
 // Buffers of the steps over 4-bit caches.
 dec_status kvq_buffers(dec_engine* e, const dec_kvq_cache* any) {
   if (e->kvq_ws) return DEC_OK;
@@ -1247,6 +1254,22 @@ dec_status kvq_buffers(dec_engine* e, const dec_kvq_cache* any) {
   if (need < 0) return fail(e, DEC_ERR_UNSUPPORTED, "caches: no attention for this shape");
   if ((st = dalloc(e, &e->kvq_ws, (size_t)need, &e->ws_bytes)) != DEC_OK) return st;
   e->kvq_ws_bytes = need;
+  return DEC_OK;
+}
+
+// And of those with several rows a sequence. Rows of no sequence leave the attention's output as it was: zeros at first.
+dec_status kvq_rows_buffers(dec_engine* e, const dec_kvq_cache* any, cudaStream_t s) {
+  if (e->kvq_rows_ws) return DEC_OK;
+  const dec_model_cfg& c = e->cfg;
+  dec_status st;
+  if (!e->kvq_mask && (st = dalloc(e, &e->kvq_mask, sizeof(uint32_t) * c.max_batch * kTreeWords, &e->ws_bytes)) != DEC_OK) return st;
+  if (!e->kvq_pos && (st = dalloc(e, &e->kvq_pos, sizeof(int32_t) * c.max_batch, &e->ws_bytes)) != DEC_OK) return st;
+  int64_t need = 0;
+  for (int rows = 1; rows <= c.max_batch; ++rows)
+    need = std::max(need, dec_kvq_attention_workspace(any, c.n_heads, c.max_batch, rows));
+  if ((st = dalloc(e, &e->kvq_rows_ws, (size_t)need, &e->ws_bytes)) != DEC_OK) return st;
+  e->kvq_rows_ws_bytes = need;
+  DEC_CUDA(cudaMemsetAsync(e->kvq_o, 0, sizeof(uint16_t) * c.max_batch * c.n_heads * c.head_dim, s));
   return DEC_OK;
 }
 
@@ -1307,8 +1330,11 @@ dec_status dec_step_kvq(dec_engine* e, const dec_step_kvq_args* a) {
   if ((a->logits || a->next_tokens) && c.vocab == 0) return fail(e, DEC_ERR_ARG, "no LM head");
   if ((a->hidden_in && !aligned16(a->hidden_in)) || (a->hidden_out && !aligned16(a->hidden_out)))
     return fail(e, DEC_ERR_ARG, "hidden_in and hidden_out must be 16-byte aligned");
-  if (!a->seqs || a->seqs->cu_tokens || a->seqs->batch != a->batch || a->seqs->n_tokens != a->batch)
-    return fail(e, DEC_ERR_ARG, "seqs: one row per sequence, as many as the batch");
+  const bool rows = a->seqs && a->seqs->cu_tokens;  // several a sequence
+  if (!a->seqs || a->seqs->n_tokens != a->batch || (!rows && a->seqs->batch != a->batch))
+    return fail(e, DEC_ERR_ARG, "seqs: one row per sequence, as many as the batch, or cu_tokens of as many rows");
+  if (rows ? a->seqs->batch < 1 || a->max_tokens < 1 : a->parents != nullptr)
+    return fail(e, DEC_ERR_ARG, "seqs: cu_tokens go with max_tokens, parents with cu_tokens");
   if (!a->seqs->lengths || !a->seqs->table || a->seqs->max_pages < 1 || a->seqs->table_stride < 0)
     return fail(e, DEC_ERR_ARG, "seqs: lengths and table are needed");
   if ((a->rope != nullptr) != (a->rope_len > 0)) return fail(e, DEC_ERR_ARG, "rope and rope_len go together");
@@ -1319,6 +1345,9 @@ dec_status dec_step_kvq(dec_engine* e, const dec_step_kvq_args* a) {
   if (dec_status bs = kvq_buffers(e, a->caches)) return bs;
   cudaStream_t s = a->stream ? static_cast<cudaStream_t>(a->stream) : e->stream;
   if (dec_status os = order_on(e, s)) return os;
+  if (rows)
+    if (dec_status bs = kvq_rows_buffers(e, a->caches, s)) return bs;
+  const int max_tokens = rows ? std::min(a->max_tokens, a->batch) : 1;
   DEC_CUDA(cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeMaxDynamicSharedMemorySize, e->wsmem[wi]));
   DEC_CUDA(cudaMemsetAsync(e->kvq_bar, 0, sizeof(unsigned) * 32 * (c.n_layers + 1), s));
 
@@ -1356,9 +1385,28 @@ dec_status dec_step_kvq(dec_engine* e, const dec_step_kvq_args* a) {
   at.q = ap.q_out;
   at.out = dec_rows{e->kvq_o, qd, hd};
   at.causal = 1;
-  at.max_tokens = 1;
-  at.workspace = e->kvq_ws;
-  at.workspace_bytes = e->kvq_ws_bytes;
+  at.max_tokens = max_tokens;
+  at.workspace = rows ? e->kvq_rows_ws : e->kvq_ws;
+  at.workspace_bytes = rows ? e->kvq_rows_ws_bytes : e->kvq_ws_bytes;
+  if (a->parents) {
+    dec_draft_tree_args t{};
+    t.batch = a->seqs->batch;
+    t.n_tokens = a->batch;
+    t.cu_tokens = a->seqs->cu_tokens;
+    t.parents = a->parents;
+    t.lengths = a->seqs->lengths;
+    t.max_tokens = max_tokens;
+    t.mask = e->kvq_mask;
+    t.mask_stride = kTreeWords;
+    t.positions = e->kvq_pos;
+    // (rows beyond max_tokens are not part of it: no tree, the table's first angles)
+    DEC_CUDA(cudaMemsetAsync(e->kvq_pos, 0, sizeof(int32_t) * a->batch, s));
+    if (dec_status st = dec_draft_tree(&t, s)) return op_failed(e, st);
+    ap.positions = e->kvq_pos;
+    at.tree_mask = e->kvq_mask;
+    at.tree_stride = kTreeWords;
+    at.tree_words = (max_tokens + 31) / 32;
+  }
 
   for (int seg = 0; seg <= c.n_layers; ++seg) {
     if (seg > 0) {

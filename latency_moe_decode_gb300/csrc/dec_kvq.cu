@@ -10,6 +10,7 @@
 
 #include "dec_kvq.cuh"
 #include "dec_kvq_attn.cuh"
+#include "dec_kvq_host.h"
 #include "dec_kvq_prompt.cuh"
 #include "dec_ops.h"
 
@@ -64,75 +65,6 @@ dec_status op_on_device(const void* p, const char* what) {
 namespace kvq {
 namespace {
 
-dec_status check_cache(const dec_kvq_cache* c) {
-  if (!c || !c->pages) return op_fail(DEC_ERR_ARG, "cache: NULL");
-  if (c->head_dim < 1 || c->n_kv_heads < 1 || c->page_tokens < 1 || c->n_pages < 1)
-    return op_fail(DEC_ERR_ARG, "cache: sizes must be positive");
-  if (c->head_dim != 64 && c->head_dim != 128) return op_fail(DEC_ERR_UNSUPPORTED, "cache: head_dim must be 64 or 128");
-  if (c->n_kv_heads > 1024) return op_fail(DEC_ERR_UNSUPPORTED, "cache: more than 1024 KV heads");
-  if (dec_kvq_page_bytes(c->page_tokens, c->n_kv_heads, c->head_dim) == 0)
-    return op_fail(DEC_ERR_UNSUPPORTED, "cache: page_tokens must be 16, 32, 64, 128 or 256");
-  if (!op_aligned(c->pages)) return op_fail(DEC_ERR_ARG, "cache: pages must be 16-byte aligned");
-  return DEC_OK;
-}
-
-dec_status check_seqs(const dec_kvq_seqs* s, const dec_kvq_cache* c) {
-  if (!s) return op_fail(DEC_ERR_ARG, "sequences: NULL");
-  if (s->batch < 0 || s->n_tokens < 0 || s->max_pages < 0) return op_fail(DEC_ERR_ARG, "sequences: negative size");
-  if (!s->cu_tokens && s->n_tokens != s->batch)
-    return op_fail(DEC_ERR_ARG, "sequences: without cu_tokens every sequence has one row (n_tokens == batch)");
-  if (s->batch == 0 || s->n_tokens == 0) return DEC_OK;
-  if (!s->lengths || !s->table || s->max_pages == 0) return op_fail(DEC_ERR_ARG, "sequences: lengths and table are needed");
-  // (sequences are counted in 32 bits, up to a launch's share past the last)
-  if (s->batch > INT_MAX - 4 * kMaxSeqs) return op_fail(DEC_ERR_UNSUPPORTED, "sequences: a batch of 2^31");
-  if (s->table_stride < 0) return op_fail(DEC_ERR_ARG, "sequences: negative table_stride");
-  if ((long long)s->max_pages * c->page_tokens > INT_MAX - 65536)
-    return op_fail(DEC_ERR_UNSUPPORTED, "sequences: a page table of 2^31 positions or more");
-  return DEC_OK;
-}
-
-dec_status check_rows(const dec_rows* r, dec_dtype t, const char* name) {
-  char buf[120];
-  const int per = t == DEC_F32 ? 4 : 8;
-  if (!r || !r->p) {
-    snprintf(buf, sizeof buf, "%s: NULL", name);
-    return op_fail(DEC_ERR_ARG, buf);
-  }
-  if (!op_aligned(r->p) || r->token_stride % per || r->head_stride % per) {
-    snprintf(buf, sizeof buf, "%s: rows and strides must be multiples of 16 bytes", name);
-    return op_fail(DEC_ERR_ARG, buf);
-  }
-  return DEC_OK;
-}
-
-Cache cache_of(const dec_kvq_cache* c) {
-  Cache k;
-  k.pages = static_cast<uint8_t*>(c->pages);
-  k.n_pages = c->n_pages;
-  k.page_shift = 0;
-  while ((1 << k.page_shift) < c->page_tokens) ++k.page_shift;
-  k.hkv = c->n_kv_heads;
-  k.status = c->status;
-  return k;
-}
-Seqs seqs_of(const dec_kvq_seqs* s) {
-  Seqs k;
-  k.batch = s->batch;
-  k.n_tokens = s->n_tokens;
-  k.max_pages = s->max_pages;
-  k.cu = s->cu_tokens;
-  k.lengths = s->lengths;
-  k.table = s->table;
-  k.table_stride = s->table_stride;
-  return k;
-}
-Rows rows_of(const dec_rows& r) { return Rows{r.p, r.token_stride, r.head_stride}; }
-
-dec_status launched(const char* what) {
-  const cudaError_t ce = cudaGetLastError();
-  return ce == cudaSuccess ? DEC_OK : op_cuda(ce, what);
-}
-
 // The prompt kernel takes calls whose longest sequence has more query rows per KV head than this: the
 // streaming one's time grows with every 16 rows, the prompt kernel's with every 128. Streaming against
 // prompt kernel, us: hd 128, 8 KV heads, 17 .. 32 rows, one sequence on 8 k 23.6 / 20.3, on 64 k 53.6 /
@@ -172,25 +104,25 @@ struct Variant {
   int threads, smem, rows, part, wparts;  // parts in floats; a CTA's parts of its warps
 };
 template <int HD, int NB>
-Variant streaming() {
+Variant streaming(bool tree) {
   using K = AttnCfg<HD, NB>;
-  return Variant{attention_kernel<HD, NB>, join_kernel<HD, K::ROWS>, K::THREADS, K::smem(), K::ROWS, K::PART, K::WARPS * K::PART};
+  return Variant{tree ? attention_kernel<HD, NB, true> : attention_kernel<HD, NB>, join_kernel<HD, K::ROWS>, K::THREADS, K::smem(), K::ROWS, K::PART, K::WARPS * K::PART};
 }
 template <int HD>
-Variant prompt() {
+Variant prompt(bool tree) {
   using C = PromptCfg<HD>;
-  return Variant{prompt_kernel<HD>, join_kernel<HD, C::ROWS>, C::THREADS, C::smem(), C::ROWS, C::PART, 0};
+  return Variant{tree ? prompt_kernel<HD, true> : prompt_kernel<HD>, join_kernel<HD, C::ROWS>, C::THREADS, C::smem(), C::ROWS, C::PART, 0};
 }
-Variant variant_of(int hd, int kind) {
-  if (hd == 128) return kind == 0 ? streaming<128, 1>() : kind == 1 ? streaming<128, 2>() : prompt<128>();
-  return kind == 0 ? streaming<64, 1>() : kind == 1 ? streaming<64, 2>() : prompt<64>();
+Variant variant_of(int hd, int kind, bool tree) {
+  if (hd == 128) return kind == 0 ? streaming<128, 1>(tree) : kind == 1 ? streaming<128, 2>(tree) : prompt<128>(tree);
+  return kind == 0 ? streaming<64, 1>(tree) : kind == 1 ? streaming<64, 2>(tree) : prompt<64>(tree);
 }
 int64_t workspace_of(const Variant& v, int sms) { return (int64_t)sms * (32 + 4ll * (2 * v.part + v.wparts)); }
 
 dec_status launch_attention(AttnParams p, int hd, int kind, int batch, uint8_t* ws, cudaStream_t stream) {
-  static std::atomic<unsigned long long> done[2][3];
-  const Variant v = variant_of(hd, kind);
-  if (dec_status st = raise_smem(v.kernel, v.join, v.smem, done[hd == 128][kind])) return st;
+  static std::atomic<unsigned long long> done[2][2][3];
+  const Variant v = variant_of(hd, kind, p.mask != nullptr);
+  if (dec_status st = raise_smem(v.kernel, v.join, v.smem, done[p.mask != nullptr][hd == 128][kind])) return st;
   const int sms = op_sms();
   if (sms < 1) return op_fail(DEC_ERR_CUDA, "attention: no device");
   p.meta = reinterpret_cast<int4*>(ws);
@@ -276,6 +208,7 @@ dec_status dec_kvq_append(const dec_kvq_cache* c, const dec_kvq_seqs* s, const d
   p.qn = static_cast<const uint16_t*>(a->q_norm);
   p.kn = static_cast<const uint16_t*>(a->k_norm);
   p.rope = a->rope;
+  p.at = a->positions;
   p.hq = a->n_heads;
   p.rope_len = a->rope_len;
   p.rot = a->rotary_dim;
@@ -322,7 +255,7 @@ int64_t dec_kvq_attention_workspace(const dec_kvq_cache* c, int32_t n_heads, int
   if (dec_kvq_page_bytes(c->page_tokens, c->n_kv_heads, c->head_dim) == 0) return -1;
   const int sms = op_sms();
   if (sms < 1) return -1;
-  return workspace_of(variant_of(c->head_dim, kernel_of(c->head_dim, n_heads, c->n_kv_heads, max_tokens)), sms);
+  return workspace_of(variant_of(c->head_dim, kernel_of(c->head_dim, n_heads, c->n_kv_heads, max_tokens), false), sms);
 }
 
 dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec_kvq_attention_args* a,
@@ -342,6 +275,12 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
       (long long)s->max_pages * c->page_tokens + s->n_tokens >= INT_MAX - 65536 ||
       (long long)c->n_pages * c->n_kv_heads * (c->page_tokens / kGroup) >= INT_MAX)
     return op_fail(DEC_ERR_UNSUPPORTED, "attention: 2^31 query rows, positions or cache groups");
+  if (a->tree_mask) {
+    if (!a->causal) return op_fail(DEC_ERR_ARG, "attention: a tree's rows stand in the cache (causal)");
+    if (a->tree_words < 1 || a->tree_stride < 0) return op_fail(DEC_ERR_ARG, "attention: tree_words and tree_stride");
+    if (a->tree_words > DEC_MAX_TREE / 32) return op_fail(DEC_ERR_UNSUPPORTED, "attention: a tree of more than DEC_MAX_TREE rows");
+    if (reinterpret_cast<uintptr_t>(a->tree_mask) % 4) return op_fail(DEC_ERR_ARG, "attention: tree_mask is not aligned to its type");
+  }
   if (!a->workspace || !op_aligned(a->workspace)) return op_fail(DEC_ERR_ARG, "attention: workspace missing or misaligned");
   if (dec_status st = op_on_device(c->pages, "cache: pages")) return st;
   AttnParams p;
@@ -356,6 +295,9 @@ dec_status dec_kvq_attention(const dec_kvq_cache* c, const dec_kvq_seqs* s, cons
   p.group = a->n_heads / c->n_kv_heads;
   p.ginv = reciprocal(p.group);
   p.causal = a->causal != 0;
+  p.mask = a->tree_mask;
+  p.mask_stride = a->tree_stride;
+  p.mask_words = a->tree_words;
   p.max_tokens = a->max_tokens;
   const int max_tokens = std::min(a->max_tokens, s->n_tokens);
   if (a->workspace_bytes < dec_kvq_attention_workspace(c, a->n_heads, s->batch, max_tokens))

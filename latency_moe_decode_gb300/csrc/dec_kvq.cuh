@@ -25,6 +25,7 @@ constexpr int kBlock = 16;       // values per scale
 constexpr int kGroup = 16;       // positions per group
 constexpr int kScaleMax = 167;   // the largest finite scale: 8 * 60
 constexpr int kScaleNan = 255;
+constexpr int kMaxSeqs = 256;    // sequences of one launch (their table lies in shared memory)
 
 __host__ __device__ constexpr int code_bytes(int hd) { return kGroup * hd / 2; }
 __host__ __device__ constexpr int scale_bytes(int hd) { return kGroup * hd / kBlock; }
@@ -180,6 +181,7 @@ struct AppendParams {
   Rows q, k, v, qo;
   const uint16_t *qn, *kn;
   const float* rope;
+  const int32_t* at;  // rotary positions of the token rows (null: where they stand in the cache)
   int hq, rope_len, rot, inter;
   float eps;
 };
@@ -364,7 +366,13 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
     raise(p.c.status, DEC_ERR_ARG);
     return;
   }
-  const bool turns = p.rot > 0, far = turns && pos >= p.rope_len;  // (beyond the table: the row is skipped)
+  const bool turns = p.rot > 0;
+  const int turn = turns && p.at ? __ldg(p.at + tok) : pos;
+  if (turn < 0) {
+    raise(p.c.status, DEC_ERR_ARG);
+    return;
+  }
+  const bool far = turns && turn >= p.rope_len;  // (beyond the table: the row is skipped)
   // the page, and the lane's angles: pairs (8l + i, its partner), or four pairs of neighbours
   const int e = pos >> p.c.page_shift, gpp = 1 << (p.c.page_shift - 4);
   int page = -1;
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
   const int other = mine && !p.inter ? (first ? l + half / 8 : l - half / 8) : l;
   float cs[8], sn[8];
   if (mine) {
-    const float4* t = reinterpret_cast<const float4*>(p.rope + (long long)pos * p.rot +
+    const float4* t = reinterpret_cast<const float4*>(p.rope + (long long)turn * p.rot +
                                                       (p.inter ? l * 8 : 2 * (first ? l * 8 : l * 8 - half)));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -483,7 +491,7 @@ __global__ void __launch_bounds__(T) append_kernel(const AppendParams p) {
       const int h = (key ? i : i - words) * 32 + __ffs(m) - 1;
       const Rows& in = key ? p.k : p.v;
       settle_row<HD, F32>(static_cast<const char*>(in.p) + (tok * in.ts + h * in.hs) * (F32 ? 4 : 2), key ? p.kn : nullptr,
-                          p.eps, reinterpret_cast<const float2*>(p.rope + (long long)pos * p.rot), key && turns ? p.rot : 0,
+                          p.eps, reinterpret_cast<const float2*>(p.rope + (long long)turn * p.rot), key && turns ? p.rot : 0,
                           p.inter != 0, key, pp, warp % PARTS * 32, grp + (size_t)h * gpp * group_bytes(HD));
     }
 }

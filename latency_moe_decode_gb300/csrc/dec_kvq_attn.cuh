@@ -35,7 +35,6 @@ namespace dec {
 namespace kvq {
 
 constexpr int kStages = 3;       // chunks of a warp's ring
-constexpr int kMaxSeqs = 256;    // sequences of one launch (their table lies in shared memory)
 constexpr int kUnitCost = 2;     // what beginning and ending a unit costs, in groups' time
 constexpr int kMinGroups = 8;    // groups a CTA takes at least
 constexpr float kLn2 = 0.6931471805599453f;
@@ -81,6 +80,9 @@ struct AttnParams {
   int b0;         // (without cu: token row of sequence 0)
   int min_groups; // groups a CTA takes at least
   Magic magic;
+  const uint32_t* mask;  // a tree's rows: [token row][mask_stride], bit i: sees row i of its sequence
+  long long mask_stride;
+  int mask_words;
   float* parts;   // [CTA][2] partials
   float* wparts;  // [CTA][warp] partials
   int4* meta;     // [CTA][2]: unit continued (1) and finished here (2), unit left open | the open unit's place
@@ -242,26 +244,51 @@ __device__ __forceinline__ void v_product(const uint32_t (&vw)[4][HD / 64], uint
     }
 }
 
+// A tree's masks, and the token rows of a lane's query rows (-1: none) of its n.
+template <int NB, bool TREE>
+struct TreeRows {
+  int tok[NB][2], n;
+  const uint32_t* mask;
+  long long stride;
+  int words;
+  // whether token row `row` sees the i-th of the sequence's rows
+  __device__ __forceinline__ bool bit(int row, int i) const {
+    if (row < 0 || (unsigned)i >= (unsigned)min(n, words * 32)) return false;
+    return __ldg(mask + row * stride + (i >> 5)) >> (i & 31) & 1u;
+  }
+};
+template <int NB>
+struct TreeRows<NB, false> {};
+
 // The same with each query row by itself, the positions it does not see left out.
-template <int HD, int NB>
-struct RowsApart {
+template <int HD, int NB, bool TREE>
+struct RowsApart : TreeRows<NB, TREE> {
   float acc[NB][HD / 16][4];
   uint32_t pb[NB][2];
-  int seen[NB][2];
+  int seen[NB][2];  // (of a tree: the positions before it)
   __device__ __noinline__ void add(const uint32_t (&vw)[4][HD / 64], uint32_t sb, const Magic& magic, int pos0) {
     const int t = threadIdx.x & 3;
     for (int c = 0; c < 8 * NB; ++c) {
-      int mine = 0;  // what row c sees
+      int mine = 0, row = 0;  // what row c sees
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int s0 = __shfl_sync(0xffffffffu, seen[nb][0], (c & 7) >> 1);
         const int s1 = __shfl_sync(0xffffffffu, seen[nb][1], (c & 7) >> 1);
         if (c >> 3 == nb) mine = (c & 1) ? s1 : s0;
+        if constexpr (TREE) {
+          const int r0 = __shfl_sync(0xffffffffu, this->tok[nb][0], (c & 7) >> 1);
+          const int r1 = __shfl_sync(0xffffffffu, this->tok[nb][1], (c & 7) >> 1);
+          if (c >> 3 == nb) row = (c & 1) ? r1 : r0;
+        }
       }
       uint32_t mb = sb;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (pos0 + 2 * t + (k & 1) + (k >> 1) * 8 >= mine) mb &= ~(0xFFu << (8 * k));
+      for (int k = 0; k < 4; ++k) {
+        const int pos = pos0 + 2 * t + (k & 1) + (k >> 1) * 8;
+        bool out = pos >= mine;
+        if constexpr (TREE) out = out && !this->bit(row, pos - mine);
+        if (out) mb &= ~(0xFFu << (8 * k));
+      }
       v_product<HD>(vw, mb, magic, [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -344,7 +371,8 @@ struct Joined {
   }
 };
 
-template <int HD, int NB>
+// TREE: the rows of a sequence see the positions before them, and of one another what their mask says.
+template <int HD, int NB, bool TREE = false>
 __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(const AttnParams p) {
   using K = AttnCfg<HD, NB>;
   constexpr int KS = K::KS, CH = K::CH;
@@ -439,6 +467,12 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
   float acc[NB][KS][4];
   float m[NB][2], l[NB][2], sc[NB][2];
   int seen[NB][2], smin, smax;
+  TreeRows<NB, TREE> tree;
+  if constexpr (TREE) {
+    tree.mask = p.mask;
+    tree.stride = p.mask_stride;
+    tree.words = p.mask_words;
+  }
   uint32_t qf[NB][KS][2];
 
   // ---- the unit that an entry belongs to, and its rows' queries (loaded ahead of their use)
@@ -468,11 +502,16 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int rr = row0 + nb * 8 + 2 * t + i;
-        const int x = max(0, p.causal ? sw.len + (int)fast_div(rr, p.group, p.ginv) + 1 : sw.len);
+        const int x = max(0, p.causal && !TREE ? sw.len + (int)fast_div(rr, p.group, p.ginv) + 1 : sw.len);
         seen[nb][i] = rr < rows ? x : 0;
         smin = min(smin, rr < rows ? x : 0x7FFFFFFF);
         smax = max(smax, seen[nb][i]);
+        if constexpr (TREE) tree.tok[nb][i] = rr < rows && sw.len >= 0 ? sw.tok0 + (int)fast_div(rr, p.group, p.ginv) : -1;
       }
+    if constexpr (TREE) {
+      tree.n = sw.n;
+      smax = max(0, sw.len + sw.n);
+    }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       smin = min(smin, __shfl_xor_sync(0xffffffffu, smin, o));
@@ -600,7 +639,12 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
           if (EDGE) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (i >= n || pos0 + i * kGroup + g + (j >> 1) * 8 >= seen[nb][j & 1]) s[nb][i][j] = -INFINITY;
+            {
+              const int pos = pos0 + i * kGroup + g + (j >> 1) * 8, from = seen[nb][j & 1];
+              bool out = i >= n || pos >= from;
+              if constexpr (TREE) out = i >= n || (pos >= from && !tree.bit(tree.tok[nb][j & 1], pos - from));
+              if (out) s[nb][i][j] = -INFINITY;
+            }
           }
           mx0 = fmaxf(mx0, fmaxf(s[nb][i][0], s[nb][i][2]));
           mx1 = fmaxf(mx1, fmaxf(s[nb][i][1], s[nb][i][3]));
@@ -676,7 +720,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
             for (int nb = 0; nb < NB; ++nb) mma16816(acc[nb][k], a0, a1, a2, a3, pb[nb][i][0], pb[nb][i][1]);
           });
         } else if constexpr (EDGE) {
-          RowsApart<HD, NB> r;  // (a copy: the accumulators themselves stay in registers)
+          RowsApart<HD, NB, TREE> r;  // (a copy: the accumulators themselves stay in registers)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -689,6 +733,7 @@ __global__ void __launch_bounds__(AttnCfg<HD, NB>::THREADS, 1) attention_kernel(
               r.seen[nb][j] = seen[nb][j];
             }
           }
+          if constexpr (TREE) static_cast<TreeRows<NB, TREE>&>(r) = tree;
           r.add(vw, sb, magic, pos0 + i * kGroup);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)

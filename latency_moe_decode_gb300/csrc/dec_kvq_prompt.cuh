@@ -99,8 +99,9 @@ struct Stretch {
   SeqWork sw;
   uint32_t uid;  // the unit's first entry
   int b, h, row0, t0, t1;  // sequence, KV head, first query row, tiles [t0, t1) (none where no row sees them)
-  int smin, smax;       // positions that every row, and that some row sees
+  int smin, smax;       // positions that every row, and that some row sees (of a tree: may see)
   uint32_t next;        // entry to go on from
+  template <bool TREE>
   __device__ __forceinline__ bool find(const AttnParams& p, const SeqWork* seqs, uint32_t f, uint32_t end) {
     for (;;) {
       if (f >= end) return false;
@@ -118,6 +119,10 @@ struct Stretch {
       const int last = min(row0 + 128, sw.n * p.group) - 1;
       smin = max(0, p.causal ? sw.len + (int)fast_div(row0, p.group, p.ginv) + 1 : sw.len);
       smax = max(0, p.causal ? sw.len + (int)fast_div(last, p.group, p.ginv) + 1 : sw.len);
+      if constexpr (TREE) {
+        smin = max(0, sw.len);
+        smax = max(0, sw.len + sw.n);
+      }
       t0 = (int)(f - uid);
       const uint32_t stop = min(end, uid + sw.ng);
       t1 = min((int)(stop - uid), (smax + kTile - 1) / kTile);
@@ -127,7 +132,19 @@ struct Stretch {
   }
 };
 
-template <int HD>
+// Which of 32 positions a tree's row sees, the first of them the i-th of its sequence's n rows (i < 0: before
+// them; mask: the row's words).
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* mask, int words, int i, int n) {
+  auto word = [&](int k) {
+    uint32_t w = k >= 0 && k < words && k * 32 < n ? __ldg(mask + k) : 0u;
+    return n - k * 32 < 32 && k * 32 < n ? w & ((1u << (n - k * 32)) - 1u) : w;
+  };
+  if (i <= -32) return 0xFFFFFFFFu;
+  if (i < 0) return word(0) << -i | ((1u << -i) - 1u);
+  return __funnelshift_r(word(i >> 5), word((i >> 5) + 1), i & 31);
+}
+
+template <int HD, bool TREE = false>
 __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const AttnParams p) {
   using C = PromptCfg<HD>;
   extern __shared__ uint8_t dyn[];
@@ -135,6 +152,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
   __shared__ uint32_t sh_scan[C::THREADS / 32], tmem_base;
   __shared__ float xm[2][2][128], xl[2][128];  // rows' maxima and sums, of each half
   __shared__ int nan_from[HD / kBlock];  // the first position with a NaN run of values, where rows differ in what they see
+  __shared__ uint32_t nan_rows[TREE ? HD / kBlock : 1][32];  // a tree's rows with one
   uint8_t* const smem = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
   SeqWork* const seqs = reinterpret_cast<SeqWork*>(smem + C::TABLE);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -192,7 +210,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
   if (warp == 9 + C::DW) {
     // ---- copies: lane i the tile's group i
     int n = 0;
-    for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
+    for (uint32_t f = clo; s.find<TREE>(p, seqs, f, chi); f = s.next) {
       const int gpp = 1 << (p.c.page_shift - 4);
       for (int t = s.t0; t < s.t1; ++t, ++n) {
         const int st = n % kPromptStages, pos = t * kTile + lane * kGroup;
@@ -232,7 +250,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         mma_commit(&bars.s_full[i & 1]);
         mma_commit(&bars.k_empty[i & 1]);
       };
-      for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
+      for (uint32_t f = clo; s.find<TREE>(p, seqs, f, chi); f = s.next) {
         const int tiles = s.t1 - s.t0;
         if (tiles <= 0) continue;
         wait(&bars.q_full, seg & 1);
@@ -316,7 +334,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
     const int vg = (lane & 3) | ((lane >> 4) & 1) << 2, vt = (lane >> 2) & 3, odd = HD == 128 ? vt & 1 : 0;
     const int vc = vg * (HD / 64), vr = 2 * vt + odd;  // the lane's first chunk and row
     const uint32_t va = sm + C::V + vr * 128 + (vc >> 3) * 16384 + (((vc & 7) ^ vr) << 4);
-    for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
+    for (uint32_t f = clo; s.find<TREE>(p, seqs, f, chi); f = s.next) {
       if (s.t0 < s.t1) {
         keys(n);
         wait(&bars.q_full, seg++ & 1);  // (the stretch's nan_from is set)
@@ -343,7 +361,12 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
             for (int e = 0; e < 2; ++e) {
               const int pos = t * kTile + hg * 8 + 2 * vt + e;
               const bool bad = ((sb >> (8 * e)) & 255u) == 255u;
-              if (bad && pos < s.smax) atomicMin(&nan_from[HD == 128 ? vg : vg >> 1], pos);
+              if (TREE && bad && pos >= s.smin && pos < s.smax) {
+                const int i = pos - s.smin;
+                if (i < 1024) atomicOr(&nan_rows[HD == 128 ? vg : vg >> 1][i >> 5], 1u << (i & 31));
+              } else if (bad && pos < s.smax) {
+                atomicMin(&nan_from[HD == 128 ? vg : vg >> 1], pos);
+              }
               if (bad || pos >= s.smax) sb &= ~(255u << (8 * e));
             }
           }
@@ -380,13 +403,16 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
     auto all_sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     int n = 0;
     int4 meta = make_int4(0, 0, 0, 0), mplace = make_int4(0, 0, 0, 0);
-    for (uint32_t f = clo; s.find(p, seqs, f, chi); f = s.next) {
+    for (uint32_t f = clo; s.find<TREE>(p, seqs, f, chi); f = s.next) {
       const int row = s.row0 + r, rows = s.sw.n * p.group, tj = (int)fast_div(row, p.group, p.ginv);
       const bool live = row < rows;
       const long long tok = s.sw.tok0 + tj;
       const int head = s.h * p.group + row - tj * p.group;
-      const int seen = live ? max(0, p.causal ? s.sw.len + tj + 1 : s.sw.len) : 0;
+      const int seen = live ? max(0, p.causal && !TREE ? s.sw.len + tj + 1 : s.sw.len) : 0;
       if (tid < HD / kBlock) nan_from[tid] = 0x7FFFFFFF;
+      if constexpr (TREE)
+        if (tid < HD / kBlock * 32) nan_rows[tid >> 5][tid & 31] = 0u;
+      const uint32_t* const sees = p.mask + (live ? tok : 0) * p.mask_stride;
       // queries, scaled by a power of two to magnitude 1 .. 2 (f16 then holds bf16 values down to 2^-17
       // of the largest exactly), in the order in which a word of codes gives its values
       float sc;
@@ -439,10 +465,18 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         if (lane == 0) mbar_arrive(&bars.s_empty[n & 1]);
         if ((s.t0 + i + 1) * kTile > s.smin) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 2; ++c) {
+            if constexpr (TREE) {
+              const uint32_t on = live ? tree_bits(sees, p.mask_words, pos0 + c * 32 - seen, s.sw.n) : 0u;
 #pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (pos0 + c * 32 + y >= seen) x[c][y] = -INFINITY;
+              for (int y = 0; y < 32; ++y)
+                if (!(on >> y & 1u)) x[c][y] = -INFINITY;
+            } else {
+#pragma unroll
+              for (int y = 0; y < 32; ++y)
+                if (pos0 + c * 32 + y >= seen) x[c][y] = -INFINITY;
+            }
+          }
         }
         float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
@@ -513,7 +547,13 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
         const int col = half * (HD / 2) + c * 32;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const bool nan = tiles > 0 && nan_from[(col >> 4) + (y >> 1)] < seen;  // (a run of 16 values)
+          bool nan = tiles > 0 && nan_from[(col >> 4) + (y >> 1)] < seen;  // (a run of 16 values)
+          if constexpr (TREE) {
+            if (tiles > 0 && live)
+              for (int k = 0; k * 32 < s.sw.n && k < 32; ++k)
+                if (const uint32_t w = nan_rows[(col >> 4) + (y >> 1)][k])
+                  nan |= (w & tree_bits(sees, p.mask_words, k * 32, s.sw.n)) != 0;
+          }
           float o[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) o[(k >> 1) + 4 * (k & 1)] = nan ? NAN : x[8 * y + k];

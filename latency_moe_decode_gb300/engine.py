@@ -225,14 +225,28 @@ class Engine:
     def step_kvq(self, caches: List[ops.KvqCache], lengths: torch.Tensor, table: torch.Tensor,
                  tokens: Optional[torch.Tensor] = None, hidden: Optional[torch.Tensor] = None,
                  rope: Optional[torch.Tensor] = None, logits: Optional[torch.Tensor] = None,
-                 next_tokens: Optional[torch.Tensor] = None, hidden_out: Optional[torch.Tensor] = None, stream=None):
+                 next_tokens: Optional[torch.Tensor] = None, hidden_out: Optional[torch.Tensor] = None, stream=None,
+                 cu_tokens: Optional[torch.Tensor] = None, parents: Optional[torch.Tensor] = None,
+                 max_tokens: Optional[int] = None):
         """One decode step of lengths.shape[0] sequences over the caches (dec_step_kvq): token b is
-        appended at position lengths[b] of the pages table[b]. The caller adds 1 to lengths."""
-        s = caches[0]._seqs(lengths, table, None, lengths.shape[0])
+        appended at position lengths[b] of the pages table[b]. The caller adds 1 to lengths. With cu_tokens (int32
+        [batch + 1]) a sequence has several rows, its last known token and drafts that follow one another or, with
+        parents (int32 [rows]), make a tree: ops.verify_drafts takes the step's logits, KvqCache.move its path, and
+        the caller adds its count to lengths. max_tokens: an upper bound of the rows of one sequence."""
+        n = lengths.shape[0]
+        if cu_tokens is not None:
+            if tokens is None and hidden is None:
+                raise ValueError("tokens or hidden are needed")
+            n = tokens.numel() if tokens is not None else hidden.shape[0]
+            max_tokens = n if max_tokens is None else max_tokens
+        if parents is not None and (cu_tokens is None or parents.dtype != torch.int32 or parents.numel() != n or
+                                    not parents.is_contiguous() or parents.device != caches[0].device):
+            raise ValueError(f"parents must be contiguous int32 [{n}] on {caches[0].device}, beside cu_tokens")
+        s = caches[0]._seqs(lengths, table, cu_tokens, n)
         if rope is not None and (rope.dtype != torch.float32 or not rope.is_contiguous() or
                                  tuple(rope.shape[1:]) != (self.cfg.head_dim // 2, 2) or rope.device != caches[0].device):
             raise ValueError("rope must be contiguous float32 [positions, head_dim / 2, 2] on the caches' device")
-        arr, n, c = self._caches(caches), lengths.shape[0], self.cfg
+        arr, c = self._caches(caches), self.cfg
         for name, t, dtype, per in (("tokens", tokens, torch.int32, 1), ("hidden", hidden, torch.bfloat16, c.hidden),
                                     ("logits", logits, torch.float32, c.vocab), ("next_tokens", next_tokens, torch.int32, 1),
                                     ("hidden_out", hidden_out, torch.bfloat16, c.hidden)):
@@ -240,7 +254,8 @@ class Engine:
                 raise ValueError(f"{name} must be contiguous {dtype} of {n} rows on {caches[0].device}")
         a = DecStepKvqArgs(_ptr(tokens), _ptr(hidden), n, arr, C.pointer(s), _ptr(rope),
                            0 if rope is None else rope.shape[0], _ptr(logits), _ptr(next_tokens), _ptr(hidden_out),
-                           _stream_ptr(stream if stream is not None else torch.cuda.current_stream()))
+                           _stream_ptr(stream if stream is not None else torch.cuda.current_stream()), _ptr(parents),
+                           0 if cu_tokens is None else max_tokens)
         self._check(self.lib.dec_step_kvq(self.h, C.byref(a)), "dec_step_kvq")
 
     def score(self, tokens: torch.Tensor, seq: int = 0, targets: Optional[torch.Tensor] = None, top_n: int = 0,

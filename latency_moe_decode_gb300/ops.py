@@ -1,5 +1,6 @@
-"""Operators beside the engine, torch tensors in: the paged 4-bit KV cache with its attention, and
-log-probabilities (the dec_kvq_* and dec_logprobs entry points of include/dec.h, which define them).
+"""Operators beside the engine, torch tensors in: the paged 4-bit KV cache with its attention and what keeps
+it within a bound, trees of drafted tokens and their verification, and log-probabilities (the dec_kvq_*,
+dec_draft_tree, dec_verify_drafts and dec_logprobs entry points of include/dec.h, which define them).
 
 Every call is queued on the current stream of the tensors' device (or on `stream`, a torch stream or
 a cudaStream_t) and returns without waiting; none reads device memory on the host, so all may be
@@ -14,8 +15,9 @@ from typing import NamedTuple, Optional, Tuple
 import torch
 
 from . import capi
-from .capi import (DEC_BF16, DEC_F32, DecError, DecKvqAppendArgs, DecKvqAttentionArgs, DecKvqCache, DecKvqSeqs,
-                   DecLogprobsArgs, DecRows)
+from .capi import (DEC_BF16, DEC_F32, DEC_MAX_TREE, DecDraftTreeArgs, DecError, DecKvqAppendArgs, DecKvqAttentionArgs,
+                   DecKvqCache, DecKvqHeaviestArgs, DecKvqMassArgs, DecKvqMoveArgs, DecKvqSeqs, DecLogprobsArgs, DecRows,
+                   DecVerifyDraftsArgs)
 
 _DTYPES = {torch.bfloat16: DEC_BF16, torch.float32: DEC_F32}
 
@@ -67,6 +69,13 @@ def _out(t: torch.Tensor, name: str, shape, index: int) -> torch.Tensor:
     if t.stride(2) != 1 or t.stride(0) % 8 or t.stride(1) % 8 or t.data_ptr() % 16:
         raise ValueError(f"{name}: heads contiguous, rows and strides multiples of 16 bytes")
     return t
+
+
+def _ints(t: torch.Tensor, name: str, n: int, index: int) -> int:
+    """The address of a contiguous int32 vector of n on the tensors' device."""
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name} must be contiguous int32 [{n}] on cuda:{index}")
+    return t.data_ptr()
 
 
 def rope_table(n: int, rotary_dim: int, theta: float, device="cuda") -> torch.Tensor:
@@ -137,13 +146,15 @@ class KvqCache:
                cu_tokens: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
                q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6,
                rope: Optional[torch.Tensor] = None, interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
-               stream=None) -> Optional[torch.Tensor]:
+               stream=None, positions: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
         """Append k, v ([n, n_kv_heads, head_dim], bf16 or fp32) at the sequences' positions; with q
         ([n, n_heads, head_dim], of the same type) return it normalised and rotated, in bf16. rope: a
-        rope_table() of rotary_dim = 2 * rope.shape[1]."""
+        rope_table() of rotary_dim = 2 * rope.shape[1]. positions (int32 [n]): the rows' rotary positions,
+        where those are not their places in the cache (a tree's tokens, a sequence that positions were taken from)."""
         if stream is not None:
             with _on_stream(stream, self.device):
-                return self.append(k, v, lengths, table, cu_tokens, q, q_norm, k_norm, eps, rope, interleaved, q_out)
+                return self.append(k, v, lengths, table, cu_tokens, q, q_norm, k_norm, eps, rope, interleaved, q_out,
+                                   positions=positions)
         index, hd, hkv, dtype = self._index, self.head_dim, self.n_kv_heads, k.dtype
         shape = k.shape
         dt = _DTYPES.get(dtype)
@@ -176,7 +187,8 @@ class KvqCache:
             rope_len, rot = shape[0], 2 * shape[1]
         a = DecKvqAppendArgs(dt, hq, qp, q0, q1, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, op, o0, o1,
                              None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
-                             eps, rope.data_ptr() if rot else None, rope_len, rot, interleaved)
+                             eps, rope.data_ptr() if rot else None, rope_len, rot, interleaved,
+                             None if positions is None else _ints(positions, "positions", n, index))
         st = _call(self.lib.dec_kvq_append, index, self.c, self._seqs(lengths, table, cu_tokens, n), a)
         if st:
             _raise(st, "dec_kvq_append")
@@ -204,15 +216,18 @@ class KvqCache:
 
     def attention(self, q: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor,
                   cu_tokens: Optional[torch.Tensor] = None, max_tokens: Optional[int] = None, causal: bool = True,
-                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None, return_lse: bool = False, stream=None):
+                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None, return_lse: bool = False, stream=None,
+                  tree_mask: Optional[torch.Tensor] = None):
         """Attention of q (bf16 [n, n_heads, head_dim]) over the cache: row j of a sequence attends to
         positions 0 .. lengths + j (causal) or 0 .. lengths - 1. max_tokens: an upper bound of the rows
         of one sequence, which also chooses the kernel (default: 1 without cu_tokens; with them n, and the kernel
-        that suits the sequences' mean). Returns out (bf16, shaped as q), or
+        that suits the sequences' mean). tree_mask (int32 [n, words], draft_tree's): each row attends to positions
+        0 .. lengths - 1 and, of its sequence's rows, to those whose bits are set. Returns out (bf16, shaped as q), or
         (out, lse) with lse fp32 [n, n_heads]."""
         if stream is not None:
             with _on_stream(stream, self.device):
-                return self.attention(q, lengths, table, cu_tokens, max_tokens, causal, scale, out, return_lse)
+                return self.attention(q, lengths, table, cu_tokens, max_tokens, causal, scale, out, return_lse,
+                                      tree_mask=tree_mask)
         index, hd, shape = self._index, self.head_dim, q.shape
         if q.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != hd or q.get_device() != index:
             raise ValueError(f"q must be bfloat16 [n, n_heads, {hd}] on {self.device}")
@@ -220,6 +235,16 @@ class KvqCache:
             raise ValueError("scale must be positive")
         n, hq, _ = shape
         q = _readable(q)
+        mask = None
+        mask_stride = words = 0
+        if tree_mask is not None:
+            if not causal:
+                raise ValueError("a tree's rows stand in the cache: causal")
+            if (tree_mask.dtype not in (torch.int32, torch.uint32) or tree_mask.dim() != 2 or tree_mask.shape[0] != n or
+                    tree_mask.shape[1] < 1 or (tree_mask.stride(1) != 1 and tree_mask.shape[1] > 1) or
+                    tree_mask.get_device() != index):
+                raise ValueError(f"tree_mask must be int32 [{n}, words] with adjacent words on {self.device}")
+            mask, mask_stride, words = tree_mask.data_ptr(), tree_mask.stride(0), tree_mask.shape[1]
         out = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if out is None else _out(out, "out", shape, index)
         lse = torch.empty((n, hq), dtype=torch.float32, device=self.device) if return_lse else None
         # The bound of n rows says nothing about single sequences: their mean does, unless most of them are empty.
@@ -239,11 +264,203 @@ class KvqCache:
         ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         (q0, q1, _), (o0, o1, _) = q.stride(), out.stride()
         a = DecKvqAttentionArgs(hq, q.data_ptr(), q0, q1, out.data_ptr(), o0, o1, None if lse is None else lse.data_ptr(),
-                                0.0 if scale is None else scale, causal, max_tokens, ws.data_ptr(), need, likely)
+                                0.0 if scale is None else scale, causal, max_tokens, ws.data_ptr(), need, likely, mask, mask_stride, words)
         st = _call(self.lib.dec_kvq_attention, index, self.c, s, a)
         if st:
             _raise(st, "dec_kvq_attention")
         return (out, lse) if return_lse else out
+
+    def new_mass(self) -> torch.Tensor:
+        """fp32 zeros laid out as the pages: what attention_mass adds up, one number a position and KV head."""
+        return torch.zeros((self.n_pages, self.n_kv_heads, self.page_tokens), dtype=torch.float32, device=self.device)
+
+    def _mass(self, t: torch.Tensor, name: str) -> int:
+        if (t.dtype is not torch.float32 or t.shape != (self.n_pages, self.n_kv_heads, self.page_tokens) or
+                not t.is_contiguous() or t.get_device() != self._index):
+            raise ValueError(f"{name} must be contiguous float32 [{self.n_pages}, {self.n_kv_heads}, {self.page_tokens}] on "
+                             f"{self.device}")
+        return t.data_ptr()
+
+    def attention_mass(self, q: torch.Tensor, lse: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor,
+                       mass: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None, max_tokens: Optional[int] = None,
+                       causal: bool = True, scale: Optional[float] = None, decay: float = 1.0,
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Add the attention weight that cached positions receive from q (with the lse that attention() returned
+        for it) to what they have: out = decay * mass + weights, over all rows and the heads of each KV head
+        (dec_kvq_mass). mass and out (default: mass itself) are as new_mass() makes them; positions that the
+        rows stand at begin anew."""
+        if stream is not None:
+            with _on_stream(stream, self.device):
+                return self.attention_mass(q, lse, lengths, table, mass, cu_tokens, max_tokens, causal, scale, decay, out)
+        index, hd, shape = self._index, self.head_dim, q.shape
+        if q.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != hd or q.get_device() != index:
+            raise ValueError(f"q must be bfloat16 [n, n_heads, {hd}] on {self.device}")
+        if scale is not None and not scale > 0:
+            raise ValueError("scale must be positive")
+        n, hq, _ = shape
+        if lse.dtype is not torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous() or lse.get_device() != index:
+            raise ValueError(f"lse must be contiguous float32 [{n}, {hq}] on {self.device}")
+        out = mass if out is None else out
+        q = _readable(q)
+        if max_tokens is None:
+            max_tokens = 1 if cu_tokens is None else n
+        a = DecKvqMassArgs(hq, q.data_ptr(), q.stride(0), q.stride(1), lse.data_ptr(), 0.0 if scale is None else scale, causal,
+                           max_tokens, decay, self._mass(mass, "mass"), self._mass(out, "out"))
+        st = _call(self.lib.dec_kvq_mass, index, self.c, self._seqs(lengths, table, cu_tokens, n), a)
+        if st:
+            _raise(st, "dec_kvq_mass")
+        return out
+
+    def heaviest(self, mass: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor, budget: int, sinks: int = 0,
+                 recent: int = 0, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Which positions a cache of `budget` positions a sequence keeps: the first `sinks`, the last `recent` and,
+        between them, the heaviest (dec_kvq_heaviest). Returns (kept int32 [batch, n_kv_heads, budget], ascending,
+        -1 behind the last; count int32 [batch])."""
+        if stream is not None:
+            with _on_stream(stream, self.device):
+                return self.heaviest(mass, lengths, table, budget, sinks, recent)
+        batch = lengths.numel()
+        s = self._seqs(lengths, table, None, batch)
+        if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
+            raise ValueError("budget must be positive and hold the sinks and the recent positions")
+        kept = torch.empty((batch, self.n_kv_heads, budget), dtype=torch.int32, device=self.device)
+        count = torch.empty(batch, dtype=torch.int32, device=self.device)
+        a = DecKvqHeaviestArgs(self._mass(mass, "mass"), budget, sinks, recent, kept.data_ptr(), count.data_ptr())
+        st = _call(self.lib.dec_kvq_heaviest, self._index, self.c, s, a)
+        if st:
+            _raise(st, "dec_kvq_heaviest")
+        return kept, count
+
+    def move(self, index: torch.Tensor, count: torch.Tensor, table: torch.Tensor, start: Optional[torch.Tensor] = None,
+             to: Optional[torch.Tensor] = None, mass: Optional[torch.Tensor] = None, stream=None):
+        """Move positions as they are held: position start + i of every sequence receives position start + index[.., i]
+        (dec_kvq_move). index: int32 [batch, n] for all heads alike (verify_drafts' path) or [batch, n_kv_heads, n]
+        (heaviest's kept), ascending, index[i] >= i; count int32 [batch]; start int32 [batch] (default: 0); to: a page
+        table to write to (default: in place); mass: weights to move alongside."""
+        if stream is not None:
+            with _on_stream(stream, self.device):
+                return self.move(index, count, table, start, to, mass)
+        i, batch = self._index, count.numel()
+        shape = index.shape
+        if (index.dtype is not torch.int32 or len(shape) not in (2, 3) or shape[0] != batch or index.get_device() != i or
+                (len(shape) == 3 and shape[1] != self.n_kv_heads) or (shape[-1] > 1 and index.stride(-1) != 1)):
+            raise ValueError(f"index must be int32 [{batch}, n] or [{batch}, {self.n_kv_heads}, n] with adjacent entries on "
+                             f"{self.device}")
+        s = self._seqs(count if start is None else start, table, None, batch)
+        if start is None:
+            s.lengths = None
+        tp = pages = stride = 0
+        if to is not None:
+            if (to.dtype is not torch.int32 or to.dim() != 2 or to.shape[0] != batch or to.get_device() != i or
+                    (to.shape[1] > 1 and to.stride(1) != 1)):
+                raise ValueError(f"to must be a page table, int32 [{batch}, pages] on {self.device}")
+            tp, pages, stride = to.data_ptr(), to.shape[1], to.stride(0)
+            if pages == 0 and shape[-1] > 0:
+                raise ValueError("to: no pages")
+        a = DecKvqMoveArgs(index.data_ptr(), index.stride(0), index.stride(1) if len(shape) == 3 else 0,
+                           _ints(count, "count", batch, i), shape[-1], tp, pages, stride,
+                           None if mass is None else self._mass(mass, "mass"))
+        st = _call(self.lib.dec_kvq_move, i, self.c, s, a)
+        if st:
+            _raise(st, "dec_kvq_move")
+
+    def evict(self, mass: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor, budget: int, sinks: int = 0,
+              recent: int = 0, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Bring every sequence down to `budget` positions, in place, its weights with them: heaviest() and move().
+        Returns (kept, count); count holds the new lengths. Rows appended later stand there, and keep their rotary
+        positions by append(positions=)."""
+        if stream is not None:
+            with _on_stream(stream, self.device):
+                return self.evict(mass, lengths, table, budget, sinks, recent)
+        kept, count = self.heaviest(mass, lengths, table, budget, sinks, recent)
+        self.move(kept, count, table, mass=mass)
+        return kept, count
+
+
+class DraftTree(NamedTuple):
+    mask: torch.Tensor                 # int32 [n, words]: bit i of a row: row i of its sequence is itself or above it
+    positions: Optional[torch.Tensor]  # int32 [n]: rotary positions
+
+
+def draft_tree(parents: torch.Tensor, lengths: Optional[torch.Tensor], cu_tokens: torch.Tensor,
+               max_tokens: Optional[int] = None, stream=None) -> DraftTree:
+    """What attention(tree_mask=) and append(positions=) take for trees of drafted tokens (dec_draft_tree): parents
+    (int32 [n]) is each row's parent, an earlier row of its sequence. max_tokens: an upper bound of the rows of one
+    sequence (default: n, at most 1024)."""
+    if stream is not None and parents.is_cuda:
+        with _on_stream(stream, parents.device):
+            return draft_tree(parents, lengths, cu_tokens, max_tokens)
+    if not parents.is_cuda:
+        raise ValueError("parents must be int32 [n] on a CUDA device")
+    n, index, batch = parents.numel(), parents.get_device(), cu_tokens.numel() - 1
+    max_tokens = min(n, DEC_MAX_TREE) if max_tokens is None else max_tokens
+    words = max(1, (max_tokens + 31) // 32)
+    mask = torch.empty((n, words), dtype=torch.int32, device=parents.device)
+    positions = None if lengths is None else torch.empty(n, dtype=torch.int32, device=parents.device)
+    a = DecDraftTreeArgs(batch, n, _ints(cu_tokens, "cu_tokens", batch + 1, index), _ints(parents, "parents", n, index),
+                         None if lengths is None else _ints(lengths, "lengths", batch, index), max_tokens, mask.data_ptr(),
+                         words, None if lengths is None else positions.data_ptr())
+    st = _call(capi.lib().dec_draft_tree, index, a)
+    if st:
+        _raise(st, "dec_draft_tree")
+    return DraftTree(mask, positions)
+
+
+class Verified(NamedTuple):
+    path: torch.Tensor         # int32 [batch, max_tokens]: the accepted rows, 0 first; -1 behind the last
+    count: torch.Tensor        # int32 [batch]: how many
+    next_tokens: torch.Tensor  # int32 [batch]
+
+
+def verify_drafts(logits: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Tensor, cu_tokens: torch.Tensor,
+                  parents: Optional[torch.Tensor] = None, draft_probs: Optional[torch.Tensor] = None,
+                  temperature: Optional[torch.Tensor] = None, max_tokens: Optional[int] = None, stream=None) -> Verified:
+    """Which path of each sequence's tree (parents None: chain) of drafted tokens the target's probabilities accept,
+    and the token that follows it, from given random numbers (dec_verify_drafts). logits: fp32 or bf16 [n, vocab],
+    each row the target's after that token; tokens int32 [n], row 0 of a sequence its last known one; uniforms fp32
+    [n] in [0, 1); draft_probs fp32 [n, vocab], what each row's children were drawn from (None: certainty);
+    temperature fp32 [batch] (None: 1; 0: greedy). max_tokens: an upper bound of the rows of one sequence (default: n,
+    at most 1024). path and count are what KvqCache.move takes."""
+    if stream is not None and logits.is_cuda:
+        with _on_stream(stream, logits.device):
+            return verify_drafts(logits, tokens, uniforms, cu_tokens, parents, draft_probs, temperature, max_tokens)
+    dt = _DTYPES.get(logits.dtype)
+    shape = logits.shape
+    if dt is None or len(shape) != 2 or not logits.is_cuda:
+        raise ValueError("logits must be bfloat16 or float32 [rows, vocab] on a CUDA device")
+    n, vocab = shape
+    if n >= 2 ** 31 or vocab >= 2 ** 31:
+        raise ValueError("logits: 2^31 rows or ids")
+    dev, index, batch = logits.device, logits.get_device(), cu_tokens.numel() - 1
+    if logits.stride(1) != 1 and vocab > 1:
+        logits = logits.contiguous()
+    qp = qs = 0
+    if draft_probs is not None:
+        if draft_probs.dtype is not torch.float32 or draft_probs.shape != shape or draft_probs.get_device() != index:
+            raise ValueError(f"draft_probs must be float32 {list(shape)} on {dev}")
+        if draft_probs.stride(1) != 1 and vocab > 1:
+            draft_probs = draft_probs.contiguous()
+        qp, qs = draft_probs.data_ptr(), draft_probs.stride(0)
+    for name, t, size in (("uniforms", uniforms, n), ("temperature", temperature, batch)):
+        if t is not None and (t.dtype is not torch.float32 or t.dim() != 1 or t.numel() != size or not t.is_contiguous() or
+                              t.get_device() != index):
+            raise ValueError(f"{name} must be contiguous float32 [{size}] on {dev}")
+    max_tokens = min(n, DEC_MAX_TREE) if max_tokens is None else max_tokens
+    path = torch.empty((batch, max(0, max_tokens)), dtype=torch.int32, device=dev)
+    count = torch.empty(batch, dtype=torch.int32, device=dev)
+    nxt = torch.empty(batch, dtype=torch.int32, device=dev)
+    lib = capi.lib()
+    need = lib.dec_verify_drafts_workspace(n)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    a = DecVerifyDraftsArgs(logits.data_ptr(), dt, vocab, logits.stride(0), qp, qs, batch, n,
+                            _ints(cu_tokens, "cu_tokens", batch + 1, index), _ints(tokens, "tokens", n, index),
+                            None if parents is None else _ints(parents, "parents", n, index), uniforms.data_ptr(),
+                            None if temperature is None else temperature.data_ptr(), max_tokens, path.data_ptr(),
+                            count.data_ptr(), nxt.data_ptr(), ws.data_ptr(), need)
+    st = _call(lib.dec_verify_drafts, index, a)
+    if st:
+        _raise(st, "dec_verify_drafts")
+    return Verified(path, count, nxt)
 
 
 class LogProbs(NamedTuple):
