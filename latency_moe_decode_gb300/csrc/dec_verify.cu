@@ -2,8 +2,8 @@
 //
 // Two kernels. The first reads every row of logits once: its largest logit (and that one's id) and the sum of
 // exp((x - max) / temperature) in fp32, which is what acceptance needs. The second walks the trees, a CTA or a
-// cluster of CTAs per sequence: the walk itself is arithmetic on a few numbers per draft, all fetched at once; then
-// the row that the walk ends at is summed again, for the next token. There a border between two of a
+// cluster of CTAs per sequence: the walk itself is arithmetic on a few numbers per draft, all fetched and weighed at
+// once; then the row that the walk ends at is summed again, for the next token. There a border between two of a
 // vocabulary's tokens is met with every draw, and sums that are off by 2^-24 of the whole would pick the neighbour
 // of the formula's token once in some thousand draws. So those sums, and the few acceptances that the
 // first kernel's sums leave open, are taken in unevaluated pairs of floats (some 36 bits; 64-bit arithmetic runs at a
@@ -11,10 +11,13 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "dec.h"
+#include "dec_f32x2.cuh"
 #include "dec_kvq.cuh"
 #include "dec_ops.h"
 
@@ -25,11 +28,14 @@ using kvq::Two;
 using kvq::renorm;
 
 constexpr int kRowThreads = 256;
-constexpr int kWalkThreads = 1024;
-constexpr int kMaxSplits = 32;
+constexpr int kWalkThreads = 512;
+constexpr int kWalkWarps = kWalkThreads / 32;
+constexpr int kMaxParts = 32;  // of a row
+constexpr int kRowWarps = 32;   // of the first kernel, an SM
 constexpr int kMaxCluster = 8;
 // What the first kernel's sums are trusted to: chains of at most a few hundred additions a thread, each off by 2^-24.
 constexpr float kTrust = 0x1p-15f;
+constexpr float kMagic = 12582912.f;  // 1.5 x 2^23: adding it leaves whole numbers in the low mantissa bits
 
 struct Table {
   float2 e[32];  // 2^(i / 32) as two floats
@@ -39,11 +45,12 @@ struct Params {
   const void* x;
   long long stride, prob_stride;
   const float* probs;
-  int vocab, batch, n_tokens, max_tokens, splits;
+  int vocab, batch, n_tokens, max_tokens;
+  int splits, width;  // warps a row (and the next power of two)
   const int32_t *cu, *tokens, *parents;
   const float *uniforms, *temperature;
   int32_t *path, *count, *next;
-  float4* stats;  // [n_tokens][splits]: largest logit, sum, its id (bits), unused
+  float4* stats;  // [n_tokens][width]: largest logit, sum, its id (bits), unused
   Table table;
 };
 
@@ -68,106 +75,117 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A part of a row: its largest logit, the sum relative to that, the first id of it. A NaN makes m a NaN.
+// A part of a row: its largest logit, the sum relative to that (a NaN, where the row has a NaN or +infinity), the
+// first id of it.
 struct Stat {
   float m, l;
   int id;
 };
+__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 __device__ __forceinline__ Stat merge(const Stat& a, const Stat& b, float c) {
   Stat r;
   const bool second = b.m > a.m || (b.m == a.m && b.id < a.id);
-  r.m = a.m != a.m || b.m != b.m ? NAN : second ? b.m : a.m;
+  r.m = second ? b.m : a.m;
   r.id = second ? b.id : a.id;
-  r.l = (a.m > -INFINITY ? a.l * ex2((a.m - r.m) * c) : 0.f) + (b.m > -INFINITY ? b.l * ex2((b.m - r.m) * c) : 0.f);
+  const float m = finite_or_0(r.m);
+  r.l = a.l * ex2((a.m - m) * c) + b.l * ex2((b.m - m) * c);
   return r;
+}
+__device__ __forceinline__ Stat merge_lanes(Stat a, int width, float c) {
+  const int lane = threadIdx.x & 31;
+  for (int o = width / 2; o > 0; o >>= 1) {
+    const Stat y{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.l, o), __shfl_xor_sync(0xffffffffu, a.id, o)};
+    a = (lane & o) ? merge(y, a, c) : merge(a, y, c);
+  }
+  return a;
 }
 
 // ---------------------------------------------------------------------------------------------
-// every row once: grid (rows x splits)
+// every row once
 
+// Each warp by itself, as many a row as fill the SMs: a CTA a row, or half a row, left some SMs with a wave more than
+// others.
 template <bool BF16>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const Params p) {
-  constexpr int E = BF16 ? 8 : 4, U = 2;
+__global__ void __launch_bounds__(kRowThreads, kRowWarps * 32 / kRowThreads) rows_kernel(const Params p) {
+  constexpr int E = BF16 ? 8 : 4, U = 16 / E;  // 16 values a thread at a time
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ Stat part[kRowThreads / 32];
-  const int row = blockIdx.x / p.splits, split = blockIdx.x - row * p.splits, tid = threadIdx.x;
+  const int lane = threadIdx.x & 31, me = (blockIdx.x * kRowThreads + threadIdx.x) / 32;
   kvq::Seqs s{};
   s.batch = p.batch;
   s.cu = p.cu;
+  const int row = me / p.splits, split = me - row * p.splits;
+  if (row >= p.n_tokens) return;
   int j;
   const int b = kvq::seq_of_warp(s, row, j);
   if (b < 0 || j >= p.max_tokens) return;
-  const float c = factor_of(p, b);
+  const float f = factor_of(p, b), c = f > 0.f ? f : 1.f;  // (greedy: the sum only shows a NaN)
   const char* const base = static_cast<const char*>(p.x) + row * p.stride * (BF16 ? 2 : 4);
   // 16-byte words from the last boundary before the row; the first and the last may hold values beside it
   const int lead = (int)(reinterpret_cast<uintptr_t>(base) & 15u) / (BF16 ? 2 : 4);
   const uint4* const words = reinterpret_cast<const uint4*>(base - lead * (BF16 ? 2 : 4));
-  const int n = (int)(((long long)p.vocab + lead + E - 1) / E), per = (n + p.splits - 1) / p.splits;
+  const int n = (p.vocab + lead + E - 1) / E, per = (n + p.splits - 1) / p.splits;
   const int lo = split * per, hi = min(n, lo + per);
   Stat a{-INFINITY, 0.f, 0x7FFFFFFF};
-  bool nan = false;
-  for (int w0 = lo + tid; w0 < hi; w0 += U * kRowThreads) {
-    float x[U][E];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int w = w0 + u * kRowThreads;
-      if (w < hi && w > 0 && w < n - 1) {
-        const uint4 v = __ldcs(words + w);
-        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          x[u][i] = BF16 ? __uint_as_float((i & 1) ? q[i / 2] & 0xFFFF0000u : q[i / 2] << 16) : __uint_as_float(q[i % 4]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const long long at = (long long)w * E + i - lead;
-          x[u][i] = w < hi && at >= 0 && at < p.vocab ? logit<BF16>(base, at) : -INFINITY;
-        }
-      }
-    }
+  const uint64_t cc = pair(c, c);
+  auto take = [&](const float (&x)[16], int w0) {  // 16 values of the words w0, w0 + 32, ..
     float m = a.m;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        nan |= x[u][i] != x[u][i];
-        m = fmaxf(m, x[u][i]);
-      }
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, x[i]);
     if (m > a.m) {
-      a.l = a.m > -INFINITY ? a.l * ex2((a.m - m) * c) : 0.f;
+      a.l *= ex2((a.m - m) * c);
       a.m = m;
 #pragma unroll
-      for (int u = U - 1; u >= 0; --u)
-#pragma unroll
-        for (int i = E - 1; i >= 0; --i)
-          if (x[u][i] == m) a.id = (w0 + u * kRowThreads) * E + i - lead;
+      for (int i = 15; i >= 0; --i)
+        if (x[i] == m) a.id = (w0 + i / E * 32) * E + i % E - lead;
     }
-    if (m > -INFINITY) {
-      float l = 0.f;
+    const float z = finite_or_0(m);
+    uint64_t l2 = 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < E; ++i) l += x[u][i] > -INFINITY ? ex2((x[u][i] - m) * c) : 0.f;
-      a.l += l;
+    for (int i = 0; i < 16; i += 2) {
+      const float2 y = halves(fma2(add2(pair(x[i], x[i + 1]), pair(-z, -z)), cc, 0ull));
+      l2 = add2(l2, pair(ex2(y.x), ex2(y.y)));
     }
-  }
-  if (nan) a.m = NAN;
+    a.l += halves(l2).x + halves(l2).y;
+  };
+  // the words that lie in the row whole; the next ones are on their way meanwhile
+  const int from = max(lo, lead ? 1 : 0), to = min(hi, (p.vocab + lead) / E);
+  uint4 v[U];
+  auto fetch = [&](int w) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Stat y{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.l, o), __shfl_xor_sync(0xffffffffu, a.id, o)};
-    a = (tid & o) ? merge(y, a, c) : merge(a, y, c);
-  }
-  if ((tid & 31) == 0) part[tid >> 5] = a;
-  __syncthreads();
-  if (tid < 32) {
-    a = tid < kRowThreads / 32 ? part[tid] : Stat{-INFINITY, 0.f, 0x7FFFFFFF};
+    for (int u = 0; u < U; ++u)
+      if (w + u * 32 < to) v[u] = __ldcs(words + w + u * 32);
+  };
+  int w0 = from + lane;
+  fetch(w0);
+  while (w0 < to) {
+    float x[16];
 #pragma unroll
-    for (int o = kRowThreads / 64; o > 0; o >>= 1) {
-      const Stat y{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.l, o), __shfl_xor_sync(0xffffffffu, a.id, o)};
-      a = (tid & o) ? merge(y, a, c) : merge(a, y, c);
+    for (int u = 0; u < U; ++u) {
+      const uint32_t q[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      const bool there = w0 + u * 32 < to;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float y = BF16 ? __uint_as_float((i & 1) ? q[i / 2] & 0xFFFF0000u : q[i / 2] << 16) : __uint_as_float(q[i % 4]);
+        x[u * E + i] = there ? y : -INFINITY;
+      }
     }
-    if (tid == 0) p.stats[(size_t)row * p.splits + split] = make_float4(a.m, a.l, __int_as_float(a.id), 0.f);
+    const int at = w0;
+    w0 += U * 32;
+    fetch(w0);
+    take(x, at);
   }
+  // and the first and the last one, where they do not: a value at a time
+  for (int w = lane == 0 && lead && lo == 0 ? 0 : lane == 1 && hi == n && to < n && (n > 1 || !lead) ? n - 1 : -1; w >= 0; w = -1) {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int id = w * E + i - lead;
+      x[i] = i < E && id >= 0 && id < p.vocab ? logit<BF16>(base, id) : -INFINITY;
+    }
+    take(x, w);
+  }
+  a = merge_lanes(a, 32, c);
+  if (lane == 0) p.stats[(size_t)row * p.width + split] = make_float4(a.m, a.l, __int_as_float(a.id), 0.f);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -186,9 +204,19 @@ __device__ __forceinline__ Two plus(const Two& a, const Two& b) {
   const Two y = two_sum(a.h, b.h);
   return renorm(y.h, y.l + (a.l + b.l));  // (the same whichever way round: lanes that exchange halves agree)
 }
+__device__ __forceinline__ Two times(const Two& a, float b) {
+  const float h = a.h * b;
+  return Two{h, fmaf(a.h, b, -h) + a.l * b};
+}
 __device__ __forceinline__ Two times(const Two& a, const Two& b) {
   const float h = a.h * b.h;
   return renorm(h, fmaf(a.h, b.h, -h) + fmaf(a.h, b.l, a.l * b.h));
+}
+__device__ __forceinline__ Two minus(const Two& a, const Two& b) { return plus(a, Two{-b.h, -b.l}); }
+// what is left of a when b is taken from it
+__device__ __forceinline__ Two less(const Two& a, const Two& b) {
+  const Two d = minus(a, b);
+  return d.h > 0.f ? d : Two{0.f, 0.f};
 }
 __device__ __forceinline__ Two inverse(const Two& a) {  // one Newton step from 1 / a.h
   const float r = 1.f / a.h, e = fmaf(-a.h, r, 1.f) - a.l * r;
@@ -201,27 +229,80 @@ __device__ __forceinline__ bool above(const Two& a, const Two& b) {
 __device__ __forceinline__ Two shfl(const Two& a, int lane) {
   return Two{__shfl_sync(0xffffffffu, a.h, lane), __shfl_sync(0xffffffffu, a.l, lane)};
 }
+__device__ __forceinline__ Two sum_lanes(Two a) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = plus(a, kvq::shfl_xor(a, o));
+  return a;
+}
+__device__ __forceinline__ Two scan_lanes(Two a) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Two y{__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
+    if (lane >= o) a = plus(y, a);
+  }
+  return a;
+}
+__device__ __forceinline__ Two two(float2 f) { return Two{f.x, f.y}; }
 
-// exp((x - m) / temperature), x <= m, c = log2(e) / temperature; the whole warp at once (lane i holds 2^(i / 32)).
-// With y = c (x - m) = n / 32 + f, |f| <= 1/64: 2^y = 2^(n / 32) e^(f ln 2), the second factor by its series to the
-// fifth power (a term of 2^-45 left out), whose first term alone needs both floats.
-__device__ __forceinline__ Two weight(float x, float m, const Two& c, const float2& mine) {
+// Weights of a row's logits: 2^(c x - M) for a whole number M of 32nds near c m (a row's weights all have the
+// factor 2^(c m - M) beside exp((x - m) / temperature), which no comparison sees).
+// c x is the exact product P + p; with n = round(32 (P - M)) the difference r = P - (M + n / 32) is exact, |r| <= 1/64, and
+// 2^(c x - M) = 2^(n / 32) 2^(r + p). The second factor is 1 + g + .., g = (r + p) ln 2, by its series to the fourth power
+// (a term of 2^-39.5 is left out); only g's first term needs both floats.
+struct RowScale {
+  float m, low, magic, M, kappa;  // (low: weights below some 2^-120 are 0; magic: kMagic - 32 M; kappa: 2^(c m - M))
+  bool far;                       // c m is too large for that, or c too small: weight_far
+  __device__ __forceinline__ void set(float max, const Two& c) {
+    m = max;
+    const float n = rintf(c.h * m * 32.f);
+    far = !(fabsf(n) < 2097152.f) || c.h < 1e-30f;  // (2^21)
+    M = n * 0.03125f;
+    magic = kMagic - n;
+    low = m - 120.f / c.h;
+    kappa = far ? 1.f : ex2(fmaf(c.h, m, -M) + c.l * m);
+  }
+};
+// (a whole warp at once: lane i holds 2^(i / 32) in `mine`; not normalised: the second float is up to 2^-14 of the first)
+__device__ __forceinline__ Two weight_raw(float x, const RowScale& s, const Two& c, const float2& mine) {
+  constexpr float kH = 0.693147182464599609375f, kL = -1.904654299957767e-9f;  // ln 2
+  const float y = fmaxf(x, s.low);
+  const float P = c.h * y, p = fmaf(c.l, y, fmaf(c.h, y, -P));
+  const float t = fmaf(P, 32.f, s.magic), nf = t - kMagic;
+  const int n = __float_as_int(t) - __float_as_int(kMagic);
+  const float r = P - fmaf(nf, 0.03125f, s.M);
+  const float gh = r * kH, gl = fmaf(p, kH, fmaf(r, kL, fmaf(r, kH, -gh)));
+  const float q = fmaf(r * r, fmaf(r, fmaf(r, 9.6181291e-3f, 5.5504109e-2f), 0.24022651f), gl);  // ln 2^k / k!
+  const float th = __shfl_sync(0xffffffffu, mine.x, n), tl = __shfl_sync(0xffffffffu, mine.y, n);
+  const float a = th * gh, h = th + a, e = (a - (h - th)) + fmaf(th, gh, -a);
+  const float up = x > s.low ? __int_as_float(((n & ~31) << 18) + (127 << 23)) : 0.f;
+  return Two{h * up, (fmaf(th, q, tl) + e) * up};
+}
+__device__ __forceinline__ Two weight_near(float x, const RowScale& s, const Two& c, const float2& mine) {
+  const Two v = weight_raw(x, s, c, mine);
+  return renorm(v.h, v.l);
+}
+// exp((x - m) / temperature) where c m passes 2^16 (large logits, temperatures near 0) or c is tiny: from the difference x - m, exact
+// in two floats, in the same way.
+__device__ __noinline__ Two weight_far(float x, float m, Two c, float2 mine) {
   const Two d = two_sum(x, -m);
   const float yh = d.h * c.h, yl = fmaf(d.h, c.h, -yh) + fmaf(d.h, c.l, d.l * c.h);
   const bool none = !(yh > -120.f);  // (NaN: infinity times 0)
   const float n = rintf((none ? 0.f : yh) * 32.f), r = (none ? 0.f : yh) - n * 0.03125f;
-  constexpr float kH = 0.693147182464599609375f, kL = -1.904654299957767e-9f;  // ln 2
-  const float gh = r * kH, gl = fmaf(r, kH, -gh) + fmaf(r, kL, (none ? 0.f : yl) * kH);
-  const float s = fmaf(gh * gh, fmaf(gh, fmaf(gh, fmaf(gh, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), gl);
+  constexpr float kH = 0.693147182464599609375f, kL = -1.904654299957767e-9f;
+  const float gh = r * kH, gl = fmaf(none ? 0.f : yl, kH, fmaf(r, kL, fmaf(r, kH, -gh)));
+  const float q = fmaf(r * r, fmaf(r, fmaf(r, 9.6181291e-3f, 5.5504109e-2f), 0.24022651f), gl);
   const int k = (int)n;
-  const float th = __shfl_sync(0xffffffffu, mine.x, k & 31), tl = __shfl_sync(0xffffffffu, mine.y, k & 31);
-  const float a = th * gh, ae = fmaf(th, gh, -a), h = th + a, e = a - (h - th);
-  const float l = e + ae + fmaf(th, s, tl);
+  const float th = __shfl_sync(0xffffffffu, mine.x, k), tl = __shfl_sync(0xffffffffu, mine.y, k);
+  const float a = th * gh, h = th + a, e = (a - (h - th)) + fmaf(th, gh, -a);
   const float up = __int_as_float((127 + (k >> 5)) << 23);
   if (x == m) return Two{1.f, 0.f};
   if (none || !(x > -INFINITY)) return Two{0.f, 0.f};
-  const Two w = renorm(h, l);
-  return Two{w.h * up, w.l * up};
+  const Two v = renorm(h, fmaf(th, q, tl) + e);
+  return Two{v.h * up, v.l * up};
+}
+__device__ __forceinline__ Two weight(float x, const RowScale& s, const Two& c, const float2& mine) {
+  return s.far ? weight_far(x, s.m, c, mine) : weight_near(x, s, c, mine);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -242,19 +323,41 @@ __device__ __forceinline__ void put_remote(float2* at, uint32_t cta, float2 v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
+constexpr int kParts = kWalkWarps * kMaxCluster;
 struct Walk {
-  float xd[DEC_MAX_TREE], qd[DEC_MAX_TREE], u[DEC_MAX_TREE];  // a draft's logit, draft probability, random number
-  int tok[DEC_MAX_TREE], up[DEC_MAX_TREE];
-  int gone[DEC_MAX_TREE];   // refused drafts' tokens (without draft probabilities)
-  float2 scale[DEC_MAX_TREE + 1];  // with them: what p is multiplied by before each subtraction
-  float2 sums[2][32 * kMaxCluster];  // the warps' sums, of all CTAs (two passes' in turn)
-  float2 scan[32];
+  float2 sums[2][3][kParts];  // the parts' sums, of all CTAs (two passes' in turn)
+  float2 scan[kWalkWarps];
   int found, last;
 };
+// and of every row: its draft's weight (in its parent's scale), draft probability, random number, token, parent; the
+// row's statistics; refused drafts' tokens (without draft probabilities), or sums left after each refusal
+struct Rows {
+  float2 *weight, *sum;
+  float *q, *u, *m, *l;
+  int *tok, *up, *id, *gone;
+  static constexpr int kBytes = 2 * 8 + 8 * 4;
+  __device__ __forceinline__ Rows(uint8_t* at, int n) {
+    weight = reinterpret_cast<float2*>(at);
+    sum = weight + n;
+    q = reinterpret_cast<float*>(sum + n);
+    u = q + n;
+    m = u + n;
+    l = m + n;
+    tok = reinterpret_cast<int*>(l + n);
+    up = tok + n;
+    id = up + n;
+    gone = id + n;
+  }
+};
+inline int rows_room(int max_tokens) { return (max_tokens + 31) / 32 * 32 + 32; }
 
+// What bounds it: for few sequences latency (bounds, rows, logits, statistics, one pass, its exchange, the id), for many
+// the pass's instructions, some 45 a logit.
 template <bool BF16, int CL>
 __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
   __shared__ Walk w;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  const Rows rw(dyn, (p.max_tokens + 31) / 32 * 32 + 32);
   const int b = blockIdx.x / CL, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = CL > 1 ? cluster_rank() : 0;
   const float2 mine = p.table.e[lane];
@@ -265,28 +368,25 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
   Two c{c32, 0.f};
   if (!greedy) {
     const float t = p.temperature ? __ldg(p.temperature + b) : 1.f;
-    // log2(e) / t: the quotient and its remainder
-    constexpr float kH = 1.44269502162933349609375f, kL = 1.92596299e-8f;
+    constexpr float kH = 1.44269502162933349609375f, kL = 1.92596299e-8f;  // log2(e)
     if (t > 1e-30f && t < 1e30f) c = times(Two{kH, kL}, inverse(Two{t, 0.f}));
   }
   const char* const x0 = static_cast<const char*>(p.x);
   auto row_at = [&](int j) -> const void* { return x0 + (first + j) * p.stride * (BF16 ? 2 : 4); };
-  // ---- what the walk may need of every draft
-  if (tid < n) {
-    const int up = tid == 0 ? -1 : p.parents ? __ldg(p.parents + first + tid) : tid - 1, t = __ldg(p.tokens + first + tid);
-    const bool there = up >= 0 && up < tid && t >= 0 && t < p.vocab;
-    w.up[tid] = up < tid ? up : -1;
-    w.tok[tid] = t;
-    w.u[tid] = __ldg(p.uniforms + first + tid);
-    w.xd[tid] = there ? logit<BF16>(row_at(up), t) : -INFINITY;
-    w.qd[tid] = there && soft ? __ldg(p.probs + (first + up) * p.prob_stride + t) : 1.f;
+  // ---- what the walk may need of every row
+  for (int j = tid; j < n; j += kWalkThreads) {
+    const int up = j == 0 ? -1 : p.parents ? __ldg(p.parents + first + j) : j - 1, t = __ldg(p.tokens + first + j);
+    const bool there = up >= 0 && up < j && t >= 0 && t < p.vocab;
+    rw.up[j] = up < j ? up : -1;
+    rw.tok[j] = t;
+    rw.u[j] = __ldg(p.uniforms + first + j);
+    rw.weight[j].x = there ? logit<BF16>(row_at(up), t) : -INFINITY;  // (its logit, until the statistics are there)
+    rw.q[j] = there && soft ? __ldg(p.probs + (first + up) * p.prob_stride + t) : 1.f;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // (the rows' sums)
-  __syncthreads();
   int32_t* const path = p.path + (size_t)b * p.max_tokens;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (the rows' sums)
   for (int i = tid; i < p.max_tokens && rank == 0; i += kWalkThreads)
     if (i > 0 || n == 0) path[i] = -1;
-  __syncthreads();
   if (n == 0) {
     if (rank == 0 && tid == 0) {
       p.count[b] = 0;
@@ -294,92 +394,263 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
     }
     return;  // (the same in the whole cluster)
   }
+  const float cm = greedy ? 1.f : c32;
+  const int width = p.width, group = lane / width;  // (32 / width rows a warp)
+  for (int j0 = warp * (32 / width); j0 < n; j0 += kWalkWarps * (32 / width)) {
+    const int j = j0 + group, i = lane % width;
+    Stat st{-INFINITY, 0.f, 0x7FFFFFFF};
+    if (j < n && i < p.splits) {
+      const float4 f = __ldcg(p.stats + (size_t)(first + j) * width + i);
+      st = Stat{f.x, f.y, __float_as_int(f.z)};
+    }
+    st = merge_lanes(st, width, cm);
+    if (j < n && i == 0) {
+      rw.m[j] = st.m;
+      rw.l[j] = st.l;
+      rw.id[j] = st.id;
+    }
+  }
+  __syncthreads();
+  RowScale sc;
+  if (!greedy)
+    for (int j = tid; j - lane < n; j += kWalkThreads) {
+      const int up = j < n ? max(rw.up[j], 0) : 0;
+      sc.set(rw.m[up], c);
+      const float x = j < n ? rw.weight[j].x : -INFINITY;
+      const Two near = weight_near(x, sc, c, mine);
+      Two v = near;
+      if (__any_sync(0xffffffffu, sc.far)) {
+        const Two far = weight_far(x, sc.m, c, mine);
+        if (sc.far) v = far;
+      }
+      if (j < n) rw.weight[j] = make_float2(v.h, v.l);
+    }
+  __syncthreads();
   if (rank == 0 && tid == 0) path[0] = 0;
 
-  // ---- a row's statistics, by every warp
-  Stat st;
-  auto stats = [&](int j) {
-    const float4 f = lane < p.splits ? __ldcg(p.stats + (size_t)(first + j) * p.splits + lane) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    st = Stat{f.x, f.y, lane < p.splits ? __float_as_int(f.z) : 0x7FFFFFFF};
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Stat y{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.l, o), __shfl_xor_sync(0xffffffffu, st.id, o)};
-      st = (lane & o) ? merge(y, st, c32) : merge(st, y, c32);
-    }
-  };
-
-  // ---- sums over the vocabulary of what is left of p at row `node`, in exact parts: part s of 32 CL is [s seg, ..)
-  const int parts = 32 * CL, seg = (p.vocab + parts - 1) / parts, me = (int)rank * 32 + warp;
+  // ---- sums over the vocabulary of what is left at row `node`, in parts: part k of kWalkWarps CL is [k seg, ..)
+  constexpr int parts = kWalkWarps * CL, per = (parts + 31) / 32;
+  const int seg = (p.vocab + parts - 1) / parts, me = (int)rank * kWalkWarps + warp;
   int node = 0, gone = 0, rounds = 0, pass = 0;
-  Two z{1.f, 0.f};  // the row's whole sum, and its inverse, once they are known in both floats
-  Two iz{1.f, 0.f};
-  bool exact = false;
-  auto left = [&](int i, bool in, bool whole) {  // what is left of id i; lanes of a warp together
-    const float x = in ? logit<BF16>(row_at(node), i) : -INFINITY;
-    Two v = weight(x, st.m, c, mine);
-    if (whole) return v;
-    if (!soft) {
-      for (int k = 0; k < gone; ++k)
-        if (w.gone[k] == i) v = Two{0.f, 0.f};
-      return v;
-    }
-    v = times(v, iz);
-    if (rounds > 0) {
-      const float q = in ? __ldg(p.probs + (first + node) * p.prob_stride + i) : 0.f;
-      for (int k = 0; k < rounds; ++k) {
-        const float2 f = w.scale[k];
-        v = times(v, Two{f.x, f.y});
-        const Two d = two_sum(v.h, -q);
-        v = renorm(d.h, d.l + v.l);
-        if (!(v.h > 0.f)) v = Two{0.f, 0.f};
-      }
-    }
+  enum { kNone, kWhole, kRest } summed = kNone;  // what `part` holds: nothing of this row yet, all of it, what is left
+  Two part[per] = {};  // of the parts lane per, ..: every warp has them all
+  Two z{0.f, 0.f};  // the row's whole sum
+  bool exact = false;  // (known)
+  auto enter = [&](int j) {
+    node = j;
+    gone = rounds = 0;
+    exact = false;
+    summed = kNone;
+    if (!greedy) sc.set(rw.m[j], c);
+    return fabsf(rw.m[j]) <= 3.4028235e38f && rw.l[j] == rw.l[j];
+  };
+  auto prob = [&](int i) { return __ldg(p.probs + (first + node) * p.prob_stride + i); };
+  auto take_away = [&](Two v, float q) {  // refusals, one after another
+    for (int k = 0; k < rounds; ++k) v = less(v, times(two(rw.sum[k]), q));
     return v;
   };
-  auto total = [&](bool whole) {  // every part's sum into w.sums[pass & 1], and all of them
+  auto left = [&](int i, bool in) {  // what is left of id i; lanes of a warp together
+    Two v = weight(in ? logit<BF16>(row_at(node), i) : -INFINITY, sc, c, mine);
+    if (!in) return Two{0.f, 0.f};
+    if (soft) return rounds > 0 ? take_away(v, prob(i)) : v;
+    for (int k = 0; k < gone; ++k)
+      if (rw.gone[k] == i) v = Two{0.f, 0.f};
+    return v;
+  };
+  // up to three sums of this warp's part to every CTA; then all parts' are in out[0 .. 2]
+  auto exchange = [&](const Two& a0, const Two& a1, const Two& a2, int sums) {
+    float2(*const out)[kParts] = w.sums[pass & 1];
+    const Two mine3[3] = {a0, a1, a2};
+    if (CL > 1) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k < sums && lane < CL) put_remote(&out[k][me], lane, make_float2(mine3[k].h, mine3[k].l));
+      cluster_sync();
+    } else {
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k < sums && lane == 0) out[k][me] = make_float2(mine3[k].h, mine3[k].l);
+      __syncthreads();
+    }
+    ++pass;
+  };
+  auto total = [&]() {  // of `part`: every warp by itself, all the same
+    Two a = part[0];
+#pragma unroll
+    for (int k = 1; k < per; ++k) a = plus(a, part[k]);
+    return sum_lanes(a);
+  };
+  auto read = [&](const float2* out, int k) { return lane * per + k < parts ? two(out[lane * per + k]) : Two{0.f, 0.f}; };
+  const int lo = me * seg, hi = min(p.vocab, lo + seg);
+  // what is left, id by id: any number of refusals
+  auto sum_rest = [&]() {
     Two s{0.f, 0.f};
-    const int lo = me * seg, hi = min(p.vocab, lo + seg);
     for (int i0 = lo; i0 < hi; i0 += 128) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int i = i0 + u * 32 + lane;
-        accumulate(s, left(i, i < hi, whole));
+        accumulate(s, left(i, i < hi));
       }
     }
-    s = renorm(s.h, s.l);
+    const float2* const out = w.sums[pass & 1][0];
+    exchange(sum_lanes(renorm(s.h, s.l)), s, s, 1);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s = plus(s, Two{__shfl_xor_sync(0xffffffffu, s.h, o), __shfl_xor_sync(0xffffffffu, s.l, o)});
-    float2* const out = w.sums[pass & 1];
-    if (CL > 1) {
-      if (lane < CL) put_remote(out + me, lane, make_float2(s.h, s.l));
-      cluster_sync();
-    } else {
-      if (lane == 0) out[me] = make_float2(s.h, s.l);
-      __syncthreads();
+    for (int k = 0; k < per; ++k) part[k] = read(out, k);
+    summed = kRest;
+    return total();
+  };
+  // The row's whole sum Z, part by part; with REST also what one refusal leaves: sums A of weights and B of draft
+  // probabilities over the ids where w > q Z, which A - B Z are (the first kernel's Z tells which: an id at which it is
+  // wrong has next to nothing left). A lane's sums are kept as multiples of a power of two, which add exactly, and
+  // remainders.
+  // (without_gone: refused drafts' tokens count nothing)
+  auto sum_whole = [&](auto with_rest, bool without_gone) {
+    constexpr bool REST = decltype(with_rest)::value;
+    constexpr int U = REST ? 4 : 8;
+    const void* const row = row_at(node);
+    const float* const qrow = REST ? p.probs + (first + node) * p.prob_stride : nullptr;
+    const float z0 = rw.l[node] * sc.kappa;
+    // (a lane's sum is below twice the power of two in `most`: multiples of 2^-22 of that add exactly)
+    const float most = fminf((seg / 32 + 1) * 1.03f, z0 * 1.01f);
+    const float cut = kMagic * __int_as_float((__float_as_int(most) & 0x7F800000) - (22 << 23));
+    Two sz{0.f, 0.f}, sa{0.f, 0.f}, sb{0.f, 0.f};
+    bool some_gone = false;
+    if (!REST && without_gone) {
+      for (int k = lane; k < gone; k += 32) some_gone |= rw.gone[k] >= lo && rw.gone[k] < hi;
+      some_gone = __any_sync(0xffffffffu, some_gone);
     }
-    Two a{0.f, 0.f};
-    for (int k = lane; k < parts; k += 32) a = plus(a, Two{out[k].x, out[k].y});
+    float x[U], q[U];
+    auto fetch = [&](int i0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = plus(a, Two{__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)});
-    ++pass;
-    return a;
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * 32 + lane;
+        x[u] = i < hi ? logit<BF16>(row, i) : -INFINITY;
+        if (REST) q[u] = i < hi ? __ldg(qrow + i) : 0.f;
+      }
+    };
+    fetch(lo);
+    for (int i0 = lo; i0 < hi; i0 += 32 * U) {
+      float y[U], r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        y[u] = x[u];
+        r[u] = REST ? q[u] : 0.f;
+      }
+      fetch(i0 + 32 * U);
+      if (!REST && some_gone)
+        for (int k = 0; k < gone; ++k) {
+          const int at = rw.gone[k] - i0 - lane;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (at == u * 32) y[u] = -INFINITY;
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const Two v = weight_raw(y[u], sc, c, mine);
+        const float k = (v.h + cut) - cut, d = (v.h - k) + v.l;
+        sz.h += k;
+        sz.l += d;
+        if (REST) {
+          const bool on = v.h + v.l > r[u] * z0;
+          const float kq = (r[u] + cut) - cut;
+          sa.h += on ? k : 0.f;
+          sa.l += on ? d : 0.f;
+          sb.h += on ? kq : 0.f;
+          sb.l += on ? r[u] - kq : 0.f;
+        }
+      }
+    }
+    const float2(*const out)[kParts] = w.sums[pass & 1];
+    exchange(sum_lanes(renorm(sz.h, sz.l)), sum_lanes(renorm(sa.h, sa.l)), sum_lanes(renorm(sb.h, sb.l)), REST ? 3 : 1);
+#pragma unroll
+    for (int k = 0; k < per; ++k) part[k] = read(out[0], k);
+    Two all = total();
+    if (!without_gone || gone == 0) {
+      z = all;
+      exact = true;
+    }
+    summed = REST || (without_gone && gone > 0) ? kRest : kWhole;
+    float a = 0.f;
+    if (REST) {
+#pragma unroll
+      for (int k = 0; k < per; ++k) {
+        const Two A = read(out[1], k);
+        a += A.h;
+        part[k] = less(A, times(z, read(out[2], k)));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    }
+    return a;  // (of A, where there is a rest)
   };
   auto settle = [&]() {  // the row's whole sum in both floats
     if (exact) return;
-    z = total(true);
-    iz = inverse(z);
-    exact = true;
+    if (sc.far) {
+      const int g = gone, r = rounds;
+      gone = rounds = 0;
+      z = sum_rest();
+      gone = g;
+      rounds = r;
+      exact = true;
+      summed = kNone;
+    } else {
+      sum_whole(std::false_type(), false);
+    }
   };
 
-  stats(0);
-  int taken = 1;
-  bool good = fabsf(st.m) <= 3.4028235e38f;
+  // ---- As far as the first kernel's sums leave no doubt, every draft's fate is known at once, supposing that its earlier
+  // siblings were refused (with draft probabilities only a first child's is): the first child of every row that is
+  // accepted, or left open (1 beside twice its number). Without draft probabilities a token that an earlier sibling has
+  // has nothing left.
+  int* const chosen = rw.gone;
+  auto drawn = [&](int k) { return rw.tok[k] >= 0 && rw.tok[k] < p.vocab; };
+  for (int j0 = 0; j0 < n; j0 += kWalkThreads) {
+    const int j = j0 + tid, up = j < n ? rw.up[j] : -1;
+    bool again = false;
+    if (up >= 0 && !soft)
+#pragma unroll 4
+      for (int k = up + 1; k < j; ++k) again |= rw.up[k] == up && rw.tok[k] == rw.tok[j];
+    if (again) rw.weight[j] = make_float2(0.f, 0.f);
+    if (j < n) chosen[j] = 0x7FFFFFFF;
+  }
+  __syncthreads();
+  for (int j = tid; j < n; j += kWalkThreads) {
+    const int up = rw.up[j];
+    if (up < 0 || !drawn(j) || !(fabsf(rw.m[up]) <= 3.4028235e38f) || rw.l[up] != rw.l[up]) continue;
+    bool take = rw.tok[j] == rw.id[up], open = false;
+    if (!greedy) {
+      float before = 0.f;
+      bool later = false;
+#pragma unroll 4
+      for (int k = up + 1; k < j; ++k) {
+        const bool sibling = rw.up[k] == up && drawn(k);
+        later |= sibling;
+        before += sibling ? rw.weight[k].x : 0.f;
+      }
+      if (soft && later) continue;
+      sc.set(rw.m[up], c);
+      const float s0 = rw.l[up] * sc.kappa, lhs = rw.u[j] * rw.q[j] * (s0 - before), v = rw.weight[j].x;
+      take = lhs < v;
+      open = fabsf(lhs - v) <= kTrust * fmaxf(s0 * rw.u[j] * rw.q[j], v);
+    }
+    if (take || open) atomicMin(&chosen[up], 2 * j + open);
+  }
+  __syncthreads();
+  int taken = 1, node0 = 0;
+  for (int k = chosen[0]; k != 0x7FFFFFFF && !(k & 1); k = chosen[node0]) {
+    node0 = k >> 1;
+    if (rank == 0 && tid == 0) path[taken] = node0;
+    ++taken;
+  }
+  __syncthreads();  // (chosen's room is used again)
+  // ---- from there one child at a time
+  bool good = enter(node0);
   Two rest{0.f, 0.f};  // without draft probabilities: what refused drafts took of the sum
-  for (int j = 1; good && j < n;) {
+  for (int j = node0 + 1; good && j < n;) {
     // the next child of node
     int c0 = n;
     for (int k = j & ~31; k < n; k += 32) {
-      const uint32_t m = __ballot_sync(0xffffffffu, k + lane >= j && k + lane < n && w.up[k + lane] == node);
+      const uint32_t m = __ballot_sync(0xffffffffu, k + lane >= j && k + lane < n && rw.up[k + lane] == node);
       if (m) {
         c0 = k + __ffs(m) - 1;
         break;
@@ -387,151 +658,126 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
     }
     if (c0 >= n) break;
     j = c0 + 1;
-    const int t = w.tok[c0];
+    const int t = rw.tok[c0];
     if (t < 0 || t >= p.vocab) continue;
     bool take;
     if (greedy) {
-      take = t == st.id;
+      take = t == rw.id[node];
     } else {
-      const float u = w.u[c0];
-      bool spent = false;  // (a token that was refused already has nothing left)
-      if (!soft)
-        for (int k = lane; k < gone; k += 32) spent |= w.gone[k] == t;
-      spent = __any_sync(0xffffffffu, spent);
-      const Two wd = spent ? Two{0.f, 0.f} : weight(w.xd[c0], st.m, c, mine);
+      const float u = rw.u[c0], q = rw.q[c0];
+      const Two wd = two(rw.weight[c0]);
+      // u q (what is left of the sum) against what is left of the draft's weight (q: 1 without draft probabilities)
       if (rounds == 0) {
-        // u q (sum - refused) against the draft's weight (q: 1 without draft probabilities)
-        const float lhs = u * w.qd[c0] * (soft ? st.l : st.l - rest.h);
+        const float s0 = rw.l[node] * sc.kappa, lhs = u * q * (s0 - rest.h);
         take = lhs < wd.h;
-        if (fabsf(lhs - wd.h) <= kTrust * fmaxf(st.l * u * w.qd[c0], wd.h)) {
+        if (fabsf(lhs - wd.h) <= kTrust * fmaxf(s0 * u * q, wd.h)) {
           settle();
-          const Two r = soft ? z : plus(z, Two{-rest.h, -rest.l});
-          take = above(wd, times(times(r, Two{w.qd[c0], 0.f}), Two{u, 0.f}));
+          take = above(wd, times(times(minus(z, rest), q), u));
         }
       } else {
-        Two v = times(wd, iz);
-        for (int k = 0; k < rounds; ++k) {
-          const float2 f = w.scale[k];
-          v = times(v, Two{f.x, f.y});
-          const Two d = two_sum(v.h, -w.qd[c0]);
-          v = renorm(d.h, d.l + v.l);
-          if (!(v.h > 0.f)) v = Two{0.f, 0.f};
-        }
-        const float2 f = w.scale[rounds];  // (the draft's share of what is left, over all of it)
-        take = above(times(v, Two{f.x, f.y}), times(Two{w.qd[c0], 0.f}, Two{u, 0.f}));
+        take = above(take_away(wd, q), times(times(two(rw.sum[rounds]), q), u));
       }
       if (!take) {
+        __syncthreads();
         if (!soft) {
-          __syncthreads();
-          if (tid == 0) w.gone[gone] = t;
+          if (tid == 0) rw.gone[gone] = t;
           ++gone;
           rest = plus(rest, wd);
+          summed = kNone;
           __syncthreads();
         } else {
-          settle();
-          __syncthreads();
-          if (tid == 0 && rounds == 0) w.scale[0] = make_float2(1.f, 0.f);
+          Two s{0.f, 0.f};
+          bool direct = rounds > 0 || sc.far;
+          if (!direct) {
+            const float a = sum_whole(std::true_type(), false);
+            s = total();
+            direct = s.h < 0x1p-12f * a;  // (p is all but q: which ids have something left is decided one by one)
+          } else {
+            settle();
+          }
+          if (tid == 0 && rounds == 0) rw.sum[0] = make_float2(z.h, z.l);
           ++rounds;
           __syncthreads();
-          const Two s = total(false);
-          const Two f = inverse(s);
-          if (!(s.h > 0.f)) --rounds;  // nothing would be left: p stays
-          else if (tid == 0) w.scale[rounds] = make_float2(f.h, f.l);
+          if (direct) s = sum_rest();
+          if (!(s.h > 0.f)) {  // nothing would be left: p stays
+            --rounds;
+            summed = kNone;
+          } else if (tid == 0) {
+            rw.sum[rounds] = make_float2(s.h, s.l);
+          }
           __syncthreads();
         }
       }
     }
     if (take) {
-      node = c0;
       if (rank == 0 && tid == 0) path[taken] = c0;
       ++taken;
-      gone = rounds = 0;
       rest = Two{0.f, 0.f};
-      exact = false;
-      iz = Two{1.f, 0.f};
-      stats(node);
-      good = fabsf(st.m) <= 3.4028235e38f;
+      good = enter(c0);
     }
   }
   if (rank == 0 && tid == 0) {
     p.count[b] = taken;
     if (!good) p.next[b] = -1;
-    else if (greedy) p.next[b] = st.id;
+    else if (greedy) p.next[b] = rw.id[node];
   }
   if (good && !greedy) {
-    // ---- the next token: the first id up to which the sum passes u times all of it
-    if (soft && rounds > 0) settle();
-    Two all = total(false);
+    // ---- the next token: the first id up to which what is left sums to more than u times all of it
+    if (summed == kNone || (summed == kWhole && gone + rounds > 0) || (summed == kRest && gone + rounds == 0)) {
+      if (rounds == 0 && !sc.far) sum_whole(std::false_type(), true);
+      else sum_rest();
+    }
+    Two all = total();
     if (!soft && gone > 0 && !(all.h > 0.f)) {  // nothing is left: the refusals do not count
       gone = 0;
-      all = total(false);
+      all = sum_rest();
     }
-    const float2* const sums = w.sums[(pass - 1) & 1];
-    const Two want = times(all, Two{w.u[0], 0.f});
-    // the part it lies in (by every warp): CL parts a lane, in order
-    Two own{0.f, 0.f};
+    const Two want = times(all, rw.u[0]);
+    // the part it lies in, by every warp
+    Two own = part[0];
 #pragma unroll
-    for (int k = 0; k < CL; ++k) own = plus(own, Two{sums[lane * CL + k].x, sums[lane * CL + k].y});
-    Two upto = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const Two y{__shfl_up_sync(0xffffffffu, upto.h, o), __shfl_up_sync(0xffffffffu, upto.l, o)};
-      if (lane >= o) upto = plus(y, upto);
-    }
+    for (int k = 1; k < per; ++k) own = plus(own, part[k]);
+    const Two upto = scan_lanes(own);
     const uint32_t past = __ballot_sync(0xffffffffu, above(upto, want));
     const uint32_t some = __ballot_sync(0xffffffffu, own.h > 0.f);
     const int l0 = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
     Two before{0.f, 0.f};
     if (l0 > 0) before = shfl(upto, l0 - 1);
-    int target = l0 * CL;
-    if (CL > 1) {
-      int at = -1, full = l0 * CL;
+    int target = l0 * per;
+    if (per > 1) {
+      int at = -1;
       Two run = before, start = before;
-      for (int k = 0; k < CL; ++k) {
-        const Two v{sums[l0 * CL + k].x, sums[l0 * CL + k].y};
-        const Two next = plus(run, v);
+#pragma unroll
+      for (int k = 0; k < per; ++k) {
+        const Two v = shfl(part[k], l0), next = plus(run, v);
         if (v.h > 0.f && at < 0) {
-          full = l0 * CL + k;
+          target = l0 * per + k;
           start = run;
-          if (past && above(next, want)) at = full;
+          if (past && above(next, want)) at = target;
         }
         run = next;
       }
-      target = at < 0 ? full : at;
       before = start;
     }
-    if (target / 32 == (int)rank) {
-      // the id, by the whole CTA: a stretch of 1024 at a time
-      const int lo = target * seg, hi = min(p.vocab, lo + seg);
+    if (target / kWalkWarps == (int)rank) {
+      // the id, by the whole CTA: a stretch of its threads at a time
+      const int from = target * seg, to = min(p.vocab, from + seg);
       if (tid == 0) {
         w.found = 0x7FFFFFFF;
         w.last = -1;
       }
-      for (int i0 = lo; i0 < hi; i0 += kWalkThreads) {
+      for (int i0 = from; i0 < to; i0 += kWalkThreads) {
         const int i = i0 + tid;
-        const Two v = left(i, i < hi, false);
-        Two run = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const Two y{__shfl_up_sync(0xffffffffu, run.h, o), __shfl_up_sync(0xffffffffu, run.l, o)};
-          if (lane >= o) run = plus(y, run);
-        }
+        const Two v = left(i, i < to), run = scan_lanes(v);
         __syncthreads();
         if (lane == 31) w.scan[warp] = make_float2(run.h, run.l);
         __syncthreads();
-        Two y{w.scan[lane].x, w.scan[lane].y};
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const Two a{__shfl_up_sync(0xffffffffu, y.h, o), __shfl_up_sync(0xffffffffu, y.l, o)};
-          if (lane >= o) y = plus(a, y);
-        }
-        Two base = before;
-        const Two over = shfl(y, warp > 0 ? warp - 1 : 0);
-        if (warp > 0) base = plus(base, over);
-        const bool some_here = v.h > 0.f;
-        if (some_here && above(plus(base, run), want)) atomicMin(&w.found, i);
-        if (some_here) atomicMax(&w.last, i);
-        before = plus(before, shfl(y, 31));
+        const Two y = scan_lanes(lane < kWalkWarps ? two(w.scan[lane]) : Two{0.f, 0.f});
+        const Two over = shfl(y, warp > 0 ? warp - 1 : 0), base = warp > 0 ? plus(before, over) : before;
+        const bool there = v.h > 0.f;
+        if (there && above(plus(base, run), want)) atomicMin(&w.found, i);
+        if (there) atomicMax(&w.last, i);
+        before = plus(before, shfl(y, kWalkWarps - 1));
         __syncthreads();
         if (w.found != 0x7FFFFFFF) break;  // (the same in all threads)
       }
@@ -545,15 +791,19 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
 template <bool BF16>
 cudaError_t launch(Params& p, cudaStream_t s) {
   if (p.n_tokens > 0) {
-    rows_kernel<BF16><<<(unsigned)(p.n_tokens * p.splits), kRowThreads, 0, s>>>(p);
+    const unsigned warps = kRowThreads / 32;
+    rows_kernel<BF16><<<((unsigned)p.n_tokens * p.splits + warps - 1) / warps, kRowThreads, 0, s>>>(p);
     const cudaError_t ce = cudaGetLastError();
     if (ce != cudaSuccess) return ce;
   }
   const int sms = op_sms();
-  const int cl = (long long)p.batch * 8 <= sms ? 8 : (long long)p.batch * 2 <= sms ? 2 : 1;
+  // CTAs a sequence: as many as the SMs hold, each a share of the vocabulary
+  int cl = 1;
+  while (cl < kMaxCluster && (long long)p.batch * cl * 2 <= sms) cl *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(p.batch * cl));
   cfg.blockDim = dim3(kWalkThreads);
+  cfg.dynamicSmemBytes = rows_room(p.max_tokens) * Rows::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (only behind the rows' kernel, which waits for what came before)
@@ -563,10 +813,20 @@ cudaError_t launch(Params& p, cudaStream_t s) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cl > 1 ? 2 : 1;
+  auto go = [&](void (*k)(const Params)) {
+    // (many rows a sequence pass the 48 KB that a kernel has without asking)
+    if (cfg.dynamicSmemBytes + sizeof(Walk) > 48 * 1024) {
+      const cudaError_t ce = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  rows_room(DEC_MAX_TREE) * Rows::kBytes);
+      if (ce != cudaSuccess) return ce;
+    }
+    return cudaLaunchKernelEx(&cfg, k, p);
+  };
   switch (cl) {
-    case 1: return cudaLaunchKernelEx(&cfg, walk_kernel<BF16, 1>, p);
-    case 2: return cudaLaunchKernelEx(&cfg, walk_kernel<BF16, 2>, p);
-    default: return cudaLaunchKernelEx(&cfg, walk_kernel<BF16, 8>, p);
+    case 1: return go(walk_kernel<BF16, 1>);
+    case 2: return go(walk_kernel<BF16, 2>);
+    case 4: return go(walk_kernel<BF16, 4>);
+    default: return go(walk_kernel<BF16, 8>);
   }
 }
 
@@ -587,7 +847,7 @@ Table make_table() {
 using namespace dec;
 
 extern "C" int64_t dec_verify_drafts_workspace(int32_t n_tokens) {
-  return n_tokens < 0 ? -1 : (int64_t)n_tokens * verify::kMaxSplits * (int64_t)sizeof(float4);
+  return n_tokens < 0 ? -1 : (int64_t)n_tokens * verify::kMaxParts * (int64_t)sizeof(float4);
 }
 
 extern "C" dec_status dec_verify_drafts(const dec_verify_drafts_args* a, void* stream) {
@@ -606,7 +866,7 @@ extern "C" dec_status dec_verify_drafts(const dec_verify_drafts_args* a, void* s
   if (reinterpret_cast<uintptr_t>(a->logits) % (a->dtype == DEC_BF16 ? 2 : 4) || reinterpret_cast<uintptr_t>(a->draft_probs) % 4)
     return op_fail(DEC_ERR_ARG, "verify_drafts: logits and draft_probs must be aligned to their types");
   // (what kTrust says of the rows' sums holds up to here)
-  if (a->vocab > (1 << 24) || a->n_tokens > INT_MAX / verify::kMaxSplits || a->batch > INT_MAX / verify::kMaxCluster ||
+  if (a->vocab > (1 << 24) || a->n_tokens > INT_MAX / verify::kMaxParts || a->batch > INT_MAX / verify::kMaxCluster ||
       (long long)a->batch * a->max_tokens > (1LL << 40))
     return op_fail(DEC_ERR_UNSUPPORTED, "verify_drafts: too many rows, ids or sequences");
   if (a->n_tokens > 0 && (!a->workspace || !op_aligned(a->workspace) || a->workspace_bytes < dec_verify_drafts_workspace(a->n_tokens)))
@@ -634,11 +894,14 @@ extern "C" dec_status dec_verify_drafts(const dec_verify_drafts_args* a, void* s
   p.table = table;
   const int sms = op_sms();
   if (sms < 1) return op_fail(DEC_ERR_CUDA, "verify_drafts: no device");
-  // CTAs a row: enough to fill the SMs, each with at least 8 words of 16 bytes a thread
-  p.splits = 1;
-  while (p.splits < verify::kMaxSplits && (long long)a->n_tokens * p.splits < 4 * sms &&
-         a->vocab / (p.splits * 2) >= 32 * verify::kRowThreads)
-    p.splits *= 2;
+  // Warps a row: as many as the SMs hold at once, or of many rows enough for some turns, each with at least 32 values a
+  // thread.
+  const int each = a->dtype == DEC_BF16 ? 8 : 4, words = (a->vocab + each - 1) / each;
+  const long long room = (long long)sms * verify::kRowWarps, rows = std::max(1, a->n_tokens);
+  p.splits = (int)std::max<long long>(1, std::min<long long>({verify::kMaxParts, words / (32 / each * 32),
+                                                              rows * 2 <= room ? room / rows : (4 * room + rows - 1) / rows}));
+  p.width = 1;
+  while (p.width < p.splits) p.width *= 2;
   const cudaError_t ce = a->dtype == DEC_BF16 ? verify::launch<true>(p, op_stream(stream)) : verify::launch<false>(p, op_stream(stream));
   return ce == cudaSuccess ? DEC_OK : op_cuda(ce, "verify_drafts");
 }
