@@ -521,8 +521,8 @@ dec_status dec_draft_tree(const dec_draft_tree_args* args, void* stream);
 /* Attention weight that cached positions receive, added up: for every position p that a row of the call attends to
    (causal and lengths as in dec_kvq_attention) and every KV head h
      mass_out[p] = decay * mass[p] + sum over the rows that attend to p and the heads of h's group of exp(scale q.k - lse)
-   where mass and mass_out are fp32 [n_pages][n_kv_heads][page_tokens], laid out as the cache's pages (mass_out may be
-   mass). Positions that the call's rows stand at (causal) have had nothing before, and where decay is 0 nothing is
+   where mass and mass_out are fp32 [n_pages][n_kv_heads][page_tokens], 16-byte aligned, laid out as the cache's pages
+   (mass_out may be mass, or share nothing with it). Positions that the call's rows stand at (causal) have had nothing before, and where decay is 0 nothing is
    read. Positions that no row could attend to are left as they are.
      q          bf16 rows of n_heads heads, lse device fp32 [n_tokens][n_heads], both as the attention had and gave them;
                 a row whose lse is not finite adds nothing

@@ -10,7 +10,7 @@ LIB = os.path.join(PKG, "libdec.so")
 SOURCES = ["dec_engine.cu", "dec_wide.cu", "dec_kvq.cu", "dec_logprobs.cu", "dec_step_kvq.cu", "dec_kvq_keep.cu",
            "dec_verify.cu"]
 HEADERS = ["dec_common.h", "dec_prims.cuh", "dec_kernel.cuh", "dec_wide.cuh", "dec_wide_host.h", "dec_kvq.cuh", "dec_kvq_attn.cuh",
-           "dec_kvq_prompt.cuh", "dec_kvq_host.h", "dec_kvq_keep.cuh", "dec_f32x2.cuh", "dec_ops.h"]
+           "dec_kvq_prompt.cuh", "dec_kvq_host.h", "dec_kvq_keep.cuh", "dec_kvq_mass.cuh", "dec_f32x2.cuh", "dec_ops.h"]
 
 
 def nvcc() -> str:

@@ -9,6 +9,7 @@
 
 #include "dec_kvq_host.h"
 #include "dec_kvq_keep.cuh"
+#include "dec_kvq_mass.cuh"
 
 using namespace dec;
 using namespace dec::kvq;
@@ -73,14 +74,14 @@ dec_status dec_kvq_mass(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec
   if (s->batch == 0 || s->n_tokens == 0 || a->max_tokens == 0) return DEC_OK;
   if (dec_status st = check_rows(&a->q, DEC_BF16, "mass: q")) return st;
   if (!a->lse || !a->mass_out || (a->decay != 0.f && !a->mass)) return op_fail(DEC_ERR_ARG, "mass: lse, mass or mass_out missing");
-  if (!aligned4(a->lse) || !aligned4(a->mass) || !aligned4(a->mass_out))
-    return op_fail(DEC_ERR_ARG, "mass: lse, mass and mass_out must be aligned to their type");
+  if (!aligned4(a->lse) || !op_aligned(a->mass) || !op_aligned(a->mass_out))
+    return op_fail(DEC_ERR_ARG, "mass: lse must be aligned to its type, mass and mass_out to 16 bytes");
   const int group = a->n_heads / c->n_kv_heads, max_tokens = std::min(a->max_tokens, s->n_tokens);
-  // (the list of groups, and a sequence's rows in one block, are counted in 32 bits)
+  // (the list of groups, or of tiles and blocks of rows, is counted in 32 bits, and so are a sequence's rows)
   const long long groups = ((long long)s->max_pages * c->page_tokens + s->n_tokens) / kGroup + 1;
   if ((long long)s->n_tokens * a->n_heads >= kAllRows || (long long)s->max_pages * c->page_tokens + s->n_tokens >= INT_MAX - 65536 ||
       (long long)c->n_pages * c->n_kv_heads * (c->page_tokens / kGroup) >= INT_MAX ||
-      groups * c->n_kv_heads * std::min(s->batch, kMaxSeqs) >= (1LL << 32) - 64)
+      groups * c->n_kv_heads * (std::min(s->batch, kMaxSeqs) + (long long)s->n_tokens * group / kTile) >= (1LL << 32) - 64)
     return op_fail(DEC_ERR_UNSUPPORTED, "mass: 2^30 query rows, 2^31 positions or cache groups, or too much work for one call");
   if (dec_status st = op_on_device(c->pages, "cache: pages")) return st;
   const int sms = op_sms();
@@ -103,10 +104,21 @@ dec_status dec_kvq_mass(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec
   p.out = a->mass_out;
   const long long rows = (long long)max_tokens * group;
   const int kind = rows <= 8 ? 0 : rows <= 16 ? 1 : 2;
+  if (kind == 2) p.magic.lo = 0x43004300u;  // (bf16 128, twice)
   const bool big = c->head_dim == 128;
   void (*const k)(const MassParams) = kind == 0   ? (big ? mass_kernel<128, 1> : mass_kernel<64, 1>)
                                       : kind == 1 ? (big ? mass_kernel<128, 2> : mass_kernel<64, 2>)
-                                                  : (big ? mass_many_kernel<128> : mass_many_kernel<64>);
+                                                  : (big ? mass_tile_kernel<128> : mass_tile_kernel<64>);
+  const int smem = kind < 2 ? (big ? StreamCfg<128>::smem() : StreamCfg<64>::smem()) : big ? TileCfg<128>::smem() : TileCfg<64>::smem();
+  const int threads = kind < 2 ? 256 : big ? TileCfg<128>::THREADS : TileCfg<64>::THREADS, ctas = kind < 2 ? 2 * sms : sms;
+  static std::atomic<unsigned long long> done[3][2];
+  int dev = 0;
+  cudaError_t ce = cudaGetDevice(&dev);
+  if (ce == cudaSuccess && !(done[kind][big].load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+    ce = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (ce == cudaSuccess && dev < 64) done[kind][big].fetch_or(1ull << dev, std::memory_order_release);
+  }
+  if (ce != cudaSuccess) return op_cuda(ce, "mass");
   const Seqs all = p.s;
   for (int b = 0; b < s->batch; b += kMaxSeqs) {
     p.s.batch = std::min(kMaxSeqs, s->batch - b);
@@ -114,7 +126,7 @@ dec_status dec_kvq_mass(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec
     p.s.table = all.table + b * all.table_stride;
     if (all.cu) p.s.cu = all.cu + b;
     p.b0 = b;
-    k<<<(unsigned)sms * 2, 256, 0, op_stream(stream)>>>(p);
+    k<<<(unsigned)ctas, (unsigned)threads, smem, op_stream(stream)>>>(p);
     if (dec_status st = launched("mass")) return st;
   }
   return DEC_OK;
@@ -144,17 +156,40 @@ dec_status dec_kvq_heaviest(const dec_kvq_cache* c, const dec_kvq_seqs* s, const
   p.recent = a->recent;
   p.kept = a->kept;
   p.count = a->count;
-  constexpr int kMost = 48 * 1024;
-  p.cached = (int)std::min<long long>(kMost, (long long)s->max_pages * c->page_tokens);
-  static std::atomic<unsigned long long> done{0};
+  // CTAs a list: as many as the SMs hold, each with 1024 positions at least of what the page tables can hold
+  const long long lists = (long long)s->batch * c->n_kv_heads, most = (long long)s->max_pages * c->page_tokens;
+  const int sms = op_sms();
+  if (sms < 1) return op_fail(DEC_ERR_CUDA, "heaviest: no device");
+  int cl = 1;
+  while (cl < 8 && lists * cl * 2 <= sms && most / (cl * 2) >= kKeepThreads) cl *= 2;
+  if (lists * cl > INT_MAX) return op_fail(DEC_ERR_UNSUPPORTED, "heaviest: 2^31 lists");
+  void (*const k)(const KeepParams) = cl == 1   ? heaviest_kernel<1>
+                                      : cl == 2 ? heaviest_kernel<2>
+                                      : cl == 4 ? heaviest_kernel<4>
+                                                : heaviest_kernel<8>;
+  p.cached = (int)std::min<long long>(kKeepCached, (most + cl - 1) / cl + 32);
+  static std::atomic<unsigned long long> done[4];
+  std::atomic<unsigned long long>& set = done[cl == 1 ? 0 : cl == 2 ? 1 : cl == 4 ? 2 : 3];
   int dev = 0;
   cudaError_t ce = cudaGetDevice(&dev);
-  if (ce == cudaSuccess && !(done.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
-    ce = cudaFuncSetAttribute((const void*)heaviest_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost * 4);
-    if (ce == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+  if (ce == cudaSuccess && !(set.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+    ce = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeepCached * 4);
+    if (ce == cudaSuccess && dev < 64) set.fetch_or(1ull << dev, std::memory_order_release);
   }
   if (ce != cudaSuccess) return op_cuda(ce, "heaviest");
-  heaviest_kernel<<<(unsigned)(s->batch * c->n_kv_heads), kKeepThreads, p.cached * 4, op_stream(stream)>>>(p);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(lists * cl));
+  cfg.blockDim = dim3(kKeepThreads);
+  cfg.dynamicSmemBytes = p.cached * 4;
+  cfg.stream = op_stream(stream);
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = cl;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = cl > 1 ? 1 : 0;
+  ce = cudaLaunchKernelEx(&cfg, k, p);
+  if (ce != cudaSuccess) return op_cuda(ce, "heaviest");
   return launched("heaviest");
 }
 

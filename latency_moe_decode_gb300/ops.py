@@ -276,8 +276,8 @@ class KvqCache:
 
     def _mass(self, t: torch.Tensor, name: str) -> int:
         if (t.dtype is not torch.float32 or t.shape != (self.n_pages, self.n_kv_heads, self.page_tokens) or
-                not t.is_contiguous() or t.get_device() != self._index):
-            raise ValueError(f"{name} must be contiguous float32 [{self.n_pages}, {self.n_kv_heads}, {self.page_tokens}] on "
+                not t.is_contiguous() or t.get_device() != self._index or t.data_ptr() % 16):
+            raise ValueError(f"{name} must be contiguous, 16-byte aligned float32 [{self.n_pages}, {self.n_kv_heads}, {self.page_tokens}] on "
                              f"{self.device}")
         return t.data_ptr()
 
