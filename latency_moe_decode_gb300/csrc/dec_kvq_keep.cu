@@ -231,7 +231,7 @@ dec_status dec_kvq_move(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec
   p.parts = (few ? 1 : runs / 2) + (a->mass ? 1 : 0);
   p.splits = 1;
   const long long ctas = (long long)s->batch * c->n_kv_heads * p.parts;
-  if (!p.in_place && !few) p.splits = (int)std::max<long long>(1, std::min<long long>(8 * sms / ctas, a->max_count / 1024));
+  if (!p.in_place && !few) p.splits = (int)std::max<long long>(1, std::min<long long>(8 * sms / ctas, a->max_count / 512));
   if (ctas * p.splits > INT_MAX) return op_fail(DEC_ERR_UNSUPPORTED, "move: too much work for one call");
   void (*const k)(const MoveParams) = few ? (big ? move_kernel<128, 16, 256, 4> : move_kernel<64, 8, 256, 4>)
                                           : (big ? move_kernel<128, 2, 256, 4> : move_kernel<64, 2, 256, 4>);

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kKeepThreads, 1) heaviest_kernel(const KeepPar
   constexpr int T = kKeepThreads, BINS = 2048;
   extern __shared__ uint32_t cache[];
   __shared__ uint32_t hist[3][BINS], part[32];
-  __shared__ uint32_t sh_bin, sh_left;
+  __shared__ uint32_t sh_bin, sh_left, sh_all;
   __shared__ uint2 counts[32], sums[CL];
   const uint32_t rank = CL > 1 ? cluster_rank() : 0;
   const int list = blockIdx.x / CL, b = list / p.c.hkv, h = list - b * p.c.hkv;
@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(kKeepThreads, 1) heaviest_kernel(const KeepPar
   // ---- threshold and how many of its equals belong
   uint32_t need = (uint32_t)(p.budget - p.sinks - p.recent), prefix = 0;
   const bool any = need > 0;
-  for (int d = 0; any && d < 3; ++d) {
+  bool whole = false;  // (all of the last digit's keys belong: no further digit is needed, as a rule after two)
+  for (int d = 0; any && !whole && d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bits = d == 2 ? 10 : 11;
     for (int pos = c0 + tid; pos < c1; pos += T) {
       const uint32_t k = key_of(pos);
@@ -165,10 +166,13 @@ __global__ void __launch_bounds__(kKeepThreads, 1) heaviest_kernel(const KeepPar
       const bool first = need <= before + n0;
       sh_bin = BINS - 1 - 2 * tid - (first ? 0 : 1);
       sh_left = need - before - (first ? 0u : n0);
+      sh_all = first ? n0 : n1;
     }
     __syncthreads();
     prefix = prefix << bits | sh_bin;
     need = sh_left;
+    whole = need == sh_all;
+    if (whole) prefix <<= shift;  // (the least of them)
   }
   // ---- in order
   const int seg = ((to - from + 31) / 32 + 31) / 32 * 32;
@@ -176,8 +180,8 @@ __global__ void __launch_bounds__(kKeepThreads, 1) heaviest_kernel(const KeepPar
   auto classes = [&](int pos, bool& in, bool& tie) {
     const bool mid = pos >= c0 && pos < c1;
     const uint32_t k = any && mid && pos < hi ? key_of(pos) : 0u;
-    in = pos < hi && (!mid || (any && k > prefix));
-    tie = any && mid && pos < hi && k == prefix;
+    in = pos < hi && (!mid || (any && (whole ? k >= prefix : k > prefix)));
+    tie = any && !whole && mid && pos < hi && k == prefix;
   };
   uint32_t ins = 0, ties = 0;
   for (int pos = lo + lane; pos - lane < hi; pos += 32) {

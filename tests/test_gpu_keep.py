@@ -384,3 +384,46 @@ def test_calls_with_work_in_flight_and_from_graphs():
     k4, c4 = other.heaviest(want_m, ln2, t2, 20)
     other.move(k4, c4, t2, mass=want_m)
     assert torch.equal(k4, kept) and torch.equal(want_m, mass)
+
+
+def test_heaviest_of_more_than_a_cta_keeps():
+    """Many lists, one CTA each, of more positions than their keys have room for in shared memory (sequences that share
+    their pages: nothing is written there)."""
+    hkv, page, n, batch, budget = 2, 256, 45001, 90, 3000
+    cache, row = _cache([n], hkv, 64, page)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    mass = torch.rand((cache.n_pages, hkv, page), generator=g, device="cuda")
+    mass[torch.rand(mass.shape, generator=g, device="cuda") < 0.3] = 0.25  # ties at what may be the border
+    lens = [n - 7 * b for b in range(batch)]
+    kept, count = cache.heaviest(mass, _ints(lens), row.expand(batch, -1), budget, sinks=3, recent=50)
+    cache.check()
+    assert (count == budget).all()
+    w = _paged(mass, row, [n], page)[0]
+    for b in (0, 1, 40, 89):
+        assert np.array_equal(kept[b].cpu().numpy(), _heaviest_want(w[:, :lens[b]], lens[b], budget, 3, 50)), b
+
+
+def test_pages_beyond_32_bit_offsets():
+    """A cache of more than 4 GB (and weights of more than 2^31 bytes / 16): the sequence's pages are its last ones."""
+    from latency_moe_decode_gb300 import ops
+    hkv, hd, page, n = 8, 128, 64, 300
+    each = ops.KvqCache(1, hkv, hd, page).page_bytes
+    pages = (2 ** 32 + 2 ** 29) // each + 20
+    cache = ops.KvqCache(pages, hkv, hd, page)
+    table = torch.arange(pages - 1, pages - 7, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    g = torch.Generator().manual_seed(9)
+    k, v, q = _rnd(g, n, hkv, hd), _rnd(g, n, hkv, hd), _rnd(g, n, 2 * hkv, hd)
+    cache.append(k.cuda(), v.cuda(), _ints([0]), table, cu_tokens=_ints([0, n]))
+    small, t2 = _cache([n], hkv, hd, page)
+    small.append(k.cuda(), v.cuda(), _ints([0]), t2, cu_tokens=_ints([0, n]))
+    for c, t in ((cache, table), (small, t2)):
+        m = c.new_mass()
+        for rows in (1, n):  # the kernels for few and for many rows
+            _, lse = c.attention(q[:rows].cuda(), _ints([n - rows]), t, cu_tokens=_ints([0, rows]), max_tokens=rows, return_lse=True)
+            c.attention_mass(q[:rows].cuda(), lse, _ints([n - rows]), t, m, cu_tokens=_ints([0, rows]), max_tokens=rows)
+        kept, count = c.evict(m, _ints([n]), t, 100, sinks=2, recent=9)
+        got = (kept, count, *c.gather(_ints([0]), t, 100, cu_tokens=_ints([0, 100])), torch.from_numpy(_paged(m[t[0].long()], torch.arange(t.shape[1])[None], [n], page)[0]))
+        c.check()
+        if c is cache:
+            want = got
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
