@@ -115,16 +115,27 @@ __global__ void __launch_bounds__(kRowThreads, kRowWarps * 32 / kRowThreads) row
   s.cu = p.cu;
   const int row = me / p.splits, split = me - row * p.splits;
   if (row >= p.n_tokens) return;
-  int j;
-  const int b = kvq::seq_of_warp(s, row, j);
-  if (b < 0 || j >= p.max_tokens) return;
-  const float f = factor_of(p, b), c = f > 0.f ? f : 1.f;  // (greedy: the sum only shows a NaN)
   const char* const base = static_cast<const char*>(p.x) + row * p.stride * (BF16 ? 2 : 4);
   // 16-byte words from the last boundary before the row; the first and the last may hold values beside it
   const int lead = (int)(reinterpret_cast<uintptr_t>(base) & 15u) / (BF16 ? 2 : 4);
   const uint4* const words = reinterpret_cast<const uint4*>(base - lead * (BF16 ? 2 : 4));
   const int n = (p.vocab + lead + E - 1) / E, per = (n + p.splits - 1) / p.splits;
   const int lo = split * per, hi = min(n, lo + per);
+  // the words that lie in the row whole; the next ones are on their way meanwhile
+  const int from = max(lo, lead ? 1 : 0), to = min(hi, (p.vocab + lead) / E);
+  uint4 v[U];
+  auto fetch = [&](int w) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (w + u * 32 < to) v[u] = __ldcs(words + w + u * 32);
+  };
+  int w0 = from + lane;
+  fetch(w0);
+  // (meanwhile the row's sequence)
+  int j;
+  const int b = kvq::seq_of_warp(s, row, j);
+  if (b < 0 || j >= p.max_tokens) return;
+  const float f = factor_of(p, b), c = f > 0.f ? f : 1.f;  // (greedy: the sum only shows a NaN)
   Stat a{-INFINITY, 0.f, 0x7FFFFFFF};
   const uint64_t cc = pair(c, c);
   auto take = [&](const float (&x)[16], int w0) {  // 16 values of the words w0, w0 + 32, ..
@@ -147,16 +158,6 @@ __global__ void __launch_bounds__(kRowThreads, kRowWarps * 32 / kRowThreads) row
     }
     a.l += halves(l2).x + halves(l2).y;
   };
-  // the words that lie in the row whole; the next ones are on their way meanwhile
-  const int from = max(lo, lead ? 1 : 0), to = min(hi, (p.vocab + lead) / E);
-  uint4 v[U];
-  auto fetch = [&](int w) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (w + u * 32 < to) v[u] = __ldcs(words + w + u * 32);
-  };
-  int w0 = from + lane;
-  fetch(w0);
   while (w0 < to) {
     float x[16];
 #pragma unroll
