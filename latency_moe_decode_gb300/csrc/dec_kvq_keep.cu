@@ -98,11 +98,14 @@ dec_status dec_kvq_mass(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec
   p.causal = a->causal != 0;
   p.max_tokens = a->max_tokens;
   p.magic = Magic{0x64006400u, 0x54005400u};
-  p.min_groups = 4;
+  p.min_groups = 1;  // (a warp's, at least: one token on 1 k 4.4 us, with 4 a warp 6.4)
   p.decay = a->decay;
   p.mass = a->mass;
   p.out = a->mass_out;
   const long long rows = (long long)max_tokens * group;
+  // The tile kernel's time grows with every 128 rows, the streaming one's with every 8, and it keeps no more than 16. Streaming
+  // against tile kernel, us (8 KV heads of 128): 8 rows, one sequence on 8 k 6.6 / 11.7, on 64 k 14.0 / 40.4, 16 on 2 k 9.8 / 27.4; 16
+  // rows 8.3 / 12.0, 16.9 / 40.5, 12.0 / 27.3. 8 columns for up to 8 rows against 16: 6.6 / 7.6, 14.0 / 16.7, 9.8 / 11.5.
   const int kind = rows <= 8 ? 0 : rows <= 16 ? 1 : 2;
   if (kind == 2) p.magic.lo = 0x43004300u;  // (bf16 128, twice)
   const bool big = c->head_dim == 128;
@@ -156,7 +159,9 @@ dec_status dec_kvq_heaviest(const dec_kvq_cache* c, const dec_kvq_seqs* s, const
   p.recent = a->recent;
   p.kept = a->kept;
   p.count = a->count;
-  // CTAs a list: as many as the SMs hold, each with 1024 positions at least of what the page tables can hold
+  // CTAs a list: as many as the SMs hold, each with 1024 positions at least of what the page tables can hold. 1, 2, 4, 8 CTAs,
+  // us: 8 lists of 32 k 34.5, 22.0, 15.2, 13.4; of 4 k 8.6, 7.8, 7.8, 9.3; of 1 k 5.0, 6.3, 7.2, 9.1; 32 of 8 k 12.2, 10.5, 9.2,
+  // 28.6 (more than the SMs hold); 128 of 4 k 9.5, 15.5, 28.8, 80.5.
   const long long lists = (long long)s->batch * c->n_kv_heads, most = (long long)s->max_pages * c->page_tokens;
   const int sms = op_sms();
   if (sms < 1) return op_fail(DEC_ERR_CUDA, "heaviest: no device");
@@ -227,15 +232,23 @@ dec_status dec_kvq_move(const dec_kvq_cache* c, const dec_kvq_seqs* s, const dec
   p.mass = a->mass;
   const int runs = 2 * c->head_dim / kBlock, sms = op_sms();
   if (sms < 1) return op_fail(DEC_ERR_CUDA, "move: no device");
-  const bool few = a->max_count <= 128, big = c->head_dim == 128;
-  p.parts = (few ? 1 : runs / 2) + (a->mass ? 1 : 0);
+  // How a list's positions are shared out, in us (8 KV heads of 128). Up to 64 (a path of a tree): a CTA for all 16 runs
+  // against eight with two each: 16 sequences of 16 in place 2.9 / 4.9, of 64 4.9 / 5.1, of 128 7.4 / 5.8. Beyond that, in
+  // place, where a CTA goes through the whole list: one run a CTA of 512 threads, while the SMs hold them all, against
+  // two of 256: one sequence of 8192 29 / 52, of 1024 5.5 / 8.0, four of 2048 19 / 17, 16 of 1024 33 / 21. Elsewhere the list is cut
+  // too, until there are eight CTAs an SM or 128 positions each: one of 8192 whole 45, in 8 12; of 1024 7.4 / 3.7; four of
+  // 2048 15, in 4 12; 16 of 1024 20, in 4 25.
+  const long long lists = (long long)s->batch * c->n_kv_heads;
+  const bool few = a->max_count <= 64, alone = !few && p.in_place && lists * runs <= sms, big = c->head_dim == 128;
+  p.parts = (few ? 1 : alone ? runs : runs / 2) + (a->mass ? 1 : 0);
   p.splits = 1;
-  const long long ctas = (long long)s->batch * c->n_kv_heads * p.parts;
-  if (!p.in_place && !few) p.splits = (int)std::max<long long>(1, std::min<long long>(8 * sms / ctas, a->max_count / 512));
+  const long long ctas = lists * p.parts;
+  if (!p.in_place && !few) p.splits = (int)std::max<long long>(1, std::min<long long>(8 * sms / ctas, a->max_count / 128));
   if (ctas * p.splits > INT_MAX) return op_fail(DEC_ERR_UNSUPPORTED, "move: too much work for one call");
-  void (*const k)(const MoveParams) = few ? (big ? move_kernel<128, 16, 256, 4> : move_kernel<64, 8, 256, 4>)
-                                          : (big ? move_kernel<128, 2, 256, 4> : move_kernel<64, 2, 256, 4>);
-  k<<<(unsigned)(ctas * p.splits), 256, 0, op_stream(stream)>>>(p);
+  void (*const k)(const MoveParams) = few     ? (big ? move_kernel<128, 16, 256, 4> : move_kernel<64, 8, 256, 4>)
+                                      : alone ? (big ? move_kernel<128, 1, 512, 4> : move_kernel<64, 1, 512, 4>)
+                                              : (big ? move_kernel<128, 2, 256, 4> : move_kernel<64, 2, 256, 4>);
+  k<<<(unsigned)(ctas * p.splits), alone ? 512 : 256, 0, op_stream(stream)>>>(p);
   return launched("move");
 }
 

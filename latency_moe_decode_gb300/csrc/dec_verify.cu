@@ -104,7 +104,7 @@ __device__ __forceinline__ Stat merge_lanes(Stat a, int width, float c) {
 // every row once
 
 // Each warp by itself, as many a row as fill the SMs: a CTA a row, or half a row, left some SMs with a wave more than
-// others.
+// others (12.3 us for 464 rows of 32000 fp32; 9.4 so, 6.2 TB/s. bf16 rows go at 3.9: as many exponentials in half the bytes).
 template <bool BF16>
 __global__ void __launch_bounds__(kRowThreads, kRowWarps * 32 / kRowThreads) rows_kernel(const Params p) {
   constexpr int E = BF16 ? 8 : 4, U = 16 / E;  // 16 values a thread at a time
@@ -352,8 +352,10 @@ struct Rows {
 };
 inline int rows_room(int max_tokens) { return (max_tokens + 31) / 32 * 32 + 32; }
 
-// What bounds it: for few sequences latency (bounds, rows, logits, statistics, one pass, its exchange, the id), for many
-// the pass's instructions, some 45 a logit.
+// What bounds it: for few sequences latency (bounds, rows, logits 1.7 us; statistics 1.3; weights and fates 0.8; one pass and its
+// exchange 3 to 4; the id 1), for many the pass's instructions, some 45 a logit, 60 where a refusal's rest is summed as well.
+// A call with rows of 32000 fp32 takes 14 us for one chain of 8, 24 for 64 (59 MB of logits in 9.4; three passes, 134 instructions a
+// logit, took 65), 25 for 16 trees of up to 64 rows in bf16.
 template <bool BF16, int CL>
 __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
   __shared__ Walk w;
@@ -798,9 +800,11 @@ cudaError_t launch(Params& p, cudaStream_t s) {
     if (ce != cudaSuccess) return ce;
   }
   const int sms = op_sms();
-  // CTAs a sequence: as many as the SMs hold, each a share of the vocabulary
+  // CTAs a sequence, each with a share of the vocabulary: as many as the SMs hold, 8 only where they leave a third of them
+  // (clusters of 8 do not fill every part of the chip). 1, 2, 4, 8, us a call (rows of 32000): one sequence 22.8, 16.7, 13.6, 13.1;
+  // 12 25.5, 20.1, 16.9, 16.6; 16 27.5, 20.9, 17.7, 21.1; 36 29.4, 23.2, 20.7, 34.6; 50 33.5, 27.2, 31.1, 46.1; 100 30.7, 33.3, 41.0.
   int cl = 1;
-  while (cl < kMaxCluster && (long long)p.batch * cl * 2 <= sms) cl *= 2;
+  while (cl < kMaxCluster && (long long)p.batch * cl * (cl == 4 ? 3 : 2) <= sms) cl *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(p.batch * cl));
   cfg.blockDim = dim3(kWalkThreads);
@@ -896,7 +900,8 @@ extern "C" dec_status dec_verify_drafts(const dec_verify_drafts_args* a, void* s
   const int sms = op_sms();
   if (sms < 1) return op_fail(DEC_ERR_CUDA, "verify_drafts: no device");
   // Warps a row: as many as the SMs hold at once, or of many rows enough for some turns, each with at least 32 values a
-  // thread.
+  // thread. One warp a row, 4, 8, 16, 31, us a call: 8 rows of 32000 25.2, 15.6, 14.0, 13.2, 13.1; 512 rows 40.2, 25.2, 25.2, 27.2,
+  // 34.6.
   const int each = a->dtype == DEC_BF16 ? 8 : 4, words = (a->vocab + each - 1) / each;
   const long long room = (long long)sms * verify::kRowWarps, rows = std::max(1, a->n_tokens);
   p.splits = (int)std::max<long long>(1, std::min<long long>({verify::kMaxParts, words / (32 / each * 32),
