@@ -104,7 +104,9 @@ __device__ __forceinline__ Stat merge_lanes(Stat a, int width, float c) {
 // every row once
 
 // Each warp by itself, as many a row as fill the SMs: a CTA a row, or half a row, left some SMs with a wave more than
-// others (12.3 us for 464 rows of 32000 fp32; 9.4 so, 6.2 TB/s. bf16 rows go at 3.9: as many exponentials in half the bytes).
+// others (12.3 us for 464 rows of 32000 fp32; 10.0 so, 5.9 TB/s. bf16 rows go at 4.3: as many exponentials in half the bytes).
+// The id of the largest logit is looked for at the end, and only where it counts (greedy rows): in the loop it took
+// half the instructions.
 template <bool BF16>
 __global__ void __launch_bounds__(kRowThreads, kRowWarps * 32 / kRowThreads) rows_kernel(const Params p) {
   constexpr int E = BF16 ? 8 : 4, U = 16 / E;  // 16 values a thread at a time
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowWarps * 32 / kRowThreads) row
   if (b < 0 || j >= p.max_tokens) return;
   const float f = factor_of(p, b), c = f > 0.f ? f : 1.f;  // (greedy: the sum only shows a NaN)
   Stat a{-INFINITY, 0.f, 0x7FFFFFFF};
+  int found = 0;  // the words that the largest came from first
   const uint64_t cc = pair(c, c);
   auto take = [&](const float (&x)[16], int w0) {  // 16 values of the words w0, w0 + 32, ..
     float m = a.m;
@@ -145,9 +148,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowWarps * 32 / kRowThreads) row
     if (m > a.m) {
       a.l *= ex2((a.m - m) * c);
       a.m = m;
-#pragma unroll
-      for (int i = 15; i >= 0; --i)
-        if (x[i] == m) a.id = (w0 + i / E * 32) * E + i % E - lead;
+      found = w0;
     }
     const float z = finite_or_0(m);
     uint64_t l2 = 0;
@@ -158,25 +159,8 @@ __global__ void __launch_bounds__(kRowThreads, kRowWarps * 32 / kRowThreads) row
     }
     a.l += halves(l2).x + halves(l2).y;
   };
-  while (w0 < to) {
-    float x[16];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t q[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-      const bool there = w0 + u * 32 < to;
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float y = BF16 ? __uint_as_float((i & 1) ? q[i / 2] & 0xFFFF0000u : q[i / 2] << 16) : __uint_as_float(q[i % 4]);
-        x[u * E + i] = there ? y : -INFINITY;
-      }
-    }
-    const int at = w0;
-    w0 += U * 32;
-    fetch(w0);
-    take(x, at);
-  }
-  // and the first and the last one, where they do not: a value at a time
-  for (int w = lane == 0 && lead && lo == 0 ? 0 : lane == 1 && hi == n && to < n && (n > 1 || !lead) ? n - 1 : -1; w >= 0; w = -1) {
+  // (the first and the last word, where they do not lie in the row whole: a value at a time, and in the ids' order)
+  auto edge = [&](int w) {
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -184,7 +168,32 @@ __global__ void __launch_bounds__(kRowThreads, kRowWarps * 32 / kRowThreads) row
       x[i] = i < E && id >= 0 && id < p.vocab ? logit<BF16>(base, id) : -INFINITY;
     }
     take(x, w);
+  };
+  if (lane == 0 && lead && lo == 0) edge(0);
+  while (w0 < to) {
+    float x[16];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t q[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        x[u * E + i] = BF16 ? __uint_as_float((i & 1) ? q[i / 2] & 0xFFFF0000u : q[i / 2] << 16) : __uint_as_float(q[i % 4]);
+    }
+    if (w0 - lane + U * 32 > to)  // (the last words)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = w0 + i / E * 32 < to ? x[i] : -INFINITY;
+    const int at = w0;
+    w0 += U * 32;
+    fetch(w0);
+    take(x, at);
   }
+  if (lane == 1 && hi == n && to < n && (n > 1 || !lead)) edge(n - 1);
+  if (f == 0.f && a.m > -INFINITY)  // (only greedy rows need the id)
+#pragma unroll
+    for (int i = 15; i >= 0; --i) {
+      const int id = (found + i / E * 32) * E + i % E - lead;
+      if (id >= 0 && id < p.vocab && logit<BF16>(base, id) == a.m) a.id = id;
+    }
   a = merge_lanes(a, 32, c);
   if (lane == 0) p.stats[(size_t)row * p.width + split] = make_float4(a.m, a.l, __int_as_float(a.id), 0.f);
 }
@@ -354,8 +363,8 @@ inline int rows_room(int max_tokens) { return (max_tokens + 31) / 32 * 32 + 32; 
 
 // What bounds it: for few sequences latency (bounds, rows, logits 1.7 us; statistics 1.3; weights and fates 0.8; one pass and its
 // exchange 3 to 4; the id 1), for many the pass's instructions, some 45 a logit, 60 where a refusal's rest is summed as well.
-// A call with rows of 32000 fp32 takes 14 us for one chain of 8, 24 for 64 (59 MB of logits in 9.4; three passes, 134 instructions a
-// logit, took 65), 25 for 16 trees of up to 64 rows in bf16.
+// A call with rows of 32000 fp32 takes 14 us for one chain of 8, 24 for 64 (59 MB of logits in 10; three passes, 134 instructions a
+// logit, took 65), 24 for 16 trees of up to 64 rows in bf16.
 template <bool BF16, int CL>
 __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
   __shared__ Walk w;

@@ -129,6 +129,24 @@ def test_next_tokens_at_borders(vocab):
     assert log2 > 0 and w.sum() > 0.99
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("vocab", [3, 17, 1000, 32003])
+def test_greedy_ties_wherever_a_row_begins(dtype, vocab):
+    """The first of equal logits, at every offset of a row from 16 bytes: ties with the row's first and last ids, which
+    lie in words that it shares."""
+    from latency_moe_decode_gb300 import ops
+    for off in range(1, 9):
+        pad = torch.zeros(4, vocab + 16, dtype=dtype, device="cuda")
+        x = pad[:, off:off + vocab]
+        x[1, 0], x[1, vocab // 2] = -1.0, 2.0
+        x[1, vocab - 1] = 2.0
+        x[2, vocab - 1] = 1.0
+        x[3, :vocab - 1] = -5.0
+        got = ops.verify_drafts(x, _ints([0] * 4), torch.zeros(4, device="cuda"), _cu([1] * 4), max_tokens=1,
+                                temperature=torch.zeros(4, device="cuda"))
+        assert got.next_tokens.tolist() == [0, vocab // 2, vocab - 1, vocab - 1], off
+
+
 @pytest.mark.parametrize("probs", [True, False])
 def test_tokens_are_distributed_as_the_targets(probs):
     """The property that verification is for: over many sequences the first token that comes out (an accepted draft or
