@@ -58,6 +58,9 @@ struct KeepParams {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// (the two halves apart: a CTA's shared memory may be written or read from elsewhere once it is known to have begun)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -102,6 +105,7 @@ __global__ void __launch_bounds__(kKeepThreads, 1) heaviest_kernel(const KeepPar
     for (int i = rank * T + tid; i < p.budget; i += CL * T) kept[i] = i < len ? i : -1;
     return;
   }
+  if (CL > 1) cluster_arrive();  // (every CTA has begun)
   const int32_t* const table = p.s.table + b * p.s.table_stride;
   auto load = [&](int pos) -> uint32_t {
     const int page = __ldg(table + (pos >> p.c.page_shift));
@@ -121,6 +125,7 @@ __global__ void __launch_bounds__(kKeepThreads, 1) heaviest_kernel(const KeepPar
   for (int pos = c0 + tid; pos < min(c1, from + p.cached); pos += T) cache[pos - from] = load(pos);
   for (int i = tid; i < 3 * BINS; i += T) (&hist[0][0])[i] = 0;
   __syncthreads();
+  if (CL > 1) cluster_wait();
   // ---- threshold and how many of its equals belong
   uint32_t need = (uint32_t)(p.budget - p.sinks - p.recent), prefix = 0;
   const bool any = need > 0;

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(256, 2) mass_kernel(const MassParams p) {
 //  - eight, four for each of two buffers, copy blocks of queries there as they are, with each row's lse and the positions it
 //    sees. (In f16, as the prompt kernel has them, they had to be scaled row by row: 3.7 us before the first
 //    products.) Up to 256 rows stay there for all of a KV head's tiles; more go through the two buffers in turn;
-//  - one thread issues S = K Q^T (128 x 128 x hd), four S buffers in tensor memory;
+//  - one thread issues S = K Q^T (128 x 128 x hd), two S buffers in tensor memory for each of the next two groups;
 //  - two groups of eight take the tiles in turn, one position and half a block's queries a thread: exponentials and their
 //    sum. (With all sixteen on one tile the exponentials' unit stood idle between blocks and tiles, half of the time.)
 // What bounds it: the exponentials, 16 an SM and cycle, 1 k cycles a tile and block (its products take 0.6 k), and what comes
@@ -275,14 +275,14 @@ template <int HD>
 struct TileCfg {
   static constexpr int EW = 16, DW = 4, QW = 8;  // 64 registers each
   static constexpr int THREADS = (EW + DW + QW + 2) * 32;
-  static constexpr int HP = HD / 64, OPERAND = HP * 16384, STAGES = 4, SB = 4;
+  static constexpr int HP = HD / 64, OPERAND = HP * 16384, STAGES = 4;
   static constexpr int RAW1 = code_bytes(HD) + scale_bytes(HD), RAW = kTile / kGroup * RAW1;  // a group's keys, a tile's
   static constexpr int K = 0, Q = 2 * OPERAND, RING = 4 * OPERAND, TABLE = RING + STAGES * RAW;
   static constexpr int smem() { return TABLE + kMaxSeqs * (int)sizeof(SeqWork) + 1024; }
 };
 // A tile, as all roles take it. A place is written again 16 tiles later. The copies have then waited for the decoding and
-// staging warps to be done with the tile 4 back, whose decoding waited for the products of the one 6 back, and those
-// for the sums of the one at most 10 back: only places of that tile and later ones are still read.
+// staging warps to be done with the tile 4 back, whose decoding waited for the products of the one 6 back, and those, like
+// the products before them, for the sums of one at most 5 back: only places of tiles at most 11 back are still read.
 constexpr int kInfos = 16;
 struct TileInfo {
   int pos0, held, len, n, tok0, h;  // first position, positions there are; the sequence's
@@ -292,6 +292,7 @@ struct TileInfo {
 };
 struct TileBars {
   uint64_t raw_full[4], raw_empty[4], k_full[2], k_empty[2], q_full[2], q_empty[2], s_full[4], s_empty[4], info[kInfos];
+  uint64_t half[2][4][4];  // a group's 32 positions: the second half's sums of its tile (four in turn) are there
 };
 struct TileTerms {  // of a staged block's rows
   float off[128];
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(TileCfg<HD>::THREADS, 1) mass_tile_kernel(cons
   __shared__ __align__(16) TileTerms terms[2];
   __shared__ TileInfo infos[kInfos];
   __shared__ uint32_t sh_scan[C::THREADS / 32], tmem_base;
-  __shared__ float halves_sum[2][2][128];
+  __shared__ float halves_sum[2][4][128];
   uint8_t* const smem = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
   SeqWork* const seqs = reinterpret_cast<SeqWork*>(smem + C::TABLE);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -338,11 +339,12 @@ __global__ void __launch_bounds__(TileCfg<HD>::THREADS, 1) mass_tile_kernel(cons
       mbar_init(&bars.q_full[i], C::QW / 2);
       mbar_init(&bars.q_empty[i], C::EW);
     }
-    for (int i = 0; i < C::SB; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&bars.s_full[i], 1);
       mbar_init(&bars.s_empty[i], C::EW / 2);
     }
     for (int i = 0; i < kInfos; ++i) mbar_init(&bars.info[i], 1);
+    for (int i = 0; i < 32; ++i) mbar_init(&bars.half[0][0][0] + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == C::EW + C::DW + C::QW) tmem_alloc(&tmem_base, 512);
@@ -439,30 +441,32 @@ __global__ void __launch_bounds__(TileCfg<HD>::THREADS, 1) mass_tile_kernel(cons
     // ---- products
     if (lane == 0) {
       constexpr uint32_t kId = idesc_bf16_f32(128, 128, false);
-      int n = 0;
+      int n0 = 0, n1 = 0;  // each group's steps: its tiles take its own buffers in turn, so that it waits for each of their phases
       for (const TileInfo* t; (t = next()); ++kt) {
         if (t->fresh) qs.have = 0;
         wait(&bars.k_full[kt & 1], (kt >> 1) & 1);
-        for (int rb = t->rb0; rb < t->nrb; ++rb, ++n) {
+        for (int rb = t->rb0; rb < t->nrb; ++rb) {
+          const int n = kt & 1 ? n1++ : n0++, sb = (kt & 1) * 2 + (n & 1);
           bool staged;
           int nth;
           const int buf = qs.use(*t, rb, staged, nth);
           if (staged) wait(&bars.q_full[buf], nth & 1);
-          if (n >= C::SB) wait(&bars.s_empty[n % C::SB], (n / C::SB - 1) & 1);
+          if (n >= 2) wait(&bars.s_empty[sb], ((n >> 1) - 1) & 1);
           tc_fence_after();
           const uint8_t* const k = smem + C::K + (kt & 1) * C::OPERAND;
           const uint8_t* const q = smem + C::Q + buf * C::OPERAND;
 #pragma unroll
           for (int d = 0; d < HD / 16; ++d) {
             const int at = (d >> 2) * 16384 + (d & 3) * 32;
-            mma_bf16(tmem + n % C::SB * 128, smem_desc_sw128(k + at, 16, 1024), smem_desc_sw128(q + at, 16, 1024), kId,
+            mma_bf16(tmem + sb * 128, smem_desc_sw128(k + at, 16, 1024), smem_desc_sw128(q + at, 16, 1024), kId,
                      d > 0 ? 1u : 0u);
           }
-          mma_commit(&bars.s_full[n % C::SB]);
+          mma_commit(&bars.s_full[sb]);
         }
         mma_commit(&bars.k_empty[kt & 1]);
       }
-      if (n > 0) bar_wait(&bars.s_full[(n - 1) % C::SB], ((n - 1) / C::SB) & 1);
+      if (n0 > 0) bar_wait(&bars.s_full[(n0 - 1) & 1], ((n0 - 1) >> 1) & 1);
+      if (n1 > 0) bar_wait(&bars.s_full[2 + ((n1 - 1) & 1)], ((n1 - 1) >> 1) & 1);
     }
     __syncwarp();
   } else if (warp >= C::EW + C::DW) {
@@ -578,7 +582,6 @@ __global__ void __launch_bounds__(TileCfg<HD>::THREADS, 1) mass_tile_kernel(cons
     const int group = warp >> 3, half = warp >> 2 & 1, r = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * 64;
     const uint64_t factor2 = pair(p.scale, p.scale);
-    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(2 + group * 4 + (warp & 3)) : "memory"); };  // (both halves' warps)
     int n = 0;
     for (const TileInfo* t; (t = next()); ++kt) {
       if (t->fresh) {  // the queries that stayed for the KV head before
@@ -594,21 +597,23 @@ __global__ void __launch_bounds__(TileCfg<HD>::THREADS, 1) mass_tile_kernel(cons
       const bool old = p.decay != 0.f && pos < t->len;
       const float was = half == 0 && vg >= 0 && old ? p.mass[(size_t)vg * kGroup + (pos & 15)] : 0.f;
       uint64_t sum2 = 0;
-      for (int rb = t->rb0; rb < t->nrb; ++rb, ++n) {
+      for (int rb = t->rb0; rb < t->nrb; ++rb) {
         bool staged;
         int nth;
         const int buf = qs.use(*t, rb, staged, nth);
+        if (staged) wait(&bars.q_full[buf], nth & 1);  // (of the other group's tiles too: no phase is passed over)
         if (own) {
+          const int sb = group * 2 + (n & 1);
           const TileTerms& tm = terms[buf];
-          wait(&bars.q_full[buf], nth & 1);
-          wait(&bars.s_full[n % C::SB], (n / C::SB) & 1);
+          wait(&bars.s_full[sb], (n >> 1) & 1);
+          ++n;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int part = half * 2 + c;
             if (tm.some[part] <= t->pos0) continue;  // (no row of it sees the tile)
             float x[32];
-            tmem_ld32(tl + n % C::SB * 128 + c * 32, x);
+            tmem_ld32(tl + sb * 128 + c * 32, x);
             if (end <= tm.all[part]) {
 #pragma unroll
               for (int y = 0; y < 32; y += 4) {
@@ -632,18 +637,25 @@ __global__ void __launch_bounds__(TileCfg<HD>::THREADS, 1) mass_tile_kernel(cons
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars.s_empty[n % C::SB]);
-            if (t->nrb > 2) mbar_arrive_cnt(&bars.q_empty[buf], 2);  // (for the other group too)
-          }
+          if (lane == 0) mbar_arrive(&bars.s_empty[sb]);
         }
+        if (t->nrb > 2 && lane == 0) mbar_arrive(&bars.q_empty[buf]);
       }
       if (!own) continue;
       const float sum = halves(sum2).x + halves(sum2).y;
-      float* const other = halves_sum[group][kt >> 1 & 1] + r;
-      if (half == 1) *other = sum;
-      pair_sync();
-      if (half == 0 && vg >= 0) {
+      // The halves' sums join in shared memory, four tiles of the group in turn: the products of the fourth one on wait
+      // for both halves to be done with the second one on.
+      const int turn = kt >> 1 & 3;
+      uint64_t* const there = &bars.half[group][warp & 3][turn];
+      float* const other = halves_sum[group][turn] + r;
+      if (half == 1) {
+        *other = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(there);
+        continue;
+      }
+      wait(there, kt >> 3 & 1);
+      if (vg >= 0) {
         const float all = sum + *other;
         p.out[(size_t)vg * kGroup + (pos & 15)] = old ? fmaf(p.decay, was, all) : all;
       }

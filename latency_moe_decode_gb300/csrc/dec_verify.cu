@@ -321,6 +321,9 @@ __device__ __forceinline__ Two weight(float x, const RowScale& s, const Two& c, 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// (the two halves apart: a CTA's shared memory may be written from elsewhere once it is known to have begun)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -406,6 +409,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
     }
     return;  // (the same in the whole cluster)
   }
+  if (CL > 1) cluster_arrive();  // (every CTA has begun)
   const float cm = greedy ? 1.f : c32;
   const int width = p.width, group = lane / width;  // (32 / width rows a warp)
   for (int j0 = warp * (32 / width); j0 < n; j0 += kWalkWarps * (32 / width)) {
@@ -438,6 +442,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
       if (j < n) rw.weight[j] = make_float2(v.h, v.l);
     }
   __syncthreads();
+  if (CL > 1) cluster_wait();
   if (rank == 0 && tid == 0) path[0] = 0;
 
   // ---- sums over the vocabulary of what is left at row `node`, in parts: part k of kWalkWarps CL is [k seg, ..)

@@ -28,6 +28,8 @@ MASS = [
     (64, 8, 8, 16, [1, 1], [511, 512], True),
     (64, 8, 2, 64, [70, 1, 257], [17, 255, 0], True),
     (64, 4, 1, 256, [9, 3], [700, 0], False),
+    (128, 8, 2, 16, [300, 7, 64, 1, 150, 33], [50, 700, 0, 129, 400, 1000], True),  # blocks that see some tiles only
+    (64, 16, 1, 64, [130, 40, 2, 0, 65], [3, 1500, 260, 9, 127], True),
 ]
 
 
@@ -427,3 +429,34 @@ def test_pages_beyond_32_bit_offsets():
         if c is cache:
             want = got
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("rows,batch,length", [(1, 16, 8000), (5, 12, 6007), (40, 6, 9001), (150, 3, 20000)])
+def test_many_tiles_a_cta(rows, batch, length):
+    """The kernel for many rows over long stretches of tiles (its rings wrap many times; queries that stay, and blocks in
+    turn), against the one for few rows, a few rows at a time. Both are off the definition by at most what _mass_want
+    allows, so they are off each other by twice that."""
+    hq, hkv, hd = 32, 8, 128
+    lens = [length - 131 * b for b in range(batch)]
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    n = rows * batch
+    cache, table = _cache(lens, hkv, hd, 64)
+    for b in range(batch):
+        k = torch.randn(lens[b], hkv, hd, generator=g, device="cuda").to(BF)
+        cache.append(k, k, _ints([0]), table[b:b + 1], cu_tokens=_ints([0, lens[b]]))
+    q = torch.randn(n, hq, hd, generator=g, device="cuda").to(BF)
+    _, lse = cache.attention(q, _ints(lens), table, cu_tokens=_cu([rows] * batch), max_tokens=rows, causal=False, return_lse=True)
+    was = torch.rand((cache.n_pages, hkv, 64), generator=g, device="cuda")
+    many = cache.attention_mass(q, lse, _ints(lens), table, was, cu_tokens=_cu([rows] * batch), max_tokens=max(rows, 5), causal=False,
+                                out=torch.zeros_like(was))
+    few, step = was.clone(), 4
+    for r0 in range(0, rows, step):
+        m = min(step, rows - r0)
+        pick = torch.cat([torch.arange(b * rows + r0, b * rows + r0 + m) for b in range(batch)]).cuda()
+        cache.attention_mass(q[pick], lse[pick], _ints(lens), table, few, cu_tokens=_cu([m] * batch), max_tokens=m, causal=False)
+    cache.check()
+    # |q| and |k| of 128 normal values: sum |q k| / sqrt(128) below 20 (its mean is 7.2, deviation 0.7), |lse| below 32
+    d = hd * 2.0 ** -23 * 20 + 2.0 ** -14 / hd * 20 * 2.0 ** -9 + 2.0 ** -21 * 21 + 2.0 ** -22 * 32
+    rel = 2 * (d + 2.0 ** -23 * (rows * 4 + 8) + 2.0 ** -22)
+    for a, b in zip(_paged(many, table, lens, 64), _paged(few, table, lens, 64)):
+        assert (np.abs(a - b) <= rel * np.abs(b)).all()
