@@ -460,3 +460,29 @@ def test_many_tiles_a_cta(rows, batch, length):
     rel = 2 * (d + 2.0 ** -23 * (rows * 4 + 8) + 2.0 ** -22)
     for a, b in zip(_paged(many, table, lens, 64), _paged(few, table, lens, 64)):
         assert (np.abs(a - b) <= rel * np.abs(b)).all()
+
+
+def test_more_sequences_than_a_launch_takes():
+    """300 sequences: what the calls give does not depend on how they are launched, nor on the other sequences."""
+    hq, hkv, hd, batch = 8, 2, 64, 300
+    lens = [(37 * b) % 90 for b in range(batch)]
+    g = torch.Generator().manual_seed(8)
+    t = sum(lens) + batch
+    k = _rnd(g, t, hkv, hd).cuda()
+    cache, table = _cache([n + 1 for n in lens], hkv, hd, 16)
+    cache.append(k, k, _ints([0] * batch), table, cu_tokens=_cu([n + 1 for n in lens]))
+    q = _rnd(g, batch, hq, hd).cuda()
+    chain = torch.ones(batch, 1, dtype=torch.int32, device="cuda")  # each row sees itself
+    out, lse = cache.attention(q, _ints(lens), table, return_lse=True)
+    out2, lse2 = cache.attention(q, _ints(lens), table, return_lse=True, tree_mask=chain)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    for most in (1, 8):  # the kernels for few and for many rows
+        whole, parts = cache.new_mass(), cache.new_mass()
+        cache.attention_mass(q, lse, _ints(lens), table, whole, max_tokens=most)
+        for b in (slice(0, 7), slice(7, 290), slice(290, 300)):
+            cache.attention_mass(q[b], lse[b], _ints(lens[b]), table[b].contiguous(), parts, max_tokens=most)
+        assert torch.equal(whole, parts)
+    kept, count = cache.heaviest(whole, _ints(lens), table, 20, recent=3)
+    for b, w in enumerate(_paged(whole, table, lens, 16)):
+        assert np.array_equal(kept[b].cpu().numpy(), _heaviest_want(w, lens[b], 20, 0, 3))
+    cache.check()
