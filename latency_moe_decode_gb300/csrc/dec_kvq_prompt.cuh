@@ -133,16 +133,29 @@ struct Stretch {
 };
 
 // Which of 32 positions a tree's row sees, the first of them the i-th of its sequence's n rows (i < 0: before
-// them; mask: the row's words).
-__device__ __forceinline__ uint32_t tree_bits(const uint32_t* mask, int words, int i, int n) {
-  auto word = [&](int k) {
-    uint32_t w = k >= 0 && k < words && k * 32 < n ? __ldg(mask + k) : 0u;
+// them); word(k): the row's k-th word.
+template <class F>
+__device__ __forceinline__ uint32_t tree_bits(int words, int i, int n, F&& word) {
+  auto at = [&](int k) {
+    const uint32_t w = k >= 0 && k < words && k * 32 < n ? word(k) : 0u;
     return n - k * 32 < 32 && k * 32 < n ? w & ((1u << (n - k * 32)) - 1u) : w;
   };
   if (i <= -32) return 0xFFFFFFFFu;
-  if (i < 0) return word(0) << -i | ((1u << -i) - 1u);
-  return __funnelshift_r(word(i >> 5), word((i >> 5) + 1), i & 31);
+  if (i < 0) return at(0) << -i | ((1u << -i) - 1u);
+  return __funnelshift_r(at(i >> 5), at((i >> 5) + 1), i & 31);
 }
+// Which of a head's runs of values hold a NaN that a tree's row sees (rows: bits of the rows with one, 32 words a run).
+// (Apart: in the kernel's own code it cost every tile some spilled registers, 10 % of the time.)
+static __device__ __noinline__ uint32_t tree_nan_runs(const uint32_t* rows, int runs, const uint32_t* mask, int words, int n) {
+  uint32_t out = 0;
+  for (int k = 0; k < words && k * 32 < n; ++k) {
+    uint32_t w = __ldg(mask + k);
+    if (n - k * 32 < 32) w &= (1u << (n - k * 32)) - 1u;
+    for (int r = 0; r < runs; ++r) out |= (w & rows[r * 32 + k]) != 0 ? 1u << r : 0u;
+  }
+  return out;
+}
+constexpr int kNearWords = 4;  // words of a row that the prompt kernel keeps in shared memory
 
 template <int HD, bool TREE = false>
 __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const AttnParams p) {
@@ -152,7 +165,9 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
   __shared__ uint32_t sh_scan[C::THREADS / 32], tmem_base;
   __shared__ float xm[2][2][128], xl[2][128];  // rows' maxima and sums, of each half
   __shared__ int nan_from[HD / kBlock];  // the first position with a NaN run of values, where rows differ in what they see
-  __shared__ uint32_t nan_rows[TREE ? HD / kBlock : 1][32];  // a tree's rows with one
+  __shared__ uint32_t nan_rows[TREE ? HD / kBlock : 1][32];  // a tree's rows with one, and whether there are any
+  __shared__ int nan_some;
+  __shared__ uint32_t row_mask[TREE ? kNearWords : 1][128];  // the query rows' first words
   uint8_t* const smem = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
   SeqWork* const seqs = reinterpret_cast<SeqWork*>(smem + C::TABLE);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -364,6 +379,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
               if (TREE && bad && pos >= s.smin && pos < s.smax) {
                 const int i = pos - s.smin;
                 if (i < 1024) atomicOr(&nan_rows[HD == 128 ? vg : vg >> 1][i >> 5], 1u << (i & 31));
+                nan_some = 1;
               } else if (bad && pos < s.smax) {
                 atomicMin(&nan_from[HD == 128 ? vg : vg >> 1], pos);
               }
@@ -412,7 +428,13 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
       if (tid < HD / kBlock) nan_from[tid] = 0x7FFFFFFF;
       if constexpr (TREE)
         if (tid < HD / kBlock * 32) nan_rows[tid >> 5][tid & 31] = 0u;
-      const uint32_t* const sees = p.mask + (live ? tok : 0) * p.mask_stride;
+      if (TREE && tid == 0) nan_some = 0;
+      auto mask_word = [&](int k) {
+        if (k < kNearWords) return row_mask[k][r];
+        return __ldg(p.mask + tok * p.mask_stride + k);
+      };
+      if constexpr (TREE)
+        for (int k = half; k < min(p.mask_words, kNearWords); k += 2) row_mask[k][r] = live ? __ldg(p.mask + tok * p.mask_stride + k) : 0u;
       // queries, scaled by a power of two to magnitude 1 .. 2 (f16 then holds bf16 values down to 2^-17
       // of the largest exactly), in the order in which a word of codes gives its values
       float sc;
@@ -467,7 +489,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             if constexpr (TREE) {
-              const uint32_t on = live ? tree_bits(sees, p.mask_words, pos0 + c * 32 - seen, s.sw.n) : 0u;
+              const uint32_t on = live ? tree_bits(p.mask_words, pos0 + c * 32 - seen, s.sw.n, mask_word) : 0u;
 #pragma unroll
               for (int y = 0; y < 32; ++y)
                 if (!(on >> y & 1u)) x[c][y] = -INFINITY;
@@ -535,6 +557,10 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
       const bool cont = s.uid < clo, open = u1 > chi;
       float* const part = p.parts + ((size_t)cta * 2 + (cont ? 0 : 1)) * C::PART;
       const float inv = l == 0.f ? 0.f : 8.0f / l;
+      uint32_t nan_runs = 0;
+      if constexpr (TREE)
+        if (tiles > 0 && nan_some && live)
+          nan_runs = tree_nan_runs(&nan_rows[0][0], HD / kBlock, p.mask + tok * p.mask_stride, p.mask_words, s.sw.n);
 #pragma unroll
       for (int c = 0; c < HD / 64; ++c) {
         float x[32];
@@ -548,12 +574,7 @@ __global__ void __launch_bounds__(PromptCfg<HD>::THREADS, 1) prompt_kernel(const
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           bool nan = tiles > 0 && nan_from[(col >> 4) + (y >> 1)] < seen;  // (a run of 16 values)
-          if constexpr (TREE) {
-            if (tiles > 0 && live)
-              for (int k = 0; k * 32 < s.sw.n && k < 32; ++k)
-                if (const uint32_t w = nan_rows[(col >> 4) + (y >> 1)][k])
-                  nan |= (w & tree_bits(sees, p.mask_words, k * 32, s.sw.n)) != 0;
-          }
+          if constexpr (TREE) nan |= (nan_runs >> ((col >> 4) + (y >> 1)) & 1u) != 0;
           float o[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) o[(k >> 1) + 4 * (k & 1)] = nan ? NAN : x[8 * y + k];
