@@ -22,6 +22,7 @@
 // 180 us. A tile takes 2.6 k cycles, 1 k of them on the tensor cores; softmax is busy for 1.8 k (0.9 k of
 // exponentials in all warps at once), decoding for 2 k; issue slots are 60 % full. Issuing whichever of the
 // next scores and the outputs is ready first changed nothing. A unit's begin and end take 10 k cycles more.
+// With a tree's masks (TREE): 32 trees of 24 to 64 rows on 0.5 k to 4 k 128 us, causal rows alike 122.
 #pragma once
 #include "dec_f32x2.cuh"
 #include "dec_kvq_attn.cuh"

@@ -366,7 +366,7 @@ inline int rows_room(int max_tokens) { return (max_tokens + 31) / 32 * 32 + 32; 
 
 // What bounds it: for few sequences latency (bounds, rows, logits 1.7 us; statistics 1.3; weights and fates 0.8; one pass and its
 // exchange 3 to 4; the id 1), for many the pass's instructions, some 45 a logit, 60 where a refusal's rest is summed as well.
-// A call with rows of 32000 fp32 takes 14 us for one chain of 8, 24 for 64 (59 MB of logits in 10; three passes, 134 instructions a
+// A call with rows of 32000 fp32 takes 14 us for one chain of 8, 25 for 64 (59 MB of logits in 10; three passes, 134 instructions a
 // logit, took 65), 24 for 16 trees of up to 64 rows in bf16.
 template <bool BF16, int CL>
 __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
