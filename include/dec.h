@@ -528,8 +528,9 @@ dec_status dec_draft_tree(const dec_draft_tree_args* args, void* stream);
                 a row whose lse is not finite adds nothing
      max_tokens an upper bound of the rows of one sequence (host); rows beyond it add nothing
    Scores and sums are fp32 (as the attention's: queries enter exactly); no sum's order depends on the call's other
-   sequences, and a call repeated gives the same bits. Bad pages are skipped and recorded in the cache's status. A page
-   that several sequences of the call share is left with the sums of one of them. */
+   sequences, and a call repeated gives the same bits. Bad pages are skipped and recorded in the cache's status. What a page
+   that several sequences of one call share is left with depends on their order, which is not fixed: sequences that share
+   pages take calls of their own, one after the other. */
 typedef struct {
   int32_t n_heads;
   dec_rows q;
