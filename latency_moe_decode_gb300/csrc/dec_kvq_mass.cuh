@@ -21,6 +21,12 @@ struct MassParams : AttnParams {  // (lse is read)
 
 constexpr int kAllRows = 1 << 30;  // (one block of rows: a unit is a sequence's KV head)
 
+// How many positions a sequence has: with its rows' own (causal), but none beyond its page table, where entries are
+// another sequence's, or no table any more. (A tile of 128 positions may pass the table's end; a group of 16 does not.)
+__device__ __forceinline__ int held_of(const MassParams& p, const SeqWork& sw) {
+  return min(max(0, p.causal ? sw.len + sw.n : sw.len), p.s.max_pages << p.c.page_shift);
+}
+
 // A query row's lane share, HD / 4 values from t HD / 4 on (two a word), as the second operand of S^T = K q^T: in
 // the order in which words of codes give values, scaled by a power of two to magnitude 1 .. 2 (as in the
 // attention kernels); returns the factor that makes scores of it, in units of log2.
@@ -140,7 +146,7 @@ __global__ void __launch_bounds__(256, 2) mass_kernel(const MassParams p) {
     const int h = (int)fast_div(f - sw.pre, sw.ng, sw.inv);
     const int g0 = (int)(f - sw.pre) - h * sw.ng, n = min(sw.ng - g0, (int)(hi - f));
     f += n;
-    const int held = max(0, p.causal ? sw.len + sw.n : sw.len);
+    const int held = held_of(p, sw);
     // ---- copies, a chunk at a time
     int ahead = -1, mine = -1;  // groups in the cache of the 32 that the copies, and that the sums are in (-1: none)
     auto fetch = [&](int i) {   // groups i, i + 1
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(TileCfg<HD>::THREADS, 1) mass_tile_kernel(cons
         continue;
       }
       const int h = (int)fast_div(u, sw.ng, sw.inv), first = (int)u - h * sw.ng;
-      const int held = max(0, p.causal ? sw.len + sw.n : sw.len);
+      const int held = held_of(p, sw);
       // up to four of the KV head's tiles at once: lane 8 j + i has the j-th one's group i
       const int most = min(min(4, sw.ng - first), (int)((end - f + sw.nrb - 1) / sw.nrb));
       const int j = lane >> 3, pos = (first + j) * kTile + (lane & 7) * kGroup;
