@@ -71,6 +71,15 @@ __device__ __forceinline__ uint32_t remote(const void* at, uint32_t cta) {  // t
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(cta));
   return a;
 }
+// Pairs there (of a type that lies on 8 bytes, as the accesses ask for).
+__device__ __forceinline__ uint2 get_remote(const uint2* at, uint32_t cta) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(remote(at, cta)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void put_remote(uint2* at, uint32_t cta, uint2 v) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(remote(at, cta)), "r"(v.x), "r"(v.y) : "memory");
+}
 
 // A cluster of CL CTAs per (sequence, KV head), each with a stretch of the positions: the need-th largest weight by
 // its digits (11, 11 and 10 bits of a key that orders as the weights do; histograms are joined by every CTA), then
@@ -83,12 +92,14 @@ template <int CL>
 __global__ void __launch_bounds__(kKeepThreads, 1) heaviest_kernel(const KeepParams p) {
   constexpr int T = kKeepThreads, BINS = 2048;
   extern __shared__ uint32_t cache[];
-  __shared__ uint32_t hist[3][BINS], part[32];
+  __shared__ uint2 bins[3][BINS / 2];  // (two bins each)
+  __shared__ uint32_t part[32];
   __shared__ uint32_t sh_bin, sh_left, sh_all;
   __shared__ uint2 counts[32], sums[CL];
   const uint32_t rank = CL > 1 ? cluster_rank() : 0;
   const int list = blockIdx.x / CL, b = list / p.c.hkv, h = list - b * p.c.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto hist = [&](int d) { return reinterpret_cast<uint32_t*>(bins[d]); };
   auto sync_all = [&]() {
     if (CL > 1) cluster_sync();
     else __syncthreads();
@@ -123,7 +134,7 @@ __global__ void __launch_bounds__(kKeepThreads, 1) heaviest_kernel(const KeepPar
   auto key_of = [&](int pos) { return pos - from < p.cached ? cache[pos - from] : load(pos); };
 #pragma unroll 4
   for (int pos = c0 + tid; pos < min(c1, from + p.cached); pos += T) cache[pos - from] = load(pos);
-  for (int i = tid; i < 3 * BINS; i += T) (&hist[0][0])[i] = 0;
+  for (int i = tid; i < 3 * BINS; i += T) hist(0)[i] = 0;
   __syncthreads();
   if (CL > 1) cluster_wait();
   // ---- threshold and how many of its equals belong
@@ -134,24 +145,23 @@ __global__ void __launch_bounds__(kKeepThreads, 1) heaviest_kernel(const KeepPar
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bits = d == 2 ? 10 : 11;
     for (int pos = c0 + tid; pos < c1; pos += T) {
       const uint32_t k = key_of(pos);
-      if (d == 0 || k >> (shift + bits) == prefix) atomicAdd(&hist[d][(k >> shift) & ((1u << bits) - 1u)], 1u);
+      if (d == 0 || k >> (shift + bits) == prefix) atomicAdd(hist(d) + ((k >> shift) & ((1u << bits) - 1u)), 1u);
     }
     sync_all();
     // from the top: thread i has bins BINS - 1 - 2i and the one below
     uint32_t n0 = 0, n1 = 0;
-    const uint32_t* const at = &hist[d][BINS - 2 - 2 * tid];
+    const uint2* const at = &bins[d][BINS / 2 - 1 - tid];
     if (CL == 1) {
-      n1 = at[0];
-      n0 = at[1];
+      n1 = at->x;
+      n0 = at->y;
     } else {
-      uint32_t lo[CL], hi[CL];
+      uint2 two[CL];
 #pragma unroll
-      for (int i = 0; i < CL; ++i)
-        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(lo[i]), "=r"(hi[i]) : "r"(remote(at, i)) : "memory");
+      for (int i = 0; i < CL; ++i) two[i] = get_remote(at, i);
 #pragma unroll
       for (int i = 0; i < CL; ++i) {
-        n1 += lo[i];
-        n0 += hi[i];
+        n1 += two[i].x;
+        n0 += two[i].y;
       }
     }
     uint32_t x = n0 + n1;
@@ -207,8 +217,7 @@ __global__ void __launch_bounds__(kKeepThreads, 1) heaviest_kernel(const KeepPar
   ties = __reduce_add_sync(0xffffffffu, lane < warp ? mine.y : 0u);
   if (CL > 1) {
     const uint32_t all_in = __reduce_add_sync(0xffffffffu, mine.x), all_ties = __reduce_add_sync(0xffffffffu, mine.y);
-    if (warp == 0 && lane < CL)
-      asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(remote(&sums[rank], lane)), "r"(all_in), "r"(all_ties) : "memory");
+    if (warp == 0 && lane < CL) put_remote(&sums[rank], lane, make_uint2(all_in, all_ties));
     cluster_sync();
 #pragma unroll
     for (int i = 0; i < CL; ++i)
