@@ -649,7 +649,8 @@ dec_status dec_logprobs(const dec_logprobs_args* args, void* stream);
      next_tokens  device int32 [batch] (-1 for a sequence of no rows)
      workspace  16-byte aligned, of dec_verify_drafts_workspace() bytes
    Acceptance is decided on fp32 sums where they leave no doubt, and like the next token on sums of some 36 bits where
-   they do. Probabilities below 2^-120 of the row's largest count as 0. A call repeated gives the same. */
+   they do (temperatures from 1e-37 to 1e30). Probabilities below 2^-120 of the row's largest count as 0. A call
+   repeated gives the same. */
 typedef struct {
   const void* logits;
   dec_dtype dtype;

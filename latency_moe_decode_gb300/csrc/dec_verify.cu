@@ -214,12 +214,13 @@ __device__ __forceinline__ Two plus(const Two& a, const Two& b) {
   const Two y = two_sum(a.h, b.h);
   return renorm(y.h, y.l + (a.l + b.l));  // (the same whichever way round: lanes that exchange halves agree)
 }
+// (__fmul_rn: a product whose remainder is taken must not be fused into a sum that it enters)
 __device__ __forceinline__ Two times(const Two& a, float b) {
-  const float h = a.h * b;
+  const float h = __fmul_rn(a.h, b);
   return Two{h, fmaf(a.h, b, -h) + a.l * b};
 }
 __device__ __forceinline__ Two times(const Two& a, const Two& b) {
-  const float h = a.h * b.h;
+  const float h = __fmul_rn(a.h, b.h);
   return renorm(h, fmaf(a.h, b.h, -h) + fmaf(a.h, b.l, a.l * b.h));
 }
 __device__ __forceinline__ Two minus(const Two& a, const Two& b) { return plus(a, Two{-b.h, -b.l}); }
@@ -255,64 +256,44 @@ __device__ __forceinline__ Two scan_lanes(Two a) {
 }
 __device__ __forceinline__ Two two(float2 f) { return Two{f.x, f.y}; }
 
-// Weights of a row's logits: 2^(c x - M) for a whole number M of 32nds near c m (a row's weights all have the
-// factor 2^(c m - M) beside exp((x - m) / temperature), which no comparison sees).
-// c x is the exact product P + p; with n = round(32 (P - M)) the difference r = P - (M + n / 32) is exact, |r| <= 1/64, and
-// 2^(c x - M) = 2^(n / 32) 2^(r + p). The second factor is 1 + g + .., g = (r + p) ln 2, by its series to the fourth power
-// (a term of 2^-39.5 is left out); only g's first term needs both floats.
+// Weights of a row's logits: 2^(c (x - base) - M) for a whole number M of 32nds near c (m - base) (a row's weights all have the
+// factor 2^(c (m - base) - M) beside exp((x - m) / temperature), which no comparison sees). base is 0, and m where c m passes 256
+// either way: a logit is then within a factor of two of m, so that x - m is exact, or its weight is below 2^-120.
+// c (x - base) is the exact product P + p, p up to 2^-16; with n = round(32 (P - M)) the difference r = P - (M + n / 32) is
+// exact, |r| <= 1/64, and the weight is 2^(n / 32) 2^w with w = r + p. The second factor is 1 + g + .., g = w ln 2, by its series to
+// the fourth power (a term of 2^-39.5 is left out); g's first term needs both floats, and so does the table's entry.
+// Against 64-bit mantissas, at temperatures from 1e-35 to 1e6, weights are within 2^-35.4 of themselves.
 struct RowScale {
-  float m, low, magic, M, kappa;  // (low: weights below some 2^-120 are 0; magic: kMagic - 32 M; kappa: 2^(c m - M))
-  bool far;                       // c m is too large for that, or c too small: weight_far
+  float m, base, low, magic, M, kappa;  // (low: weights below some 2^-120 are 0; magic: kMagic - 32 M; kappa: 2^(c (m - base) - M))
   __device__ __forceinline__ void set(float max, const Two& c) {
     m = max;
     const float n = rintf(c.h * m * 32.f);
-    far = !(fabsf(n) < 2097152.f) || c.h < 1e-30f;  // (2^21)
-    M = n * 0.03125f;
-    magic = kMagic - n;
-    low = m - 120.f / c.h;
-    kappa = far ? 1.f : ex2(fmaf(c.h, m, -M) + c.l * m);
+    const bool near = fabsf(n) < 8192.f;
+    base = near ? 0.f : m;
+    M = near ? n * 0.03125f : 0.f;
+    magic = kMagic - (near ? n : 0.f);
+    low = fmaxf((near ? m : 0.f) - 120.f / c.h, -3.4028235e38f);
+    kappa = near ? ex2(fmaf(c.h, m, -M) + c.l * m) : 1.f;
   }
 };
 // (a whole warp at once: lane i holds 2^(i / 32) in `mine`; not normalised: the second float is up to 2^-14 of the first)
 __device__ __forceinline__ Two weight_raw(float x, const RowScale& s, const Two& c, const float2& mine) {
   constexpr float kH = 0.693147182464599609375f, kL = -1.904654299957767e-9f;  // ln 2
-  const float y = fmaxf(x, s.low);
-  const float P = c.h * y, p = fmaf(c.l, y, fmaf(c.h, y, -P));
+  const float d = x - s.base, y = fmaxf(d, s.low);
+  const float P = __fmul_rn(c.h, y), p = fmaf(c.l, y, fmaf(c.h, y, -P));
   const float t = fmaf(P, 32.f, s.magic), nf = t - kMagic;
   const int n = __float_as_int(t) - __float_as_int(kMagic);
-  const float r = P - fmaf(nf, 0.03125f, s.M);
-  const float gh = r * kH, gl = fmaf(p, kH, fmaf(r, kL, fmaf(r, kH, -gh)));
-  const float q = fmaf(r * r, fmaf(r, fmaf(r, 9.6181291e-3f, 5.5504109e-2f), 0.24022651f), gl);  // ln 2^k / k!
+  const float r = P - fmaf(nf, 0.03125f, s.M), w = r + p;
+  const float gh = __fmul_rn(r, kH), gl = fmaf(p, kH, fmaf(r, kL, fmaf(r, kH, -gh)));
+  const float q = fmaf(w * w, fmaf(w, fmaf(w, 9.6181291e-3f, 5.5504109e-2f), 0.24022651f), gl);  // ln 2^k / k!
   const float th = __shfl_sync(0xffffffffu, mine.x, n), tl = __shfl_sync(0xffffffffu, mine.y, n);
-  const float a = th * gh, h = th + a, e = (a - (h - th)) + fmaf(th, gh, -a);
-  const float up = x > s.low ? __int_as_float(((n & ~31) << 18) + (127 << 23)) : 0.f;
-  return Two{h * up, (fmaf(th, q, tl) + e) * up};
-}
-__device__ __forceinline__ Two weight_near(float x, const RowScale& s, const Two& c, const float2& mine) {
-  const Two v = weight_raw(x, s, c, mine);
-  return renorm(v.h, v.l);
-}
-// exp((x - m) / temperature) where c m passes 2^16 (large logits, temperatures near 0) or c is tiny: from the difference x - m, exact
-// in two floats, in the same way.
-__device__ __noinline__ Two weight_far(float x, float m, Two c, float2 mine) {
-  const Two d = two_sum(x, -m);
-  const float yh = d.h * c.h, yl = fmaf(d.h, c.h, -yh) + fmaf(d.h, c.l, d.l * c.h);
-  const bool none = !(yh > -120.f);  // (NaN: infinity times 0)
-  const float n = rintf((none ? 0.f : yh) * 32.f), r = (none ? 0.f : yh) - n * 0.03125f;
-  constexpr float kH = 0.693147182464599609375f, kL = -1.904654299957767e-9f;
-  const float gh = r * kH, gl = fmaf(none ? 0.f : yl, kH, fmaf(r, kL, fmaf(r, kH, -gh)));
-  const float q = fmaf(r * r, fmaf(r, fmaf(r, 9.6181291e-3f, 5.5504109e-2f), 0.24022651f), gl);
-  const int k = (int)n;
-  const float th = __shfl_sync(0xffffffffu, mine.x, k), tl = __shfl_sync(0xffffffffu, mine.y, k);
-  const float a = th * gh, h = th + a, e = (a - (h - th)) + fmaf(th, gh, -a);
-  const float up = __int_as_float((127 + (k >> 5)) << 23);
-  if (x == m) return Two{1.f, 0.f};
-  if (none || !(x > -INFINITY)) return Two{0.f, 0.f};
-  const Two v = renorm(h, fmaf(th, q, tl) + e);
-  return Two{v.h * up, v.l * up};
+  const float a = __fmul_rn(th, gh), h = th + a, e = (a - (h - th)) + fmaf(th, gh, -a);
+  const float up = d >= s.low ? __int_as_float(((n & ~31) << 18) + (127 << 23)) : 0.f;
+  return Two{h * up, (fmaf(th, q, fmaf(tl, gh, tl)) + e) * up};
 }
 __device__ __forceinline__ Two weight(float x, const RowScale& s, const Two& c, const float2& mine) {
-  return s.far ? weight_far(x, s.m, c, mine) : weight_near(x, s, c, mine);
+  const Two v = weight_raw(x, s, c, mine);
+  return renorm(v.h, v.l);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -384,7 +365,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
   if (!greedy) {
     const float t = p.temperature ? __ldg(p.temperature + b) : 1.f;
     constexpr float kH = 1.44269502162933349609375f, kL = 1.92596299e-8f;  // log2(e)
-    if (t > 1e-30f && t < 1e30f) c = times(Two{kH, kL}, inverse(Two{t, 0.f}));
+    if (t > 1e-37f && t < 1e30f) c = times(Two{kH, kL}, inverse(Two{t, 0.f}));
   }
   const char* const x0 = static_cast<const char*>(p.x);
   auto row_at = [&](int j) -> const void* { return x0 + (first + j) * p.stride * (BF16 ? 2 : 4); };
@@ -432,13 +413,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
     for (int j = tid; j - lane < n; j += kWalkThreads) {
       const int up = j < n ? max(rw.up[j], 0) : 0;
       sc.set(rw.m[up], c);
-      const float x = j < n ? rw.weight[j].x : -INFINITY;
-      const Two near = weight_near(x, sc, c, mine);
-      Two v = near;
-      if (__any_sync(0xffffffffu, sc.far)) {
-        const Two far = weight_far(x, sc.m, c, mine);
-        if (sc.far) v = far;
-      }
+      const Two v = weight(j < n ? rw.weight[j].x : -INFINITY, sc, c, mine);
       if (j < n) rw.weight[j] = make_float2(v.h, v.l);
     }
   __syncthreads();
@@ -601,18 +576,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
     return a;  // (of A, where there is a rest)
   };
   auto settle = [&]() {  // the row's whole sum in both floats
-    if (exact) return;
-    if (sc.far) {
-      const int g = gone, r = rounds;
-      gone = rounds = 0;
-      z = sum_rest();
-      gone = g;
-      rounds = r;
-      exact = true;
-      summed = kNone;
-    } else {
-      sum_whole(std::false_type(), false);
-    }
+    if (!exact) sum_whole(std::false_type(), false);
   };
 
   // ---- As far as the first kernel's sums leave no doubt, every draft's fate is known at once, supposing that its earlier
@@ -704,7 +668,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
           __syncthreads();
         } else {
           Two s{0.f, 0.f};
-          bool direct = rounds > 0 || sc.far;
+          bool direct = rounds > 0;
           if (!direct) {
             const float a = sum_whole(std::true_type(), false);
             s = total();
@@ -741,7 +705,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
   if (good && !greedy) {
     // ---- the next token: the first id up to which what is left sums to more than u times all of it
     if (summed == kNone || (summed == kWhole && gone + rounds > 0) || (summed == kRest && gone + rounds == 0)) {
-      if (rounds == 0 && !sc.far) sum_whole(std::false_type(), true);
+      if (rounds == 0) sum_whole(std::false_type(), true);
       else sum_rest();
     }
     Two all = total();

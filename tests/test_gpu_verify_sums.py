@@ -1,0 +1,83 @@
+"""Verification's sums where they are hardest to hold."""
+import numpy as np
+import pytest
+import torch
+
+import drafts_ref as dr
+from test_gpu_kvq import F32, _cu, _ints
+from test_gpu_verify import _same
+
+pytestmark = pytest.mark.gpu
+
+# temperature, the largest logit
+SCALES = [(1.0, 12.0), (1.0, 300.0), (1.0, -200.0), (0.4, 30.0), (0.05, 30.0), (0.01, 30.0), (0.001, 30.0), (1e-4, 20.0),
+          (1e-6, -5.0), (30.0, 1e4), (1e-3, 1e-3), (1e3, 1e6), (2.5, 1e7), (1e-35, 2e-33)]
+
+
+def _rows(t, top, vocab, seed):
+    """A row of logits at temperature t (fp32): a dozen ids of some weight each, among others of next to none."""
+    r = np.random.default_rng(seed)
+    x = (top - t * (30.0 + 50.0 * r.random(vocab))).astype(np.float32)
+    ids = np.sort(r.choice(vocab, 12, replace=False))
+    x[ids] = (top - t * 4.0 * r.random(12)).astype(np.float32)
+    x[ids[r.integers(12)]] = top
+    x[r.choice(vocab, vocab // 8, replace=False)] = -np.inf
+    x[ids[:2]] = np.float32(top)
+    return x, ids
+
+
+def _steps(v):
+    """The two fp32 numbers beside v, in [0, 1)."""
+    a = np.float32(v)
+    b = np.nextafter(a, np.float32(0.0 if a > v else 1.0))
+    return [float(np.clip(z, 0.0, np.float32(1 - 2.0 ** -24))) for z in (a, b)]
+
+
+@pytest.mark.parametrize("t,top", SCALES)
+@pytest.mark.parametrize("vocab", [64, 5000])
+def test_next_tokens_beside_every_border(t, top, vocab):
+    """Random numbers one fp32 step or less from the borders between ids: sums hold 36 bits at any temperature and
+    wherever the logits lie."""
+    from latency_moe_decode_gb300 import ops
+    t = float(np.float32(t))
+    xs, us = [], []
+    for seed in range(4):
+        x, ids = _rows(t, top, vocab, seed)
+        c = np.cumsum(dr.softmax(x.astype(np.float64), t))
+        for i in ids:
+            for u in _steps(c[i] / c[-1]):
+                xs.append(x)
+                us.append(u)
+    n = len(us)
+    x, u, tt = torch.from_numpy(np.stack(xs)), torch.tensor(us, dtype=F32), torch.full((n,), t)
+    got = ops.verify_drafts(x.cuda(), _ints([0] * n), u.cuda(), _cu([1] * n), temperature=tt.cuda(), max_tokens=1)
+    _same(got, x, torch.zeros(n, dtype=torch.int32), u, [[-1]] * n, tt, None)
+
+
+@pytest.mark.parametrize("t,top", SCALES)
+@pytest.mark.parametrize("probs", [True, False])
+def test_acceptance_beside_the_border(t, top, probs):
+    """The same of acceptances: random numbers one fp32 step or less from p / q."""
+    from latency_moe_decode_gb300 import ops
+    t, vocab = float(np.float32(t)), 777
+    xs, us, tok, qs = [], [], [], []
+    r = np.random.default_rng(9)
+    for seed in range(4):
+        x, ids = _rows(t, top, vocab, seed)
+        p = dr.softmax(x.astype(np.float64), t)
+        for i in ids[p[ids] > 0]:
+            q = np.float32(p * np.exp(0.3 * r.standard_normal(vocab)))
+            q[i] = np.float32(min(1.0, p[i] * (1.0 + r.random())))
+            for u in _steps(p[i] / float(q[i]) if probs else p[i]):
+                xs += [x, x]
+                us += [0.4, u]
+                tok += [0, i]
+                qs += [q, q]
+    n = len(us) // 2
+    x, u, tt = torch.from_numpy(np.stack(xs)), torch.tensor(us, dtype=F32), torch.full((n,), t)
+    q = torch.from_numpy(np.stack(qs)) if probs else None
+    tok = torch.tensor(tok, dtype=torch.int32)
+    got = ops.verify_drafts(x.cuda(), tok.cuda(), u.cuda(), _cu([2] * n), temperature=tt.cuda(), max_tokens=2,
+                            draft_probs=None if q is None else q.cuda())
+    _same(got, x, tok, u, [[-1, 0]] * n, tt, q)
+    assert len(set(got.count.tolist())) == 2
