@@ -648,6 +648,7 @@ dec_status dec_logprobs(const dec_logprobs_args* args, void* stream);
      count      device int32 [batch]: how many (1 + the accepted drafts; 0 for a sequence of no rows)
      next_tokens  device int32 [batch] (-1 for a sequence of no rows)
      workspace  16-byte aligned, of dec_verify_drafts_workspace() bytes
+   More than 2^24 ids or 2^26 rows are DEC_ERR_UNSUPPORTED.
    Acceptance is decided on fp32 sums where they leave no doubt, and like the next token on sums of some 36 bits where
    they do (temperatures from 1e-37 to 1e30). Probabilities below 2^-120 of the row's largest count as 0. A call
    repeated gives the same. */

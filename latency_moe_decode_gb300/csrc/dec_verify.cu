@@ -33,8 +33,15 @@ constexpr int kWalkWarps = kWalkThreads / 32;
 constexpr int kMaxParts = 32;  // of a row
 constexpr int kRowWarps = 32;   // of the first kernel, an SM
 constexpr int kMaxCluster = 8;
-// What the first kernel's sums are trusted to: chains of at most a few hundred additions a thread, each off by 2^-24.
-constexpr float kTrust = 0x1p-15f;
+// What the first kernel's sums are trusted to, relative to themselves, where a thread makes `steps` of 16 values and a sequence
+// has up to `rows` drafts; in units of 2^-24, all of one sign. A step: one addition, and where the maximum rises a product with
+// an exponential (2^-22, and its argument's roundings): 8. Besides: a term's exponential 4, its argument's roundings and those of
+// log2(e) / temperature 70 (of an exponent of -y they are some 3 y units, and terms of 2^-y weigh no more than y <= 24 allows),
+// a step's own additions 10, merges of lanes and parts 100, the row's factor and the comparison's products 15; and refused
+// siblings' weights one an addition. 2^-15 covers the common shapes (32000 ids in 10 parts: 8 steps).
+inline float trust_of(long long steps, int rows) {
+  return std::max(0x1p-15f, (float)(8 * steps + 200 + rows) * 0x1p-24f);
+}
 constexpr float kMagic = 12582912.f;  // 1.5 x 2^23: adding it leaves whole numbers in the low mantissa bits
 
 struct Table {
@@ -47,6 +54,7 @@ struct Params {
   const float* probs;
   int vocab, batch, n_tokens, max_tokens;
   int splits, width;  // warps a row (and the next power of two)
+  float trust;        // of their sums
   const int32_t *cu, *tokens, *parents;
   const float *uniforms, *temperature;
   int32_t *path, *count, *next;
@@ -612,7 +620,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
       sc.set(rw.m[up], c);
       const float s0 = rw.l[up] * sc.kappa, lhs = rw.u[j] * rw.q[j] * (s0 - before), v = rw.weight[j].x;
       take = lhs < v;
-      open = fabsf(lhs - v) <= kTrust * fmaxf(s0 * rw.u[j] * rw.q[j], v);
+      open = fabsf(lhs - v) <= p.trust * fmaxf(s0 * rw.u[j] * rw.q[j], v);
     }
     if (take || open) atomicMin(&chosen[up], 2 * j + open);
   }
@@ -651,7 +659,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
       if (rounds == 0) {
         const float s0 = rw.l[node] * sc.kappa, lhs = u * q * (s0 - rest.h);
         take = lhs < wd.h;
-        if (fabsf(lhs - wd.h) <= kTrust * fmaxf(s0 * u * q, wd.h)) {
+        if (fabsf(lhs - wd.h) <= p.trust * fmaxf(s0 * u * q, wd.h)) {
           settle();
           take = above(wd, times(times(minus(z, rest), q), u));
         }
@@ -848,7 +856,7 @@ extern "C" dec_status dec_verify_drafts(const dec_verify_drafts_args* a, void* s
     return op_fail(DEC_ERR_ARG, "verify_drafts: logits, tokens or uniforms missing");
   if (reinterpret_cast<uintptr_t>(a->logits) % (a->dtype == DEC_BF16 ? 2 : 4) || reinterpret_cast<uintptr_t>(a->draft_probs) % 4)
     return op_fail(DEC_ERR_ARG, "verify_drafts: logits and draft_probs must be aligned to their types");
-  // (what kTrust says of the rows' sums holds up to here)
+  // (ids, rows' parts and CTAs are counted in 32 bits, up to a step past the last)
   if (a->vocab > (1 << 24) || a->n_tokens > INT_MAX / verify::kMaxParts || a->batch > INT_MAX / verify::kMaxCluster ||
       (long long)a->batch * a->max_tokens > (1LL << 40))
     return op_fail(DEC_ERR_UNSUPPORTED, "verify_drafts: too many rows, ids or sequences");
@@ -886,6 +894,8 @@ extern "C" dec_status dec_verify_drafts(const dec_verify_drafts_args* a, void* s
                                                               rows * 2 <= room ? room / rows : (4 * room + rows - 1) / rows}));
   p.width = 1;
   while (p.width < p.splits) p.width *= 2;
+  const long long per = (words + 1 + p.splits - 1) / p.splits, step = 32 * 16 / each;  // (a part's words, and a step's)
+  p.trust = verify::trust_of((per + step - 1) / step + 2, a->max_tokens);
   const cudaError_t ce = a->dtype == DEC_BF16 ? verify::launch<true>(p, op_stream(stream)) : verify::launch<false>(p, op_stream(stream));
   return ce == cudaSuccess ? DEC_OK : op_cuda(ce, "verify_drafts");
 }

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import drafts_ref as dr
-from test_gpu_kvq import F32, _cu, _ints
+from test_gpu_kvq import BF, F32, _cu, _ints
 from test_gpu_verify import _same
 
 pytestmark = pytest.mark.gpu
@@ -81,3 +81,30 @@ def test_acceptance_beside_the_border(t, top, probs):
                             draft_probs=None if q is None else q.cuda())
     _same(got, x, tok, u, [[-1, 0]] * n, tt, q)
     assert len(set(got.count.tolist())) == 2
+
+
+def test_acceptance_after_long_chains_of_additions():
+    """2^24 ids, in the few parts that many rows get: 256 ids of one weight, where the parts' lanes begin, and behind them
+    weights that are lost one by one when they are added in fp32 (16 of them are less than half a step of 1). The
+    draft is one of the 256, its random number 2^-13 from p each way; the sums that lose the others are 2^-12 short."""
+    from latency_moe_decode_gb300 import ops
+    vocab, batch = 1 << 24, 1217
+    row = torch.full((vocab,), -19.5, dtype=BF)
+    ids = (torch.arange(8)[:, None] * (vocab // 8) + 8 * torch.arange(32)).flatten()
+    row[ids] = 0.0
+    w = torch.exp(row.double())
+    z = w.sum().item()
+    d = int(ids[100])
+    assert 16 * float(w[1]) < 2.0 ** -24 and z > 256.05
+    x = row.cuda().expand(2 * batch, vocab)
+    up = torch.tensor([(1 + 2.0 ** -13) / z if b % 2 else (1 - 2.0 ** -13) / z for b in range(batch)])
+    u = torch.stack([torch.full((batch,), 0.3), up], 1).flatten()
+    tok = torch.tensor([0, d] * batch, dtype=torch.int32)
+    got = ops.verify_drafts(x, tok.cuda(), u.cuda(), _cu([2] * batch), max_tokens=2)
+    want = [1 if b % 2 else 2 for b in range(batch)]
+    assert got.count.tolist() == want
+    for b in (0, 1):
+        c = torch.cumsum(w if b == 0 else torch.where(torch.arange(vocab) == d, 0.0, w), 0)
+        at = int(torch.searchsorted(c, float(u[0]) * c[-1].item(), right=True))
+        assert abs(c[at].item() / c[-1].item() - 0.3) > 2.0 ** -20
+        assert set(got.next_tokens[b::2].tolist()) == {at}
