@@ -326,8 +326,9 @@ __device__ __forceinline__ void put_remote(float2* at, uint32_t cta, float2 v) {
 }
 
 constexpr int kParts = kWalkWarps * kMaxCluster;
+constexpr float kBeside = 0x1p-19f;  // ids whose weight is this near to q Z count as beside the border (twice what the sums are off by, or more)
 struct Walk {
-  float2 sums[2][3][kParts];  // the parts' sums, of all CTAs (two passes' in turn)
+  float2 sums[2][4][kParts];  // the parts' sums, of all CTAs (two passes' in turn)
   float2 scan[kWalkWarps];
   int found, last;
 };
@@ -457,19 +458,18 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
       if (rw.gone[k] == i) v = Two{0.f, 0.f};
     return v;
   };
-  // up to three sums of this warp's part to every CTA; then all parts' are in out[0 .. 2]
-  auto exchange = [&](const Two& a0, const Two& a1, const Two& a2, int sums) {
+  // sums of this warp's part, one or four, to every CTA; then all parts' are in out[0 ..]
+  auto exchange = [&](const Two (&own)[4], int sums) {
     float2(*const out)[kParts] = w.sums[pass & 1];
-    const Two mine3[3] = {a0, a1, a2};
     if (CL > 1) {
 #pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (k < sums && lane < CL) put_remote(&out[k][me], lane, make_float2(mine3[k].h, mine3[k].l));
+      for (int k = 0; k < 4; ++k)
+        if (k < sums && lane < CL) put_remote(&out[k][me], lane, make_float2(own[k].h, own[k].l));
       cluster_sync();
     } else {
 #pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (k < sums && lane == 0) out[k][me] = make_float2(mine3[k].h, mine3[k].l);
+      for (int k = 0; k < 4; ++k)
+        if (k < sums && lane == 0) out[k][me] = make_float2(own[k].h, own[k].l);
       __syncthreads();
     }
     ++pass;
@@ -493,17 +493,20 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
       }
     }
     const float2* const out = w.sums[pass & 1][0];
-    exchange(sum_lanes(renorm(s.h, s.l)), s, s, 1);
+    exchange({sum_lanes(renorm(s.h, s.l))}, 1);
 #pragma unroll
     for (int k = 0; k < per; ++k) part[k] = read(out, k);
     summed = kRest;
     return total();
   };
   // The row's whole sum Z, part by part; with REST also what one refusal leaves: sums A of weights and B of draft
-  // probabilities over the ids where w > q Z, which A - B Z are (the first kernel's Z tells which: an id at which it is
-  // wrong has next to nothing left). A lane's sums are kept as multiples of a power of two, which add exactly, and
-  // remainders.
+  // probabilities over the ids where w > q Z, which A - B Z are. The first kernel's Z tells which. An id for which it is
+  // wrong lies within that Z's own error of the border, and A - B Z is off by q times that error: so the draft probabilities
+  // near the border are summed as well, and where they make more than 2^-34 of A of it, `doubt` (the draft model is all but the
+  // target; of other rows some one in a thousand). A lane's sums are kept as multiples of a power of two, which add exactly,
+  // and remainders.
   // (without_gone: refused drafts' tokens count nothing)
+  bool doubt = false;
   auto sum_whole = [&](auto with_rest, bool without_gone) {
     constexpr bool REST = decltype(with_rest)::value;
     constexpr int U = REST ? 4 : 8;
@@ -514,6 +517,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
     const float most = fminf((seg / 32 + 1) * 1.03f, z0 * 1.01f);
     const float cut = kMagic * __int_as_float((__float_as_int(most) & 0x7F800000) - (22 << 23));
     Two sz{0.f, 0.f}, sa{0.f, 0.f}, sb{0.f, 0.f};
+    float beside = 0.f;  // draft probabilities near the border
     bool some_gone = false;
     if (!REST && without_gone) {
       for (int k = lane; k < gone; k += 32) some_gone |= rw.gone[k] >= lo && rw.gone[k] < hi;
@@ -551,8 +555,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
         sz.h += k;
         sz.l += d;
         if (REST) {
-          const bool on = v.h + v.l > r[u] * z0;
-          const float kq = (r[u] + cut) - cut;
+          const float bound = r[u] * z0, over = (v.h + v.l) - bound, kq = (r[u] + cut) - cut;
+          const bool on = over > 0.f;
+          beside += fabsf(over) <= kBeside * bound ? r[u] : 0.f;
           sa.h += on ? k : 0.f;
           sa.l += on ? d : 0.f;
           sb.h += on ? kq : 0.f;
@@ -561,7 +566,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
       }
     }
     const float2(*const out)[kParts] = w.sums[pass & 1];
-    exchange(sum_lanes(renorm(sz.h, sz.l)), sum_lanes(renorm(sa.h, sa.l)), sum_lanes(renorm(sb.h, sb.l)), REST ? 3 : 1);
+    if (REST) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) beside += __shfl_xor_sync(0xffffffffu, beside, o);
+      exchange({sum_lanes(renorm(sz.h, sz.l)), sum_lanes(renorm(sa.h, sa.l)), sum_lanes(renorm(sb.h, sb.l)), Two{beside, 0.f}}, 4);
+    } else {
+      exchange({sum_lanes(renorm(sz.h, sz.l))}, 1);
+    }
 #pragma unroll
     for (int k = 0; k < per; ++k) part[k] = read(out[0], k);
     Two all = total();
@@ -572,14 +583,22 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
     summed = REST || (without_gone && gone > 0) ? kRest : kWhole;
     float a = 0.f;
     if (REST) {
+      beside = 0.f;
 #pragma unroll
       for (int k = 0; k < per; ++k) {
         const Two A = read(out[1], k);
         a += A.h;
+        beside += read(out[3], k).h;
         part[k] = less(A, times(z, read(out[2], k)));
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+      for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        beside += __shfl_xor_sync(0xffffffffu, beside, o);
+      }
+      // (the error of the first kernel's Z, and the comparison's roundings)
+      const float off = fabsf((z.h - z0) + z.l) + 0x1p-23f * z0;
+      doubt = off > 0.5f * kBeside * z0 || beside * off > 0x1p-34f * a;
     }
     return a;  // (of A, where there is a rest)
   };
@@ -680,7 +699,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
           if (!direct) {
             const float a = sum_whole(std::true_type(), false);
             s = total();
-            direct = s.h < 0x1p-12f * a;  // (p is all but q: which ids have something left is decided one by one)
+            direct = doubt || s.h < 0x1p-12f * a;  // (p is all but q: which ids have something left is decided one by one)
           } else {
             settle();
           }

@@ -108,3 +108,40 @@ def test_acceptance_after_long_chains_of_additions():
         at = int(torch.searchsorted(c, float(u[0]) * c[-1].item(), right=True))
         assert abs(c[at].item() / c[-1].item() - 0.3) > 2.0 ** -20
         assert set(got.next_tokens[b::2].tolist()) == {at}
+
+
+@pytest.mark.parametrize("vocab", [900, 32000])
+def test_drafts_from_all_but_the_target(vocab):
+    """Draft probabilities that differ from the target's by an fp32 step or less, but for the refused draft and one
+    other id (2^-9 of the sum): what is left of the other ids is 2^-24 of the sum, and whether an id has something left
+    must not go by sums that are off by as much. Random numbers a tenth beside the border that they make; the id that
+    comes out holds them within 2^-26 (a weight's 2^-36, over the 2^-9 that are left, and what roundings add)."""
+    from latency_moe_decode_gb300 import ops
+    xs, us, tok, qs, lefts = [], [], [], [], []
+    for seed, step in enumerate([0.0, 2.0 ** -24, -2.0 ** -24, 2.0 ** -23, -2.0 ** -23, -2.0 ** -22] * 6):
+        r = np.random.default_rng(seed)
+        x = (1.5 * r.standard_normal(vocab)).astype(np.float32)
+        a, d = vocab // 2 + seed, vocab // 3
+        x[a] = x[d] = np.float32(np.log(np.exp(x.astype(np.float64)).sum() * 0.02))
+        p = dr.softmax(x.astype(np.float64), 1.0)
+        q = (p * (1 + step)).astype(np.float32)
+        q[a], q[d] = np.float32(p[a] - 2.0 ** -9), np.float32(4 * p[d])
+        left = np.maximum(p - q.astype(np.float64), 0)
+        edge = left[:a].sum() / left.sum()
+        for u0 in (0.9 * edge, 1.1 * edge):
+            xs += [x, x]
+            us += [u0, 0.9]
+            tok += [0, d]
+            qs += [q, q]
+            lefts.append(left)
+    n = len(us) // 2
+    x, u, q = torch.from_numpy(np.stack(xs)), torch.tensor(us, dtype=F32), torch.from_numpy(np.stack(qs))
+    got = ops.verify_drafts(x.cuda(), _ints(tok), u.cuda(), _cu([2] * n), max_tokens=2, draft_probs=q.cuda())
+    assert got.count.tolist() == [1] * n
+    far = []
+    for b, i in enumerate(got.next_tokens.tolist()):
+        c = np.cumsum(lefts[b]) / lefts[b].sum()
+        want = float(u[2 * b])
+        assert lefts[b][i] > 0
+        far.append(max((c[i - 1] if i else 0.0) - want, want - c[i], 0.0))
+    assert max(far) <= 2.0 ** -26, (np.log2(max(far)), far)
