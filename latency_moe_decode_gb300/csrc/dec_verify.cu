@@ -326,6 +326,7 @@ __device__ __forceinline__ void put_remote(float2* at, uint32_t cta, float2 v) {
 }
 
 constexpr int kParts = kWalkWarps * kMaxCluster;
+constexpr int kChain = 64;  // values that a lane adds up in one go
 constexpr float kBeside = 0x1p-19f;  // ids whose weight is this near to q Z count as beside the border (twice what the sums are off by, or more)
 struct Walk {
   float2 sums[2][4][kParts];  // the parts' sums, of all CTAs (two passes' in turn)
@@ -504,7 +505,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
   // wrong lies within that Z's own error of the border, and A - B Z is off by q times that error: so the draft probabilities
   // near the border are summed as well, and where they make more than 2^-34 of A of it, `doubt` (the draft model is all but the
   // target; of other rows some one in a thousand). A lane's sums are kept as multiples of a power of two, which add exactly,
-  // and remainders.
+  // and remainders, in chains: remainders that are all alike round alike, and are off by n^2 2^-48 of the sum after n of them
+  // (64: 2^-36; the 32768 that a lane has of 2^24 ids: 2^-18).
   // (without_gone: refused drafts' tokens count nothing)
   bool doubt = false;
   auto sum_whole = [&](auto with_rest, bool without_gone) {
@@ -513,10 +515,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
     const void* const row = row_at(node);
     const float* const qrow = REST ? p.probs + (first + node) * p.prob_stride : nullptr;
     const float z0 = rw.l[node] * sc.kappa;
-    // (a lane's sum is below twice the power of two in `most`: multiples of 2^-22 of that add exactly)
-    const float most = fminf((seg / 32 + 1) * 1.03f, z0 * 1.01f);
+    // (a chain's sum is below twice the power of two in `most`: multiples of 2^-22 of that add exactly)
+    const float most = fminf(min(seg / 32 + 1, kChain) * 1.03f, z0 * 1.01f);
     const float cut = kMagic * __int_as_float((__float_as_int(most) & 0x7F800000) - (22 << 23));
-    Two sz{0.f, 0.f}, sa{0.f, 0.f}, sb{0.f, 0.f};
+    Two sz{0.f, 0.f}, sa{0.f, 0.f}, sb{0.f, 0.f};           // a lane's chain
+    Two whole{0.f, 0.f}, above_q{0.f, 0.f}, of_q{0.f, 0.f};  // its sums
     float beside = 0.f;  // draft probabilities near the border
     bool some_gone = false;
     if (!REST && without_gone) {
@@ -530,6 +533,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
         const int i = i0 + u * 32 + lane;
         x[u] = i < hi ? logit<BF16>(row, i) : -INFINITY;
         if (REST) q[u] = i < hi ? __ldg(qrow + i) : 0.f;
+      }
+    };
+    auto fold = [&]() {
+      whole = plus(whole, renorm(sz.h, sz.l));
+      sz = Two{0.f, 0.f};
+      if (REST) {
+        above_q = plus(above_q, renorm(sa.h, sa.l));
+        of_q = plus(of_q, renorm(sb.h, sb.l));
+        sa = sb = Two{0.f, 0.f};
       }
     };
     fetch(lo);
@@ -564,14 +576,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
           sb.l += on ? r[u] - kq : 0.f;
         }
       }
+      if ((i0 - lo) % (32 * kChain) == 32 * (kChain - U)) fold();
     }
+    fold();
     const float2(*const out)[kParts] = w.sums[pass & 1];
     if (REST) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) beside += __shfl_xor_sync(0xffffffffu, beside, o);
-      exchange({sum_lanes(renorm(sz.h, sz.l)), sum_lanes(renorm(sa.h, sa.l)), sum_lanes(renorm(sb.h, sb.l)), Two{beside, 0.f}}, 4);
+      exchange({sum_lanes(whole), sum_lanes(above_q), sum_lanes(of_q), Two{beside, 0.f}}, 4);
     } else {
-      exchange({sum_lanes(renorm(sz.h, sz.l))}, 1);
+      exchange({sum_lanes(whole)}, 1);
     }
 #pragma unroll
     for (int k = 0; k < per; ++k) part[k] = read(out[0], k);

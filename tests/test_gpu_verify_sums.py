@@ -145,3 +145,29 @@ def test_drafts_from_all_but_the_target(vocab):
         assert lefts[b][i] > 0
         far.append(max((c[i - 1] if i else 0.0) - want, want - c[i], 0.0))
     assert max(far) <= 2.0 ** -26, (np.log2(max(far)), far)
+
+
+def test_sums_over_many_equal_weights():
+    """2^24 ids of one weight that is no whole power of two: a random number half an id's share from the borders picks
+    that id. (A lane's remainders, all alike, round alike: in one chain they are off by 2^-20 of the sum and more.)"""
+    from latency_moe_decode_gb300 import ops
+    vocab, batch = 1 << 24, 100
+    at = torch.from_numpy(np.sort(np.random.default_rng(0).choice(vocab // 2, batch, replace=False)))
+    for value, t in ((0.3, 1.0), (-7.7, 1.0), (0.123, 0.9)):
+        row = torch.full((vocab,), value, device="cuda")
+        u = ((at.double() + 0.5) / vocab).to(F32)
+        assert torch.equal(u.double() * vocab, at + 0.5)
+        got = ops.verify_drafts(row.expand(batch, vocab), _ints([0] * batch), u.cuda(), _cu([1] * batch), max_tokens=1,
+                                temperature=torch.full((batch,), t).cuda())
+        assert got.next_tokens.tolist() == at.tolist()
+        # behind a refused draft, the first id, where all of the draft probability lies: the others are left
+        u2 = torch.stack([u, torch.full((batch,), 0.5)], 1).flatten()
+        q = torch.zeros(vocab, device="cuda")
+        q[:1] = 1.0
+        got = ops.verify_drafts(row.expand(2 * batch, vocab), _ints([0] * 2 * batch), u2.cuda(), _cu([2] * batch),
+                                draft_probs=q.expand(2 * batch, vocab), max_tokens=2, temperature=torch.full((batch,), t).cuda())
+        assert got.count.tolist() == [1] * batch
+        for i, v in zip(got.next_tokens.tolist(), u.tolist()):
+            want = (vocab - 1) * v  # (in ids; exact)
+            if abs(want - round(want)) > 0.1:
+                assert i == 1 + int(want)
