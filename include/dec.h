@@ -522,15 +522,20 @@ dec_status dec_draft_tree(const dec_draft_tree_args* args, void* stream);
    (causal and lengths as in dec_kvq_attention) and every KV head h
      mass_out[p] = decay * mass[p] + sum over the rows that attend to p and the heads of h's group of exp(scale q.k - lse)
    where mass and mass_out are fp32 [n_pages][n_kv_heads][page_tokens], 16-byte aligned, laid out as the cache's pages
-   (mass_out may be mass, or share nothing with it). Positions that the call's rows stand at (causal) have had nothing before, and where decay is 0 nothing is
-   read. Positions that no row could attend to are left as they are.
+   (mass_out may be mass, or share nothing with it). Positions that the call's rows stand at (causal) have had nothing
+   before, and where decay is 0 nothing is read. Positions that no row could attend to are left as they are.
      q          bf16 rows of n_heads heads, lse device fp32 [n_tokens][n_heads], both as the attention had and gave them;
                 a row whose lse is not finite adds nothing
-     max_tokens an upper bound of the rows of one sequence (host); rows beyond it add nothing
-   Scores and sums are fp32 (as the attention's: queries enter exactly); no sum's order depends on the call's other
-   sequences, and a call repeated gives the same bits. Bad pages are skipped and recorded in the cache's status. What a page
-   that several sequences of one call share is left with depends on their order, which is not fixed: sequences that share
-   pages take calls of their own, one after the other. */
+     max_tokens an upper bound of the rows of one sequence (host); rows beyond it add nothing. With n_tokens, where that
+                is less, it chooses among kernels for up to 8, up to 16 and more query rows a KV head
+   Scores and sums are fp32; queries enter the products exactly (in the kernels for up to 16 query rows values below
+   2^-17 of their head's largest: to 2^-25 of it). A call repeated gives the same bits, and no sum's order depends on the
+   call's other sequences but by the kernel that they choose. Bad pages, and positions beyond the page table, are
+   skipped and recorded in the cache's status. What a page that several sequences of one call share is left with
+   depends on their order, which is not fixed: sequences that share pages take calls of their own, one after the other.
+   Calls of 2^30 query rows or 2^31 positions or cache groups are DEC_ERR_UNSUPPORTED, and so are those for which
+   n_kv_heads * (max_pages * page_tokens + n_tokens) / 16 * (min(batch, 256) + n_tokens * n_heads / n_kv_heads / 128)
+   passes 2^32. */
 typedef struct {
   int32_t n_heads;
   dec_rows q;

@@ -288,8 +288,9 @@ class KvqCache:
         """Add the attention weight that cached positions receive from q (with the lse that attention() returned
         for it) to what they have: out = decay * mass + weights, over all rows and the heads of each KV head
         (dec_kvq_mass). mass and out (default: mass itself) are as new_mass() makes them; positions that the
-        rows stand at begin anew. Sequences that share pages take calls of their own, one after the other: within
-        one call their order on such a page is not fixed."""
+        rows stand at begin anew. max_tokens: an upper bound of the rows of one sequence, which also chooses the kernel
+        (default: 1 without cu_tokens; with them n). Sequences that share pages take calls of their own, one after the
+        other: within one call their order on such a page is not fixed."""
         if stream is not None:
             with _on_stream(stream, self.device):
                 return self.attention_mass(q, lse, lengths, table, mass, cu_tokens, max_tokens, causal, scale, decay, out)
