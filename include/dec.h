@@ -525,7 +525,9 @@ dec_status dec_draft_tree(const dec_draft_tree_args* args, void* stream);
    (mass_out may be mass, or share nothing with it). Positions that the call's rows stand at (causal) have had nothing
    before, and where decay is 0 nothing is read. Positions that no row could attend to are left as they are.
      q          bf16 rows of n_heads heads, lse device fp32 [n_tokens][n_heads], both as the attention had and gave them;
-                a row whose lse is not finite adds nothing
+                a row whose lse is not finite adds nothing. A tree's rows see less than causal says: after a step of
+                drafts it is the accepted rows' queries and lse that go in, as a chain at the same lengths, once
+                dec_kvq_move has brought their path into place
      max_tokens an upper bound of the rows of one sequence (host); rows beyond it add nothing. With n_tokens, where that
                 is less, it chooses among kernels for up to 8, up to 16 and more query rows a KV head
    Scores and sums are fp32; queries enter the products exactly (in the kernels for up to 16 query rows values below
@@ -557,7 +559,10 @@ dec_status dec_kvq_mass(const dec_kvq_cache* cache, const dec_kvq_seqs* seqs, co
      count      device int32 [batch]: how many
    seqs: n_tokens is of no interest, cu_tokens NULL and n_tokens == batch. Positions in bad pages (recorded in the
    cache's status) weigh nothing; a sequence whose length is negative (DEC_ERR_ARG) or beyond the page table
-   (DEC_ERR_CAPACITY) keeps none. sinks + recent <= budget. */
+   (DEC_ERR_CAPACITY) keeps none. sinks + recent <= budget.
+   Keys keep the angles of the positions that they had. Rows that are appended behind a list that was moved together
+   need theirs from dec_kvq_append's positions; the engine's steps, which turn a row by its place (dec_step_kvq,
+   and any after dec_kvq_load), must not follow. */
 typedef struct {
   const float* mass; /* fp32 [n_pages][n_kv_heads][page_tokens] */
   int32_t budget;
@@ -690,7 +695,8 @@ int64_t dec_verify_drafts_workspace(int32_t n_tokens);
    per layer, in place of the engine's own bf16 cache (which it neither reads nor writes; an engine
    used only this way can have max_ctx 1 and a rotation table of its caller's). Token b stands at
    position lengths[b] of seqs, is appended there in every layer, and attends to positions 0 ..
-   lengths[b]. lengths are the caller's: add 1 before the next step.
+   lengths[b]. lengths are the caller's: add 1 before the next step. Its rotary position is its place (or lengths[b]
+   and its depth in a tree): sequences that positions were taken from (dec_kvq_heaviest) are not for these steps.
      caches       host array [n_layers] of the engine's KV heads and head_dim
      seqs         cu_tokens NULL, n_tokens == batch <= max_batch. Or, to verify drafts, several token rows a sequence
                   (cu_tokens given): batch counts the rows, n_tokens == batch, max_tokens bounds the rows of one

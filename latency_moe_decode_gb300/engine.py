@@ -232,7 +232,8 @@ class Engine:
         appended at position lengths[b] of the pages table[b]. The caller adds 1 to lengths. With cu_tokens (int32
         [batch + 1]) a sequence has several rows, its last known token and drafts that follow one another or, with
         parents (int32 [rows]), make a tree: ops.verify_drafts takes the step's logits, KvqCache.move its path, and
-        the caller adds its count to lengths. max_tokens: an upper bound of the rows of one sequence."""
+        the caller adds its count to lengths. max_tokens: an upper bound of the rows of one sequence. Rows turn by their
+        place (or depth): sequences that KvqCache.evict has shortened are not for these steps."""
         n = lengths.shape[0]
         if cu_tokens is not None:
             if tokens is None and hidden is None:

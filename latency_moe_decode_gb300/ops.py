@@ -288,7 +288,8 @@ class KvqCache:
         """Add the attention weight that cached positions receive from q (with the lse that attention() returned
         for it) to what they have: out = decay * mass + weights, over all rows and the heads of each KV head
         (dec_kvq_mass). mass and out (default: mass itself) are as new_mass() makes them; positions that the
-        rows stand at begin anew. max_tokens: an upper bound of the rows of one sequence, which also chooses the kernel
+        rows stand at begin anew. A tree's rows go in when their path is accepted and moved into place, as a chain:
+        those rows' q and lse at the same lengths. max_tokens: an upper bound of the rows of one sequence, which also chooses the kernel
         (default: 1 without cu_tokens; with them n). Sequences that share pages take calls of their own, one after the
         other: within one call their order on such a page is not fixed."""
         if stream is not None:
@@ -370,7 +371,8 @@ class KvqCache:
               recent: int = 0, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Bring every sequence down to `budget` positions, in place, its weights with them: heaviest() and move().
         Returns (kept, count); count holds the new lengths. Rows appended later stand there, and keep their rotary
-        positions by append(positions=). Pages in which positions move belong to one sequence."""
+        positions by append(positions=): the engine's steps turn rows by their place and must not follow
+        (Engine.step_kvq, kvq_load). Pages in which positions move belong to one sequence."""
         if stream is not None:
             with _on_stream(stream, self.device):
                 return self.evict(mass, lengths, table, budget, sinks, recent)
