@@ -344,8 +344,8 @@ void dec_destroy(dec_engine* eng);
 
 /* ------------------------------------------------------------------------------------------
    Operators beside the engine: a paged KV cache held in 4 bits, attention over it (for trees of drafted
-   tokens too), what keeps it within a bound, log-probabilities, and the verification of drafts. They keep no state of their own: the caller owns every buffer. Unlike the
-   engine's entry points they take no engine, so:
+   tokens too), what keeps it within a bound, log-probabilities, and the verification of drafts. They keep no state of
+   their own: the caller owns every buffer. Unlike the engine's entry points they take no engine, so:
     - stream == NULL is the legacy default stream; work is queued on `stream`, nothing is
       synchronised, no call allocates device memory, and every call may be captured into a graph;
     - the buffers must live on the current CUDA device (DEC_ERR_ARG when the cache's or the
@@ -638,8 +638,8 @@ dec_status dec_logprobs(const dec_logprobs_args* args, void* stream);
    distributed as the target's own ("vLLM's Kimi K3 Backend Hits 842 Tokens per Second", section "Throughput holds
    across the tested range": verifying speculative drafts). Sequence b's rows are cu_tokens[b] .. cu_tokens[b + 1] - 1:
    row 0 its last known token, every other one a draft with a parent as in dec_draft_tree (parents NULL: each row's
-   parent is the row before, a chain). p_j = softmax(logits of row j / temperature[b]) is the target's distribution
-   after row j, q_j the one that the children of row j were drawn from, independently of one another: row j of
+   parent is the row before, a chain). cu_tokens ascend; where they do not, nothing that comes out is of use.
+   p_j = softmax(logits of row j / temperature[b]) is the target's distribution after row j, q_j the one that the children of row j were drawn from, independently of one another: row j of
    draft_probs, or (draft_probs NULL) certainty of the child's token. From row 0 on, at row j with p = p_j, its
    children c in ascending order:
      uniforms[c] q(tokens[c]) < p(tokens[c]): c is accepted, and it goes on at row c;

@@ -106,12 +106,24 @@ struct Variant {
 template <int HD, int NB>
 Variant streaming(bool tree) {
   using K = AttnCfg<HD, NB>;
-  return Variant{tree ? attention_kernel<HD, NB, true> : attention_kernel<HD, NB>, join_kernel<HD, K::ROWS>, K::THREADS, K::smem(), K::ROWS, K::PART, K::WARPS * K::PART};
+  return Variant{tree ? attention_kernel<HD, NB, true> : attention_kernel<HD, NB>,
+                 join_kernel<HD, K::ROWS>,
+                 K::THREADS,
+                 K::smem(),
+                 K::ROWS,
+                 K::PART,
+                 K::WARPS * K::PART};
 }
 template <int HD>
 Variant prompt(bool tree) {
   using C = PromptCfg<HD>;
-  return Variant{tree ? prompt_kernel<HD, true> : prompt_kernel<HD>, join_kernel<HD, C::ROWS>, C::THREADS, C::smem(), C::ROWS, C::PART, 0};
+  return Variant{tree ? prompt_kernel<HD, true> : prompt_kernel<HD>,
+                 join_kernel<HD, C::ROWS>,
+                 C::THREADS,
+                 C::smem(),
+                 C::ROWS,
+                 C::PART,
+                 0};
 }
 Variant variant_of(int hd, int kind, bool tree) {
   if (hd == 128) return kind == 0 ? streaming<128, 1>(tree) : kind == 1 ? streaming<128, 2>(tree) : prompt<128>(tree);

@@ -108,7 +108,8 @@ __device__ __forceinline__ void row_terms(const MassParams& p, const SeqWork& sw
 // ring with bulk copies (of a group's codes, scales and, where they count, the weights that its positions have), two
 // groups at a time, some ahead, without ever waiting for another warp.
 // Measured (32 query, 8 KV heads of 128, one row a sequence): 16 sequences of 8 k to 32 k 53 us, 3.7 TB/s; issue slots are 62 %
-// full (230 instructions a group, 80 of them make operands of its codes), and no pipe is. Groups loaded into
+// full (230 instructions a group, 80 of them make operands of its codes), and no pipe is: warps wait for their own
+// instructions, two chains of eight dependent products first of all. Groups loaded into
 // registers two ahead took 65, four ahead 64; their old weights loaded where they are needed 61. Comparisons left out where
 // every row sees the whole group changed nothing.
 template <int HD>

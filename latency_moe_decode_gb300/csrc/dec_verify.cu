@@ -267,7 +267,7 @@ __device__ __forceinline__ Two two(float2 f) { return Two{f.x, f.y}; }
 // Weights of a row's logits: 2^(c (x - base) - M) for a whole number M of 32nds near c (m - base) (a row's weights all have the
 // factor 2^(c (m - base) - M) beside exp((x - m) / temperature), which no comparison sees). base is 0, and m where c m passes 256
 // either way: a logit is then within a factor of two of m, so that x - m is exact, or its weight is below 2^-120.
-// c (x - base) is the exact product P + p, p up to 2^-16; with n = round(32 (P - M)) the difference r = P - (M + n / 32) is
+// c (x - base) is the exact product P + p, p up to 2^-15; with n = round(32 (P - M)) the difference r = P - (M + n / 32) is
 // exact, |r| <= 1/64, and the weight is 2^(n / 32) 2^w with w = r + p. The second factor is 1 + g + .., g = w ln 2, by its series to
 // the fourth power (a term of 2^-39.5 is left out); g's first term needs both floats, and so does the table's entry.
 // Against 64-bit mantissas, at temperatures from 1e-35 to 1e6, weights are within 2^-35.4 of themselves.
@@ -327,7 +327,8 @@ __device__ __forceinline__ void put_remote(float2* at, uint32_t cta, float2 v) {
 
 constexpr int kParts = kWalkWarps * kMaxCluster;
 constexpr int kChain = 64;  // values that a lane adds up in one go
-constexpr float kBeside = 0x1p-19f;  // ids whose weight is this near to q Z count as beside the border (twice what the sums are off by, or more)
+// ids whose weight is this near to q Z count as beside the border (twice what the first kernel's sums are off by, or more)
+constexpr float kBeside = 0x1p-19f;
 struct Walk {
   float2 sums[2][4][kParts];  // the parts' sums, of all CTAs (two passes' in turn)
   float2 scan[kWalkWarps];
@@ -356,8 +357,8 @@ struct Rows {
 inline int rows_room(int max_tokens) { return (max_tokens + 31) / 32 * 32 + 32; }
 
 // What bounds it: for few sequences latency (bounds, rows, logits 1.7 us; statistics 1.3; weights and fates 0.8; one pass and its
-// exchange 3 to 4; the id 1), for many the pass's instructions, some 45 a logit, 60 where a refusal's rest is summed as well.
-// A call with rows of 32000 fp32 takes 14 us for one chain of 8, 25 for 64 (59 MB of logits in 10; three passes, 134 instructions a
+// exchange 3 to 4; the id 1), for many the pass's instructions, some 49 a logit, 67 where a refusal's rest is summed as well.
+// A call with rows of 32000 fp32 takes 15 us for one chain of 8, 25 for 64 (59 MB of logits in 10; three passes, 134 instructions a
 // logit, took 65), 24 for 16 trees of up to 64 rows in bf16.
 template <bool BF16, int CL>
 __global__ void __launch_bounds__(kWalkThreads, 1) walk_kernel(const Params p) {
